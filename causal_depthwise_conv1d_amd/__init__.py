@@ -12,6 +12,9 @@ Low level (same names as the C ABI):
     ccv_bwd(args, stream=None), ccv_bwd_check(args), ccv_bwd_plan(args),
     ccv_bwd_workspace_size(args),
     ccv_status_str(code), ccv_abi_version()
+    ccv_delta_fwd, ccv_delta_bwd, ccv_delta_update, ccv_norm_fwd, ccv_norm_bwd and
+    ccv_seq_tables (args, stream=None), their ccv_*_check(args) and, where they need a
+    workspace, ccv_*_workspace_size(args)
 High level (the full-sequence contract of Ch.4 "Dao interface and source map",
 section "Contract of the full-sequence interface"; and the update kernel of the
 same page's section "Reading the source along the call chain"):
@@ -24,6 +27,15 @@ same page's section "Reading the source along the call chain"):
     causal_conv1d_fn(x, weight, bias=None, seq_idx=None, initial_states=None,
                      return_final_states=False, final_states_out=None, activation=None)
         (differentiable: a torch.autograd.Function over the forward and backward)
+The operators of a gated linear-attention layer around the conv:
+    gated_delta_rule_fwd(q, k, v, g, beta, scale=None, cu_seqlens=None,
+                         initial_state=None, return_final_state=False, ...)
+    gated_delta_rule_bwd(q, k, v, g, beta, dout, ...)
+    gated_delta_rule_fn(...)            (differentiable)
+    gated_delta_rule_update(q, k, v, g, beta, state, state_indices=None, ...)
+    layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, ...), layer_norm_bwd(...),
+    layer_norm_fn(...)                  (differentiable)
+    sequence_tables(lengths, total)     -> (cu_seqlens, seq_idx, positions)
 """
 from __future__ import annotations
 
@@ -49,6 +61,7 @@ STATUS = {
 CCV_BWD_STATIC_SCRATCH_BYTES = 64 << 20
 DTYPE_CODE = {torch.float32: CCV_F32, torch.float16: CCV_F16, torch.bfloat16: CCV_BF16}
 
+_I64x2 = ctypes.c_int64 * 2
 _I64x3 = ctypes.c_int64 * 3
 
 
@@ -131,6 +144,87 @@ class ccv_plan_t(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class _Args(ctypes.Structure):
+    """A struct whose first field is its own size."""
+
+    def __init__(self, **kw):
+        super().__init__(**kw)
+        self.struct_size = ctypes.sizeof(type(self))
+
+
+def _strided(*names):
+    """(pointer, three strides) field pairs."""
+    out = []
+    for n, s in names:
+        out += [(n, ctypes.c_void_p), (s, _I64x3)]
+    return out
+
+
+_DELTA_SIZES = [("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64), ("Dk", ctypes.c_int64), ("Dv", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("beta_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+_DELTA_INPUTS = _strided(("q", "q_stride"), ("k", "k_stride"), ("v", "v_stride"), ("g", "g_stride"),
+                         ("beta", "beta_stride"))
+
+
+class ccv_delta_fwd_args_t(_Args):
+    """Mirror of ``ccv_delta_fwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("N", ctypes.c_int64),
+                *_DELTA_SIZES, *_DELTA_INPUTS, ("cu_seqlens", ctypes.c_void_p),
+                *_strided(("initial_state", "init_stride"), ("final_state", "final_stride"), ("out", "out_stride")),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ccv_delta_bwd_args_t(_Args):
+    """Mirror of ``ccv_delta_bwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("N", ctypes.c_int64),
+                *_DELTA_SIZES, *_DELTA_INPUTS, ("cu_seqlens", ctypes.c_void_p),
+                *_strided(("initial_state", "init_stride"), ("dout", "dout_stride"), ("dfinal_state", "dfinal_stride"),
+                          ("dq", "dq_stride"), ("dk", "dk_stride"), ("dv", "dv_stride"), ("dg", "dg_stride"),
+                          ("dbeta", "dbeta_stride"), ("dinitial_state", "dinit_stride")),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ccv_delta_update_args_t(_Args):
+    """Mirror of ``ccv_delta_update_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("B", ctypes.c_int64), ("L", ctypes.c_int64),
+                ("slots", ctypes.c_int64), *_DELTA_SIZES, *_DELTA_INPUTS, ("state_indices", ctypes.c_void_p),
+                *_strided(("state", "state_stride"), ("out", "out_stride"))]
+
+
+class ccv_norm_fwd_args_t(_Args):
+    """Mirror of ``ccv_norm_fwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("n0", ctypes.c_int64), ("n1", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", _I64x2), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_stride", _I64x2), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class ccv_norm_bwd_args_t(_Args):
+    """Mirror of ``ccv_norm_bwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("n0", ctypes.c_int64), ("n1", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", _I64x2), ("weight", ctypes.c_void_p),
+                ("dout", ctypes.c_void_p), ("dout_stride", _I64x2), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_stride", _I64x2), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ccv_seq_tables_args_t(_Args):
+    """Mirror of ``ccv_seq_tables_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("N", ctypes.c_int64), ("total", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("seq_idx", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p)]
+
+
+_LAYER_CALLS = {
+    "ccv_delta_fwd": (ccv_delta_fwd_args_t, True), "ccv_delta_bwd": (ccv_delta_bwd_args_t, True),
+    "ccv_delta_update": (ccv_delta_update_args_t, False), "ccv_norm_fwd": (ccv_norm_fwd_args_t, False),
+    "ccv_norm_bwd": (ccv_norm_bwd_args_t, True), "ccv_seq_tables": (ccv_seq_tables_args_t, False),
+}
+
+
 class CcvError(RuntimeError):
     def __init__(self, status: int, where: str = "ccv_fwd"):
         self.status = status
@@ -181,6 +275,14 @@ def lib() -> ctypes.CDLL:
         L.ccv_status_str.restype = ctypes.c_char_p
         L.ccv_abi_version.argtypes = []
         L.ccv_abi_version.restype = ctypes.c_int
+        for name, (args_t, workspace) in _LAYER_CALLS.items():
+            A = ctypes.POINTER(args_t)
+            call, check = getattr(L, name), getattr(L, name + "_check")
+            call.argtypes, call.restype = [A, ctypes.c_void_p], ctypes.c_int
+            check.argtypes, check.restype = [A], ctypes.c_int
+            if workspace:
+                size = getattr(L, name + "_workspace_size")
+                size.argtypes, size.restype = [A], ctypes.c_int64
         if L.ccv_abi_version() != CCV_ABI_VERSION:
             raise RuntimeError("libccv ABI version mismatch")
         _lib = L
@@ -263,6 +365,75 @@ def ccv_status_str(status: int) -> str:
 
 def ccv_abi_version() -> int:
     return lib().ccv_abi_version()
+
+
+def ccv_delta_fwd(args: ccv_delta_fwd_args_t, stream=None) -> int:
+    """Enqueue the gated delta rule's forward on `stream`; returns the status code."""
+    return lib().ccv_delta_fwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_delta_fwd_check(args: ccv_delta_fwd_args_t) -> int:
+    return lib().ccv_delta_fwd_check(ctypes.byref(args))
+
+
+def ccv_delta_fwd_workspace_size(args: ccv_delta_fwd_args_t) -> int:
+    """Workspace bytes the forward needs (>= 0), or a negative status."""
+    return lib().ccv_delta_fwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_delta_bwd(args: ccv_delta_bwd_args_t, stream=None) -> int:
+    """Enqueue the gated delta rule's backward on `stream`; returns the status code."""
+    return lib().ccv_delta_bwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_delta_bwd_check(args: ccv_delta_bwd_args_t) -> int:
+    return lib().ccv_delta_bwd_check(ctypes.byref(args))
+
+
+def ccv_delta_bwd_workspace_size(args: ccv_delta_bwd_args_t) -> int:
+    """Workspace bytes the backward needs (>= 0), or a negative status."""
+    return lib().ccv_delta_bwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_delta_update(args: ccv_delta_update_args_t, stream=None) -> int:
+    """Enqueue new steps against cached states on `stream`; returns the status code."""
+    return lib().ccv_delta_update(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_delta_update_check(args: ccv_delta_update_args_t) -> int:
+    return lib().ccv_delta_update_check(ctypes.byref(args))
+
+
+def ccv_norm_fwd(args: ccv_norm_fwd_args_t, stream=None) -> int:
+    """Enqueue layer norm on `stream`; returns the status code."""
+    return lib().ccv_norm_fwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_norm_fwd_check(args: ccv_norm_fwd_args_t) -> int:
+    return lib().ccv_norm_fwd_check(ctypes.byref(args))
+
+
+def ccv_norm_bwd(args: ccv_norm_bwd_args_t, stream=None) -> int:
+    """Enqueue layer norm's backward on `stream`; returns the status code."""
+    return lib().ccv_norm_bwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_norm_bwd_check(args: ccv_norm_bwd_args_t) -> int:
+    return lib().ccv_norm_bwd_check(ctypes.byref(args))
+
+
+def ccv_norm_bwd_workspace_size(args: ccv_norm_bwd_args_t) -> int:
+    """Workspace bytes the backward needs (>= 0), or a negative status."""
+    return lib().ccv_norm_bwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_seq_tables(args: ccv_seq_tables_args_t, stream=None) -> int:
+    """Enqueue the tables of a packed row on `stream`; returns the status code."""
+    return lib().ccv_seq_tables(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_seq_tables_check(args: ccv_seq_tables_args_t) -> int:
+    return lib().ccv_seq_tables_check(ctypes.byref(args))
 
 
 # ---- tensors -> args -------------------------------------------------------------------
@@ -602,3 +773,401 @@ def causal_conv1d_fn(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
     causal_conv1d_bwd)."""
     return _CausalConv1dFn.apply(x, weight, bias, seq_idx, initial_states, return_final_states,
                                  final_states_out, activation)
+
+
+# ---- the gated delta rule ------------------------------------------------------------------
+
+def _same_device(x, **others):
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a GPU (there is no CPU path)")
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} must be on {x.device}")
+
+
+def _delta_sizes(q, k, v, g, beta):
+    """(B, L, Hk, Hv, Dk, Dv) of the five inputs, checked against each other."""
+    if q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[:2] != q.shape[:2]:
+        raise ValueError("expected q and k [B, L, Hk, Dk] and v [B, L, Hv, Dv]")
+    B, L, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    if Hk < 1 or Hv < 1 or Hv % Hk:
+        raise ValueError("the value heads must be a multiple of the key heads")
+    if not 1 <= Dk <= 128 or Dv < 1:
+        raise ValueError("key heads must be 1 to 128 wide, value heads at least 1")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have one dtype")
+    for name, t in (("g", g), ("beta", beta)):
+        if tuple(t.shape) != (B, L, Hv):
+            raise ValueError(f"{name} must be [B, L, Hv]")
+    for name, t in (("q", q), ("g", g), ("beta", beta)):
+        if t.dtype not in DTYPE_CODE:
+            raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    return B, L, Hk, Hv, Dk, Dv
+
+
+def _unit_heads(t):
+    """t as it is when its last dimension has unit stride, else a contiguous copy."""
+    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
+
+
+def _delta_states(name, t, shape):
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be float32 {list(shape)}")
+    return t
+
+
+def _put(a, name, stride, t):
+    """A tensor's pointer and leading strides into fields of an args struct."""
+    if t is not None:
+        setattr(a, name, t.data_ptr())
+        setattr(a, stride, _I64x3(*t.stride()[:3]))
+
+
+def _delta_args(a, q, k, v, g, beta, scale):
+    a.B, a.L = q.shape[:2]
+    a.Hk, a.Dk = q.shape[2:]
+    a.Hv, a.Dv = v.shape[2:]
+    a.x_dtype, a.g_dtype, a.beta_dtype = DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype]
+    a.scale = q.shape[3] ** -0.5 if scale is None else scale
+    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
+        _put(a, name, name + "_stride", t)
+    return a
+
+
+def _delta_sequences(a, cu_seqlens, B):
+    """The packed sequences into the args; returns how many sequences have states."""
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [N + 1]")
+    if B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1")
+    a.N = cu_seqlens.numel() - 1
+    a.cu_seqlens = cu_seqlens.data_ptr()
+    return a.N
+
+
+def _workspace(size, where, device):
+    _raise(int(size) if size < 0 else 0, where)
+    return torch.empty(max(int(size), 16), dtype=torch.uint8, device=device)
+
+
+def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                         initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False,
+                         final_state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         info: Optional[dict] = None):
+    """The gated delta rule over whole sequences on the GPU.
+
+    With a state S [Dk, Dv] per sequence and value head:
+    ``S <- e^g S; u = beta (v - S^T k); S <- S + k u^T; out = scale S^T q``.
+
+    q, k [B, L, Hk, Dk] and v [B, L, Hv, Dv] in one dtype (Hv a multiple of Hk, Dk at most
+    128); g (log decay) and beta [B, L, Hv] in any of the three dtypes each.  Strided views
+    are used as they are when a head's elements are unit-stride; others are copied
+    (``info["copied"]`` lists them).  ``scale`` defaults to Dk^-1/2.  ``cu_seqlens`` (int32
+    [N + 1], on the GPU) packs N sequences in one row (B = 1).  States are float32
+    [sequences, Hv, Dk, Dv]; ``final_state_out`` may be ``initial_state`` itself.  Returns
+    out [B, L, Hv, Dv] in v's dtype, or (out, final_state).
+    """
+    if final_state_out is not None and not return_final_state:
+        raise ValueError("final_state_out given but return_final_state is False")
+    B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    _same_device(q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                 final_state_out=final_state_out, out=out)
+    given = {"q": q, "k": k, "v": v, "initial_state": initial_state}
+    q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
+    a = _delta_args(ccv_delta_fwd_args_t(), q, k, v, g, beta, scale)
+    shape = (_delta_sequences(a, cu_seqlens, B), Hv, Dk, Dv)
+    if _delta_states("initial_state", initial_state, shape) is not None:
+        initial_state = _unit_heads(initial_state)
+    if out is None:
+        out = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=v.device)
+    elif out.dtype != v.dtype or tuple(out.shape) != (B, L, Hv, Dv) or (out.stride(-1) != 1 and Dv > 1):
+        raise ValueError("out must be [B, L, Hv, Dv] in v's dtype with unit stride in its last dimension")
+    ht = None
+    if return_final_state:
+        ht = torch.empty(shape, dtype=torch.float32, device=v.device) if final_state_out is None else final_state_out
+        _delta_states("final_state_out", ht, shape)
+        if ht.stride(-1) != 1 and Dv > 1:
+            raise ValueError("final_state_out must have unit stride in its last dimension")
+    _put(a, "initial_state", "init_stride", initial_state)
+    _put(a, "final_state", "final_stride", ht)
+    _put(a, "out", "out_stride", out)
+    ws = _workspace(ccv_delta_fwd_workspace_size(a), "ccv_delta_fwd", v.device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    with torch.cuda.device(v.device):
+        st = ccv_delta_fwd(a)
+    _raise(st, "ccv_delta_fwd")
+    if info is not None:
+        now = {"q": q, "k": k, "v": v, "initial_state": initial_state}
+        info["copied"] = [n for n in given if given[n] is not now[n]]
+    return (out, ht) if return_final_state else out
+
+
+def gated_delta_rule_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         dout: torch.Tensor, scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                         initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                         return_dinitial_state: bool = False):
+    """Gradients of gated_delta_rule_fwd: (dq, dk, dv, dg, dbeta, dinitial_state).
+
+    dout [B, L, Hv, Dv] in v's dtype; dfinal_state float32 like the states, or None (zeros).
+    Each gradient has its input's shape and dtype, contiguous; dinitial_state (float32)
+    only with return_dinitial_state, which needs initial_state.
+    """
+    B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    _same_device(q, k=k, v=v, g=g, beta=beta, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                 dfinal_state=dfinal_state)
+    if dout.dtype != v.dtype or dout.shape != v.shape:
+        raise ValueError("dout must be [B, L, Hv, Dv] in v's dtype")
+    if return_dinitial_state and initial_state is None:
+        raise ValueError("dinitial_state needs initial_state")
+    q, k, v, dout = _unit_heads(q), _unit_heads(k), _unit_heads(v), _unit_heads(dout)
+    a = _delta_args(ccv_delta_bwd_args_t(), q, k, v, g, beta, scale)
+    shape = (_delta_sequences(a, cu_seqlens, B), Hv, Dk, Dv)
+    if _delta_states("initial_state", initial_state, shape) is not None:
+        initial_state = _unit_heads(initial_state)
+    if _delta_states("dfinal_state", dfinal_state, shape) is not None:
+        dfinal_state = _unit_heads(dfinal_state)
+    dq, dk, dv, dg, db = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v, g, beta))
+    dh = torch.empty(shape, dtype=torch.float32, device=v.device) if return_dinitial_state else None
+    for name, stride, t in (("initial_state", "init_stride", initial_state), ("dout", "dout_stride", dout),
+                            ("dfinal_state", "dfinal_stride", dfinal_state), ("dq", "dq_stride", dq),
+                            ("dk", "dk_stride", dk), ("dv", "dv_stride", dv), ("dg", "dg_stride", dg),
+                            ("dbeta", "dbeta_stride", db), ("dinitial_state", "dinit_stride", dh)):
+        _put(a, name, stride, t)
+    ws = _workspace(ccv_delta_bwd_workspace_size(a), "ccv_delta_bwd", v.device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    with torch.cuda.device(v.device):
+        st = ccv_delta_bwd(a)
+    _raise(st, "ccv_delta_bwd")
+    return dq, dk, dv, dg, db, dh
+
+
+class _GatedDeltaRuleFn(torch.autograd.Function):
+    """Forward and backward through the C ABI; saves the inputs, and the backward makes
+    everything else again."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, scale, cu_seqlens, initial_state, return_final_state):
+        res = gated_delta_rule_fwd(q, k, v, g, beta, scale, cu_seqlens, initial_state, return_final_state)
+        ctx.save_for_backward(q, k, v, g, beta, cu_seqlens, initial_state)
+        ctx.scale = scale
+        ctx.return_final_state = return_final_state
+        ctx.set_materialize_grads(False)
+        return res
+
+    @staticmethod
+    def backward(ctx, dout, *rest):
+        q, k, v, g, beta, cu_seqlens, initial_state = ctx.saved_tensors
+        dht = rest[0] if ctx.return_final_state and rest else None
+        dout = torch.zeros_like(v) if dout is None else dout.to(v.dtype)
+        want_dh = initial_state is not None and ctx.needs_input_grad[7]
+        dq, dk, dv, dg, db, dh = gated_delta_rule_bwd(q, k, v, g, beta, dout, ctx.scale, cu_seqlens, initial_state,
+                                                      None if dht is None else dht.float(), want_dh)
+        return dq, dk, dv, dg, db, None, None, dh, None
+
+
+def gated_delta_rule_fn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                        scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                        initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False):
+    """Differentiable gated delta rule (gated_delta_rule_fwd, with gradients for q, k, v, g,
+    beta and initial_state through gated_delta_rule_bwd)."""
+    return _GatedDeltaRuleFn.apply(q, k, v, g, beta, scale, cu_seqlens, initial_state, return_final_state)
+
+
+def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                            state: torch.Tensor, scale: Optional[float] = None,
+                            state_indices: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """New steps of the gated delta rule against cached states, advanced in place.
+
+    q, k [B, Hk, Dk], v [B, Hv, Dv], g and beta [B, Hv] (one step), or with a dimension of L
+    steps after B; state float32 [slots, Hv, Dk, Dv].  Row b uses slot ``state_indices[b]``
+    (int32, on the GPU), or slot b without; a row whose index is outside [0, slots) is idle:
+    its outputs are zeros.  Two rows may not use one slot.  Returns out with v's shape.
+    """
+    one = q.dim() == 3
+    if one:
+        q, k, v, g, beta = (t.unsqueeze(1) for t in (q, k, v, g, beta))
+    B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    _same_device(q, k=k, v=v, g=g, beta=beta, state=state, state_indices=state_indices, out=out)
+    if state.dtype != torch.float32 or state.dim() != 4 or tuple(state.shape[1:]) != (Hv, Dk, Dv):
+        raise ValueError("state must be float32 [slots, Hv, Dk, Dv]")
+    if state.stride(-1) != 1 and Dv > 1:
+        raise ValueError("state must have unit stride in its last dimension")
+    if state_indices is not None and (state_indices.dtype != torch.int32 or tuple(state_indices.shape) != (B,)
+                                      or not state_indices.is_contiguous()):
+        raise ValueError("state_indices must be contiguous int32 [B]")
+    if state_indices is None and B > state.shape[0]:
+        raise ValueError("more rows than states")
+    q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
+    if out is None:
+        o = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=v.device)
+    else:
+        o = out.unsqueeze(1) if one else out
+        if o.dtype != v.dtype or tuple(o.shape) != (B, L, Hv, Dv) or (o.stride(-1) != 1 and Dv > 1):
+            raise ValueError("out must have v's shape and dtype with unit stride in its last dimension")
+    a = _delta_args(ccv_delta_update_args_t(), q, k, v, g, beta, scale)
+    a.slots = state.shape[0]
+    a.state_indices = _ptr(state_indices)
+    _put(a, "state", "state_stride", state)
+    _put(a, "out", "out_stride", o)
+    with torch.cuda.device(v.device):
+        st = ccv_delta_update(a)
+    _raise(st, "ccv_delta_update")
+    return o.squeeze(1) if one else o
+
+
+# ---- layer norm ------------------------------------------------------------------------------
+
+def _norm_rows(x):
+    """x as [n0, n1, width] with unit stride along the width, copied only where its strides
+    allow no such view."""
+    if x.dim() < 1:
+        raise ValueError("x needs a last dimension to be normalised")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        x = x.contiguous()
+    if x.dim() <= 3:
+        return x[(None,) * (3 - x.dim())]
+    try:
+        return x.view(-1, x.shape[-2], x.shape[-1])
+    except RuntimeError:
+        return x.contiguous().view(-1, x.shape[-2], x.shape[-1])
+
+
+def _norm_weights(x, weight, bias):
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (tuple(t.shape) != (x.shape[-1],) or t.dtype not in DTYPE_CODE):
+            raise ValueError(f"{name} must be [width] in float32, float16 or bfloat16")
+    if weight is not None and bias is not None and bias.dtype != weight.dtype:
+        raise ValueError("bias must have the weight's dtype")
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"x must be float32, float16 or bfloat16, not {x.dtype}")
+    return (t if t is None else t.contiguous() for t in (weight, bias))
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5, return_stats: bool = False, out: Optional[torch.Tensor] = None):
+    """Layer norm over x's last dimension on the GPU: (x - mean) rstd weight + bias.
+
+    x [..., width], any strides (views of up to three dimensions that are unit-stride along
+    the width are used as they are); weight and bias [width] or None.  Returns out
+    (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [...].
+    """
+    weight, bias = _norm_weights(x, weight, bias)
+    _same_device(x, weight=weight, bias=bias, out=out)
+    rows = _norm_rows(x)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous with x's shape and dtype")
+    o = out.view(rows.shape) if out.numel() else out.reshape(rows.shape)
+    stats = [torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2)] if return_stats else [None] * 2
+    a = ccv_norm_fwd_args_t()
+    a.n0, a.n1, a.width = rows.shape
+    a.x_dtype = DTYPE_CODE[x.dtype]
+    a.w_dtype = DTYPE_CODE[(weight if weight is not None else bias if bias is not None else x).dtype]
+    a.eps = eps
+    a.x, a.x_stride = rows.data_ptr(), _I64x2(*rows.stride()[:2])
+    a.weight, a.bias = _ptr(weight), _ptr(bias)
+    a.out, a.out_stride = o.data_ptr(), _I64x2(*o.stride()[:2])
+    a.mean, a.rstd = _ptr(stats[0]), _ptr(stats[1])
+    with torch.cuda.device(x.device):
+        st = ccv_norm_fwd(a)
+    _raise(st, "ccv_norm_fwd")
+    return (out, *stats) if return_stats else out
+
+
+def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tensor, mean: torch.Tensor,
+                   rstd: torch.Tensor, want_dx: bool = True, want_dweight: bool = True, want_dbias: bool = True,
+                   weight_dtype: Optional[torch.dtype] = None):
+    """Gradients of layer_norm_fwd: (dx, dweight, dbias), None where not wanted.
+
+    dout has x's shape and dtype; mean and rstd are the forward's.  dweight and dbias come in
+    ``weight_dtype`` (the weight's dtype by default, x's without a weight), summed in float32
+    in a fixed order.
+    """
+    weight, _ = _norm_weights(x, weight, None)
+    _same_device(x, weight=weight, dout=dout, mean=mean, rstd=rstd)
+    if dout.dtype != x.dtype or dout.shape != x.shape:
+        raise ValueError("dout must have x's shape and dtype")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 with x's leading shape")
+    wd = weight.dtype if weight is not None else weight_dtype or x.dtype
+    if wd not in DTYPE_CODE:
+        raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
+    rows, drows = _norm_rows(x), _norm_rows(dout)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
+    dw = torch.empty(x.shape[-1], dtype=wd, device=x.device) if want_dweight else None
+    db = torch.empty(x.shape[-1], dtype=wd, device=x.device) if want_dbias else None
+    a = ccv_norm_bwd_args_t()
+    a.n0, a.n1, a.width = rows.shape
+    a.x_dtype, a.w_dtype = DTYPE_CODE[x.dtype], DTYPE_CODE[wd]
+    a.x, a.x_stride = rows.data_ptr(), _I64x2(*rows.stride()[:2])
+    a.dout, a.dout_stride = drows.data_ptr(), _I64x2(*drows.stride()[:2])
+    a.weight, a.mean, a.rstd = _ptr(weight), mean.data_ptr(), rstd.data_ptr()
+    if dx is not None:
+        o = dx.view(rows.shape) if dx.numel() else dx.reshape(rows.shape)
+        a.dx, a.dx_stride = o.data_ptr(), _I64x2(*o.stride()[:2])
+    a.dweight, a.dbias = _ptr(dw), _ptr(db)
+    ws = _workspace(ccv_norm_bwd_workspace_size(a), "ccv_norm_bwd", x.device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    with torch.cuda.device(x.device):
+        st = ccv_norm_bwd(a)
+    _raise(st, "ccv_norm_bwd")
+    return dx, dw, db
+
+
+class _LayerNormFn(torch.autograd.Function):
+    """Forward and backward through the C ABI; saves x, weight and the rows' statistics."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        out, mean, rstd = layer_norm_fwd(x, weight, bias, eps, return_stats=True)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = layer_norm_bwd(x, weight, dout.to(x.dtype), mean, rstd, need[0], need[1], need[2], ctx.bias_dtype)
+        return dx, dw, db, None
+
+
+def layer_norm_fn(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable layer norm (layer_norm_fwd, with gradients for x, weight and bias
+    through layer_norm_bwd)."""
+    return _LayerNormFn.apply(x, weight, bias, eps)
+
+
+# ---- sequence tables -------------------------------------------------------------------------
+
+def sequence_tables(lengths: torch.Tensor, total: int):
+    """The tables of a row of ``total`` steps that packs sequences of the given lengths
+    (int32 [N], on the GPU): (cu_seqlens [N + 1], seq_idx [1, total], positions [1, total]),
+    all int32, made on the GPU without a look by the host.
+
+    seq_idx is what causal_conv1d_fwd takes and cu_seqlens what gated_delta_rule_fwd takes.
+    Steps past the last sequence have seq_idx -1 and position 0; lengths that do not fit
+    are cut at ``total``, negative ones count as 0.
+    """
+    if lengths.dtype != torch.int32 or lengths.dim() != 1 or not lengths.is_contiguous():
+        raise ValueError("lengths must be contiguous int32 [N]")
+    if total < 0:
+        raise ValueError("total must not be negative")
+    _same_device(lengths)
+    cu = torch.empty(lengths.numel() + 1, dtype=torch.int32, device=lengths.device)
+    seq, pos = (torch.empty(1, total, dtype=torch.int32, device=lengths.device) for _ in range(2))
+    a = ccv_seq_tables_args_t()
+    a.N, a.total = lengths.numel(), total
+    a.lengths, a.cu_seqlens, a.seq_idx, a.positions = _ptr(lengths), cu.data_ptr(), seq.data_ptr(), pos.data_ptr()
+    with torch.cuda.device(lengths.device):
+        st = ccv_seq_tables(a)
+    _raise(st, "ccv_seq_tables")
+    return cu, seq, pos

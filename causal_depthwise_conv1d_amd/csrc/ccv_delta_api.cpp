@@ -1,0 +1,440 @@
+// ccv_delta_api.cpp -- C ABI of the gated delta rule: argument checks, the workspace's
+// layout and the launches.  The operation and its contract are stated in ccv.h beside
+// ccv_delta_fwd, ccv_delta_bwd and ccv_delta_update.  Host code; nothing here touches a
+// device except the launches.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ccv.h"
+#include "ccv_checks.hpp"
+#include "ccv_delta_launch.hpp"
+#include "ccv_launch.hpp"
+
+namespace {
+
+using namespace ccv;
+using namespace ccv::checks;
+
+// A strided view: up to four extents with their element strides, outermost first, the
+// innermost of unit stride.
+struct View {
+  const void* p;
+  int64_t n[4], s[4];
+  int elt;
+};
+
+View view(const void* p, int64_t a, int64_t b, int64_t c, int64_t d, const int64_t s[3], int elt) {
+  return {p, {a, b, c, d}, {s[0], s[1], s[2], 1}, elt};
+}
+
+// A negative stride, or offsets that do not fit.
+int check_view(const View& v) {
+  int64_t total = 0;
+  for (int i = 0; i < 4; ++i) {
+    if (v.s[i] < 0) return CCV_E_LAYOUT;
+    if (v.n[i] <= 1) continue;
+    int64_t p;
+    if (__builtin_mul_overflow(v.n[i] - 1, v.s[i], &p) || __builtin_add_overflow(total, p, &total)) return CCV_E_SHAPE;
+  }
+  return fits_bytes(total, v.elt) ? CCV_OK : CCV_E_SHAPE;
+}
+
+// No two indexes share an element, by the sufficient test of checks::non_overlapping.
+bool apart(const View& v) {
+  int o[4] = {0, 1, 2, 3};
+  std::sort(o, o + 4, [&](int p, int q) { return v.s[p] < v.s[q]; });
+  int64_t reach = 0;
+  for (int i : o) {
+    if (v.n[i] <= 1) continue;
+    if (v.s[i] <= reach) return false;
+    reach += (v.n[i] - 1) * v.s[i];
+  }
+  return true;
+}
+
+int check_written(const View& v) {
+  const int st = check_view(v);
+  return st != CCV_OK ? st : apart(v) ? CCV_OK : CCV_E_LAYOUT;
+}
+
+// Rows of `unit` elements move as whole vectors of `bytes` bytes.
+bool vectors(const View& v, int unit, int bytes) {
+  if (v.n[3] % unit != 0 || ((uintptr_t)v.p & (uintptr_t)(bytes - 1)) != 0) return false;
+  for (int i = 0; i < 3; ++i)
+    if (v.n[i] > 1 && (v.s[i] * v.elt) % bytes != 0) return false;
+  return true;
+}
+
+bool dtype_ok(int d) { return d >= 0 && d <= 2; }
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Hands out 256-byte aligned pieces of the workspace; with a null base it only measures.
+struct Pieces {
+  char* base;
+  int64_t used;
+  bool over;
+  template <class T>
+  void take(T** p, int64_t count, int64_t each) {
+    int64_t n;
+    if (__builtin_mul_overflow(count, each, &n) || __builtin_mul_overflow(n, (int64_t)sizeof(T), &n) || n > INT64_MAX / 64) {
+      over = true;
+      return;
+    }
+    *p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    if (__builtin_add_overflow(used, round_up(n, 256), &used)) over = true;
+  }
+};
+
+// The sizes that forward and backward share.
+struct Sizes {
+  int64_t B, L, N, Hk, Hv, Dk, Dv;
+  const int32_t* cu;
+  int x_dtype, g_dtype, b_dtype;
+};
+
+int check_sizes(const Sizes& z) {
+  if (z.B < 0 || z.L < 0 || z.N < 0 || z.Hk < 1 || z.Hv < 1 || z.Dk < 1 || z.Dv < 1) return CCV_E_SHAPE;
+  if (z.Hv % z.Hk != 0) return CCV_E_SHAPE;
+  if (z.cu ? z.B != 1 : z.N != 0) return CCV_E_SHAPE;
+  if (!dtype_ok(z.x_dtype) || !dtype_ok(z.g_dtype) || !dtype_ok(z.b_dtype)) return CCV_E_DTYPE;
+  if (z.Dk > kDeltaMaxDk) return CCV_E_UNSUPPORTED;
+  const int64_t most = INT32_MAX - 2 * kDeltaChunk;
+  if (z.L > most || z.B > most || z.N > most || z.Hv > most || z.Dv > most) return CCV_E_SHAPE;
+  return CCV_OK;
+}
+
+// Fills the counts and the workspace's pieces; *bytes is what they take.
+int plan(const Sizes& z, bool bwd, void* ws, DeltaArgs* a, int* nt, int64_t* bytes) {
+  *a = DeltaArgs{};
+  const bool packed = z.cu && z.L > 0;
+  a->cu = z.cu;
+  a->packed = packed;
+  a->L = z.L;
+  a->nseq = (int32_t)(z.cu ? z.N : z.B);
+  a->chunks_per_row = packed ? 0 : (int32_t)((z.L + kDeltaChunk - 1) / kDeltaChunk);
+  const int64_t nch = packed ? z.L / kDeltaChunk + z.N + 1 : z.B * a->chunks_per_row;
+  a->Hk = (int32_t)z.Hk;
+  a->Hv = (int32_t)z.Hv;
+  a->Dk = (int32_t)z.Dk;
+  a->Dv = (int32_t)z.Dv;
+  a->Dkp = z.Dk <= 64 ? 64 : 128;
+  a->Dvp = (int32_t)round_up(z.Dv, 32);
+  a->x_dtype = z.x_dtype;
+  a->g_dtype = z.g_dtype;
+  a->b_dtype = z.b_dtype;
+  int64_t heads, groups;
+  if (__builtin_mul_overflow(nch, z.Hv, &heads) || heads > INT32_MAX) return CCV_E_SHAPE;
+  if (__builtin_mul_overflow((int64_t)a->nseq + 1, z.Hv, &groups) || groups > INT32_MAX / 2) return CCV_E_SHAPE;
+  groups = round_up(groups, 8);
+  if (groups * (a->Dvp / 16) > INT32_MAX) return CCV_E_SHAPE;
+  a->nchunks = (int32_t)nch;
+  *nt = z.x_dtype == CCV_F32 || groups * (a->Dvp / 32) < 512 ? 1 : 2;
+  a->slices = a->Dvp / (16 * *nt);
+
+  Pieces w{static_cast<char*>(ws), 0, false};
+  if (packed) {
+    w.take(&a->table, nch, 4);
+    w.take(&a->cstart, a->nseq + 2, 2);
+  }
+  w.take(&a->W, heads, 4096);
+  w.take(&a->P, heads, 4096);
+  w.take(&a->dec, heads, kDeltaDec);
+  if (bwd) {
+    w.take(&a->WT, heads, 4096);
+    w.take(&a->S, heads, (int64_t)a->Dkp * a->Dvp);
+    w.take(&a->dS, heads, (int64_t)a->Dkp * a->Dvp);
+    w.take(&a->N, heads, 64 * (int64_t)a->Dvp);
+    w.take(&a->R, heads, 64 * (int64_t)a->Dvp);
+    w.take(&a->Y, heads, 64 * (int64_t)a->Dvp);
+    w.take(&a->part, heads, a->Dvp / 16 * kDeltaPart);
+  }
+  if (w.over) return CCV_E_SHAPE;
+  *bytes = w.used;
+  return CCV_OK;
+}
+
+void copy3(int64_t to[3], const int64_t from[3]) {
+  for (int i = 0; i < 3; ++i) to[i] = from[i];
+}
+
+int check_workspace(const void* ws, int64_t given, int64_t need) {
+  if (need == 0) return CCV_OK;
+  if (!ws) return CCV_E_NULL;
+  if (!aligned16(ws)) return CCV_E_LAYOUT;
+  return given < need ? CCV_E_SHAPE : CCV_OK;
+}
+
+// What validate leaves to be launched.
+struct Work {
+  DeltaArgs a;
+  int nt;
+  int64_t bytes;
+  bool chunks, states;     // there are steps; there are states to be written without any
+};
+
+int validate_fwd(const ccv_delta_fwd_args_t* p, Work* w, bool with_ws) {
+  if (!p) return CCV_E_NULL;
+  if (p->struct_size != (int64_t)sizeof(ccv_delta_fwd_args_t)) return CCV_E_ABI;
+  const Sizes z{p->B, p->L, p->N, p->Hk, p->Hv, p->Dk, p->Dv, p->cu_seqlens, p->x_dtype, p->g_dtype, p->beta_dtype};
+  int st = check_sizes(z);
+  if (st != CCV_OK) return st;
+  st = plan(z, false, with_ws ? p->workspace : nullptr, &w->a, &w->nt, &w->bytes);
+  if (st != CCV_OK) return st;
+  DeltaArgs& a = w->a;
+  const int es = elt_size(p->x_dtype);
+  w->chunks = p->B > 0 && p->L > 0;
+  w->states = p->final_state && a.nseq > 0;
+  const View q = view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), k = view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es),
+             v = view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), o = view(p->out, p->B, p->L, p->Hv, p->Dv, p->out_stride, es),
+             g = view(p->g, p->B, p->L, p->Hv, 1, p->g_stride, 4), b = view(p->beta, p->B, p->L, p->Hv, 1, p->beta_stride, 4),
+             h0 = view(p->initial_state, a.nseq, p->Hv, p->Dk, p->Dv, p->init_stride, 4),
+             ht = view(p->final_state, a.nseq, p->Hv, p->Dk, p->Dv, p->final_stride, 4);
+  if (w->chunks) {
+    if (!p->q || !p->k || !p->v || !p->g || !p->beta || !p->out) return CCV_E_NULL;
+    for (const View& x : {q, k, v, g, b})
+      if ((st = check_view(x)) != CCV_OK) return st;
+    if ((st = check_written(o)) != CCV_OK) return st;
+    for (const void* x : {p->q, p->k, p->v, p->g, p->beta, (const void*)p->initial_state, (const void*)p->final_state})
+      if (x == p->out) return CCV_E_ALIAS;
+  }
+  if (p->initial_state && (st = check_view(h0)) != CCV_OK) return st;
+  if (p->final_state) {
+    if ((st = check_written(ht)) != CCV_OK) return st;
+    for (const void* x : {p->q, p->k, p->v, p->g, p->beta})
+      if (x == p->final_state) return CCV_E_ALIAS;
+    if (p->final_state == p->initial_state)      // in place, element by element
+      for (int i = 0; i < 3; ++i)
+        if (ht.n[i] > 1 && ht.s[i] != h0.s[i]) return CCV_E_ALIAS;
+  }
+  if (!w->chunks) w->bytes = 0;
+  if (with_ws && (st = check_workspace(p->workspace, p->workspace_bytes, w->bytes)) != CCV_OK) return st;
+  a.q = p->q;
+  a.k = p->k;
+  a.v = p->v;
+  a.g = p->g;
+  a.beta = p->beta;
+  a.out = p->out;
+  a.h0 = p->initial_state;
+  a.ht = p->final_state;
+  copy3(a.q_s, p->q_stride);
+  copy3(a.k_s, p->k_stride);
+  copy3(a.v_s, p->v_stride);
+  copy3(a.g_s, p->g_stride);
+  copy3(a.b_s, p->beta_stride);
+  copy3(a.o_s, p->out_stride);
+  copy3(a.h0_s, p->init_stride);
+  copy3(a.ht_s, p->final_stride);
+  a.scale = p->scale;
+  a.vec_qk = vectors(q, 8, 16) && vectors(k, 8, 16);
+  a.vec_o = vectors(o, 4, 4 * es);
+  return CCV_OK;
+}
+
+int validate_bwd(const ccv_delta_bwd_args_t* p, Work* w, bool with_ws) {
+  if (!p) return CCV_E_NULL;
+  if (p->struct_size != (int64_t)sizeof(ccv_delta_bwd_args_t)) return CCV_E_ABI;
+  const Sizes z{p->B, p->L, p->N, p->Hk, p->Hv, p->Dk, p->Dv, p->cu_seqlens, p->x_dtype, p->g_dtype, p->beta_dtype};
+  int st = check_sizes(z);
+  if (st != CCV_OK) return st;
+  st = plan(z, true, with_ws ? p->workspace : nullptr, &w->a, &w->nt, &w->bytes);
+  if (st != CCV_OK) return st;
+  DeltaArgs& a = w->a;
+  const int es = elt_size(p->x_dtype);
+  w->chunks = p->B > 0 && p->L > 0;
+  w->states = p->dinitial_state && a.nseq > 0;
+  const View q = view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), k = view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es),
+             v = view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), d = view(p->dout, p->B, p->L, p->Hv, p->Dv, p->dout_stride, es),
+             g = view(p->g, p->B, p->L, p->Hv, 1, p->g_stride, 4), b = view(p->beta, p->B, p->L, p->Hv, 1, p->beta_stride, 4),
+             h0 = view(p->initial_state, a.nseq, p->Hv, p->Dk, p->Dv, p->init_stride, 4),
+             dht = view(p->dfinal_state, a.nseq, p->Hv, p->Dk, p->Dv, p->dfinal_stride, 4),
+             dh0 = view(p->dinitial_state, a.nseq, p->Hv, p->Dk, p->Dv, p->dinit_stride, 4),
+             dq = view(p->dq, p->B, p->L, p->Hk, p->Dk, p->dq_stride, es), dk = view(p->dk, p->B, p->L, p->Hk, p->Dk, p->dk_stride, es),
+             dv = view(p->dv, p->B, p->L, p->Hv, p->Dv, p->dv_stride, es), dg = view(p->dg, p->B, p->L, p->Hv, 1, p->dg_stride, 4),
+             db = view(p->dbeta, p->B, p->L, p->Hv, 1, p->dbeta_stride, 4);
+  if (p->dinitial_state && !p->initial_state) return CCV_E_UNSUPPORTED;
+  if (w->chunks) {
+    if (!p->q || !p->k || !p->v || !p->g || !p->beta || !p->dout || !p->dq || !p->dk || !p->dv || !p->dg || !p->dbeta)
+      return CCV_E_NULL;
+    for (const View& x : {q, k, v, g, b, d})
+      if ((st = check_view(x)) != CCV_OK) return st;
+    const View written[] = {dq, dk, dv, dg, db, dh0};
+    for (int i = 0; i < 6; ++i) {
+      if (!written[i].p) continue;
+      if ((st = check_written(written[i])) != CCV_OK) return st;
+      for (const void* x : {p->q, p->k, p->v, p->g, p->beta, p->dout, (const void*)p->initial_state, (const void*)p->dfinal_state})
+        if (x && x == written[i].p && !(i == 5 && x == (const void*)p->dfinal_state)) return CCV_E_ALIAS;
+      for (int j = 0; j < i; ++j)
+        if (written[j].p == written[i].p) return CCV_E_ALIAS;
+    }
+  }
+  if (p->initial_state && (st = check_view(h0)) != CCV_OK) return st;
+  if (p->dfinal_state && (st = check_view(dht)) != CCV_OK) return st;
+  if (p->dinitial_state) {
+    if ((st = check_written(dh0)) != CCV_OK) return st;
+    if (p->dinitial_state == p->initial_state) return CCV_E_ALIAS;
+    if (p->dinitial_state == p->dfinal_state)
+      for (int i = 0; i < 3; ++i)
+        if (dh0.n[i] > 1 && dh0.s[i] != dht.s[i]) return CCV_E_ALIAS;
+  }
+  if (!w->chunks) w->bytes = 0;
+  if (with_ws && (st = check_workspace(p->workspace, p->workspace_bytes, w->bytes)) != CCV_OK) return st;
+  a.q = p->q;
+  a.k = p->k;
+  a.v = p->v;
+  a.g = p->g;
+  a.beta = p->beta;
+  a.dout = p->dout;
+  a.h0 = p->initial_state;
+  a.dht = p->dfinal_state;
+  a.dh0 = p->dinitial_state;
+  a.dq = p->dq;
+  a.dk = p->dk;
+  a.dv = p->dv;
+  a.dg = p->dg;
+  a.dbeta = p->dbeta;
+  copy3(a.q_s, p->q_stride);
+  copy3(a.k_s, p->k_stride);
+  copy3(a.v_s, p->v_stride);
+  copy3(a.g_s, p->g_stride);
+  copy3(a.b_s, p->beta_stride);
+  copy3(a.do_s, p->dout_stride);
+  copy3(a.h0_s, p->init_stride);
+  copy3(a.dht_s, p->dfinal_stride);
+  copy3(a.dh0_s, p->dinit_stride);
+  copy3(a.dq_s, p->dq_stride);
+  copy3(a.dk_s, p->dk_stride);
+  copy3(a.dv_s, p->dv_stride);
+  copy3(a.dg_s, p->dg_stride);
+  copy3(a.db_s, p->dbeta_stride);
+  a.scale = p->scale;
+  a.vec_qk = vectors(q, 8, 16) && vectors(k, 8, 16);
+  a.vec_do = vectors(d, 8, 16);
+  a.vec_dqk = vectors(dq, 4, 4 * es) && vectors(dk, 4, 4 * es);
+  return CCV_OK;
+}
+
+int validate_step(const ccv_delta_update_args_t* p, DeltaStepArgs* a, bool* work) {
+  if (!p) return CCV_E_NULL;
+  if (p->struct_size != (int64_t)sizeof(ccv_delta_update_args_t)) return CCV_E_ABI;
+  int st = check_sizes({p->B, p->L, 0, p->Hk, p->Hv, p->Dk, p->Dv, nullptr, p->x_dtype, p->g_dtype, p->beta_dtype});
+  if (st != CCV_OK) return st;
+  if (p->slots < 0) return CCV_E_SHAPE;
+  if (!p->state_indices && p->B > p->slots) return CCV_E_SHAPE;
+  *work = p->B > 0 && p->L > 0;
+  if (!*work) return CCV_OK;
+  if (!p->q || !p->k || !p->v || !p->g || !p->beta || !p->out || (!p->state && p->slots > 0)) return CCV_E_NULL;
+  const int es = elt_size(p->x_dtype);
+  const View q = view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), k = view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es),
+             v = view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), o = view(p->out, p->B, p->L, p->Hv, p->Dv, p->out_stride, es),
+             g = view(p->g, p->B, p->L, p->Hv, 1, p->g_stride, 4), b = view(p->beta, p->B, p->L, p->Hv, 1, p->beta_stride, 4),
+             s = view(p->state, p->slots, p->Hv, p->Dk, p->Dv, p->state_stride, 4);
+  for (const View& x : {q, k, v, g, b})
+    if ((st = check_view(x)) != CCV_OK) return st;
+  if ((st = check_written(o)) != CCV_OK || (st = check_written(s)) != CCV_OK) return st;
+  for (const void* x : {p->q, p->k, p->v, p->g, p->beta})
+    if (x == p->out || x == (const void*)p->state) return CCV_E_ALIAS;
+  if (p->out == (void*)p->state) return CCV_E_ALIAS;
+  int64_t items;
+  if (__builtin_mul_overflow(p->B, p->Hv, &items) || __builtin_mul_overflow(items, (p->Dv + 31) / 32, &items) ||
+      items / 4 >= INT32_MAX)
+    return CCV_E_SHAPE;
+  *a = DeltaStepArgs{};
+  a->q = p->q;
+  a->k = p->k;
+  a->v = p->v;
+  a->g = p->g;
+  a->beta = p->beta;
+  a->out = p->out;
+  a->state = p->state;
+  a->slots = p->state_indices;
+  a->nslots = p->slots;
+  copy3(a->q_s, p->q_stride);
+  copy3(a->k_s, p->k_stride);
+  copy3(a->v_s, p->v_stride);
+  copy3(a->g_s, p->g_stride);
+  copy3(a->b_s, p->beta_stride);
+  copy3(a->o_s, p->out_stride);
+  copy3(a->st_s, p->state_stride);
+  a->B = (int32_t)p->B;
+  a->T = (int32_t)p->L;
+  a->Hk = (int32_t)p->Hk;
+  a->Hv = (int32_t)p->Hv;
+  a->Dk = (int32_t)p->Dk;
+  a->Dv = (int32_t)p->Dv;
+  a->x_dtype = p->x_dtype;
+  a->g_dtype = p->g_dtype;
+  a->b_dtype = p->beta_dtype;
+  a->scale = p->scale;
+  a->vec = vectors(q, 4, 4 * es) && vectors(k, 4, 4 * es) && vectors(v, 4, 4 * es) && vectors(o, 4, 4 * es) && vectors(s, 4, 16);
+  return CCV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ccv_delta_fwd_check(const ccv_delta_fwd_args_t* args) {
+  Work w;
+  return validate_fwd(args, &w, true);
+}
+
+int64_t ccv_delta_fwd_workspace_size(const ccv_delta_fwd_args_t* args) {
+  Work w;
+  const int st = validate_fwd(args, &w, false);
+  return st != CCV_OK ? st : w.bytes;
+}
+
+int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream) {
+  Work w;
+  const int st = validate_fwd(args, &w, true);
+  if (st != CCV_OK) return st;
+  if (!w.chunks && !w.states) return CCV_OK;
+  if (w.chunks) {
+    if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
+    if (launch_delta_prep(w.a, false, hip_stream) != 0) return CCV_E_HIP;
+  }
+  return launch_delta_scan(w.a, false, w.nt, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
+}
+
+int ccv_delta_bwd_check(const ccv_delta_bwd_args_t* args) {
+  Work w;
+  return validate_bwd(args, &w, true);
+}
+
+int64_t ccv_delta_bwd_workspace_size(const ccv_delta_bwd_args_t* args) {
+  Work w;
+  const int st = validate_bwd(args, &w, false);
+  return st != CCV_OK ? st : w.bytes;
+}
+
+int ccv_delta_bwd(const ccv_delta_bwd_args_t* args, void* hip_stream) {
+  Work w;
+  const int st = validate_bwd(args, &w, true);
+  if (st != CCV_OK) return st;
+  if (!w.chunks && !w.states) return CCV_OK;
+  if (w.chunks) {
+    if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
+    if (launch_delta_prep(w.a, true, hip_stream) != 0) return CCV_E_HIP;
+    if (launch_delta_scan(w.a, true, w.nt, hip_stream) != 0) return CCV_E_HIP;
+  }
+  if (launch_delta_reverse(w.a, w.nt, hip_stream) != 0) return CCV_E_HIP;
+  if (!w.chunks) return CCV_OK;
+  return launch_delta_grads(w.a, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
+}
+
+int ccv_delta_update_check(const ccv_delta_update_args_t* args) {
+  DeltaStepArgs a;
+  bool work;
+  return validate_step(args, &a, &work);
+}
+
+int ccv_delta_update(const ccv_delta_update_args_t* args, void* hip_stream) {
+  DeltaStepArgs a;
+  bool work;
+  const int st = validate_step(args, &a, &work);
+  if (st != CCV_OK || !work) return st;
+  return launch_delta_step(a, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,71 @@
+// ccv_delta_launch.hpp -- launch descriptors of the gated delta rule's kernels, seen
+// by the host validation code and the kernels.  No HIP types.
+#pragma once
+
+#include <stdint.h>
+
+namespace ccv {
+
+constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 16-row matrix tiles
+constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
+constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, dbeta, dG by R, c
+constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
+
+// One forward or backward call.  Strides are in elements: (row, step, head), unit inside
+// a head; states (sequence, head, key), unit along the values.
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta, *dout;
+  void* out;                                    // [B, L, Hv, Dv]; nullptr in the backward
+  int64_t q_s[3], k_s[3], v_s[3], g_s[3], b_s[3], o_s[3], do_s[3];
+  const float* h0;  int64_t h0_s[3];            // nullptr: zeros
+  float* ht;        int64_t ht_s[3];            // nullptr: not wanted
+  const float* dht; int64_t dht_s[3];
+  float* dh0;       int64_t dh0_s[3];
+  void *dq, *dk, *dv, *dg, *dbeta;
+  int64_t dq_s[3], dk_s[3], dv_s[3], dg_s[3], db_s[3];
+  const int32_t* cu;                            // [nseq + 1] or nullptr
+  int64_t L;
+  int32_t nseq;                                 // sequences: N of a packed row, else B
+  int32_t packed;
+  int32_t chunks_per_row;                       // ceil(L / 64), not packed
+  int32_t nchunks;                              // upper bound of the chunks of all sequences
+  int32_t Hk, Hv, Dk, Dv;
+  int32_t Dvp;                                  // Dv rounded up to 32: the workspace's value width
+  int32_t x_dtype, g_dtype, b_dtype;
+  int32_t vec_qk, vec_o, vec_do, vec_dqk;        // rows may move as whole vectors
+  float scale;
+  // workspace (element counts below), ch = chunk * Hv + head
+  int32_t* table;                               // packed: [nchunks] x (sequence, first step, steps, -)
+  int32_t* cstart;                              // packed: [nseq + 2] first chunk of each sequence
+  float* W;                                     // [ch][64][64] (1 + A)^-1
+  float* P;                                     // [ch][64][64]; the backward holds it transposed
+  float* WT;                                    // backward: W transposed
+  float* dec;                                   // [ch][kDeltaDec]: e^G, e^(G63 - G), beta, and G log2(e) as 64 doubles
+  float *S, *dS;                                // backward: [ch][Dkp][Dvp] state at a chunk's start, gradient at its end
+  float *N, *R, *Y;                             // backward: [ch][64][Dvp]
+  float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
+  int32_t Dkp, slices;
+};
+
+// Single steps against states in a cache.
+struct DeltaStepArgs {
+  const void *q, *k, *v, *g, *beta;
+  void* out;
+  int64_t q_s[3], k_s[3], v_s[3], g_s[3], b_s[3], o_s[3];   // (row, step, head)
+  float* state; int64_t st_s[3];                            // (slot, head, key)
+  const int32_t* slots;                                     // [B] or nullptr: row b uses slot b
+  int64_t nslots;
+  int32_t B, T, Hk, Hv, Dk, Dv;
+  int32_t x_dtype, g_dtype, b_dtype, vec;
+  float scale;
+};
+
+// Each returns a hipError_t value (0 = success).
+int launch_delta_table(const DeltaArgs& a, void* stream);
+int launch_delta_prep(const DeltaArgs& a, bool backward, void* stream);
+int launch_delta_scan(const DeltaArgs& a, bool backward, int nt, void* stream);
+int launch_delta_reverse(const DeltaArgs& a, int nt, void* stream);
+int launch_delta_grads(const DeltaArgs& a, void* stream);
+int launch_delta_step(const DeltaStepArgs& a, void* stream);
+
+}  // namespace ccv

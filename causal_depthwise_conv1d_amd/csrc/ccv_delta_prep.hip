@@ -1,0 +1,273 @@
+// ccv_delta_prep.hip -- gated delta rule: the part of a chunk that no state enters.
+//
+// For the 64 steps of a chunk and one value head, with G the running sum of g inside the
+// chunk:   A_ij = beta_i e^(G_i - G_j) k_i.k_j  (i > j),   P_ij = e^(G_i - G_j) q_i.k_j  (i >= j),
+//          W = (1 + A)^-1.
+// G is summed in 64 bits, so that differences of steps that lie far down a strongly
+// decaying chunk keep 32 bits.  A decay of g < -2000 (and -inf, a forgotten state) counts
+// as -2000: e^-2000 is 0 in fp32 with room to spare, and no inf - inf arises.
+#include "ccv_delta_device.hpp"
+
+namespace ccv {
+namespace {
+
+// ---- packed rows: the chunks of each sequence ---------------------------------------
+//
+// Sequence s holds the steps [cu[s], cu[s + 1]); the offsets count as their running maximum,
+// clamped to [0, L], so that no table can lead outside the row.  The steps past the last
+// sequence are sequence `nseq`, whose outputs are zeros.  One workgroup: the longest part
+// is a binary search a chunk.
+__global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
+  __shared__ int mx[1024], sm[1024];
+  const int tid = threadIdx.x, n = a.nseq + 1, L = (int)a.L;
+  int32_t* begin = a.cstart + (a.nseq + 2);
+  int cmax = 0, csum = 0;
+  for (int base = 0; base < n; base += 1024) {
+    const int i = base + tid;
+    int e = 0;
+    if (i < a.nseq) {
+      const int x = a.cu[i + 1];
+      e = x < 0 ? 0 : x > L ? L : x;
+    } else if (i == a.nseq) {
+      e = L;
+    }
+    mx[tid] = e;
+    __syncthreads();
+    for (int d = 1; d < 1024; d <<= 1) {
+      const int o = tid >= d ? mx[tid - d] : 0;
+      __syncthreads();
+      mx[tid] = mx[tid] > o ? mx[tid] : o;
+      __syncthreads();
+    }
+    const int end = mx[tid] > cmax ? mx[tid] : cmax;
+    const int before = tid ? (mx[tid - 1] > cmax ? mx[tid - 1] : cmax) : cmax;
+    sm[tid] = i < n ? (end - before + kDeltaChunk - 1) / kDeltaChunk : 0;
+    __syncthreads();
+    for (int d = 1; d < 1024; d <<= 1) {
+      const int o = tid >= d ? sm[tid - d] : 0;
+      __syncthreads();
+      sm[tid] += o;
+      __syncthreads();
+    }
+    if (i < n) {
+      a.cstart[i + 1] = csum + sm[tid];
+      begin[i] = before;
+      if (i == a.nseq) begin[n] = L;
+    }
+    const int m1 = mx[1023], s1 = sm[1023];
+    __syncthreads();
+    cmax = m1 > cmax ? m1 : cmax;
+    csum += s1;
+  }
+  if (tid == 0) a.cstart[0] = 0;
+  __threadfence_block();
+  __syncthreads();
+  for (int c = tid; c < a.nchunks; c += 1024) {
+    int s = a.nseq, t0 = 0, len = 0;
+    if (c < csum) {
+      int lo = 0, hi = a.nseq;                       // the last sequence whose first chunk is <= c
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (a.cstart[m] <= c) lo = m;
+        else hi = m - 1;
+      }
+      s = lo;
+      t0 = begin[s] + (c - a.cstart[s]) * kDeltaChunk;
+      len = begin[s + 1] - t0;
+      len = len < kDeltaChunk ? len : kDeltaChunk;
+    }
+    a.table[4 * c] = s;
+    a.table[4 * c + 1] = t0;
+    a.table[4 * c + 2] = len;
+    a.table[4 * c + 3] = 0;
+  }
+}
+
+// ---- A, P and W of a chunk -----------------------------------------------------------
+//
+// One workgroup a (chunk, head); wave w holds rows 16 w .. 16 w + 15 of every 64 x 64 matrix.
+// W by blocks: each wave solves its 16 x 16 diagonal block by substitution (a lane a
+// column), then blocks join in pairs, [X 0; Y Z]^-1 = [X' 0; -Z' Y X' Z'], on the fp32
+// matrix instruction, whose accumulator layout is the next product's operand.
+template <int DT, int DKP, bool BWD>
+__global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
+  constexpr int NA = InPlanes<DT>::n, LDK = DKP + 8, LDA = 68;
+  __shared__ __bf16 Kp[NA][64][LDK];
+  __shared__ float Al[64][LDA], Wl[64][LDA];
+  __shared__ double G[64];
+  __shared__ float bt[64];
+  const int ch = blockIdx.x, c = ch / a.Hv, h = ch - c * a.Hv, hk = h / (a.Hv / a.Hk);
+  const Chunk k = chunk_at(a, c);
+  if (k.n <= 0 || k.seq >= a.nseq) return;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
+
+  // gates: wave 0, a step a lane
+  if (w == 0) {
+    double g = 0;
+    float b = 0;
+    if (l < k.n) {
+      const int64_t t = k.t0 + l;
+      float x = load_param(a.g, a.g_dtype, k.row * a.g_s[0] + t * a.g_s[1] + h * a.g_s[2]);
+      x = x < -2000.0f ? -2000.0f : x;
+      g = (double)x * 1.4426950408889634;
+      b = load_param(a.beta, a.b_dtype, k.row * a.b_s[0] + t * a.b_s[1] + h * a.b_s[2]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double o = __shfl_up(g, d);
+      if (l >= d) g += o;
+    }
+    const double last = __shfl(g, 63);
+    G[l] = g;
+    bt[l] = b;
+    float* dec = a.dec + (int64_t)ch * kDeltaDec;
+    dec[l] = __builtin_amdgcn_exp2f((float)g);
+    dec[64 + l] = __builtin_amdgcn_exp2f((float)(last - g));
+    dec[128 + l] = b;
+    reinterpret_cast<double*>(dec + 192)[l] = g;
+  }
+
+  // K's planes into LDS; this wave's 16 rows of Q stay in registers
+  const int row = 16 * w + r;
+  const bool live = row < k.n;
+  const char* kp = row_ptr<DT>(a.k, a.k_s, k.row, k.t0 + (live ? row : 0), hk);
+  const char* qp = row_ptr<DT>(a.q, a.q_s, k.row, k.t0 + (live ? row : 0), hk);
+  Frag<NA> qf[DKP / 32];
+#pragma unroll
+  for (int s = 0; s < DKP / 32; ++s) {
+    const int d = 32 * s + 8 * g4, left = live ? a.Dk - d : 0, es = DT == CCV_DT_F32 ? 4 : 2;
+    const Frag<NA> kf = planes<DT>(load8<DT>(kp + d * es, left, a.vec_qk));
+    qf[s] = planes<DT>(load8<DT>(qp + d * es, left, a.vec_qk));
+#pragma unroll
+    for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(&Kp[p][row][d]) = kf.p[p];
+  }
+  for (int i = tid; i < 64 * LDA / 4; i += 256) reinterpret_cast<f32x4*>(&Wl[0][0])[i] = f32x4{0, 0, 0, 0};
+  __syncthreads();
+
+  float* P = a.P + (int64_t)ch * 4096;
+  double Gi[4];
+  float bi[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    Gi[e] = G[16 * w + 4 * g4 + e];
+    bi[e] = bt[16 * w + 4 * g4 + e];
+  }
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb) {
+    f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
+    const int j = 16 * jb + r;
+    if (jb <= w) {
+#pragma unroll
+      for (int s = 0; s < DKP / 32; ++s) {
+        const Frag<NA> bf = get8<NA>(&Kp[0][j][32 * s + 8 * g4], 64 * LDK);
+        const Frag<NA> af = get8<NA>(&Kp[0][row][32 * s + 8 * g4], 64 * LDK);
+        kk = mma<2>(af, bf, kk);
+        qk = mma<2>(qf[s], bf, qk);
+      }
+    }
+    f32x4 pv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * w + 4 * g4 + e;
+      const float d = i >= j ? __builtin_amdgcn_exp2f((float)(Gi[e] - G[j])) : 0.0f;
+      pv[e] = i >= j ? d * qk[e] : 0.0f;
+      Al[i][j] = i > j ? bi[e] * d * kk[e] : 0.0f;
+    }
+    if constexpr (BWD) {
+      *reinterpret_cast<f32x4*>(P + j * 64 + 16 * w + 4 * g4) = pv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) P[(16 * w + 4 * g4 + e) * 64 + j] = pv[e];
+    }
+  }
+  __syncthreads();
+
+  // diagonal blocks: column r of block w, the four groups of lanes alike
+  {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float acc = i == r ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < i) acc = __builtin_fmaf(-Al[16 * w + i][16 * w + j], x[j], acc);
+      x[i] = acc;
+      if (i / 4 == g4) Wl[16 * w + i][16 * w + r] = acc;
+    }
+  }
+  __syncthreads();
+  if (w < 2) {                                       // blocks of 32
+    const int r0 = 32 * w, r1 = r0 + 16;
+    f32x4 t = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      t = __builtin_amdgcn_mfma_f32_16x16x4f32(Al[r1 + r][r0 + 4 * s + g4], Wl[r0 + 4 * s + g4][r0 + r], t, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      y = __builtin_amdgcn_mfma_f32_16x16x4f32(Wl[r1 + r][r1 + 4 * g4 + e], t[e], y, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Wl[r1 + 4 * g4 + e][r0 + r] = -y[e];
+  }
+  __syncthreads();
+  {                                                  // 64: wave w makes block (w / 2, w % 2) of the lower left
+    const int rb = w >> 1, cb = w & 1;
+    f32x4 y = {0, 0, 0, 0};
+    for (int s = 0; s <= rb; ++s) {
+      f32x4 t = {0, 0, 0, 0};
+      for (int u = cb; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          t = __builtin_amdgcn_mfma_f32_16x16x4f32(Al[32 + 16 * s + r][16 * u + 4 * q + g4],
+                                                   Wl[16 * u + 4 * q + g4][16 * cb + r], t, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(Wl[32 + 16 * rb + r][32 + 16 * s + 4 * g4 + e], t[e], y, 0, 0, 0);
+    }
+    // rows 32.. of columns 0..31 are read by nobody in this step
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Wl[32 + 16 * rb + 4 * g4 + e][16 * cb + r] = -y[e];
+  }
+  __syncthreads();
+  float* W = a.W + (int64_t)ch * 4096;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = i * 256 + tid, ro = e >> 4, co = 4 * (e & 15);
+    *reinterpret_cast<f32x4*>(W + ro * 64 + co) = *reinterpret_cast<const f32x4*>(&Wl[ro][co]);
+    if constexpr (BWD) {
+      const int tc = e & 63, tr = 4 * (e >> 6);
+      f32x4 x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = Wl[tr + q][tc];
+      *reinterpret_cast<f32x4*>(a.WT + (int64_t)ch * 4096 + tc * 64 + tr) = x;
+    }
+  }
+}
+
+template <int DT, int DKP>
+void launch_prep(const DeltaArgs& a, bool bwd, hipStream_t st) {
+  const dim3 grid((uint32_t)((int64_t)a.nchunks * a.Hv));
+  if (bwd) prep_kernel<DT, DKP, true><<<grid, 256, 0, st>>>(a);
+  else prep_kernel<DT, DKP, false><<<grid, 256, 0, st>>>(a);
+}
+template <int DT>
+void launch_prep(const DeltaArgs& a, bool bwd, hipStream_t st) {
+  if (a.Dkp == 64) launch_prep<DT, 64>(a, bwd, st);
+  else launch_prep<DT, 128>(a, bwd, st);
+}
+
+}  // namespace
+
+int launch_delta_table(const DeltaArgs& a, void* stream) {
+  table_kernel<<<1, 1024, 0, static_cast<hipStream_t>(stream)>>>(a);
+  return (int)hipGetLastError();
+}
+
+int launch_delta_prep(const DeltaArgs& a, bool backward, void* stream) {
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.x_dtype == CCV_DT_F32) launch_prep<CCV_DT_F32>(a, backward, st);
+  else if (a.x_dtype == CCV_DT_F16) launch_prep<CCV_DT_F16>(a, backward, st);
+  else launch_prep<CCV_DT_BF16>(a, backward, st);
+  return (int)hipGetLastError();
+}
+
+}  // namespace ccv

@@ -1,0 +1,422 @@
+// ccv_norm.hip -- layer norm over the last dimension and its gradients.
+//
+//   n = (x - mean) rstd,  out = n w + b;     a = dout w,
+//   dx = rstd (a - mean(a) - n mean(a n)),   dw = sum over rows of dout n,   db = sum of dout.
+// Bound by memory: x in, out out; in the backward x and dout in, dx out.  A row is read
+// once into registers, `lanes` threads a row (16 for a head's width, up to 512), and the
+// variance is summed from the deviations there, in fp32.  Workgroups walk rows at a
+// stride, so a thread always has the same columns: the weights stay in registers, and in
+// the backward so do the thread's sums of dw and db.  Each workgroup leaves one partial
+// row, and a second kernel adds the partial rows in a fixed order.
+#include "ccv_delta_device.hpp"
+#include "ccv_norm_launch.hpp"
+
+namespace ccv {
+namespace {
+
+template <int DT> struct Vec { static constexpr int n = DT == CCV_DT_F32 ? 4 : 8; };
+
+// 16 bytes of a row, widened; zeros past the first `left` elements.
+template <int DT>
+__device__ inline void load_vec(const void* p, int left, bool vec, float* x) {
+  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  if (vec && left >= V) {
+    const u32x4 d = load16(p);
+    if constexpr (DT == CCV_DT_F32) F32::unpack(d, x);
+    else if constexpr (DT == CCV_DT_BF16) BF16::unpack(d, x);
+    else F16::unpack(d, x);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = i < left ? load1<DT>(static_cast<const char*>(p) + i * ES) : 0.0f;
+}
+template <int DT>
+__device__ inline void store_vec(void* p, int left, bool vec, const float* y) {
+  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  if (vec && left >= V) {
+    if constexpr (DT == CCV_DT_F32) store16(p, F32::pack(y));
+    else if constexpr (DT == CCV_DT_BF16) store16(p, BF16::pack(y));
+    else store16(p, F16::pack(y));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < left) store1<DT>(static_cast<char*>(p) + i * ES, y[i]);
+}
+
+// Vec<DT>::n weights from element `col`; `other` past the width or where there are none.
+template <int V>
+__device__ inline void load_weights(const void* p, int dtype, int col, int width, bool vec, float other, float* w) {
+  if (p && vec && col + V <= width) {
+    if (dtype == CCV_DT_F32) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) F32::unpack(load16(static_cast<const float*>(p) + col + i), w + i);
+      return;
+    }
+    if constexpr (V == 8) {
+      const u32x4 d = load16(static_cast<const uint16_t*>(p) + col);
+      if (dtype == CCV_DT_BF16) BF16::unpack(d, w);
+      else F16::unpack(d, w);
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) w[e] = p && col + e < width ? load_param(p, dtype, col + e) : other;
+}
+
+// Sum over the `LANES` threads of a row; every one of them gets it.  Rows of more than a
+// wave: through `red`, two rows of it in turn, so that one barrier a sum suffices.
+template <int LANES>
+__device__ inline float row_sum(float v, float (*red)[8], int& turn) {
+  v = sum16(v);
+  if constexpr (LANES >= 64) v = sum4rows(v);
+  if constexpr (LANES > 64) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[turn][w] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < LANES / 64; ++i) v += red[turn][i];
+    turn ^= 1;
+  }
+  return v;
+}
+
+template <int DT>
+__device__ inline const char* norm_row(const void* p, const int64_t* s, int64_t r, int64_t n1) {
+  const int64_t i = r / n1;
+  return static_cast<const char*>(p) + (i * s[0] + (r - i * n1) * s[1]) * (DT == CCV_DT_F32 ? 4 : 2);
+}
+template <int DT>
+__device__ inline char* norm_row(void* p, const int64_t* s, int64_t r, int64_t n1) {
+  const int64_t i = r / n1;
+  return static_cast<char*>(p) + (i * s[0] + (r - i * n1) * s[1]) * (DT == CCV_DT_F32 ? 4 : 2);
+}
+
+template <int LANES> constexpr int kThreads = LANES > 256 ? LANES : 256;
+
+template <int DT, int LANES, int NV>
+__global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, TH = kThreads<LANES>, RW = TH / LANES, ES = DT == CCV_DT_F32 ? 4 : 2;
+  __shared__ float red[2][8];
+  int turn = 0;
+  const int lane = threadIdx.x % LANES;
+  float w[NV][V], b[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * LANES + lane) * V;
+    load_weights<V>(a.w, a.w_dtype, col, a.width, a.vec_w, 1.0f, w[i]);
+    load_weights<V>(a.b, a.w_dtype, col, a.width, a.vec_w, 0.0f, b[i]);
+  }
+  const float inv = 1.0f / (float)a.width;
+  // the trip count is the same for every thread of a workgroup whose rows share barriers
+  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += (int64_t)gridDim.x * RW) {
+    const int64_t row = base + threadIdx.x / LANES;
+    const bool live = row < a.rows;
+    const char* xp = norm_row<DT>(a.x, a.x_s, live ? row : 0, a.n1);
+    float x[NV][V], s = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * LANES + lane) * V;
+      load_vec<DT>(xp + col * ES, live ? a.width - col : 0, a.vec, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += x[i][e];
+    const float mean = row_sum<LANES>(s, red, turn) * inv;
+    float q = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int col = (i * LANES + lane) * V + e;
+        x[i][e] = col < a.width ? x[i][e] - mean : 0.0f;
+        q = __builtin_fmaf(x[i][e], x[i][e], q);
+      }
+    const float rstd = 1.0f / __builtin_sqrtf(row_sum<LANES>(q, red, turn) * inv + a.eps);
+    if (!live) continue;
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    char* op = norm_row<DT>(a.out, a.o_s, row, a.n1);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * LANES + lane) * V;
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf(x[i][e] * rstd, w[i][e], b[i][e]);
+      store_vec<DT>(op + col * ES, a.width - col, a.vec, y);
+    }
+  }
+}
+
+template <int DT, int LANES, int NV>
+__global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, TH = kThreads<LANES>, RW = TH / LANES, ES = DT == CCV_DT_F32 ? 4 : 2;
+  __shared__ float red[2][8];
+  __shared__ float sums[RW > 1 ? TH * V : 1];
+  int turn = 0;
+  const int lane = threadIdx.x % LANES;
+  float w[NV][V], dw[NV][V], db[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    load_weights<V>(a.w, a.w_dtype, (i * LANES + lane) * V, a.width, a.vec_w, 1.0f, w[i]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
+  }
+  const float inv = 1.0f / (float)a.width;
+  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += (int64_t)gridDim.x * RW) {
+    const int64_t row = base + threadIdx.x / LANES;
+    const bool live = row < a.rows;
+    const char* xp = norm_row<DT>(a.x, a.x_s, live ? row : 0, a.n1);
+    const char* dp = norm_row<DT>(a.dout, a.do_s, live ? row : 0, a.n1);
+    float x[NV][V], d[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * LANES + lane) * V;
+      load_vec<DT>(xp + col * ES, live ? a.width - col : 0, a.vec, x[i]);
+      load_vec<DT>(dp + col * ES, live ? a.width - col : 0, a.vec, d[i]);
+    }
+    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
+    float s1 = 0, s2 = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const bool in = (i * LANES + lane) * V + e < a.width;
+        x[i][e] = in ? (x[i][e] - mean) * rstd : 0.0f;
+        dw[i][e] = __builtin_fmaf(d[i][e], x[i][e], dw[i][e]);
+        db[i][e] += d[i][e];
+        d[i][e] *= w[i][e];
+        s1 += d[i][e];
+        s2 = __builtin_fmaf(d[i][e], x[i][e], s2);
+      }
+    const float m1 = row_sum<LANES>(s1, red, turn) * inv, m2 = row_sum<LANES>(s2, red, turn) * inv;
+    if (!live || !a.dx) continue;
+    char* op = norm_row<DT>(a.dx, a.dx_s, row, a.n1);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * LANES + lane) * V;
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = rstd * (d[i][e] - m1 - x[i][e] * m2);
+      store_vec<DT>(op + col * ES, a.width - col, a.vec, y);
+    }
+  }
+  if (!a.part) return;
+  // the workgroup's partial row: its RW threads of a column in their order
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.width;
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * LANES + lane) * V;
+      float* src = side ? db[i] : dw[i];
+      if constexpr (RW > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) sums[threadIdx.x * V + e] = src[e];
+        __syncthreads();
+        if (threadIdx.x < LANES)
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            float s = 0;
+            for (int r = 0; r < RW; ++r) s += sums[(r * LANES + lane) * V + e];
+            if (col + e < a.width) part[side * (int64_t)a.width + col + e] = s;
+          }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (col + e < a.width) part[side * (int64_t)a.width + col + e] = src[e];
+      }
+    }
+}
+
+// Column sums of the partial rows: a workgroup has 32 columns of one side, 32 threads a
+// column, joined through LDS.
+__global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
+  __shared__ float t[32][33];
+  const int side = blockIdx.y, c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  void* out = side ? a.db : a.dw;
+  if (!out) return;
+  float s = 0;
+  if (col < a.width)
+    for (int r = g; r < a.groups; r += 32) s += a.part[((int64_t)r * 2 + side) * a.width + col];
+  t[g][c] = s;
+  __syncthreads();
+  for (int h = 16; h; h >>= 1) {
+    if (g < h) t[g][c] += t[g + h][c];
+    __syncthreads();
+  }
+  if (g == 0 && col < a.width) store_gate(out, a.w_dtype, col, t[0][c]);
+}
+
+// ---- rows wider than 512 threads hold: walked again for each sum (they stay in L2) ------
+
+__device__ inline float block_sum(float v, float* red) {
+  v = sum4rows(sum16(v));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < 16; ++i) v += red[i];
+  return v;
+}
+
+template <int DT>
+__global__ __launch_bounds__(1024) void wide_fwd_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  __shared__ float red[16];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const char* xp = norm_row<DT>(a.x, a.x_s, row, a.n1);
+    char* op = norm_row<DT>(a.out, a.o_s, row, a.n1);
+    float s = 0, q = 0, x[V], w[V], b[V];
+    for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
+      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += x[e];
+    }
+    const float mean = block_sum(s, red) / (float)a.width;
+    for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
+      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = i + e < a.width ? x[e] - mean : 0.0f;
+        q = __builtin_fmaf(d, d, q);
+      }
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(block_sum(q, red) / (float)a.width + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
+      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
+      load_weights<V>(a.b, a.w_dtype, i, a.width, a.vec_w, 0.0f, b);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = __builtin_fmaf((x[e] - mean) * rstd, w[e], b[e]);
+      store_vec<DT>(op + (int64_t)i * ES, a.width - i, a.vec, x);
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(1024) void wide_dx_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  __shared__ float red[16];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const char* xp = norm_row<DT>(a.x, a.x_s, row, a.n1);
+    const char* dp = norm_row<DT>(a.dout, a.do_s, row, a.n1);
+    char* op = norm_row<DT>(a.dx, a.dx_s, row, a.n1);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s1 = 0, s2 = 0, x[V], d[V], w[V];
+    for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
+      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+      load_vec<DT>(dp + (int64_t)i * ES, a.width - i, a.vec, d);
+      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float n = i + e < a.width ? (x[e] - mean) * rstd : 0.0f, y = d[e] * w[e];
+        s1 += y;
+        s2 = __builtin_fmaf(y, n, s2);
+      }
+    }
+    const float m1 = block_sum(s1, red) / (float)a.width, m2 = block_sum(s2, red) / (float)a.width;
+    for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
+      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+      load_vec<DT>(dp + (int64_t)i * ES, a.width - i, a.vec, d);
+      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = rstd * (d[e] * w[e] - m1 - (x[e] - mean) * rstd * m2);
+      store_vec<DT>(op + (int64_t)i * ES, a.width - i, a.vec, x);
+    }
+  }
+}
+
+// Partial sums of dw and db: a thread has one vector of columns, blockIdx.y its rows.
+template <int DT>
+__global__ __launch_bounds__(256) void wide_sums_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (col >= a.width) return;
+  float dw[V] = {}, db[V] = {}, x[V], d[V];
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    load_vec<DT>(norm_row<DT>(a.dout, a.do_s, row, a.n1) + col * ES, a.width - (int)col, a.vec, d);
+    load_vec<DT>(norm_row<DT>(a.x, a.x_s, row, a.n1) + col * ES, a.width - (int)col, a.vec, x);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      dw[e] = __builtin_fmaf(d[e], (x[e] - mean) * rstd, dw[e]);
+      db[e] += d[e];
+    }
+  }
+  for (int e = 0; e < V && col + e < a.width; ++e) {
+    a.part[((int64_t)blockIdx.y * 2) * a.width + col + e] = dw[e];
+    a.part[((int64_t)blockIdx.y * 2 + 1) * a.width + col + e] = db[e];
+  }
+}
+
+int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
+
+template <int DT, int LANES, int NV>
+void go(const NormArgs& a, bool bwd, int grid, hipStream_t st) {
+  if (bwd) bwd_kernel<DT, LANES, NV><<<grid, kThreads<LANES>, 0, st>>>(a);
+  else fwd_kernel<DT, LANES, NV><<<grid, kThreads<LANES>, 0, st>>>(a);
+}
+template <int DT, int LANES>
+void go(const NormArgs& a, bool bwd, int nv, int grid, hipStream_t st) {
+  if (nv == 1) go<DT, LANES, 1>(a, bwd, grid, st);
+  else if (nv == 2) go<DT, LANES, 2>(a, bwd, grid, st);
+  else go<DT, LANES, 4>(a, bwd, grid, st);
+}
+template <int DT>
+void go(const NormArgs& a, bool bwd, int cus, hipStream_t st) {
+  const NormShape s = norm_shape(a.width, DT == CCV_DT_F32 ? 4 : 2);
+  if (!s.lanes) {
+    const int grid = (int)min64(a.rows, 4096);
+    if (!bwd) {
+      wide_fwd_kernel<DT><<<grid, 1024, 0, st>>>(a);
+    } else {
+      if (a.dx) wide_dx_kernel<DT><<<grid, 1024, 0, st>>>(a);
+      if (a.part) wide_sums_kernel<DT><<<dim3((a.width + 256 * Vec<DT>::n - 1) / (256 * Vec<DT>::n), a.groups), 256, 0, st>>>(a);
+    }
+    return;
+  }
+  const int rows_per = (s.lanes > 256 ? s.lanes : 256) / s.lanes;
+  const int64_t need = (a.rows + rows_per - 1) / rows_per;
+  const int grid = bwd ? a.groups : (int)min64(need, (int64_t)cus * (s.lanes > 256 ? 2 : 8));
+  if (s.lanes == 16) go<DT, 16>(a, bwd, s.nv, grid, st);
+  else if (s.lanes == 64) go<DT, 64>(a, bwd, s.nv, grid, st);
+  else if (s.lanes == 256) go<DT, 256>(a, bwd, s.nv, grid, st);
+  else go<DT, 512>(a, bwd, s.nv, grid, st);
+}
+
+void any(const NormArgs& a, bool bwd, int cus, hipStream_t st) {
+  if (a.x_dtype == CCV_DT_F32) go<CCV_DT_F32>(a, bwd, cus, st);
+  else if (a.x_dtype == CCV_DT_F16) go<CCV_DT_F16>(a, bwd, cus, st);
+  else go<CCV_DT_BF16>(a, bwd, cus, st);
+}
+
+}  // namespace
+
+int launch_norm_fwd(const NormArgs& a, int cus, void* stream) {
+  any(a, false, cus, static_cast<hipStream_t>(stream));
+  return (int)hipGetLastError();
+}
+
+int launch_norm_bwd(const NormArgs& a, void* stream) {
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  int e = 0;
+  if (a.rows > 0) {
+    any(a, true, 0, st);
+    e = (int)hipGetLastError();
+  }
+  if (e || (!a.dw && !a.db)) return e;
+  reduce_kernel<<<dim3((a.width + 31) / 32, 2), 1024, 0, st>>>(a);      // no rows: zeros
+  return (int)hipGetLastError();
+}
+
+}  // namespace ccv

@@ -46,6 +46,10 @@
  * different streams.  `out` must not overlap any input; views interleaved in one
  * parent buffer are fine as long as the elements touched are disjoint.
  *
+ * Beside the conv stand the operators of the layer around it: the gated delta rule
+ * (ccv_delta_*), layer norm (ccv_norm_*) and the tables of packed rows
+ * (ccv_seq_tables), under the same rules.
+ *
  * Errors: every call returns a ccv_status (0 = success, negative = error).  All
  * argument checks run before anything is enqueued, so a call that fails writes
  * nothing.  No C++ exception crosses this boundary.
@@ -350,6 +354,200 @@ int ccv_bwd_plan(const ccv_bwd_args_t* args, ccv_plan_t* plan);
  * calls (each call writes every partial sum it reads).  Other errors as ccv_bwd. */
 #define CCV_BWD_STATIC_SCRATCH_BYTES ((int64_t)64 << 20)
 int ccv_bwd_static(const ccv_bwd_args_t* args, void* hip_stream);
+
+/* ---- gated delta rule -----------------------------------------------------------------
+ *
+ * The recurrence of a gated linear-attention layer, which takes its queries, keys and
+ * values from the conv above.  For each sequence and value head, with a state S of
+ * [Dk, Dv] fp32 values:
+ *
+ *   S <- e^g[t] S;   u = beta[t] (v[t] - S^T k[t]);   S <- S + k[t] u^T;
+ *   out[t] = scale S^T q[t]
+ *
+ *   - q, k: [B, L, Hk, Dk]; v, out: [B, L, Hv, Dv]; g (log decay) and beta (write
+ *     strength): [B, L, Hv].  Hv is a multiple of Hk; value head h uses key head
+ *     h / (Hv / Hk).  1 <= Dk <= 128 (else CCV_E_UNSUPPORTED), Dv >= 1.
+ *   - x_dtype is the storage type of q, k, v and out, g_dtype of g, beta_dtype of beta;
+ *     states and every sum are fp32.  out is rounded once.
+ *   - cu_seqlens NULL: each of the B rows is one sequence (N must be 0).  Otherwise B is 1
+ *     and the row packs N sequences: s has the steps cu_seqlens[s] .. cu_seqlens[s + 1] - 1
+ *     (int32, on the device, never read by the host).  Offsets count as their running
+ *     maximum, clamped to [0, L], and the first as 0.  Steps past the last sequence give
+ *     zeros, in out and in every gradient, and their inputs are not looked at.  A sequence
+ *     may be empty: its final state is its initial state.
+ *   - g of -inf (or any below -2000) forgets the state.  A NaN or an infinity in a step
+ *     stays in its own sequence and head; steps of the same group of 64 (counted from the
+ *     sequence's first step) before it may be reached as well as all later ones.
+ *   - Element (b, t, h, d) of a [B, L, H, D] array lies at b s[0] + t s[1] + h s[2] + d
+ *     elements: unit stride inside a head.  States: (sequence, head, key) strides, unit
+ *     along the values.  Inputs may have zero strides (broadcast); written arrays may not
+ *     map two elements to one address (CCV_E_LAYOUT).
+ *
+ * ccv_delta_fwd works by groups of 64 steps, whose inner products are matrix products: a
+ * first kernel makes what no state enters, a second carries the states along the
+ * sequences (a packed row's sequences at the same time).  It needs a workspace of
+ * ccv_delta_fwd_workspace_size bytes (16-byte aligned, contents immaterial, free again
+ * when the call's work is done): CCV_E_NULL without, CCV_E_SHAPE when smaller.
+ * final_state may be initial_state itself, with the same strides; out may be no input. */
+typedef struct ccv_delta_fwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_delta_fwd_args_t) */
+  int64_t B, L, N;              /* rows, steps a row, packed sequences (0: not packed) */
+  int64_t Hk, Hv, Dk, Dv;
+  int32_t x_dtype, g_dtype, beta_dtype;   /* ccv_dtype_t */
+  float scale;                  /* of the outputs, usually Dk^-1/2 */
+  const void* q;                int64_t q_stride[3];      /* (row, step, head) */
+  const void* k;                int64_t k_stride[3];
+  const void* v;                int64_t v_stride[3];
+  const void* g;                int64_t g_stride[3];
+  const void* beta;             int64_t beta_stride[3];
+  const int32_t* cu_seqlens;    /* device [N + 1], or NULL */
+  const float* initial_state;   int64_t init_stride[3];   /* [sequences, Hv, Dk, Dv], or NULL: zeros */
+  float* final_state;           int64_t final_stride[3];  /* or NULL: not wanted */
+  void* out;                    int64_t out_stride[3];
+  void* workspace;              int64_t workspace_bytes;
+} ccv_delta_fwd_args_t;
+
+int64_t ccv_delta_fwd_workspace_size(const ccv_delta_fwd_args_t* args);
+int ccv_delta_fwd_check(const ccv_delta_fwd_args_t* args);
+int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream);
+
+/* The gradients: dq, dk, dv in x_dtype, dg in g_dtype, dbeta in beta_dtype, dinitial_state
+ * fp32 (NULL: not wanted; needs initial_state, else CCV_E_UNSUPPORTED), from dout (x_dtype)
+ * and dfinal_state (fp32, NULL: zeros).  Everything is made again from the inputs; nothing
+ * of the forward call is kept.  Sums are fp32 in a fixed order (no atomics), those over the
+ * value heads that share a key head included, so results repeat bit for bit.
+ * dinitial_state may be dfinal_state itself, with the same strides; other outputs may be
+ * no input and no other output (CCV_E_ALIAS).  The workspace holds the states at
+ * both ends of every group of 64 steps: about (2 Dk + 352) Dv fp32 values a group and head, with
+ * Dk rounded up to 64 or 128 and Dv to a multiple of 32 (for 128 and 128: 0.3 MB). */
+typedef struct ccv_delta_bwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_delta_bwd_args_t) */
+  int64_t B, L, N;
+  int64_t Hk, Hv, Dk, Dv;
+  int32_t x_dtype, g_dtype, beta_dtype;
+  float scale;
+  const void* q;                int64_t q_stride[3];
+  const void* k;                int64_t k_stride[3];
+  const void* v;                int64_t v_stride[3];
+  const void* g;                int64_t g_stride[3];
+  const void* beta;             int64_t beta_stride[3];
+  const int32_t* cu_seqlens;
+  const float* initial_state;   int64_t init_stride[3];
+  const void* dout;             int64_t dout_stride[3];
+  const float* dfinal_state;    int64_t dfinal_stride[3];
+  void* dq;                     int64_t dq_stride[3];
+  void* dk;                     int64_t dk_stride[3];
+  void* dv;                     int64_t dv_stride[3];
+  void* dg;                     int64_t dg_stride[3];
+  void* dbeta;                  int64_t dbeta_stride[3];
+  float* dinitial_state;        int64_t dinit_stride[3];
+  void* workspace;              int64_t workspace_bytes;
+} ccv_delta_bwd_args_t;
+
+int64_t ccv_delta_bwd_workspace_size(const ccv_delta_bwd_args_t* args);
+int ccv_delta_bwd_check(const ccv_delta_bwd_args_t* args);
+int ccv_delta_bwd(const ccv_delta_bwd_args_t* args, void* hip_stream);
+
+/* Decoding: the recurrence over L new steps of B rows (one after the other; many steps
+ * belong to ccv_delta_fwd) against fp32 states in a cache [slots, Hv, Dk, Dv], advanced in
+ * place.  Row b uses slot state_indices[b] (int32, device), or slot b when state_indices is
+ * NULL (then B <= slots, else CCV_E_SHAPE).  A row whose index lies outside [0, slots) is idle: its
+ * outputs are zeros and no state is touched.  Two rows may not use one slot in the same
+ * call.  Needs no workspace. */
+typedef struct ccv_delta_update_args {
+  int64_t struct_size;          /* = sizeof(ccv_delta_update_args_t) */
+  int64_t B, L, slots;
+  int64_t Hk, Hv, Dk, Dv;
+  int32_t x_dtype, g_dtype, beta_dtype;
+  float scale;
+  const void* q;                int64_t q_stride[3];
+  const void* k;                int64_t k_stride[3];
+  const void* v;                int64_t v_stride[3];
+  const void* g;                int64_t g_stride[3];
+  const void* beta;             int64_t beta_stride[3];
+  const int32_t* state_indices; /* device [B], or NULL */
+  float* state;                 int64_t state_stride[3];  /* (slot, head, key) */
+  void* out;                    int64_t out_stride[3];
+} ccv_delta_update_args_t;
+
+int ccv_delta_update_check(const ccv_delta_update_args_t* args);
+int ccv_delta_update(const ccv_delta_update_args_t* args, void* hip_stream);
+
+/* ---- layer norm -------------------------------------------------------------------------
+ *
+ * Over the last dimension of x [n0, n1, width], row (i, j) at i s[0] + j s[1] elements:
+ *
+ *   mean = sum x / width;  rstd = (sum (x - mean)^2 / width + eps)^-1/2;  n = (x - mean) rstd
+ *   out  = n weight + bias
+ *
+ * weight and bias ([width], contiguous, w_dtype) may each be NULL (ones, zeros); out has x's
+ * dtype; mean and rstd (fp32 [n0 n1], row by row) are written when not NULL.  eps >= 0 and
+ * finite, else CCV_E_UNSUPPORTED.  out may not be x.  Statistics are fp32, the variance
+ * summed from the deviations. */
+typedef struct ccv_norm_fwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_norm_fwd_args_t) */
+  int64_t n0, n1, width;
+  int32_t x_dtype, w_dtype;
+  float eps;
+  int32_t reserved;             /* 0 */
+  const void* x;                int64_t x_stride[2];
+  const void* weight;
+  const void* bias;
+  void* out;                    int64_t out_stride[2];
+  float* mean;
+  float* rstd;
+} ccv_norm_fwd_args_t;
+
+int ccv_norm_fwd_check(const ccv_norm_fwd_args_t* args);
+int ccv_norm_fwd(const ccv_norm_fwd_args_t* args, void* hip_stream);
+
+/* Its gradients, with a = dout weight:
+ *   dx = rstd (a - mean(a) - n mean(a n)),  dweight = sum of dout n,  dbias = sum of dout
+ * from x, dout and the forward's mean and rstd.  dx, dweight, dbias may each be NULL (not
+ * wanted); dweight and dbias are summed in fp32 over all rows, in a fixed order, and rounded
+ * once to w_dtype (zeros when there are no rows).  They need a workspace of
+ * ccv_norm_bwd_workspace_size bytes, 16-byte aligned. */
+typedef struct ccv_norm_bwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_norm_bwd_args_t) */
+  int64_t n0, n1, width;
+  int32_t x_dtype, w_dtype;
+  const void* x;                int64_t x_stride[2];
+  const void* weight;
+  const void* dout;             int64_t dout_stride[2];
+  const float* mean;
+  const float* rstd;
+  void* dx;                     int64_t dx_stride[2];
+  void* dweight;
+  void* dbias;
+  void* workspace;              int64_t workspace_bytes;
+} ccv_norm_bwd_args_t;
+
+int64_t ccv_norm_bwd_workspace_size(const ccv_norm_bwd_args_t* args);
+int ccv_norm_bwd_check(const ccv_norm_bwd_args_t* args);
+int ccv_norm_bwd(const ccv_norm_bwd_args_t* args, void* hip_stream);
+
+/* ---- sequence tables ----------------------------------------------------------------------
+ *
+ * A packed row's tables, made on the GPU from the lengths of its N sequences (int32, device;
+ * a negative length counts as 0), with no look by the host:
+ *
+ *   cu_seqlens[0] = 0;  cu_seqlens[s + 1] = min(cu_seqlens[s] + lengths[s], total)
+ *   seq_idx[t] = s and positions[t] = t - cu_seqlens[s] for t in sequence s;
+ *   seq_idx[t] = -1 and positions[t] = 0 for cu_seqlens[N] <= t < total
+ *
+ * seq_idx is what the conv takes (as [1, total]), cu_seqlens what ccv_delta_fwd takes.
+ * seq_idx and positions may be NULL. */
+typedef struct ccv_seq_tables_args {
+  int64_t struct_size;          /* = sizeof(ccv_seq_tables_args_t) */
+  int64_t N, total;
+  const int32_t* lengths;       /* device [N] */
+  int32_t* cu_seqlens;          /* device [N + 1] */
+  int32_t* seq_idx;             /* device [total] or NULL */
+  int32_t* positions;           /* device [total] or NULL */
+} ccv_seq_tables_args_t;
+
+int ccv_seq_tables_check(const ccv_seq_tables_args_t* args);
+int ccv_seq_tables(const ccv_seq_tables_args_t* args, void* hip_stream);
 
 /* Static, NUL-terminated name of a status code ("CCV_OK", ...). */
 const char* ccv_status_str(int status);
