@@ -66,6 +66,12 @@ bool vectors(const View& v, int unit, int bytes) {
   return true;
 }
 
+// Whether the kernels' buffer loads take the view's rows as they are: steps apart from each
+// other and near enough for a 32-bit offset over 64 of them, `unit` elements a load.
+bool loadable(const View& v, int unit, int bytes) {
+  return vectors(v, unit, bytes) && (v.n[1] <= 1 || (v.s[1] >= v.n[3] && v.s[1] <= (1 << 22)));
+}
+
 bool dtype_ok(int d) { return d >= 0 && d <= 2; }
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -104,8 +110,20 @@ int check_sizes(const Sizes& z) {
   return CCV_OK;
 }
 
-// Fills the counts and the workspace's pieces; *bytes is what they take.
-int plan(const Sizes& z, bool bwd, void* ws, DeltaArgs* a, int* nt, int64_t* bytes) {
+// What validate leaves to be launched.
+struct Work {
+  DeltaArgs a;
+  int nt;
+  int64_t bytes;
+  bool chunks, states;     // there are steps; there are states to be written without any
+  bool pack[4];            // q, k, v, dout: need a copy before the kernels' loads take them
+  void* packed[4];
+};
+
+// Fills the counts and the workspace's pieces.
+int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
+  DeltaArgs* a = &out->a;
+  int* nt = &out->nt;
   *a = DeltaArgs{};
   const bool packed = z.cu && z.L > 0;
   a->cu = z.cu;
@@ -137,11 +155,11 @@ int plan(const Sizes& z, bool bwd, void* ws, DeltaArgs* a, int* nt, int64_t* byt
     w.take(&a->table, nch, 4);
     w.take(&a->cstart, a->nseq + 2, 2);
   }
-  w.take(&a->W, heads, 4096);
-  w.take(&a->P, heads, 4096);
+  w.take(&a->W, heads, kDeltaMatrix);
+  w.take(&a->P, heads, kDeltaMatrix);
   w.take(&a->dec, heads, kDeltaDec);
   if (bwd) {
-    w.take(&a->WT, heads, 4096);
+    w.take(&a->WT, heads, kDeltaMatrix);
     w.take(&a->S, heads, (int64_t)a->Dkp * a->Dvp);
     w.take(&a->dS, heads, (int64_t)a->Dkp * a->Dvp);
     w.take(&a->N, heads, 64 * (int64_t)a->Dvp);
@@ -149,8 +167,16 @@ int plan(const Sizes& z, bool bwd, void* ws, DeltaArgs* a, int* nt, int64_t* byt
     w.take(&a->Y, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->part, heads, a->Dvp / 16 * kDeltaPart);
   }
+  const int64_t steps = z.B * z.L, wk = z.Hk * round_up(z.Dk, 8), wv = z.Hv * round_up(z.Dv, 8);
+  char* p[4] = {};
+  for (int i = 0; i < 4; ++i)
+    if (pack[i]) w.take(&p[i], steps, (i < 2 ? wk : wv) * elt_size(z.x_dtype));
   if (w.over) return CCV_E_SHAPE;
-  *bytes = w.used;
+  for (int i = 0; i < 4; ++i) {
+    out->pack[i] = pack[i];
+    out->packed[i] = p[i];
+  }
+  out->bytes = w.used;
   return CCV_OK;
 }
 
@@ -165,24 +191,19 @@ int check_workspace(const void* ws, int64_t given, int64_t need) {
   return given < need ? CCV_E_SHAPE : CCV_OK;
 }
 
-// What validate leaves to be launched.
-struct Work {
-  DeltaArgs a;
-  int nt;
-  int64_t bytes;
-  bool chunks, states;     // there are steps; there are states to be written without any
-};
-
 int validate_fwd(const ccv_delta_fwd_args_t* p, Work* w, bool with_ws) {
   if (!p) return CCV_E_NULL;
   if (p->struct_size != (int64_t)sizeof(ccv_delta_fwd_args_t)) return CCV_E_ABI;
   const Sizes z{p->B, p->L, p->N, p->Hk, p->Hv, p->Dk, p->Dv, p->cu_seqlens, p->x_dtype, p->g_dtype, p->beta_dtype};
   int st = check_sizes(z);
   if (st != CCV_OK) return st;
-  st = plan(z, false, with_ws ? p->workspace : nullptr, &w->a, &w->nt, &w->bytes);
+  const int es = elt_size(p->x_dtype);
+  const bool pack[4] = {!loadable(view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), 8, 16),
+                        !loadable(view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es), 8, 16),
+                        !loadable(view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), 1, es), false};
+  st = plan(z, false, with_ws ? p->workspace : nullptr, w, pack);
   if (st != CCV_OK) return st;
   DeltaArgs& a = w->a;
-  const int es = elt_size(p->x_dtype);
   w->chunks = p->B > 0 && p->L > 0;
   w->states = p->final_state && a.nseq > 0;
   const View q = view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), k = view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es),
@@ -226,7 +247,6 @@ int validate_fwd(const ccv_delta_fwd_args_t* p, Work* w, bool with_ws) {
   copy3(a.h0_s, p->init_stride);
   copy3(a.ht_s, p->final_stride);
   a.scale = p->scale;
-  a.vec_qk = vectors(q, 8, 16) && vectors(k, 8, 16);
   a.vec_o = vectors(o, 4, 4 * es);
   return CCV_OK;
 }
@@ -237,10 +257,14 @@ int validate_bwd(const ccv_delta_bwd_args_t* p, Work* w, bool with_ws) {
   const Sizes z{p->B, p->L, p->N, p->Hk, p->Hv, p->Dk, p->Dv, p->cu_seqlens, p->x_dtype, p->g_dtype, p->beta_dtype};
   int st = check_sizes(z);
   if (st != CCV_OK) return st;
-  st = plan(z, true, with_ws ? p->workspace : nullptr, &w->a, &w->nt, &w->bytes);
+  const int es = elt_size(p->x_dtype);
+  const bool pack[4] = {!loadable(view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), 8, 16),
+                        !loadable(view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es), 8, 16),
+                        !loadable(view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), 1, es),
+                        !loadable(view(p->dout, p->B, p->L, p->Hv, p->Dv, p->dout_stride, es), 8, 16)};
+  st = plan(z, true, with_ws ? p->workspace : nullptr, w, pack);
   if (st != CCV_OK) return st;
   DeltaArgs& a = w->a;
-  const int es = elt_size(p->x_dtype);
   w->chunks = p->B > 0 && p->L > 0;
   w->states = p->dinitial_state && a.nseq > 0;
   const View q = view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), k = view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es),
@@ -308,8 +332,6 @@ int validate_bwd(const ccv_delta_bwd_args_t* p, Work* w, bool with_ws) {
   copy3(a.dg_s, p->dg_stride);
   copy3(a.db_s, p->dbeta_stride);
   a.scale = p->scale;
-  a.vec_qk = vectors(q, 8, 16) && vectors(k, 8, 16);
-  a.vec_do = vectors(d, 8, 16);
   a.vec_dqk = vectors(dq, 4, 4 * es) && vectors(dk, 4, 4 * es);
   return CCV_OK;
 }
@@ -370,6 +392,31 @@ int validate_step(const ccv_delta_update_args_t* p, DeltaStepArgs* a, bool* work
   return CCV_OK;
 }
 
+// Copies what the kernels' loads cannot take, and points the call at the copies.
+int pack(Work* w, void* stream) {
+  DeltaArgs& a = w->a;
+  if (a.L == 1) {                // a stride that is never used may be anything: the kernels' bound on
+    a.q_s[1] = a.k_s[1] = kDeltaMaxDk;      // a chunk's rows counts on steps that lie apart
+    a.v_s[1] = a.do_s[1] = round_up(a.Dv, 8);
+  }
+  const int64_t B = a.packed ? 1 : a.nseq;
+  const auto one = [&](const void** src, int64_t* s, int32_t H, int32_t D, void* dst) {
+    const int32_t Dp = (int32_t)round_up(D, 8);
+    DeltaPackArgs p{*src, {s[0], s[1], s[2]}, dst, B * a.L * H, a.L, H, D, Dp, a.x_dtype};
+    *src = dst;
+    s[2] = Dp;
+    s[1] = (int64_t)H * Dp;
+    s[0] = s[1] * a.L;
+    return launch_delta_pack(p, stream);
+  };
+  int e = 0;
+  if (w->pack[0]) e = one(&a.q, a.q_s, a.Hk, a.Dk, w->packed[0]);
+  if (!e && w->pack[1]) e = one(&a.k, a.k_s, a.Hk, a.Dk, w->packed[1]);
+  if (!e && w->pack[2]) e = one(&a.v, a.v_s, a.Hv, a.Dv, w->packed[2]);
+  if (!e && w->pack[3]) e = one(&a.dout, a.do_s, a.Hv, a.Dv, w->packed[3]);
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -391,6 +438,7 @@ int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream) {
   if (st != CCV_OK) return st;
   if (!w.chunks && !w.states) return CCV_OK;
   if (w.chunks) {
+    if (pack(&w, hip_stream) != 0) return CCV_E_HIP;
     if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_prep(w.a, false, hip_stream) != 0) return CCV_E_HIP;
   }
@@ -414,6 +462,7 @@ int ccv_delta_bwd(const ccv_delta_bwd_args_t* args, void* hip_stream) {
   if (st != CCV_OK) return st;
   if (!w.chunks && !w.states) return CCV_OK;
   if (w.chunks) {
+    if (pack(&w, hip_stream) != 0) return CCV_E_HIP;
     if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_prep(w.a, true, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_scan(w.a, true, w.nt, hip_stream) != 0) return CCV_E_HIP;

@@ -23,16 +23,6 @@ namespace {
 
 constexpr int LDT = 72;
 
-template <int DT, int KS, int NT>
-struct LoadedBack {
-  Raw8<DT> k[KS], q[KS];
-  f32x8 WT[2], PT[2];
-  float d[NT][4], v[NT][4], R[NT][4], N[NT][4];
-  f32x4 gam, del, beta;
-  float last;
-  int n, row, t0;
-};
-
 template <int DT, int DKP, int NT>
 __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
@@ -57,8 +47,8 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
     }
     return;
   }
-  int c0, c1;
-  chunks_of(a, seq, &c0, &c1);
+  const Sequence sq = sequence_at(a, seq);
+  const int c0 = sq.first, c1 = sq.end;
 
   f32x4 S[MT][NT];
 #pragma unroll
@@ -71,77 +61,120 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
         S[m][j][e] = a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
       }
 
-  auto load = [&](int c) {
-    LoadedBack<DT, KS, NT> x;
-    const Chunk k = chunk_at(a, c);
-    x.n = k.n;
-    x.row = k.row;
-    x.t0 = k.t0;
-    const int64_t ch = (int64_t)c * a.Hv + h;
-    const int i = 16 * w + r;
-    const bool live = i < k.n;
-    const char* kp = row_ptr<DT>(a.k, a.k_s, k.row, k.t0 + (live ? i : 0), hk);
-    const char* qp = row_ptr<DT>(a.q, a.q_s, k.row, k.t0 + (live ? i : 0), hk);
+  // loaded a chunk ahead, each part when the one before it has been used
+  const int i = 16 * w + r;
+  Chunk k;
+  Raw8<DT> xk[KS], xq[KS];
+  Frag<3> xW[2], xP[2];
+  typename Stored<DT>::type xd[NT][4], xv[NT][4];
+  float xR[NT][4], xN[NT][4];
+  struct Gates {
+    f32x4 gam, del, beta;
+    float last;
+  } gt, gn;
+  uint32_t ok[KS], oq[KS], ov[NT][4], odo[NT][4];      // byte offsets of this lane's parts
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = 32 * s + 8 * g4, left = live ? a.Dk - d : 0;
-      x.k[s] = load8<DT>(kp + d * ES, left, a.vec_qk);
-      x.q[s] = load8<DT>(qp + d * ES, left, a.vec_qk);
-    }
+  for (int s = 0; s < KS; ++s) {
+    const int d = 32 * s + 8 * g4;
+    ok[s] = d < a.Dk ? i * (uint32_t)(a.k_s[1] * ES) + d * ES : kNowhere;
+    oq[s] = d < a.Dk ? i * (uint32_t)(a.q_s[1] * ES) + d * ES : kNowhere;
+  }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      x.WT[s] = load_f8(a.WT + ch * 4096 + i * 64 + 32 * s + 8 * g4);
-      x.PT[s] = load_f8(a.P + ch * 4096 + i * 64 + 32 * s + 8 * g4);
-    }
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int t = 16 * w + 4 * g4 + e;
-      const bool in = t < k.n;
-      const char* vp = row_ptr<DT>(a.v, a.v_s, k.row, k.t0 + (in ? t : 0), h);
-      const char* dp = row_ptr<DT>(a.dout, a.do_s, k.row, k.t0 + (in ? t : 0), h);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int dv = dv0 + 16 * j + r;
-        x.v[j][e] = in && dv < a.Dv ? load1<DT>(vp + dv * ES) : 0.0f;
-        x.d[j][e] = in && dv < a.Dv ? load1<DT>(dp + dv * ES) : 0.0f;
-        x.R[j][e] = a.R[(ch * 64 + t) * a.Dvp + dv];
-        x.N[j][e] = a.N[(ch * 64 + t) * a.Dvp + dv];
-      }
+      const int dv = dv0 + 16 * j + r, t = 16 * w + 4 * g4 + e;
+      ov[j][e] = dv < a.Dv ? t * (uint32_t)(a.v_s[1] * ES) + dv * ES : kNowhere;
+      odo[j][e] = dv < a.Dv ? t * (uint32_t)(a.do_s[1] * ES) + dv * ES : kNowhere;
     }
-    const float* dec = a.dec + ch * kDeltaDec;
-    x.gam = *reinterpret_cast<const f32x4*>(dec + 16 * w + 4 * g4);
-    x.del = *reinterpret_cast<const f32x4*>(dec + 64 + 16 * w + 4 * g4);
-    x.beta = *reinterpret_cast<const f32x4*>(dec + 128 + 16 * w + 4 * g4);
-    x.last = dec[63];
-    return x;
+  const uint32_t om = (2 * w * 64 + l) * 16, od = (16 * w + 4 * g4) * 4,
+                 orow = ((16 * w + 4 * g4) * (uint32_t)a.Dvp + dv0 + r) * 4;
+  auto load_kq = [&](const Chunk& n) {
+    const __amdgpu_buffer_rsrc_t kb = chunk_rows<DT>(a.k, a.k_s, n, hk, (a.Dk + 7) & ~7);
+    const __amdgpu_buffer_rsrc_t qb = chunk_rows<DT>(a.q, a.q_s, n, hk, (a.Dk + 7) & ~7);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      xk[s] = buf8<DT>(kb, ok[s]);
+      xq[s] = buf8<DT>(qb, oq[s]);
+    }
+  };
+  auto load_v = [&](const Chunk& n) {
+    const __amdgpu_buffer_rsrc_t b = chunk_rows<DT>(a.v, a.v_s, n, h, a.Dv);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xv[j][e] = buf_raw<DT>(b, ov[j][e]);
+  };
+  auto load_d = [&](const Chunk& n) {
+    const __amdgpu_buffer_rsrc_t b = chunk_rows<DT>(a.dout, a.do_s, n, h, a.Dv);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) xd[j][e] = buf_raw<DT>(b, odo[j][e]);
+  };
+  auto load_rows = [&](float (&x)[NT][4], const float* base, int64_t ch) {
+    const __amdgpu_buffer_rsrc_t b = buffer(base + ch * 64 * a.Dvp, 256u * a.Dvp);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) x[j][e] = buf1<CCV_DT_F32>(b, orow + e * 4 * a.Dvp + 64 * j);
+  };
+  auto load_matrix = [&](Frag<3> (&x)[2], const uint16_t* base, int64_t ch) {
+    const __amdgpu_buffer_rsrc_t b = buffer(base + ch * kDeltaMatrix, 2 * kDeltaMatrix);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) x[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+  };
+  auto load_dec = [&](int64_t ch) {
+    const __amdgpu_buffer_rsrc_t b = buffer(a.dec + ch * kDeltaDec, 4 * kDeltaDec);
+    Gates g;
+    g.gam = buf_f4(b, od);
+    g.del = buf_f4(b, od + 256);
+    g.beta = buf_f4(b, od + 512);
+    g.last = buf1<CCV_DT_F32>(b, 4 * 63);
+    return g;
   };
 
-  LoadedBack<DT, KS, NT> x;
-  if (c0 < c1) x = load(c1 - 1);
+  if (c0 < c1) {
+    const int64_t ch = (int64_t)(c1 - 1) * a.Hv + h;
+    k = sq.chunk(seq, c1 - 1);
+    load_kq(k);
+    load_d(k);
+    gn = load_dec(ch);
+    load_matrix(xP, a.P, ch);
+    load_rows(xN, a.N, ch);
+    load_matrix(xW, a.WT, ch);
+    load_v(k);
+    load_rows(xR, a.R, ch);
+  }
   for (int c = c1 - 1; c >= c0; --c) {
     const int64_t ch = (int64_t)c * a.Hv + h;
-    const LoadedBack<DT, KS, NT> y = x;
-    if (c > c0) x = load(c - 1);
+    const int cn = c > c0 ? c - 1 : c;
+    const int64_t chn = (int64_t)cn * a.Hv + h;
+    const Chunk kn = sq.chunk(seq, cn);
+    gt = gn;
     float* part = a.part + (ch * a.slices + slice) * kDeltaPart;
 
     // the planes of this chunk
     Frag<NA> kf[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      kf[s] = planes<DT>(y.k[s]);
-      const Frag<NA> qf = planes<DT>(y.q[s]);
+      kf[s] = planes<DT>(xk[s]);
+      const Frag<NA> qf = planes<DT>(xq[s]);
 #pragma unroll
       for (int p = 0; p < NA; ++p) {
         *reinterpret_cast<bf16x8*>(&Kl[p][16 * w + r][32 * s + 8 * g4]) = kf[s].p[p];
         *reinterpret_cast<bf16x8*>(&Ql[p][16 * w + r][32 * s + 8 * g4]) = qf.p[p];
       }
     }
+    load_kq(kn);
+    gn = load_dec(chn);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const f32x4 d = {y.d[j][0], y.d[j][1], y.d[j][2], y.d[j][3]};
+      const f32x4 d = {widen<DT>(xd[j][0]), widen<DT>(xd[j][1]), widen<DT>(xd[j][2]), widen<DT>(xd[j][3])};
       put4<NA>(&Dp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d);
-      put4<3>(&Dd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d * y.gam * a.scale);
+      put4<3>(&Dd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d * gt.gam * a.scale);
     }
+    load_d(kn);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -151,7 +184,7 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
         for (int e = 0; e < 4; ++e)
           a.dS[(ch * DKP + 16 * (MT * w + m) + 4 * g4 + e) * a.Dvp + dv0 + 16 * j + r] = S[m][j][e];
       }
-    __syncthreads();
+    lds_barrier();
 
     // dN
     f32x4 kd[NT], pd[NT];
@@ -165,19 +198,20 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (2 * s + 1 < w) continue;           // P^T is upper triangular
-      const Frag<3> pf = split8<3>(y.PT[s]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) pd[j] = mma<2>(pf, get8<NA>(&Dp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), pd[j]);
+      for (int j = 0; j < NT; ++j) pd[j] = mma<2>(xP[s], get8<NA>(&Dp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), pd[j]);
     }
     f32x4 cs = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      kd[j] *= y.del;
+      kd[j] *= gt.del;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cs[e] = __builtin_fmaf(kd[j][e], y.N[j][e], cs[e]);
+      for (int e = 0; e < 4; ++e) cs[e] = __builtin_fmaf(kd[j][e], xN[j][e], cs[e]);
       put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, pd[j] * a.scale + kd[j]);
     }
-    __syncthreads();
+    load_matrix(xP, a.P, chn);
+    load_rows(xN, a.N, chn);
+    lds_barrier();
 
     // Y, dv
     f32x4 Y[NT], bs = {0, 0, 0, 0}, gs = {0, 0, 0, 0};
@@ -186,24 +220,26 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (2 * s + 1 < w) continue;
-      const Frag<3> wf = split8<3>(y.WT[s]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) Y[j] = mma<2>(wf, get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), Y[j]);
+      for (int j = 0; j < NT; ++j) Y[j] = mma<2>(xW[s], get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), Y[j]);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int dv = dv0 + 16 * j + r;
-      const f32x4 dR = Y[j] * y.beta;
+      const f32x4 dR = Y[j] * gt.beta;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * w + 4 * g4 + e;
-        bs[e] = __builtin_fmaf(Y[j][e], y.R[j][e], bs[e]);
-        gs[e] = __builtin_fmaf(dR[e], y.R[j][e] - y.v[j][e], gs[e]);
+        bs[e] = __builtin_fmaf(Y[j][e], xR[j][e], bs[e]);
+        gs[e] = __builtin_fmaf(dR[e], xR[j][e] - widen<DT>(xv[j][e]), gs[e]);
         a.Y[(ch * 64 + t) * a.Dvp + dv] = Y[j][e];
-        if (t < y.n && dv < a.Dv) store1<DT>(row_ptr<DT>(a.dv, a.dv_s, y.row, (int64_t)y.t0 + t, h) + dv * ES, dR[e]);
+        if (t < k.n && dv < a.Dv) store1<DT>(row_ptr<DT>(a.dv, a.dv_s, k.row, (int64_t)k.t0 + t, h) + dv * ES, dR[e]);
       }
-      put4<3>(&Yp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, dR * -y.gam);
+      put4<3>(&Yp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, dR * -gt.gam);
     }
+    load_matrix(xW, a.WT, chn);
+    load_v(kn);
+    load_rows(xR, a.R, chn);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float b = sum16(bs[e]), g = sum16(gs[e]), q = sum16(cs[e]);
@@ -213,13 +249,13 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
         part[192 + 16 * w + 4 * g4 + e] = q;
       }
     }
-    __syncthreads();
+    lds_barrier();
 
     // dS at the chunk's start
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) S[m][j] *= y.last;
+      for (int j = 0; j < NT; ++j) S[m][j] *= gt.last;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -232,7 +268,8 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
           S[m][j] = mma<2>(kt, get8<3>(&Yp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), S[m][j]);
         }
       }
-    __syncthreads();
+    k = kn;
+    lds_barrier();
   }
   if (a.dh0) {
 #pragma unroll
@@ -280,11 +317,13 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   for (int n = 0; n < TK; ++n) dq[n] = dk[n] = f32x4{0, 0, 0, 0};
 
   if (k.seq < a.nseq) {
-    const char* kp = row_ptr<DT>(half ? a.k : a.q, half ? a.k_s : a.q_s, k.row, k.t0 + (live ? t : 0), hk);
+    const __amdgpu_buffer_rsrc_t kb = half ? chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7)
+                                           : chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7);
+    const uint32_t ks = t * (uint32_t)((half ? a.k_s[1] : a.q_s[1]) * ES);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const int d = 32 * s + 8 * g4;
-      const Frag<NA> f = planes<DT>(load8<DT>(kp + d * ES, live ? a.Dk - d : 0, a.vec_qk));
+      const Frag<NA> f = planes<DT>(buf8<DT>(kb, d < a.Dk ? ks + d * ES : kNowhere));
 #pragma unroll
       for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(half ? &Kl[p][t][d] : &Ql[p][t][d]) = f.p[p];
     }
@@ -295,8 +334,9 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
       const float* Sg = a.S + ch * DKP * a.Dvp;
       const float* Dg = a.dS + ch * DKP * a.Dvp;
       const float* Ng = a.N + ch * 64 * a.Dvp;
-      const float* Yg = a.Y + (ch * 64 + t) * a.Dvp;
-      const char* dop = row_ptr<DT>(a.dout, a.do_s, k.row, (int64_t)k.t0 + (live ? t : 0), h);
+      const __amdgpu_buffer_rsrc_t Yb = buffer(a.Y + ch * 64 * a.Dvp, 256u * a.Dvp);
+      const __amdgpu_buffer_rsrc_t dob = chunk_rows<DT>(a.dout, a.do_s, k, h, (a.Dv + 7) & ~7);
+      const uint32_t dos = t * (uint32_t)(a.do_s[1] * ES);
       if (tid < 64) G[tid] = reinterpret_cast<const double*>(dec + 192)[tid];
       f32x4 zq[TK], zy[TK], zn[TK], pr[4];
       float dot = 0;
@@ -319,13 +359,14 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(s4[i][e], d4[i][e], dot);
         }
         const int dv = v0 + 8 * g4;
-        const Frag<NA> of = planes<DT>(load8<DT>(dop + dv * ES, live ? a.Dv - dv : 0, a.vec_do));
-        const Frag<3> yf = split8<3>(load_f8(Yg + dv));
-        __syncthreads();
+        const Frag<NA> of = planes<DT>(buf8<DT>(dob, dv < a.Dv ? dos + dv * ES : kNowhere));
+        const uint32_t oy = (t * (uint32_t)a.Dvp + dv) * 4;
+        const Frag<3> yf = split8<3>(__builtin_shufflevector(buf_f4(Yb, oy), buf_f4(Yb, oy + 16), 0, 1, 2, 3, 4, 5, 6, 7));
+        lds_barrier();
         put4<3>(Ns + sr * LDV + sc, 64 * LDV, n4);
 #pragma unroll
         for (int i = 0; i < RS; ++i) put4<OP>(St + (64 * i + sr) * LDV + sc, DKP * LDV, s4[i]);
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int n = 0; n < TK; ++n) {
           const Frag<OP> sf = get8<OP>(St + (16 * (TK * half + n) + r) * LDV + 8 * g4, DKP * LDV);
@@ -339,10 +380,10 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           pr[n] = half ? mma<2>(yf, nf, pr[n]) : mma<2>(of, nf, pr[n]);
         }
         const Frag<OP> nown = get8<OP>(Ns + t * LDV + 8 * g4, 64 * LDV);
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int i = 0; i < RS; ++i) put4<OP>(St + (64 * i + sr) * LDV + sc, DKP * LDV, d4[i]);
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int n = 0; n < TK; ++n)
           zn[n] = mma<OO>(get8<OP>(St + (16 * (TK * half + n) + r) * LDV + 8 * g4, DKP * LDV), nown, zn[n]);
@@ -360,7 +401,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
       }
 
       // F (waves 0..3) and E (4..7), their products with Q K^T and K K^T
-      __syncthreads();
+      lds_barrier();
       f32x4 rs = {0, 0, 0, 0}, bs = {0, 0, 0, 0};
       double Gi[4];
       float bi[4];
@@ -406,7 +447,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           if (half) bsum[16 * w + 4 * g4 + e] = bv;
         }
       }
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const bool lo = 2 * s <= w, up = 2 * s + 1 >= w;      // rows i >= j; rows j <= i
@@ -465,7 +506,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         }
       }
       // the next head's first barrier comes before it writes any of this
-      __syncthreads();
+      lds_barrier();
     }
   } else if (tid < 64 && tid < k.n) {
     for (int h = hk * group; h < (hk + 1) * group; ++h) {

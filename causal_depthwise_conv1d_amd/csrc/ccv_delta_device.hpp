@@ -30,13 +30,26 @@ template <int DT> struct OutOrder { static constexpr int n = DT == CCV_DT_F32 ? 
 
 template <int P> struct Frag { bf16x8 p[P]; };
 
+// Two values rounded to bf16 in one dword, and taken off: x, y keep the remainders.
+__device__ inline uint32_t take2(float& x, float& y) {
+  const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  x -= __builtin_bit_cast(float, h << 16);
+  y -= __builtin_bit_cast(float, h & 0xffff0000u);
+  return h;
+}
+
 template <int P>
 __device__ inline Frag<P> split8(f32x8 x) {
   Frag<P> f;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = x[j];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    f.p[i] = __builtin_convertvector(x, bf16x8);
-    if (i + 1 < P) x -= __builtin_convertvector(f.p[i], f32x8);
+    u32x4 d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = take2(v[2 * j], v[2 * j + 1]);
+    f.p[i] = __builtin_bit_cast(bf16x8, d);
   }
   return f;
 }
@@ -52,34 +65,101 @@ __device__ inline f32x4 mma(const Frag<PA>& a, const Frag<PB>& b, f32x4 acc) {
   return acc;
 }
 
+// The same with a sum for each size of term: chains of dependent instructions a third as long.
+template <int ORDER> struct Sums {
+  f32x4 s[ORDER + 1];
+  __device__ inline Sums() {
+#pragma unroll
+    for (int i = 0; i <= ORDER; ++i) s[i] = f32x4{0, 0, 0, 0};
+  }
+  template <int PA, int PB>
+  __device__ inline void add(const Frag<PA>& a, const Frag<PB>& b) {
+#pragma unroll
+    for (int i = 0; i < PA; ++i)
+#pragma unroll
+      for (int j = 0; j < PB; ++j)
+        if (i + j <= ORDER) s[i + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], s[i + j], 0, 0, 0);
+  }
+  __device__ inline f32x4 total() const {
+    f32x4 t = s[ORDER];
+#pragma unroll
+    for (int i = ORDER - 1; i >= 0; --i) t += s[i];
+    return t;
+  }
+};
+
 // Eight consecutive elements of a row, as stored.
 template <int DT> struct Raw8 { u32x4 d[DT == CCV_DT_F32 ? 2 : 1]; };
 
-// The first `left` of 8 consecutive elements from p; zeros for the others.  vec: all or
-// none of them are there and p is aligned for whole vectors.
+// Loads of a chunk's rows go through buffer descriptors: a uniform base in scalar registers,
+// one 32-bit byte offset a lane that stays the same from chunk to chunk, and the
+// descriptor's bound, past which a load gives zeros without a branch (a branch around a
+// load makes the compiler wait for it where the paths join).  The bound ends the rows of
+// a short last chunk; a lane whose columns lie past the row's width has kNowhere.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+__device__ inline u32x4 buf16(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+}
+__device__ inline f32x4 buf_f4(__amdgpu_buffer_rsrc_t b, uint32_t off) { return __builtin_bit_cast(f32x4, buf16(b, off)); }
+
+template <int P>
+__device__ inline Frag<P> buf_planes(__amdgpu_buffer_rsrc_t b, uint32_t off, uint32_t plane) {
+  Frag<P> f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) f.p[i] = __builtin_bit_cast(bf16x8, buf16(b, off + i * plane));
+  return f;
+}
 template <int DT>
-__device__ inline Raw8<DT> load8(const void* p, int left, bool vec) {
+__device__ inline Raw8<DT> buf8(__amdgpu_buffer_rsrc_t b, uint32_t off) {
   Raw8<DT> r;
 #pragma unroll
-  for (int i = 0; i < (DT == CCV_DT_F32 ? 2 : 1); ++i) r.d[i] = u32x4{0, 0, 0, 0};
-  if (left <= 0) return r;
-  if (vec) {
-    r.d[0] = load16(p);
-    if constexpr (DT == CCV_DT_F32) r.d[1] = load16(static_cast<const char*>(p) + 16);
-    return r;
-  }
-  if constexpr (DT == CCV_DT_F32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) r.d[i / 4][i % 4] = static_cast<const uint32_t*>(p)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) r.d[0][i / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[i] << (16 * (i % 2));
-  }
+  for (int i = 0; i < (DT == CCV_DT_F32 ? 2 : 1); ++i) r.d[i] = buf16(b, off + 16 * i);
   return r;
 }
+// One element as stored, and its value: the conversion stands where the value is used, so that
+// the load may still be under way until then.
+template <int DT> struct Stored { using type = uint16_t; };
+template <> struct Stored<CCV_DT_F32> { using type = uint32_t; };
 
+template <int DT>
+__device__ inline typename Stored<DT>::type buf_raw(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  if constexpr (DT == CCV_DT_F32) return __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b16(b, off, 0, 0);
+}
+template <int DT>
+__device__ inline float widen(typename Stored<DT>::type r) {
+  if constexpr (DT == CCV_DT_F32) return __builtin_bit_cast(float, r);
+  else return DT == CCV_DT_BF16 ? BF16::to_f(r) : F16::to_f(r);
+}
+template <int DT> struct Raw4 { u32x4 d; };      // four elements; 16-bit ones in the first two dwords
+template <int DT>
+__device__ inline Raw4<DT> buf_raw4(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  if constexpr (DT == CCV_DT_F32) return {buf16(b, off)};
+  const u32x2 d = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0));
+  return {u32x4{d[0], d[1], 0, 0}};
+}
+template <int DT>
+__device__ inline f32x4 widen4(const Raw4<DT>& r) {
+  if constexpr (DT == CCV_DT_F32) return __builtin_bit_cast(f32x4, r.d);
+  f32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = r.d[i / 2];
+    const uint16_t h = (uint16_t)(two >> (16 * (i % 2)));
+    x[i] = DT == CCV_DT_BF16 ? BF16::to_f(h) : F16::to_f(h);
+  }
+  return x;
+}
+template <int DT>
+__device__ inline float buf1(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  if constexpr (DT == CCV_DT_F32) return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0));
+  const uint16_t h = __builtin_amdgcn_raw_buffer_load_b16(b, off, 0, 0);
+  return DT == CCV_DT_BF16 ? BF16::to_f(h) : F16::to_f(h);
+}
 template <int DT>
 __device__ inline Frag<InPlanes<DT>::n> planes(const Raw8<DT>& r) {
   Frag<InPlanes<DT>::n> f;
@@ -94,11 +174,6 @@ __device__ inline Frag<InPlanes<DT>::n> planes(const Raw8<DT>& r) {
     f = split8<3>(x);
   }
   return f;
-}
-
-__device__ inline f32x8 load_f8(const float* p) {
-  const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
-  return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 template <int DT>
@@ -164,11 +239,13 @@ __device__ inline f32x4 load4(const void* p, int left, bool vec) {
 // Four fp32 values into P planes of an LDS array whose planes are `plane` elements apart.
 template <int P>
 __device__ inline void put4(__bf16* at, int plane, f32x4 x) {
+  float v[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const bf16x4 h = __builtin_convertvector(x, bf16x4);
-    *reinterpret_cast<bf16x4*>(at + i * plane) = h;
-    if (i + 1 < P) x -= __builtin_convertvector(h, f32x4);
+    u32x2 d;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) d[j] = take2(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<u32x2*>(at + i * plane) = d;
   }
 }
 template <int P>
@@ -212,15 +289,20 @@ __device__ inline float sum4rows(float v) {
   return v;
 }
 
-// Where a chunk lies.
+// A workgroup barrier for data in LDS: every wave's LDS accesses before it are done, while its
+// global loads and stores stay in flight (__syncthreads would wait for them too, which costs
+// a prefetch its point).
+__device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Where a chunk lies; the same in every lane.
 struct Chunk { int seq, row, t0, n; };
 
 __device__ inline Chunk chunk_at(const DeltaArgs& a, int c) {
   Chunk k;
   if (a.packed) {
-    k.seq = a.table[4 * c];
-    k.t0 = a.table[4 * c + 1];
-    k.n = a.table[4 * c + 2];
+    k.seq = __builtin_amdgcn_readfirstlane(a.table[4 * c]);
+    k.t0 = __builtin_amdgcn_readfirstlane(a.table[4 * c + 1]);
+    k.n = __builtin_amdgcn_readfirstlane(a.table[4 * c + 2]);
     k.row = 0;
   } else {
     k.seq = c / a.chunks_per_row;
@@ -232,10 +314,34 @@ __device__ inline Chunk chunk_at(const DeltaArgs& a, int c) {
   return k;
 }
 
-// Sequence s's chunks are first .. end - 1.
-__device__ inline void chunks_of(const DeltaArgs& a, int s, int* first, int* end) {
-  *first = a.packed ? a.cstart[s] : s * a.chunks_per_row;
-  *end = a.packed ? a.cstart[s + 1] : (s + 1) * a.chunks_per_row;
+// A sequence: its chunks are first .. end - 1, its steps t0 .. t0 + len - 1 of `row`.  A pass
+// over its chunks needs no further look at the tables.
+struct Sequence {
+  int first, end, row, t0;
+  int64_t len;
+  __device__ inline Chunk chunk(int seq, int c) const {
+    const int64_t left = len - (int64_t)(c - first) * kDeltaChunk;
+    return {seq, row, t0 + (c - first) * kDeltaChunk, left < kDeltaChunk ? (int)left : kDeltaChunk};
+  }
+};
+
+__device__ inline Sequence sequence_at(const DeltaArgs& a, int s) {
+  Sequence q;
+  if (a.packed) {
+    const int32_t* begin = a.cstart + (a.nseq + 2);
+    q.first = __builtin_amdgcn_readfirstlane(a.cstart[s]);
+    q.end = __builtin_amdgcn_readfirstlane(a.cstart[s + 1]);
+    q.t0 = __builtin_amdgcn_readfirstlane(begin[s]);
+    q.len = __builtin_amdgcn_readfirstlane(begin[s + 1]) - q.t0;
+    q.row = 0;
+  } else {
+    q.first = s * a.chunks_per_row;
+    q.end = q.first + a.chunks_per_row;
+    q.row = s;
+    q.t0 = 0;
+    q.len = a.L;
+  }
+  return q;
 }
 
 template <int DT>
@@ -245,6 +351,110 @@ __device__ inline const char* row_ptr(const void* base, const int64_t* s, int ro
 template <int DT>
 __device__ inline char* row_ptr(void* base, const int64_t* s, int row, int64_t t, int h) {
   return static_cast<char*>(base) + (row * s[0] + t * s[1] + h * s[2]) * (DT == CCV_DT_F32 ? 4 : 2);
+}
+
+// A chunk's rows of a [B, L, H, D] array, `width` elements of each.
+template <int DT>
+__device__ inline __amdgpu_buffer_rsrc_t chunk_rows(const void* base, const int64_t* s, const Chunk& k, int h, int width) {
+  constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
+  const uint32_t bytes = (uint32_t)((k.n - 1) * (int32_t)(s[1] * ES) + width * ES);
+  return buffer(row_ptr<DT>(base, s, k.row, k.t0, h), bytes);
+}
+
+// A sequence's chunks of such rows one after the other: the address moves by a constant.
+template <int DT>
+struct Rows {
+  static constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
+  const char* at;
+  int64_t step;              // bytes from chunk to chunk
+  uint32_t stride, width;    // bytes from step to step, and of a row
+  __device__ inline Rows(const void* base, const int64_t* s, const Sequence& q, int h, int elements, int chunk)
+      : at(row_ptr<DT>(base, s, q.row, q.t0 + (int64_t)(chunk - q.first) * kDeltaChunk, h)),
+        step(s[1] * (kDeltaChunk * ES)), stride((uint32_t)(s[1] * ES)), width(elements * ES) {}
+  // the chunk at hand, n steps of it (0: loads give zeros, stores do nothing)
+  __device__ inline __amdgpu_buffer_rsrc_t rows(int n) const { return buffer(at, n > 0 ? (n - 1) * stride + width : 0); }
+};
+
+// The workspace's piece of a chunk, likewise.
+template <class T>
+struct Piece {
+  const T* at;
+  int64_t step;
+  uint32_t bytes;
+  __device__ inline Piece(const T* base, int64_t each, int hv, int64_t ch)
+      : at(base + ch * each), step(each * hv), bytes((uint32_t)(each * sizeof(T))) {}
+  __device__ inline __amdgpu_buffer_rsrc_t piece(bool there) const { return buffer(at, there ? bytes : 0); }
+};
+
+template <int DT>
+__device__ inline void buf_store1(__amdgpu_buffer_rsrc_t b, uint32_t off, float x) {
+  if constexpr (DT == CCV_DT_F32) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), b, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b16(DT == CCV_DT_BF16 ? BF16::from_f(x) : F16::from_f(x), b, off, 0, 0);
+}
+// Four values, rounded; vec: the address takes them as one, and all four are in the row.
+template <int DT>
+__device__ inline void buf_store4(__amdgpu_buffer_rsrc_t b, uint32_t off, f32x4 x, int left, bool vec) {
+  if (vec) {
+    if constexpr (DT == CCV_DT_F32) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, off, 0, 0);
+    } else {
+      u32x2 d;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f32x2 y = {as_f32(x[2 * i]), as_f32(x[2 * i + 1])};
+        if constexpr (DT == CCV_DT_BF16) d[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+        else d[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, f16x2));
+      }
+      __builtin_amdgcn_raw_buffer_store_b64(d, b, off, 0, 0);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) buf_store1<DT>(b, i < left ? off + i * (DT == CCV_DT_F32 ? 4 : 2) : kNowhere, x[i]);
+}
+
+// 16 rows of a chunk's 64, as a wave moves them: 16 bytes a lane with consecutive lanes on
+// consecutive bytes, to LDS planes of row stride LD.  (Loading matrix fragments straight
+// from rows puts 16 neighbouring lanes on 16 rows: 64 cache accesses an instruction where
+// this takes 16.)
+template <int DT, int DKP, int LD>
+struct RowTile {
+  static constexpr int ES = DT == CCV_DT_F32 ? 4 : 2, kLanes = DKP * ES / 16, kLoads = kLanes / 4, NA = InPlanes<DT>::n;
+  u32x4 raw[kLoads];
+  uint32_t off;          // byte offset of the first load; the others follow by 64 / kLanes rows
+  uint32_t next;
+  int at;                // element offset in a plane of LDS, likewise
+  __device__ inline RowTile(int w, int l, uint32_t stride, int width) {
+    const int row = 16 * w + l / kLanes, c = l % kLanes * (16 / ES);
+    off = c < width ? row * stride + c * ES : kNowhere;
+    next = c < width ? 64 / kLanes * stride : 0;
+    at = row * LD + c;
+  }
+  __device__ inline void load(__amdgpu_buffer_rsrc_t b) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) raw[i] = buf16(b, off + i * next);
+  }
+  __device__ inline void store(__bf16* lds, int plane) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      __bf16* p = lds + at + i * (64 / kLanes) * LD;
+      if constexpr (DT == CCV_DT_BF16) {
+        *reinterpret_cast<u32x4*>(p) = raw[i];
+      } else if constexpr (DT == CCV_DT_F16) {
+        const Frag<2> f = split8<2>(__builtin_convertvector(__builtin_bit_cast(f16x8, raw[i]), f32x8));
+        *reinterpret_cast<bf16x8*>(p) = f.p[0];
+        *reinterpret_cast<bf16x8*>(p + plane) = f.p[1];
+      } else {
+        put4<3>(p, plane, __builtin_bit_cast(f32x4, raw[i]));
+      }
+    }
+  }
+};
+
+// Where element (m, k .. k + 7) of a 64 x 64 matrix lies in a plane of the workspace: in the
+// order in which a wave's lanes hold it as fragments, so that they load it in a row.
+__device__ inline int fragment_at(int m, int k) {
+  return (((m >> 4) * 2 + (k >> 5)) * 64 + ((k >> 3) & 3) * 16 + (m & 15)) * 8;
 }
 
 }  // namespace ccv

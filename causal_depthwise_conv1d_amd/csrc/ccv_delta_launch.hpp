@@ -7,6 +7,7 @@
 namespace ccv {
 
 constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 16-row matrix tiles
+constexpr int kDeltaMatrix = 3 * 64 * 64;   // elements of a chunk's W or P
 constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
 constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, dbeta, dG by R, c
 constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
@@ -32,14 +33,14 @@ struct DeltaArgs {
   int32_t Hk, Hv, Dk, Dv;
   int32_t Dvp;                                  // Dv rounded up to 32: the workspace's value width
   int32_t x_dtype, g_dtype, b_dtype;
-  int32_t vec_qk, vec_o, vec_do, vec_dqk;        // rows may move as whole vectors
+  int32_t vec_o, vec_dqk;                       // rows of out, of dq and dk, may be written as whole vectors
   float scale;
   // workspace (element counts below), ch = chunk * Hv + head
   int32_t* table;                               // packed: [nchunks] x (sequence, first step, steps, -)
   int32_t* cstart;                              // packed: [nseq + 2] first chunk of each sequence
-  float* W;                                     // [ch][64][64] (1 + A)^-1
-  float* P;                                     // [ch][64][64]; the backward holds it transposed
-  float* WT;                                    // backward: W transposed
+  uint16_t* W;                                  // [ch][3][64 x 64, fragment_at]: (1 + A)^-1 as bf16 planes
+  uint16_t* P;                                  // likewise, kDeltaMatrix a chunk and head; the backward holds it transposed
+  uint16_t* WT;                                 // backward: W transposed
   float* dec;                                   // [ch][kDeltaDec]: e^G, e^(G63 - G), beta, and G log2(e) as 64 doubles
   float *S, *dS;                                // backward: [ch][Dkp][Dvp] state at a chunk's start, gradient at its end
   float *N, *R, *Y;                             // backward: [ch][64][Dvp]
@@ -60,7 +61,17 @@ struct DeltaStepArgs {
   float scale;
 };
 
+// A [B, L, H, D] array into a contiguous one of Dp >= D elements a head, zeros behind the D:
+// rows of odd widths, strides or addresses, made ready for 16-byte loads.
+struct DeltaPackArgs {
+  const void* src; int64_t s[3];
+  void* dst;
+  int64_t rows, L;      // rows = B * L * H
+  int32_t H, D, Dp, dtype;
+};
+
 // Each returns a hipError_t value (0 = success).
+int launch_delta_pack(const DeltaPackArgs& a, void* stream);
 int launch_delta_table(const DeltaArgs& a, void* stream);
 int launch_delta_prep(const DeltaArgs& a, bool backward, void* stream);
 int launch_delta_scan(const DeltaArgs& a, bool backward, int nt, void* stream);

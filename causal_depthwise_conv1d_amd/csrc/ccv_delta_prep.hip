@@ -8,8 +8,21 @@
 // as -2000: e^-2000 is 0 in fp32 with room to spare, and no inf - inf arises.
 #include "ccv_delta_device.hpp"
 
+#include <type_traits>
+
 namespace ccv {
 namespace {
+
+// ---- rows that 16-byte loads cannot take, copied -------------------------------------
+template <class T>
+__global__ __launch_bounds__(256) void pack_kernel(DeltaPackArgs a) {
+  const int64_t n = a.rows * a.Dp;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / a.Dp, d = i - r * a.Dp, bl = r / a.H, b = bl / a.L;
+    const T* src = static_cast<const T*>(a.src) + b * a.s[0] + (bl - b * a.L) * a.s[1] + (r - bl * a.H) * a.s[2];
+    static_cast<T*>(a.dst)[i] = d < a.D ? src[d] : T{0};
+  }
+}
 
 // ---- packed rows: the chunks of each sequence ---------------------------------------
 //
@@ -91,8 +104,11 @@ __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
 // matrix instruction, whose accumulator layout is the next product's operand.
 template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
-  constexpr int NA = InPlanes<DT>::n, LDK = DKP + 8, LDA = 68;
-  __shared__ __bf16 Kp[NA][64][LDK];
+  constexpr int NA = InPlanes<DT>::n, LDK = DKP + 8, LDA = 68, ES = DT == CCV_DT_F32 ? 4 : 2;
+  constexpr int OP = OutOrder<DT>::n + 1;
+  __shared__ union { __bf16 k[NA][64][LDK]; float p[64][LDA]; } kp;    // K's planes, then P
+  auto& Kp = kp.k;
+  auto& Pl = kp.p;
   __shared__ float Al[64][LDA], Wl[64][LDA];
   __shared__ double G[64];
   __shared__ float bt[64];
@@ -127,24 +143,22 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     reinterpret_cast<double*>(dec + 192)[l] = g;
   }
 
-  // K's planes into LDS; this wave's 16 rows of Q stay in registers
+  // K's planes into LDS, and Q's; this wave's 16 rows of Q then stay in registers
   const int row = 16 * w + r;
-  const bool live = row < k.n;
-  const char* kp = row_ptr<DT>(a.k, a.k_s, k.row, k.t0 + (live ? row : 0), hk);
-  const char* qp = row_ptr<DT>(a.q, a.q_s, k.row, k.t0 + (live ? row : 0), hk);
   Frag<NA> qf[DKP / 32];
+  {
+    RowTile<DT, DKP, LDK> kt(w, l, (uint32_t)(a.k_s[1] * ES), a.Dk), qt(w, l, (uint32_t)(a.q_s[1] * ES), a.Dk);
+    kt.load(chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7));
+    qt.load(chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7));
+    qt.store(&Kp[0][0][0], 64 * LDK);          // each wave's own rows
 #pragma unroll
-  for (int s = 0; s < DKP / 32; ++s) {
-    const int d = 32 * s + 8 * g4, left = live ? a.Dk - d : 0, es = DT == CCV_DT_F32 ? 4 : 2;
-    const Frag<NA> kf = planes<DT>(load8<DT>(kp + d * es, left, a.vec_qk));
-    qf[s] = planes<DT>(load8<DT>(qp + d * es, left, a.vec_qk));
-#pragma unroll
-    for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(&Kp[p][row][d]) = kf.p[p];
+    for (int s = 0; s < DKP / 32; ++s) qf[s] = get8<NA>(&Kp[0][row][32 * s + 8 * g4], 64 * LDK);
+    kt.store(&Kp[0][0][0], 64 * LDK);
   }
   for (int i = tid; i < 64 * LDA / 4; i += 256) reinterpret_cast<f32x4*>(&Wl[0][0])[i] = f32x4{0, 0, 0, 0};
   __syncthreads();
 
-  float* P = a.P + (int64_t)ch * 4096;
+  f32x4 pv[4];
   double Gi[4];
   float bi[4];
 #pragma unroll
@@ -165,22 +179,20 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
         qk = mma<2>(qf[s], bf, qk);
       }
     }
-    f32x4 pv;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = 16 * w + 4 * g4 + e;
       const float d = i >= j ? __builtin_amdgcn_exp2f((float)(Gi[e] - G[j])) : 0.0f;
-      pv[e] = i >= j ? d * qk[e] : 0.0f;
+      pv[jb][e] = i >= j ? d * qk[e] : 0.0f;
       Al[i][j] = i > j ? bi[e] * d * kk[e] : 0.0f;
-    }
-    if constexpr (BWD) {
-      *reinterpret_cast<f32x4*>(P + j * 64 + 16 * w + 4 * g4) = pv;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) P[(16 * w + 4 * g4 + e) * 64 + j] = pv[e];
     }
   }
   __syncthreads();
+  // P over K's planes
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Pl[16 * w + 4 * g4 + e][16 * jb + r] = pv[jb][e];
 
   // diagonal blocks: column r of block w, the four groups of lanes alike
   {
@@ -228,18 +240,26 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     for (int e = 0; e < 4; ++e) Wl[32 + 16 * rb + 4 * g4 + e][16 * cb + r] = -y[e];
   }
   __syncthreads();
-  float* W = a.W + (int64_t)ch * 4096;
+  // out as planes: a thread takes 8 consecutive elements of two rows (columns when transposed)
+  const auto write = [&](uint16_t* out, const float (*m)[LDA], auto nplanes, bool transposed) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = i * 256 + tid, ro = e >> 4, co = 4 * (e & 15);
-    *reinterpret_cast<f32x4*>(W + ro * 64 + co) = *reinterpret_cast<const f32x4*>(&Wl[ro][co]);
-    if constexpr (BWD) {
-      const int tc = e & 63, tr = 4 * (e >> 6);
-      f32x4 x;
+    for (int i = 0; i < 2; ++i) {
+      const int e = i * 256 + tid, ro = transposed ? e & 63 : e >> 3, co = 8 * (transposed ? e >> 6 : e & 7);
+      f32x8 x;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = Wl[tr + q][tc];
-      *reinterpret_cast<f32x4*>(a.WT + (int64_t)ch * 4096 + tc * 64 + tr) = x;
+      for (int q = 0; q < 8; ++q) x[q] = transposed ? m[co + q][ro] : m[ro][co + q];
+      const auto f = split8<nplanes.value>(x);
+#pragma unroll
+      for (int p = 0; p < nplanes.value; ++p)
+        *reinterpret_cast<bf16x8*>(out + (int64_t)ch * kDeltaMatrix + p * 4096 + fragment_at(ro, co)) = f.p[p];
     }
+  };
+  write(a.W, Wl, std::integral_constant<int, 3>(), false);
+  if constexpr (BWD) {
+    write(a.WT, Wl, std::integral_constant<int, 3>(), true);
+    write(a.P, Pl, std::integral_constant<int, 3>(), true);
+  } else {
+    write(a.P, Pl, std::integral_constant<int, OP>(), false);
   }
 }
 
@@ -256,6 +276,15 @@ void launch_prep(const DeltaArgs& a, bool bwd, hipStream_t st) {
 }
 
 }  // namespace
+
+int launch_delta_pack(const DeltaPackArgs& a, void* stream) {
+  const int64_t need = (a.rows * a.Dp + 255) / 256;
+  const uint32_t grid = (uint32_t)(need < 65536 ? need : 65536);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.dtype == CCV_DT_F32) pack_kernel<uint32_t><<<grid, 256, 0, st>>>(a);
+  else pack_kernel<uint16_t><<<grid, 256, 0, st>>>(a);
+  return (int)hipGetLastError();
+}
 
 int launch_delta_table(const DeltaArgs& a, void* stream) {
   table_kernel<<<1, 1024, 0, static_cast<hipStream_t>(stream)>>>(a);

@@ -5,10 +5,12 @@
 // [Dk, Dv] at the chunk's start:
 //   R = v - gam K S,  N = W (beta R),  o = scale (gam Q S + P N),  S <- gam63 S + K^T (del N).
 // Columns of S (values) do not mix, so a workgroup takes CB = 16 NT of them for one
-// sequence and head, and its four waves share the rows: 16 of a chunk's 64 steps and a
-// quarter of the state's rows each, S staying in fp32 accumulators from the first chunk
-// to the last.  What a wave needs of the others' rows (S, beta R, N as right-hand sides)
-// passes through LDS as bf16 planes, three barriers a chunk.
+// sequence and head.  Four of its waves hold the state and share the rows: 16 of a chunk's
+// 64 steps and a quarter of the state's rows each, S staying in fp32 accumulators from
+// the first chunk to the last.  What a wave needs of the others' rows (S, beta R, N as
+// right-hand sides) passes through LDS as bf16 planes, three barriers a chunk.  The other
+// four waves make the outputs from the same planes, so that the chain from state to state,
+// which nothing else can shorten, holds no work of theirs.
 #include "ccv_delta_device.hpp"
 
 namespace ccv {
@@ -16,35 +18,31 @@ namespace {
 
 constexpr int LDT = 72;      // row stride of an LDS array of 64 steps
 
-// What a wave loads of a chunk before it computes on it.
-template <int DT, int KS, int NT>
-struct Loaded {
-  Raw8<DT> k[KS], q[KS];
-  f32x8 W[2], P[2];
-  float v[NT][4];
-  f32x4 gam, del, beta;
-  float gam_row, last;
-  int n, row, t0;
-};
-
 template <int DT, int DKP, int NT, bool BWD>
-__global__ __launch_bounds__(256) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
+__global__ __launch_bounds__(512, 4) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int OO = OutOrder<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // S by columns
   __shared__ __bf16 Rp[3][CB][LDT];        // beta R by columns
-  __shared__ __bf16 Np[OO + 1][CB][LDT];   // N
-  __shared__ __bf16 Nd[3][CB][LDT];        // del N
   __shared__ __bf16 Kl[NA][64][LDK];
+  __shared__ union {                       // Q until the first barrier of a chunk, N from then on
+    __bf16 q[NA][64][LDK];
+    struct {
+      __bf16 p[OO + 1][CB][LDT], d[3][CB][LDT];      // N, del N
+    } n;
+  } qn;
+  auto& Ql = qn.q;
+  auto& Np = qn.n.p;
+  auto& Nd = qn.n.d;
   const uint32_t hs = blockIdx.x % heads_pad, slice = blockIdx.x / heads_pad;
   if (hs >= heads) return;
   const int seq = hs / a.Hv, h = hs - seq * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
-  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
+  const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // the steps of a packed row that belong to no sequence
     if constexpr (!BWD) {
       const int32_t* begin = a.cstart + (a.nseq + 2);
-      for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 256) {
+      for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 512) {
         const int64_t t = i / CB;
         const int d = dv0 + (int)(i - t * CB);
         if (d < a.Dv) store1<DT>(row_ptr<DT>(a.out, a.o_s, 0, t, h) + d * ES, 0.0f);
@@ -52,195 +50,17 @@ __global__ __launch_bounds__(256) void scan_kernel(DeltaArgs a, uint32_t heads, 
     }
     return;
   }
-  int c0, c1;
-  chunks_of(a, seq, &c0, &c1);
+  const Sequence sq = sequence_at(a, seq);
+  const int c0 = sq.first, c1 = sq.end;
+  const int64_t ch0 = (int64_t)c0 * a.Hv + h;
+  const int i = 16 * w + r;                // the step whose row of K, Q, W, P this lane holds
+  const uint32_t om = (2 * w * 64 + l) * 16;     // its fragments of W and P
+  const auto steps = [](int64_t left) { return left < kDeltaChunk ? (int)left : kDeltaChunk; };
+  int64_t left = sq.len;                   // steps from the chunk at hand on
 
-  // the state: rows 16 (MT w + m) + 4 g4 + e, column 16 j + r
-  f32x4 S[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-        S[m][j][e] = a.h0 && dk < a.Dk && dv < a.Dv ? a.h0[seq * a.h0_s[0] + h * a.h0_s[1] + dk * a.h0_s[2] + dv] : 0.0f;
-      }
-
-  auto load = [&](int c) {
-    Loaded<DT, KS, NT> x;
-    const Chunk k = chunk_at(a, c);
-    x.n = k.n;
-    x.row = k.row;
-    x.t0 = k.t0;
-    const int64_t ch = (int64_t)c * a.Hv + h;
-    const int i = 16 * w + r;
-    const bool live = i < k.n;
-    const char* kp = row_ptr<DT>(a.k, a.k_s, k.row, k.t0 + (live ? i : 0), hk);
-    const char* qp = row_ptr<DT>(a.q, a.q_s, k.row, k.t0 + (live ? i : 0), hk);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = 32 * s + 8 * g4, left = live ? a.Dk - d : 0;
-      x.k[s] = load8<DT>(kp + d * ES, left, a.vec_qk);
-      x.q[s] = load8<DT>(qp + d * ES, left, a.vec_qk);
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      x.W[s] = load_f8(a.W + ch * 4096 + i * 64 + 32 * s + 8 * g4);
-      if constexpr (!BWD) x.P[s] = load_f8(a.P + ch * 4096 + i * 64 + 32 * s + 8 * g4);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = 16 * w + 4 * g4 + e;
-      const char* vp = row_ptr<DT>(a.v, a.v_s, k.row, k.t0 + (t < k.n ? t : 0), h);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int dv = dv0 + 16 * j + r;
-        x.v[j][e] = t < k.n && dv < a.Dv ? load1<DT>(vp + dv * ES) : 0.0f;
-      }
-    }
-    const float* dec = a.dec + ch * kDeltaDec;
-    x.gam = *reinterpret_cast<const f32x4*>(dec + 16 * w + 4 * g4);
-    x.del = *reinterpret_cast<const f32x4*>(dec + 64 + 16 * w + 4 * g4);
-    x.beta = *reinterpret_cast<const f32x4*>(dec + 128 + 16 * w + 4 * g4);
-    x.gam_row = dec[i];
-    x.last = dec[63];
-    return x;
-  };
-  auto put_state = [&]() {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) put4<3>(&Sp[0][16 * j + r][16 * (MT * w + m) + 4 * g4], CB * LDK, S[m][j]);
-  };
-
-  Loaded<DT, KS, NT> x;
-  if (c0 < c1) x = load(c0);
-  put_state();
-  __syncthreads();
-  for (int c = c0; c < c1; ++c) {
-    const int64_t ch = (int64_t)c * a.Hv + h;
-    const Loaded<DT, KS, NT> y = x;
-    if (c + 1 < c1) x = load(c + 1);
-    if constexpr (BWD) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            a.S[(ch * DKP + 16 * (MT * w + m) + 4 * g4 + e) * a.Dvp + dv0 + 16 * j + r] = S[m][j][e];
-    }
-
-    // K S (rows: steps) and S^T Q^T (columns: steps)
-    f32x4 ks[NT], qs[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) ks[j] = qs[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const Frag<NA> kf = planes<DT>(y.k[s]), qf = planes<DT>(y.q[s]);
-#pragma unroll
-      for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(&Kl[p][16 * w + r][32 * s + 8 * g4]) = kf.p[p];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const Frag<3> sf = get8<3>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK);
-        ks[j] = mma<2>(kf, sf, ks[j]);
-        qs[j] = mma<BWD ? 2 : OO>(sf, qf, qs[j]);
-      }
-    }
-    // beta R
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      f32x4 R;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) R[e] = __builtin_fmaf(-y.gam[e], ks[j][e], y.v[j][e]);
-      if constexpr (BWD) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a.R[(ch * 64 + 16 * w + 4 * g4 + e) * a.Dvp + dv0 + 16 * j + r] = R[e];
-      }
-      put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, R * y.beta);
-    }
-    __syncthreads();
-
-    // N = W (beta R); W is lower triangular
-    f32x4 N[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) N[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (2 * s > w) continue;
-      const Frag<3> wf = split8<3>(y.W[s]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) N[j] = mma<2>(wf, get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), N[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      if constexpr (BWD) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a.N[(ch * 64 + 16 * w + 4 * g4 + e) * a.Dvp + dv0 + 16 * j + r] = N[j][e];
-      } else {
-        put4<OO + 1>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
-      }
-      put4<3>(&Nd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j] * y.del);
-    }
-    __syncthreads();
-
-    // the state at the chunk's end
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) S[m][j] *= y.last;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Frag<3> nf[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) nf[j] = get8<3>(&Nd[0][16 * j + r][32 * s + 8 * g4], CB * LDT);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const Frag<NA> kt = get8t<NA>(&Kl[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) S[m][j] = mma<2>(kt, nf[j], S[m][j]);
-      }
-    }
-    put_state();      // nobody has read the planes since the first barrier
-
-    const int t = 16 * w + r;
-    if constexpr (!BWD) {
-      // o, four consecutive values of one step a lane
-      Frag<OO + 1> pf[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) pf[s] = split8<OO + 1>(y.P[s]);
-      char* op = row_ptr<DT>(a.out, a.o_s, y.row, (int64_t)y.t0 + t, h);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        f32x4 o = qs[j] * y.gam_row;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (2 * s > w) continue;
-          o = mma<OO>(get8<OO + 1>(&Np[0][16 * j + r][32 * s + 8 * g4], CB * LDT), pf[s], o);
-        }
-        const int dv = dv0 + 16 * j + 4 * g4;
-        if (t < y.n) store4<DT>(op + dv * ES, o * a.scale, a.Dv - dv, a.vec_o);
-      }
-    } else {
-      // scale gam dO . (Q S): the part of dG that comes by the state
-      const char* dp = row_ptr<DT>(a.dout, a.do_s, y.row, (int64_t)y.t0 + (t < y.n ? t : 0), h);
-      float dot = 0;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int dv = dv0 + 16 * j + 4 * g4;
-        const f32x4 d = load4<DT>(dp + dv * ES, t < y.n ? a.Dv - dv : 0, a.vec_do);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], qs[j][e], dot);
-      }
-      dot = sum4rows(dot) * y.gam_row * a.scale;
-      if (g4 == 0) a.part[(ch * a.slices + slice) * kDeltaPart + t] = dot;
-    }
-    __syncthreads();
-  }
-  if (a.ht) {
+  if (w8 < 4) {
+    // ---- the state: rows 16 (MT w + m) + 4 g4 + e, column 16 j + r ----------------------
+    f32x4 S[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -248,8 +68,268 @@ __global__ __launch_bounds__(256) void scan_kernel(DeltaArgs a, uint32_t heads, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-          if (dk < a.Dk && dv < a.Dv) a.ht[seq * a.ht_s[0] + h * a.ht_s[1] + dk * a.ht_s[2] + dv] = S[m][j][e];
+          S[m][j][e] = a.h0 && dk < a.Dk && dv < a.Dv ? a.h0[seq * a.h0_s[0] + h * a.h0_s[1] + dk * a.h0_s[2] + dv] : 0.0f;
         }
+    const auto put_state = [&]() {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) put4<3>(&Sp[0][16 * j + r][16 * (MT * w + m) + 4 * g4], CB * LDK, S[m][j]);
+    };
+    // What a chunk needs is loaded a chunk ahead, each part as soon as the one before it has
+    // been used, so that a load has most of a chunk's time to arrive.
+    Frag<3> xW[2];
+    uint32_t ov[NT][4];
+    typename Stored<DT>::type xv[NT][4];
+    struct Gates {
+      f32x4 gam, del, beta;
+      float last;
+    } gt, gn;
+    Rows<DT> K(a.k, a.k_s, sq, hk, (a.Dk + 7) & ~7, c0), V(a.v, a.v_s, sq, h, a.Dv, c0);
+    Piece<uint16_t> W(a.W, kDeltaMatrix, a.Hv, ch0);
+    Piece<float> D(a.dec, kDeltaDec, a.Hv, ch0);
+    Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0), Ro(a.R, 64 * (int64_t)a.Dvp, a.Hv, ch0);
+    const uint32_t od = (16 * w + 4 * g4) * 4, ldv = 4 * a.Dvp;
+    const uint32_t os = (16 * MT * w + 4 * g4) * ldv + (dv0 + r) * 4, on = (16 * w + 4 * g4) * ldv + (dv0 + r) * 4;
+    RowTile<DT, DKP, LDK> kt(w, l, K.stride, a.Dk);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int dv = dv0 + 16 * j + r;
+        ov[j][e] = dv < a.Dv ? (16 * w + 4 * g4 + e) * V.stride + dv * ES : kNowhere;
+      }
+    const auto load_K = [&](int n) {
+      kt.load(K.rows(n));
+      K.at += K.step;
+    };
+    const auto load_gates = [&](int n) {
+      const __amdgpu_buffer_rsrc_t d = D.piece(n > 0);
+      gn.gam = buf_f4(d, od);
+      gn.del = buf_f4(d, od + 256);
+      gn.beta = buf_f4(d, od + 512);
+      gn.last = buf1<CCV_DT_F32>(d, 4 * 63);
+      D.at += D.step;
+    };
+    const auto load_V = [&](int n) {
+      const __amdgpu_buffer_rsrc_t b = V.rows(n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xv[j][e] = buf_raw<DT>(b, ov[j][e]);
+      V.at += V.step;
+    };
+    const auto load_W = [&](int n) {
+      const __amdgpu_buffer_rsrc_t b = W.piece(n > 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      W.at += W.step;
+    };
+    const auto ahead = [&](int chunks) {       // steps of a chunk further on, 0 past the last
+      const int64_t n = left - chunks * kDeltaChunk;
+      return n > 0 ? steps(n) : 0;
+    };
+    if (c0 < c1) {
+      load_K(ahead(0));
+      load_gates(ahead(0));
+      load_V(ahead(0));
+      load_W(ahead(0));
+    }
+    put_state();
+    lds_barrier();
+    for (int c = c0; c < c1; ++c) {
+      const int nn = ahead(1);
+      gt = gn;
+      kt.store(&Kl[0][0][0], 64 * LDK);
+      load_K(nn);
+      // K S (rows: steps)
+      Sums<2> ks[NT];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const Frag<NA> kf = get8<NA>(&Kl[0][i][32 * s + 8 * g4], 64 * LDK);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ks[j].add(kf, get8<3>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK));
+      }
+      load_gates(nn);
+      // beta R
+      f32x4 R[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 x = ks[j].total();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) R[j][e] = __builtin_fmaf(-gt.gam[e], x[e], widen<DT>(xv[j][e]));
+        put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, R[j] * gt.beta);
+      }
+      load_V(nn);
+      lds_barrier();
+      if constexpr (BWD) {
+        const __amdgpu_buffer_rsrc_t sb = So.piece(true), rb = Ro.piece(true);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(sb, os + (16 * m + e) * ldv + 64 * j, S[m][j][e]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(rb, on + e * ldv + 64 * j, R[j][e]);
+        So.at += So.step;
+        Ro.at += Ro.step;
+      }
+
+      // N = W (beta R); W is lower triangular
+      Sums<2> ws[NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (2 * s > w) continue;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ws[j].add(xW[s], get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT));
+      }
+      load_W(nn);
+      f32x4 N[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        N[j] = ws[j].total();
+        put4<3>(&Nd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j] * gt.del);
+        if constexpr (!BWD) put4<OO + 1>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
+      }
+      lds_barrier();
+      if constexpr (BWD) {
+        const __amdgpu_buffer_rsrc_t nb = No.piece(true);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(nb, on + e * ldv + 64 * j, N[j][e]);
+        No.at += No.step;
+      }
+
+      // the state at the chunk's end
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[m][j] *= gt.last;
+      Sums<2> sn[MT][NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<3> nf[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) nf[j] = get8<3>(&Nd[0][16 * j + r][32 * s + 8 * g4], CB * LDT);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const Frag<NA> kt = get8t<NA>(&Kl[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) sn[m][j].add(kt, nf[j]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[m][j] += sn[m][j].total();
+      put_state();      // nobody has read the planes since the first barrier
+      left -= kDeltaChunk;
+      lds_barrier();
+    }
+    if (a.ht) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
+            if (dk < a.Dk && dv < a.Dv) a.ht[seq * a.ht_s[0] + h * a.ht_s[1] + dk * a.ht_s[2] + dv] = S[m][j][e];
+          }
+    }
+  } else {
+    // ---- the outputs: step i, four consecutive values 16 j + 4 g4 a lane; the same barriers ----
+    Frag<OO + 1> xP[2];
+    Raw4<DT> xd[NT];
+    float gam, gam_next;
+    uint32_t oo[NT];
+    Rows<DT> Q(a.q, a.q_s, sq, hk, (a.Dk + 7) & ~7, c0);
+    Rows<DT> O(BWD ? a.dout : a.out, BWD ? a.do_s : a.o_s, sq, h, BWD ? (a.Dv + 7) & ~7 : a.Dv, c0);
+    Piece<uint16_t> P(a.P, kDeltaMatrix, a.Hv, ch0);
+    Piece<float> D(a.dec, kDeltaDec, a.Hv, ch0);
+    const float scale = a.scale;
+    const bool vec = a.vec_o;
+    const int dleft = a.Dv - dv0 - 4 * g4;
+    RowTile<DT, DKP, LDK> qt(w, l, Q.stride, a.Dk);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) oo[j] = dleft > 16 * j ? i * O.stride + (dv0 + 16 * j + 4 * g4) * ES : kNowhere;
+    const auto load_Q = [&](int n) {
+      qt.load(Q.rows(n));
+      Q.at += Q.step;
+      gam_next = buf1<CCV_DT_F32>(D.piece(n > 0), 4 * i);
+      D.at += D.step;
+    };
+    const auto load_P = [&](int n) {
+      if constexpr (BWD) {
+        const __amdgpu_buffer_rsrc_t b = O.rows(n);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) xd[j] = buf_raw4<DT>(b, oo[j]);
+        O.at += O.step;
+      } else {
+        const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) xP[s] = buf_planes<OO + 1>(b, om + 1024 * s, 8192);
+        P.at += P.step;
+      }
+    };
+    if (c0 < c1) {
+      const int n = steps(left);
+      load_Q(n);
+      load_P(n);
+    }
+    lds_barrier();
+    for (int c = c0; c < c1; ++c) {
+      const int n = steps(left);
+      left -= kDeltaChunk;
+      const int nn = left > 0 ? steps(left) : 0;
+      gam = gam_next;
+      qt.store(&Ql[0][0][0], 64 * LDK);      // this wave's own rows: no barrier
+      Sums<BWD ? 2 : OO> qs[NT];      // S^T Q^T (columns: steps)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const Frag<NA> qf = get8<NA>(&Ql[0][i][32 * s + 8 * g4], 64 * LDK);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) qs[j].add(get8<BWD ? 3 : OO + 1>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK), qf);
+      }
+      load_Q(nn);
+      lds_barrier();
+      if constexpr (BWD) {
+        // scale gam dO . (Q S): the part of dG that comes by the state
+        float dot = 0;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const f32x4 x = qs[j].total(), d = widen4<DT>(xd[j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], x[e], dot);
+        }
+        load_P(nn);
+        dot = sum4rows(dot) * gam * scale;
+        if (g4 == 0) a.part[(((int64_t)c * a.Hv + h) * a.slices + slice) * kDeltaPart + i] = dot;
+        lds_barrier();
+      } else {
+        f32x4 o[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j] = qs[j].total() * gam;
+        lds_barrier();
+        Sums<OO> ps[NT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (2 * s > w) continue;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) ps[j].add(get8<OO + 1>(&Np[0][16 * j + r][32 * s + 8 * g4], CB * LDT), xP[s]);
+        }
+        load_P(nn);
+        const __amdgpu_buffer_rsrc_t b = O.rows(n);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) buf_store4<DT>(b, oo[j], (o[j] + ps[j].total()) * scale, dleft - 16 * j, vec);
+        O.at += O.step;
+      }
+      lds_barrier();
+    }
   }
 }
 
@@ -260,8 +340,8 @@ void launch(const DeltaArgs& a, bool bwd, hipStream_t st) {
   // chunk's K, Q, W and P once for all of them
   const uint32_t pad = (heads + 7) / 8 * 8;
   const dim3 grid(pad * ((a.Dvp + 16 * NT - 1) / (16 * NT)));
-  if (bwd) scan_kernel<DT, DKP, NT, true><<<grid, 256, 0, st>>>(a, heads, pad);
-  else scan_kernel<DT, DKP, NT, false><<<grid, 256, 0, st>>>(a, heads, pad);
+  if (bwd) scan_kernel<DT, DKP, NT, true><<<grid, 512, 0, st>>>(a, heads, pad);
+  else scan_kernel<DT, DKP, NT, false><<<grid, 512, 0, st>>>(a, heads, pad);
 }
 template <int DT>
 void launch(const DeltaArgs& a, bool bwd, int nt, hipStream_t st) {
