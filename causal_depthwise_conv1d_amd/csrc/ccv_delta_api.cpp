@@ -66,10 +66,12 @@ bool vectors(const View& v, int unit, int bytes) {
   return true;
 }
 
+constexpr int64_t kMostStep = 1 << 25;      // bytes from step to step, so that 64 of them fit 31 bits
+
 // Whether the kernels' buffer loads take the view's rows as they are: steps apart from each
 // other and near enough for a 32-bit offset over 64 of them, `unit` elements a load.
 bool loadable(const View& v, int unit, int bytes) {
-  return vectors(v, unit, bytes) && (v.n[1] <= 1 || (v.s[1] >= v.n[3] && v.s[1] <= (1 << 22)));
+  return vectors(v, unit, bytes) && (v.n[1] <= 1 || (v.s[1] >= v.n[3] && v.s[1] <= kMostStep / v.elt));
 }
 
 bool dtype_ok(int d) { return d >= 0 && d <= 2; }
@@ -106,7 +108,7 @@ int check_sizes(const Sizes& z) {
   if (!dtype_ok(z.x_dtype) || !dtype_ok(z.g_dtype) || !dtype_ok(z.b_dtype)) return CCV_E_DTYPE;
   if (z.Dk > kDeltaMaxDk) return CCV_E_UNSUPPORTED;
   const int64_t most = INT32_MAX - 2 * kDeltaChunk;
-  if (z.L > most || z.B > most || z.N > most || z.Hv > most || z.Dv > most) return CCV_E_SHAPE;
+  if (z.L > most || z.B > most || z.N > most || z.Hv > most || z.Dv > (1 << 20)) return CCV_E_SHAPE;
   return CCV_OK;
 }
 
@@ -147,7 +149,7 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   groups = round_up(groups, 8);
   if (groups * (a->Dvp / 16) > INT32_MAX) return CCV_E_SHAPE;
   a->nchunks = (int32_t)nch;
-  *nt = z.x_dtype == CCV_F32 || groups * (a->Dvp / 32) < 512 ? 1 : 2;
+  *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
   a->slices = a->Dvp / (16 * *nt);
 
   Pieces w{static_cast<char*>(ws), 0, false};
@@ -163,7 +165,6 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
     w.take(&a->S, heads, (int64_t)a->Dkp * a->Dvp);
     w.take(&a->dS, heads, (int64_t)a->Dkp * a->Dvp);
     w.take(&a->N, heads, 64 * (int64_t)a->Dvp);
-    w.take(&a->R, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->Y, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->part, heads, a->Dvp / 16 * kDeltaPart);
   }
@@ -201,6 +202,7 @@ int validate_fwd(const ccv_delta_fwd_args_t* p, Work* w, bool with_ws) {
   const bool pack[4] = {!loadable(view(p->q, p->B, p->L, p->Hk, p->Dk, p->q_stride, es), 8, 16),
                         !loadable(view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es), 8, 16),
                         !loadable(view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), 1, es), false};
+  if (p->L > 1 && p->out_stride[1] > kMostStep / es) return CCV_E_LAYOUT;
   st = plan(z, false, with_ws ? p->workspace : nullptr, w, pack);
   if (st != CCV_OK) return st;
   DeltaArgs& a = w->a;
@@ -262,6 +264,8 @@ int validate_bwd(const ccv_delta_bwd_args_t* p, Work* w, bool with_ws) {
                         !loadable(view(p->k, p->B, p->L, p->Hk, p->Dk, p->k_stride, es), 8, 16),
                         !loadable(view(p->v, p->B, p->L, p->Hv, p->Dv, p->v_stride, es), 1, es),
                         !loadable(view(p->dout, p->B, p->L, p->Hv, p->Dv, p->dout_stride, es), 8, 16)};
+  // dv goes out through a buffer descriptor too
+  if (p->L > 1 && p->dv_stride[1] > kMostStep / es) return CCV_E_LAYOUT;
   st = plan(z, true, with_ws ? p->workspace : nullptr, w, pack);
   if (st != CCV_OK) return st;
   DeltaArgs& a = w->a;
@@ -397,7 +401,7 @@ int pack(Work* w, void* stream) {
   DeltaArgs& a = w->a;
   if (a.L == 1) {                // a stride that is never used may be anything: the kernels' bound on
     a.q_s[1] = a.k_s[1] = kDeltaMaxDk;      // a chunk's rows counts on steps that lie apart
-    a.v_s[1] = a.do_s[1] = round_up(a.Dv, 8);
+    a.v_s[1] = a.do_s[1] = a.o_s[1] = a.dv_s[1] = round_up(a.Dv, 8);
   }
   const int64_t B = a.packed ? 1 : a.nseq;
   const auto one = [&](const void** src, int64_t* s, int32_t H, int32_t D, void* dst) {

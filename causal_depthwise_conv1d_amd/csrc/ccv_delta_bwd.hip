@@ -9,13 +9,14 @@
 //   dA = -Y N^T,  E = beta e^(Gi - Gj) dA (i > j),   F = scale e^(Gi - Gj) dO N^T (i >= j),
 //   dq = scale gam S dO + F K,
 //   dk = -gam beta S Y + del dS' N + E K + F^T Q + E^T K,
-//   dbeta_i = Y_i . R_i + sum_j e^(Gi - Gj) k_i.k_j dA_ij,
-// and the gradient of G_i, with M = F o (Q K^T) + E o (K K^T) below the diagonal and
-// c_j = del_j (K dS')_j . N_j:
-//   dG_i = scale gam_i dO_i.(Q S)_i + dR_i.(R_i - v_i) + sum_j M_ij - sum_j M_ji - c_i,
-//   dG_63 += sum_j c_j + gam63 <S, dS'>,          dg_t = sum of dG_i over i >= t.
-// Terms whose two ends are the same step are left out of both sums, so gradients that are
-// zero by the formula (a sequence of one step without a state) come out as zero.
+//   dbeta_i = Y_i . R_i + sum_j e^(Gi - Gj) k_i.k_j dA_ij = Y_i . N_i / beta_i,
+// the last since N + A N = beta R.  The gradient of G_i, with c_j = del_j (K dS')_j . N_j and
+// sums over j below or above the diagonal:
+//   dG_i = scale gam_i dO_i.(Q S)_i + sum_j F_ij q_i.k_j - sum_j F_ji q_j.k_i
+//          + (Y_i . N_i - dv_i . v_i) - sum_j E_ji k_j.k_i - c_i,
+//   dG_63 += sum_j c_j + gam63 <S, dS'>,          dg_t = sum of dG_i over i >= t;
+// the term in brackets is all that k_i's own row of A and of R gives, by the same identity.
+// The first step of a sequence without an initial state decays nothing: its dg is 0.
 #include "ccv_delta_device.hpp"
 
 namespace ccv {
@@ -23,24 +24,32 @@ namespace {
 
 constexpr int LDT = 72;
 
+// Waves 0..3 hold dS, as the forward's hold S; waves 4..7 stay a chunk ahead of them with what
+// needs no dS (scale P^T dO, and Q^T (scale gam dO), which dS only has added), and a phase
+// behind them with what nothing waits for (the sums of Y.N, dv.v and c over this slice's
+// values, dv and Y to memory).  Both sides of such an exchange hold the same elements lane
+// by lane, so it takes one 16-byte LDS access a tile and needs no other order than the
+// three barriers.
 template <int DT, int DKP, int NT>
-__global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
+__global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // dS by columns
-  __shared__ __bf16 Dp[NA][CB][LDT];       // dO
-  __shared__ __bf16 Dd[3][CB][LDT];        // scale gam dO
   __shared__ __bf16 Rp[3][CB][LDT];        // dN
   __shared__ __bf16 Yp[3][CB][LDT];        // -gam beta Y
+  __shared__ __bf16 Dp[NA][CB][LDT];       // dO of the next chunk
+  __shared__ __bf16 Dd[3][CB][LDT];        // scale gam dO of the next chunk
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
+  __shared__ f32x4 Pd[NT][4][64];          // scale P^T dO; then del (K dS'), from the lane that read it
+  __shared__ f32x4 Ud[MT][NT][4][64];      // Q^T (scale gam dO); then Y in its first tile, likewise
   const uint32_t hs = blockIdx.x % heads_pad, slice = blockIdx.x / heads_pad;
   if (hs >= heads) return;
   const int seq = hs / a.Hv, h = hs - seq * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
-  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
+  const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // steps of no sequence have no gradient
     const int32_t* begin = a.cstart + (a.nseq + 2);
-    for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 256) {
+    for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 512) {
       const int64_t t = i / CB;
       const int d = dv0 + (int)(i - t * CB);
       if (d < a.Dv) store1<DT>(row_ptr<DT>(a.dv, a.dv_s, 0, t, h) + d * ES, 0.0f);
@@ -49,229 +58,18 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
   }
   const Sequence sq = sequence_at(a, seq);
   const int c0 = sq.first, c1 = sq.end;
-
-  f32x4 S[MT][NT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-        S[m][j][e] = a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
-      }
-
-  // loaded a chunk ahead, each part when the one before it has been used
-  const int i = 16 * w + r;
-  Chunk k;
-  Raw8<DT> xk[KS], xq[KS];
-  Frag<3> xW[2], xP[2];
-  typename Stored<DT>::type xd[NT][4], xv[NT][4];
-  float xR[NT][4], xN[NT][4];
-  struct Gates {
-    f32x4 gam, del, beta;
-    float last;
-  } gt, gn;
-  uint32_t ok[KS], oq[KS], ov[NT][4], odo[NT][4];      // byte offsets of this lane's parts
-#pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const int d = 32 * s + 8 * g4;
-    ok[s] = d < a.Dk ? i * (uint32_t)(a.k_s[1] * ES) + d * ES : kNowhere;
-    oq[s] = d < a.Dk ? i * (uint32_t)(a.q_s[1] * ES) + d * ES : kNowhere;
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int dv = dv0 + 16 * j + r, t = 16 * w + 4 * g4 + e;
-      ov[j][e] = dv < a.Dv ? t * (uint32_t)(a.v_s[1] * ES) + dv * ES : kNowhere;
-      odo[j][e] = dv < a.Dv ? t * (uint32_t)(a.do_s[1] * ES) + dv * ES : kNowhere;
-    }
-  const uint32_t om = (2 * w * 64 + l) * 16, od = (16 * w + 4 * g4) * 4,
-                 orow = ((16 * w + 4 * g4) * (uint32_t)a.Dvp + dv0 + r) * 4;
-  auto load_kq = [&](const Chunk& n) {
-    const __amdgpu_buffer_rsrc_t kb = chunk_rows<DT>(a.k, a.k_s, n, hk, (a.Dk + 7) & ~7);
-    const __amdgpu_buffer_rsrc_t qb = chunk_rows<DT>(a.q, a.q_s, n, hk, (a.Dk + 7) & ~7);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      xk[s] = buf8<DT>(kb, ok[s]);
-      xq[s] = buf8<DT>(qb, oq[s]);
-    }
-  };
-  auto load_v = [&](const Chunk& n) {
-    const __amdgpu_buffer_rsrc_t b = chunk_rows<DT>(a.v, a.v_s, n, h, a.Dv);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) xv[j][e] = buf_raw<DT>(b, ov[j][e]);
-  };
-  auto load_d = [&](const Chunk& n) {
-    const __amdgpu_buffer_rsrc_t b = chunk_rows<DT>(a.dout, a.do_s, n, h, a.Dv);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) xd[j][e] = buf_raw<DT>(b, odo[j][e]);
-  };
-  auto load_rows = [&](float (&x)[NT][4], const float* base, int64_t ch) {
-    const __amdgpu_buffer_rsrc_t b = buffer(base + ch * 64 * a.Dvp, 256u * a.Dvp);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) x[j][e] = buf1<CCV_DT_F32>(b, orow + e * 4 * a.Dvp + 64 * j);
-  };
-  auto load_matrix = [&](Frag<3> (&x)[2], const uint16_t* base, int64_t ch) {
-    const __amdgpu_buffer_rsrc_t b = buffer(base + ch * kDeltaMatrix, 2 * kDeltaMatrix);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) x[s] = buf_planes<3>(b, om + 1024 * s, 8192);
-  };
-  auto load_dec = [&](int64_t ch) {
-    const __amdgpu_buffer_rsrc_t b = buffer(a.dec + ch * kDeltaDec, 4 * kDeltaDec);
-    Gates g;
-    g.gam = buf_f4(b, od);
-    g.del = buf_f4(b, od + 256);
-    g.beta = buf_f4(b, od + 512);
-    g.last = buf1<CCV_DT_F32>(b, 4 * 63);
-    return g;
+  const int64_t chl = (int64_t)(c1 - 1) * a.Hv + h;
+  const uint32_t om = (2 * w * 64 + l) * 16, od = (16 * w + 4 * g4) * 4;
+  const uint32_t on = ((slice * NT * 4 + w) * 64 + l) * 16;
+  const auto steps_of = [&](int c) {       // 0 before the first chunk
+    if (c < c0) return 0;
+    const int64_t left = sq.len - (int64_t)(c - c0) * kDeltaChunk;
+    return left < kDeltaChunk ? (int)left : kDeltaChunk;
   };
 
-  if (c0 < c1) {
-    const int64_t ch = (int64_t)(c1 - 1) * a.Hv + h;
-    k = sq.chunk(seq, c1 - 1);
-    load_kq(k);
-    load_d(k);
-    gn = load_dec(ch);
-    load_matrix(xP, a.P, ch);
-    load_rows(xN, a.N, ch);
-    load_matrix(xW, a.WT, ch);
-    load_v(k);
-    load_rows(xR, a.R, ch);
-  }
-  for (int c = c1 - 1; c >= c0; --c) {
-    const int64_t ch = (int64_t)c * a.Hv + h;
-    const int cn = c > c0 ? c - 1 : c;
-    const int64_t chn = (int64_t)cn * a.Hv + h;
-    const Chunk kn = sq.chunk(seq, cn);
-    gt = gn;
-    float* part = a.part + (ch * a.slices + slice) * kDeltaPart;
-
-    // the planes of this chunk
-    Frag<NA> kf[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      kf[s] = planes<DT>(xk[s]);
-      const Frag<NA> qf = planes<DT>(xq[s]);
-#pragma unroll
-      for (int p = 0; p < NA; ++p) {
-        *reinterpret_cast<bf16x8*>(&Kl[p][16 * w + r][32 * s + 8 * g4]) = kf[s].p[p];
-        *reinterpret_cast<bf16x8*>(&Ql[p][16 * w + r][32 * s + 8 * g4]) = qf.p[p];
-      }
-    }
-    load_kq(kn);
-    gn = load_dec(chn);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const f32x4 d = {widen<DT>(xd[j][0]), widen<DT>(xd[j][1]), widen<DT>(xd[j][2]), widen<DT>(xd[j][3])};
-      put4<NA>(&Dp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d);
-      put4<3>(&Dd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d * gt.gam * a.scale);
-    }
-    load_d(kn);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        put4<3>(&Sp[0][16 * j + r][16 * (MT * w + m) + 4 * g4], CB * LDK, S[m][j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          a.dS[(ch * DKP + 16 * (MT * w + m) + 4 * g4 + e) * a.Dvp + dv0 + 16 * j + r] = S[m][j][e];
-      }
-    lds_barrier();
-
-    // dN
-    f32x4 kd[NT], pd[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) kd[j] = pd[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        kd[j] = mma<2>(kf[s], get8<3>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK), kd[j]);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (2 * s + 1 < w) continue;           // P^T is upper triangular
-#pragma unroll
-      for (int j = 0; j < NT; ++j) pd[j] = mma<2>(xP[s], get8<NA>(&Dp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), pd[j]);
-    }
-    f32x4 cs = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      kd[j] *= gt.del;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) cs[e] = __builtin_fmaf(kd[j][e], xN[j][e], cs[e]);
-      put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, pd[j] * a.scale + kd[j]);
-    }
-    load_matrix(xP, a.P, chn);
-    load_rows(xN, a.N, chn);
-    lds_barrier();
-
-    // Y, dv
-    f32x4 Y[NT], bs = {0, 0, 0, 0}, gs = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) Y[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (2 * s + 1 < w) continue;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) Y[j] = mma<2>(xW[s], get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), Y[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int dv = dv0 + 16 * j + r;
-      const f32x4 dR = Y[j] * gt.beta;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * w + 4 * g4 + e;
-        bs[e] = __builtin_fmaf(Y[j][e], xR[j][e], bs[e]);
-        gs[e] = __builtin_fmaf(dR[e], xR[j][e] - widen<DT>(xv[j][e]), gs[e]);
-        a.Y[(ch * 64 + t) * a.Dvp + dv] = Y[j][e];
-        if (t < k.n && dv < a.Dv) store1<DT>(row_ptr<DT>(a.dv, a.dv_s, k.row, (int64_t)k.t0 + t, h) + dv * ES, dR[e]);
-      }
-      put4<3>(&Yp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, dR * -gt.gam);
-    }
-    load_matrix(xW, a.WT, chn);
-    load_v(kn);
-    load_rows(xR, a.R, chn);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float b = sum16(bs[e]), g = sum16(gs[e]), q = sum16(cs[e]);
-      if (r == 0) {
-        part[64 + 16 * w + 4 * g4 + e] = b;
-        part[128 + 16 * w + 4 * g4 + e] = g;
-        part[192 + 16 * w + 4 * g4 + e] = q;
-      }
-    }
-    lds_barrier();
-
-    // dS at the chunk's start
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) S[m][j] *= gt.last;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const Frag<NA> kt = get8t<NA>(&Kl[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
-        const Frag<NA> qt = get8t<NA>(&Ql[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          S[m][j] = mma<2>(qt, get8<3>(&Dd[0][16 * j + r][32 * s + 8 * g4], CB * LDT), S[m][j]);
-          S[m][j] = mma<2>(kt, get8<3>(&Yp[0][16 * j + r][32 * s + 8 * g4], CB * LDT), S[m][j]);
-        }
-      }
-    k = kn;
-    lds_barrier();
-  }
-  if (a.dh0) {
+  if (w8 < 4) {
+    // ---- dS: rows 16 (MT w + m) + 4 g4 + e, column 16 j + r ------------------------------
+    f32x4 S[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -279,8 +77,282 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-          if (dk < a.Dk && dv < a.Dv) a.dh0[seq * a.dh0_s[0] + h * a.dh0_s[1] + dk * a.dh0_s[2] + dv] = S[m][j][e];
+          S[m][j][e] = a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
         }
+    const auto put_state = [&]() {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) put4<3>(&Sp[0][16 * j + r][16 * (MT * w + m) + 4 * g4], CB * LDK, S[m][j]);
+    };
+    Frag<3> xW[2];
+    struct Gates {
+      f32x4 gam, del, beta;
+      float last;
+    } gt, gn;
+    Rows<DT> K(a.k, a.k_s, sq, hk, (a.Dk + 7) & ~7, c1 - 1);
+    Piece<uint16_t> W(a.WT, kDeltaMatrix, a.Hv, chl);
+    Piece<float> D(a.dec, kDeltaDec, a.Hv, chl), So(a.dS, (int64_t)DKP * a.Dvp, a.Hv, chl);
+    const uint32_t os = ((slice * NT * (DKP / 16) + MT * w) * 64 + l) * 16;
+    RowTile<DT, DKP, LDK> kt(w, l, K.stride, a.Dk);
+    const auto load_K = [&](int n) {
+      kt.load(K.rows(n));
+      K.at -= K.step;
+    };
+    const auto load_gates = [&](int n) {
+      const __amdgpu_buffer_rsrc_t d = D.piece(n > 0);
+      gn.gam = buf_f4(d, od);
+      gn.del = buf_f4(d, od + 256);
+      gn.beta = buf_f4(d, od + 512);
+      gn.last = buf1<CCV_DT_F32>(d, 4 * 63);
+      D.at -= D.step;
+    };
+    const auto load_W = [&](int n) {
+      const __amdgpu_buffer_rsrc_t b = W.piece(n > 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      W.at -= W.step;
+    };
+    if (c0 < c1) {
+      load_K(steps_of(c1 - 1));
+      load_gates(steps_of(c1 - 1));
+      load_W(steps_of(c1 - 1));
+    }
+    put_state();
+    lds_barrier();
+    lds_barrier();
+    for (int c = c1 - 1; c >= c0; --c) {
+      const int nn = steps_of(c - 1);
+      gt = gn;
+      kt.store(&Kl[0][0][0], 64 * LDK);
+      load_K(nn);
+      // dN = scale P^T dO + del (K dS')
+      Sums<2> kd[NT];
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const Frag<NA> kf = get8<NA>(&Kl[0][16 * w + r][32 * s + 8 * g4], 64 * LDK);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) kd[j].add(kf, get8<3>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK));
+      }
+      load_gates(nn);
+      {
+        const __amdgpu_buffer_rsrc_t sb = So.piece(true);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            buf_store_f4(sb, os + (j * (DKP / 16) + m) * 1024, S[m][j]);
+            S[m][j] = S[m][j] * gt.last + Ud[m][j][w][l];
+          }
+        So.at -= So.step;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 x = kd[j].total() * gt.del;
+        put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, Pd[j][w][l] + x);
+        Pd[j][w][l] = x;
+      }
+      lds_barrier();
+
+      // Y = W^T dN; W^T is upper triangular
+      Sums<2> ys[NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (2 * s + 1 < w) continue;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ys[j].add(xW[s], get8<3>(&Rp[0][16 * j + r][32 * s + 8 * g4], CB * LDT));
+      }
+      load_W(nn);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 y = ys[j].total();
+        put4<3>(&Yp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, y * gt.beta * -gt.gam);
+        Ud[0][j][w][l] = y;
+      }
+      lds_barrier();
+
+      // dS at the chunk's start
+      Sums<2> sn[MT][NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<3> yf[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) yf[j] = get8<3>(&Yp[0][16 * j + r][32 * s + 8 * g4], CB * LDT);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const Frag<NA> kf = get8t<NA>(&Kl[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) sn[m][j].add(kf, yf[j]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) S[m][j] += sn[m][j].total();
+      put_state();
+      lds_barrier();
+    }
+    if (a.dh0) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
+            if (dk < a.Dk && dv < a.Dv) a.dh0[seq * a.dh0_s[0] + h * a.dh0_s[1] + dk * a.dh0_s[2] + dv] = S[m][j][e];
+          }
+    }
+  } else {
+    // ---- ahead and behind: steps 16 w + 4 g4 + e, column 16 j + r ---------------------------
+    typename Stored<DT>::type xd[NT][4], xv[NT][4];
+    f32x4 xN[NT];
+    Frag<3> xP[2];
+    f32x4 gam, beta;
+    Rows<DT> Q(a.q, a.q_s, sq, hk, (a.Dk + 7) & ~7, c1 - 1), O(a.dout, a.do_s, sq, h, a.Dv, c1 - 1), V(a.v, a.v_s, sq, h, a.Dv, c1 - 1),
+        dV(a.dv, a.dv_s, sq, h, a.Dv, c1 - 1);
+    Piece<uint16_t> P(a.P, kDeltaMatrix, a.Hv, chl);
+    Piece<float> Dg(a.dec, kDeltaDec, a.Hv, chl), Db(a.dec, kDeltaDec, a.Hv, chl);
+    Piece<float> Ni(a.N, 64 * (int64_t)a.Dvp, a.Hv, chl), Yo(a.Y, 64 * (int64_t)a.Dvp, a.Hv, chl);
+    const float scale = a.scale;
+    RowTile<DT, DKP, LDK> qt(w, l, Q.stride, a.Dk);
+    uint32_t ov[NT], oo[NT], odv[NT];      // of the lane's first step; the others follow a stride apart
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int dv = dv0 + 16 * j + r, t = 16 * w + 4 * g4;
+      ov[j] = dv < a.Dv ? t * V.stride + dv * ES : kNowhere;
+      oo[j] = dv < a.Dv ? t * O.stride + dv * ES : kNowhere;
+      odv[j] = dv < a.Dv ? t * dV.stride + dv * ES : kNowhere;
+    }
+    const auto load_QD = [&](int n) {
+      qt.load(Q.rows(n));
+      Q.at -= Q.step;
+      const __amdgpu_buffer_rsrc_t b = O.rows(n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xd[j][e] = buf_raw<DT>(b, oo[j] == kNowhere ? kNowhere : oo[j] + e * O.stride);
+      O.at -= O.step;
+      gam = buf_f4(Dg.piece(n > 0), od);
+      Dg.at -= Dg.step;
+    };
+    const auto load_P = [&](int n) {
+      const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) xP[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      P.at -= P.step;
+    };
+    const auto load_NV = [&](int n) {
+      const __amdgpu_buffer_rsrc_t nb = Ni.piece(n > 0), vb = V.rows(n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        xN[j] = buf_f4(nb, on + j * 4096);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) xv[j][e] = buf_raw<DT>(vb, ov[j] == kNowhere ? kNowhere : ov[j] + e * V.stride);
+      }
+      beta = buf_f4(Db.piece(n > 0), od + 512);
+      Ni.at -= Ni.step;
+      V.at -= V.step;
+      Db.at -= Db.step;
+    };
+    const auto stage = [&]() {
+      qt.store(&Ql[0][0][0], 64 * LDK);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 d = {widen<DT>(xd[j][0]), widen<DT>(xd[j][1]), widen<DT>(xd[j][2]), widen<DT>(xd[j][3])};
+        put4<NA>(&Dp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d);
+        put4<3>(&Dd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, d * gam * scale);
+      }
+    };
+    f32x4 pd[NT], ud[MT][NT];
+    const auto products = [&]() {
+      Sums<2> ps[NT], us[MT][NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (2 * s + 1 < w) continue;           // P^T is upper triangular
+#pragma unroll
+        for (int j = 0; j < NT; ++j) ps[j].add(xP[s], get8<NA>(&Dp[0][16 * j + r][32 * s + 8 * g4], CB * LDT));
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const Frag<NA> qf = get8t<NA>(&Ql[0][32 * s][16 * (MT * w + m)], LDK, 64 * LDK, l);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) us[m][j].add(qf, get8<3>(&Dd[0][16 * j + r][32 * s + 8 * g4], CB * LDT));
+        }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        pd[j] = ps[j].total() * scale;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) ud[m][j] = us[m][j].total();
+      }
+    };
+    const auto hand_over = [&]() {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        Pd[j][w][l] = pd[j];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) Ud[m][j][w][l] = ud[m][j];
+      }
+    };
+    if (c0 < c1) {
+      load_QD(steps_of(c1 - 1));
+      load_P(steps_of(c1 - 1));
+      load_NV(steps_of(c1 - 1));
+      stage();
+      load_QD(steps_of(c1 - 2));
+    }
+    lds_barrier();
+    if (c0 < c1) {
+      products();
+      load_P(steps_of(c1 - 2));
+      hand_over();
+    }
+    lds_barrier();
+    for (int c = c1 - 1; c >= c0; --c) {
+      const int n = steps_of(c);
+      stage();                                 // of chunk c - 1; zeros before the first
+      load_QD(steps_of(c - 2));
+      lds_barrier();
+      products();
+      load_P(steps_of(c - 2));
+      f32x4 cs = {0, 0, 0, 0}, bs = {0, 0, 0, 0}, gs = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 x = Pd[j][w][l];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = __builtin_fmaf(x[e], xN[j][e], cs[e]);
+      }
+      lds_barrier();
+      const __amdgpu_buffer_rsrc_t yb = Yo.piece(true), vb = dV.rows(n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const f32x4 y = Ud[0][j][w][l], dR = y * beta;
+        buf_store_f4(yb, on + j * 4096, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          bs[e] = __builtin_fmaf(y[e], xN[j][e], bs[e]);
+          gs[e] = __builtin_fmaf(dR[e], widen<DT>(xv[j][e]), gs[e]);
+          buf_store1<DT>(vb, odv[j] == kNowhere ? kNowhere : odv[j] + e * dV.stride, dR[e]);
+        }
+      }
+      Yo.at -= Yo.step;
+      dV.at -= dV.step;
+      load_NV(steps_of(c - 1));
+      hand_over();
+      float* part = a.part + (((int64_t)c * a.Hv + h) * a.slices + slice) * kDeltaPart + 16 * w + 4 * g4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float b = sum16(bs[e]), g = sum16(gs[e]), q = sum16(cs[e]);
+        if (r == 0) {
+          part[64 + e] = b;
+          part[128 + e] = b - g;
+          part[192 + e] = q;
+        }
+      }
+      lds_barrier();
+    }
   }
 }
 
@@ -289,18 +361,25 @@ __global__ __launch_bounds__(256) void reverse_kernel(DeltaArgs a, uint32_t head
 // One workgroup a (chunk, key head): it adds up the key head's value heads in their order, so the
 // gradients of shared heads need no atomics.  Eight waves: wave w has the steps of block
 // w % 4; waves 0..3 the first half of the keys' columns and F, waves 4..7 the other half
-// and E.  Contractions over the values go through LDS 32 values at a time.
+// and E.  Contractions over the values go through LDS 32 values at a time, the next 32
+// under way in registers; S, dS', N and Y lie there by values, and the transposing read
+// makes fragments of them.
 template <int DT, int DKP>
 __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
-  constexpr int NA = InPlanes<DT>::n, OO = OutOrder<DT>::n, OP = OO + 1, KS = DKP / 32, LDK = DKP + 8, LDV = 40;
+  constexpr int NA = InPlanes<DT>::n, OO = OutOrder<DT>::n, OP = OO + 1, KS = DKP / 32, LDK = DKP + 8, LDO = 40;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2, TK = DKP / 32;       // TK: a wave's 16-column tiles of the keys
-  constexpr int kStage = (OP * DKP + 3 * 64) * LDV, kPair = 2 * OP * 64 * LDT;
+  constexpr bool TWO = DT != CCV_DT_F32;                            // LDS for S and dS' at once
+  constexpr int kS = OP * 32 * LDK, kN = 3 * 32 * LDT, kO = TWO ? NA * 64 * LDO : 0;
+  constexpr int kStage = (TWO ? 2 : 1) * kS + 2 * kN + kO, kPair = 2 * OP * 64 * LDT;
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
   __shared__ __bf16 un[kStage > kPair ? kStage : kPair];
   __shared__ double G[64];
-  __shared__ float rows[2][64], cols[8][64], bsum[64], dots[8];
-  __bf16* St = un;                                  // [OP][DKP][LDV]
-  __bf16* Ns = un + OP * DKP * LDV;                 // [3][64][LDV]
+  __shared__ float rows[64], cols[8][64], dots[8];
+  __bf16* St = un;                                  // [OP][32][LDK]
+  __bf16* Dt = TWO ? St + kS : St;
+  __bf16* Nt = Dt + kS;                             // [3][32][LDT]
+  __bf16* Yt = Nt + kN;
+  __bf16* Ol = Yt + kN;                             // [NA][64][LDO]: dO, by steps; fp32 has no room for it
   __bf16* Ft = un;                                  // [OP][64][LDT], by columns j
   __bf16* Et = un + OP * 64 * LDT;
   const int c = blockIdx.x / a.Hk, hk = blockIdx.x - c * a.Hk, group = a.Hv / a.Hk;
@@ -310,33 +389,46 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
             g4 = l >> 4;
   const int t = 16 * w + r;
   const bool live = t < k.n;
-  char* dqp = row_ptr<DT>(a.dq, a.dq_s, k.row, (int64_t)k.t0 + (live ? t : 0), hk);
-  char* dkp = row_ptr<DT>(a.dk, a.dk_s, k.row, (int64_t)k.t0 + (live ? t : 0), hk);
   f32x4 dq[TK], dk[TK];
 #pragma unroll
   for (int n = 0; n < TK; ++n) dq[n] = dk[n] = f32x4{0, 0, 0, 0};
 
   if (k.seq < a.nseq) {
-    const __amdgpu_buffer_rsrc_t kb = half ? chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7)
-                                           : chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7);
-    const uint32_t ks = t * (uint32_t)((half ? a.k_s[1] : a.q_s[1]) * ES);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d = 32 * s + 8 * g4;
-      const Frag<NA> f = planes<DT>(buf8<DT>(kb, d < a.Dk ? ks + d * ES : kNowhere));
-#pragma unroll
-      for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(half ? &Kl[p][t][d] : &Ql[p][t][d]) = f.p[p];
+    if (half) {
+      RowTile<DT, DKP, LDK> x(w, l, (uint32_t)(a.k_s[1] * ES), a.Dk);
+      x.load(chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7));
+      x.store(&Kl[0][0][0], 64 * LDK);
+    } else {
+      RowTile<DT, DKP, LDK> x(w, l, (uint32_t)(a.q_s[1] * ES), a.Dk);
+      x.load(chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7));
+      x.store(&Ql[0][0][0], 64 * LDK);
     }
+    // what a thread moves of 32 values: RS times 4 keys of one value of S and dS', 4 steps of one
+    // value of N and Y, and 8 values of one step of dO
+    constexpr int RS = DKP / 64, kLanesO = 4;
+    const int lv = tid >> 6;                        // its 1 KB tile of the 32 values' (16 of S: RS rounds)
+    f32x4 s4[RS], d4[RS], n4, y4;
+    u32x4 o4;
+    const int orow = TWO ? tid / kLanesO : 64, oc = tid % kLanesO * (16 / ES);
     for (int hg = 0; hg < group; ++hg) {
       const int h = hk * group + hg;
       const int64_t ch = (int64_t)c * a.Hv + h;
       const float* dec = a.dec + ch * kDeltaDec;
-      const float* Sg = a.S + ch * DKP * a.Dvp;
-      const float* Dg = a.dS + ch * DKP * a.Dvp;
-      const float* Ng = a.N + ch * 64 * a.Dvp;
-      const __amdgpu_buffer_rsrc_t Yb = buffer(a.Y + ch * 64 * a.Dvp, 256u * a.Dvp);
-      const __amdgpu_buffer_rsrc_t dob = chunk_rows<DT>(a.dout, a.do_s, k, h, (a.Dv + 7) & ~7);
-      const uint32_t dos = t * (uint32_t)(a.do_s[1] * ES);
+      const __amdgpu_buffer_rsrc_t sb = buffer(a.S + ch * DKP * a.Dvp, 4u * DKP * a.Dvp), db = buffer(a.dS + ch * DKP * a.Dvp, 4u * DKP * a.Dvp),
+                                   nb = buffer(a.N + ch * 64 * a.Dvp, 256u * a.Dvp), yb = buffer(a.Y + ch * 64 * a.Dvp, 256u * a.Dvp),
+                                   ob = chunk_rows<DT>(a.dout, a.do_s, k, h, (a.Dv + 7) & ~7);
+      const auto load = [&](int v0) {
+        const uint32_t os = (uint32_t)v0 * DKP * 4 + tid * 16, on = (uint32_t)v0 * 256 + tid * 16;
+#pragma unroll
+        for (int i = 0; i < RS; ++i) {
+          s4[i] = buf_f4(sb, os + i * 8192);
+          d4[i] = buf_f4(db, os + i * 8192);
+        }
+        n4 = buf_f4(nb, on);
+        y4 = buf_f4(yb, on);
+        if constexpr (TWO)
+          o4 = buf16(ob, orow < 64 && v0 + oc < a.Dv ? orow * (uint32_t)(a.do_s[1] * ES) + (v0 + oc) * ES : kNowhere);
+      };
       if (tid < 64) G[tid] = reinterpret_cast<const double*>(dec + 192)[tid];
       f32x4 zq[TK], zy[TK], zn[TK], pr[4];
       float dot = 0;
@@ -345,54 +437,67 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) pr[n] = f32x4{0, 0, 0, 0};
 
+      load(0);
       for (int v0 = 0; v0 < a.Dvp; v0 += 32) {
-        // S and N; a thread moves 4 values of DKP / 64 rows
-        constexpr int RS = DKP / 64;
-        f32x4 s4[RS], d4[RS];
-        const int sr = tid >> 3, sc = 4 * (tid & 7);
-        const f32x4 n4 = *reinterpret_cast<const f32x4*>(Ng + sr * a.Dvp + v0 + sc);
+        lds_barrier();
+        // 1 KB tiles [lane][4 rows]: tile (16 values, 16 keys) of S, (16 values, 16 steps) of N and Y
+        const auto put_S = [&](__bf16* to, const f32x4 (&x)[RS]) {
 #pragma unroll
-        for (int i = 0; i < RS; ++i) {
-          s4[i] = *reinterpret_cast<const f32x4*>(Sg + (64 * i + sr) * (int64_t)a.Dvp + v0 + sc);
-          d4[i] = *reinterpret_cast<const f32x4*>(Dg + (64 * i + sr) * (int64_t)a.Dvp + v0 + sc);
+          for (int i = 0; i < RS; ++i) {
+            const int tile = 8 * i + lv, tv = tile / (DKP / 16), tk = tile % (DKP / 16);
+            put4<OP>(to + (16 * tv + r) * LDK + 16 * tk + 4 * g4, 32 * LDK, x[i]);
+          }
+        };
+        put_S(St, s4);
+        if constexpr (TWO) put_S(Dt, d4);
+        put4<3>(Nt + (16 * (lv >> 2) + r) * LDT + 16 * (lv & 3) + 4 * g4, 32 * LDT, n4);
+        put4<3>(Yt + (16 * (lv >> 2) + r) * LDT + 16 * (lv & 3) + 4 * g4, 32 * LDT, y4);
+        if constexpr (TWO) {
+          if (orow < 64) {
+            const Frag<NA> f = planes<DT>(Raw8<DT>{{o4}});
+#pragma unroll
+            for (int p = 0; p < NA; ++p) *reinterpret_cast<bf16x8*>(Ol + p * 64 * LDO + orow * LDO + oc) = f.p[p];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < RS; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(s4[i][e], d4[i][e], dot);
-        }
-        const int dv = v0 + 8 * g4;
-        const Frag<NA> of = planes<DT>(buf8<DT>(dob, dv < a.Dv ? dos + dv * ES : kNowhere));
-        const uint32_t oy = (t * (uint32_t)a.Dvp + dv) * 4;
-        const Frag<3> yf = split8<3>(__builtin_shufflevector(buf_f4(Yb, oy), buf_f4(Yb, oy + 16), 0, 1, 2, 3, 4, 5, 6, 7));
-        lds_barrier();
-        put4<3>(Ns + sr * LDV + sc, 64 * LDV, n4);
+        f32x4 later[RS];
 #pragma unroll
-        for (int i = 0; i < RS; ++i) put4<OP>(St + (64 * i + sr) * LDV + sc, DKP * LDV, s4[i]);
+        for (int i = 0; i < RS; ++i) later[i] = d4[i];
+        if (v0 + 32 < a.Dvp) load(v0 + 32);
         lds_barrier();
+        Frag<NA> of;
+        if constexpr (TWO) of = get8<NA>(Ol + t * LDO + 8 * g4, 64 * LDO);
+        else of = planes<DT>(buf8<DT>(ob, v0 + 8 * g4 < a.Dv ? t * (uint32_t)(a.do_s[1] * ES) + (v0 + 8 * g4) * ES : kNowhere));
+        const Frag<3> yf = get8t<3>(Yt + 16 * w, LDT, 32 * LDT, l);
+        const Frag<OP> nown = get8t<OP>(Nt + 16 * w, LDT, 32 * LDT, l);
 #pragma unroll
         for (int n = 0; n < TK; ++n) {
-          const Frag<OP> sf = get8<OP>(St + (16 * (TK * half + n) + r) * LDV + 8 * g4, DKP * LDV);
+          const Frag<OP> sf = get8t<OP>(St + 16 * (TK * half + n), LDK, 32 * LDK, l);
           zq[n] = mma<OO>(sf, of, zq[n]);
           zy[n] = mma<OO>(sf, yf, zy[n]);
+          if constexpr (TWO) zn[n] = mma<OO>(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           if (n > w) continue;
-          const Frag<3> nf = get8<3>(Ns + (16 * n + r) * LDV + 8 * g4, 64 * LDV);
-          pr[n] = half ? mma<2>(yf, nf, pr[n]) : mma<2>(of, nf, pr[n]);
+          const Frag<3> nf = get8t<3>(Nt + 16 * n, LDT, 32 * LDT, l);
+          if (half) pr[n] = mma<2>(yf, nf, pr[n]);
+          else pr[n] = mma<2>(of, nf, pr[n]);
         }
-        const Frag<OP> nown = get8<OP>(Ns + t * LDV + 8 * g4, 64 * LDV);
-        lds_barrier();
+        if constexpr (!TWO) {
+          lds_barrier();
+          put_S(Dt, later);
+          lds_barrier();
 #pragma unroll
-        for (int i = 0; i < RS; ++i) put4<OP>(St + (64 * i + sr) * LDV + sc, DKP * LDV, d4[i]);
-        lds_barrier();
-#pragma unroll
-        for (int n = 0; n < TK; ++n)
-          zn[n] = mma<OO>(get8<OP>(St + (16 * (TK * half + n) + r) * LDV + 8 * g4, DKP * LDV), nown, zn[n]);
+          for (int n = 0; n < TK; ++n) zn[n] = mma<OO>(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
+        }
       }
-      {
 #pragma unroll
-        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-        if (l == 0) dots[w8] = dot;
-      }
+      for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
+      if (l == 0) dots[w8] = dot;
       const float gam = dec[t], del = dec[64 + t], bet = dec[128 + t];
 #pragma unroll
       for (int n = 0; n < TK; ++n) {
@@ -402,13 +507,13 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 
       // F (waves 0..3) and E (4..7), their products with Q K^T and K K^T
       lds_barrier();
-      f32x4 rs = {0, 0, 0, 0}, bs = {0, 0, 0, 0};
+      f32x4 rs = {0, 0, 0, 0};
       double Gi[4];
       float bi[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         Gi[e] = G[16 * w + 4 * g4 + e];
-        bi[e] = half ? dec[128 + 16 * w + 4 * g4 + e] : a.scale;
+        bi[e] = half ? -dec[128 + 16 * w + 4 * g4 + e] : a.scale;
       }
       __bf16* Pt = half ? Et : Ft;
 #pragma unroll
@@ -426,11 +531,9 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           for (int e = 0; e < 4; ++e) {
             const int i = 16 * w + 4 * g4 + e;
             if (i < j || (half && i == j)) continue;
-            const float d = __builtin_amdgcn_exp2f((float)(Gi[e] - G[j])) * (half ? -pr[n][e] : pr[n][e]);
-            f[e] = d * bi[e];
+            f[e] = __builtin_amdgcn_exp2f((float)(Gi[e] - G[j])) * pr[n][e] * bi[e];
             if (i > j) {
               rs[e] = __builtin_fmaf(f[e], x[e], rs[e]);
-              bs[e] = __builtin_fmaf(d, x[e], bs[e]);
               cs = __builtin_fmaf(f[e], x[e], cs);
             }
           }
@@ -439,12 +542,11 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         cs = sum4rows(cs);
         if (g4 == 0) cols[w8][j] = cs;
       }
+      if (!half) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float rv = sum16(rs[e]), bv = sum16(bs[e]);
-        if (r == 0) {
-          rows[half][16 * w + 4 * g4 + e] = rv;
-          if (half) bsum[16 * w + 4 * g4 + e] = bv;
+        for (int e = 0; e < 4; ++e) {
+          const float rv = sum16(rs[e]);
+          if (r == 0) rows[16 * w + 4 * g4 + e] = rv;
         }
       }
       lds_barrier();
@@ -475,7 +577,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         }
       }
       if (w8 == 0) {                                          // a step a lane
-        float g = rows[0][l] + rows[1][l], b = bsum[l], cj = 0, cc = 0, sd = 0;
+        float g = rows[l], b = 0, cj = 0, cc = 0, sd = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           cc += cols[i][l];
@@ -488,7 +590,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           b += part[64 + l];
           cj += part[192 + l];
         }
-        if (l >= k.n - 1) cj = 0;
+        if (l >= k.n - 1) cj = 0;      // the last step's decay to the end is 1, whatever its g
         float tot = cj;
 #pragma unroll
         for (int d = 32; d; d >>= 1) tot += __shfl_xor(tot, d);
@@ -499,14 +601,15 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           const float o = __shfl_down(g, d);
           if (l + d < 64) g += o;
         }
+        const int begin = a.packed ? a.cstart[a.nseq + 2 + k.seq] : 0;
+        if (l == 0 && k.t0 == begin && !a.h0) g = 0;
         if (l < k.n) {
           const int64_t s = (int64_t)k.t0 + l;
           store_gate(a.dg, a.g_dtype, k.row * a.dg_s[0] + s * a.dg_s[1] + h * a.dg_s[2], g);
-          store_gate(a.dbeta, a.b_dtype, k.row * a.db_s[0] + s * a.db_s[1] + h * a.db_s[2], b);
+          store_gate(a.dbeta, a.b_dtype, k.row * a.db_s[0] + s * a.db_s[1] + h * a.db_s[2], b / dec[128 + l]);
         }
       }
-      // the next head's first barrier comes before it writes any of this
-      lds_barrier();
+      lds_barrier();      // before the next head writes what is read here
     }
   } else if (tid < 64 && tid < k.n) {
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
@@ -516,6 +619,8 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
     }
   }
   if (live) {
+    char* dqp = row_ptr<DT>(a.dq, a.dq_s, k.row, (int64_t)k.t0 + t, hk);
+    char* dkp = row_ptr<DT>(a.dk, a.dk_s, k.row, (int64_t)k.t0 + t, hk);
 #pragma unroll
     for (int n = 0; n < TK; ++n) {
       const int d = 16 * (TK * half + n) + 4 * g4;
@@ -529,20 +634,19 @@ template <int DT, int DKP, int NT>
 void launch_rev(const DeltaArgs& a, hipStream_t st) {
   const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
   const dim3 grid(pad * ((a.Dvp + 16 * NT - 1) / (16 * NT)));
-  reverse_kernel<DT, DKP, NT><<<grid, 256, 0, st>>>(a, heads, pad);
+  reverse_kernel<DT, DKP, NT><<<grid, 512, 0, st>>>(a, heads, pad);
 }
 template <int DT>
 void launch_rev(const DeltaArgs& a, int nt, hipStream_t st) {
-  if constexpr (DT == CCV_DT_F32) {
-    if (a.Dkp == 64) launch_rev<DT, 64, 1>(a, st);
-    else launch_rev<DT, 128, 1>(a, st);
-  } else if (a.Dkp == 64) {
-    if (nt == 1) launch_rev<DT, 64, 1>(a, st);
-    else launch_rev<DT, 64, 2>(a, st);
-  } else {
-    if (nt == 1) launch_rev<DT, 128, 1>(a, st);
-    else launch_rev<DT, 128, 2>(a, st);
+  if constexpr (DT == CCV_DT_BF16) {       // 32 columns of two or three planes of K and Q exceed the LDS
+    if (nt == 2) {
+      if (a.Dkp == 64) launch_rev<DT, 64, 2>(a, st);
+      else launch_rev<DT, 128, 2>(a, st);
+      return;
+    }
   }
+  if (a.Dkp == 64) launch_rev<DT, 64, 1>(a, st);
+  else launch_rev<DT, 128, 1>(a, st);
 }
 template <int DT>
 void launch_grads(const DeltaArgs& a, hipStream_t st) {

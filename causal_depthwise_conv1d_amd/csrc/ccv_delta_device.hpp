@@ -386,6 +386,9 @@ struct Piece {
   __device__ inline __amdgpu_buffer_rsrc_t piece(bool there) const { return buffer(at, there ? bytes : 0); }
 };
 
+__device__ inline void buf_store_f4(__amdgpu_buffer_rsrc_t b, uint32_t off, f32x4 x) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, off, 0, 0);
+}
 template <int DT>
 __device__ inline void buf_store1(__amdgpu_buffer_rsrc_t b, uint32_t off, float x) {
   if constexpr (DT == CCV_DT_F32) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), b, off, 0, 0);

@@ -9,7 +9,7 @@ namespace ccv {
 constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 16-row matrix tiles
 constexpr int kDeltaMatrix = 3 * 64 * 64;   // elements of a chunk's W or P
 constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
-constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, dbeta, dG by R, c
+constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, Y.N, Y.N - dv.v, c
 constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
 
 // One forward or backward call.  Strides are in elements: (row, step, head), unit inside
@@ -42,8 +42,10 @@ struct DeltaArgs {
   uint16_t* P;                                  // likewise, kDeltaMatrix a chunk and head; the backward holds it transposed
   uint16_t* WT;                                 // backward: W transposed
   float* dec;                                   // [ch][kDeltaDec]: e^G, e^(G63 - G), beta, and G log2(e) as 64 doubles
-  float *S, *dS;                                // backward: [ch][Dkp][Dvp] state at a chunk's start, gradient at its end
-  float *N, *R, *Y;                             // backward: [ch][64][Dvp]
+  // backward, in 16 x 16 tiles as a wave's accumulators hold them, [tile][lane][4 rows], tiles of
+  // one 16 values together:
+  float *S, *dS;                                // [ch][Dvp / 16][Dkp / 16] tiles: state at a chunk's start, gradient at its end
+  float *N, *Y;                                 // [ch][Dvp / 16][4] tiles
   float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
   int32_t Dkp, slices;
 };

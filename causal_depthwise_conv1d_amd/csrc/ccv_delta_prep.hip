@@ -127,6 +127,9 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
       x = x < -2000.0f ? -2000.0f : x;
       g = (double)x * 1.4426950408889634;
       b = load_param(a.beta, a.b_dtype, k.row * a.b_s[0] + t * a.b_s[1] + h * a.b_s[2]);
+      // the backward divides N by beta (dbeta = Y . N / beta): a beta of 0 is there the smallest that
+      // keeps N / beta in fp32, and N stays below anything it is added to
+      if (BWD && __builtin_fabsf(b) < 1e-30f) b = __builtin_copysignf(1e-30f, b);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

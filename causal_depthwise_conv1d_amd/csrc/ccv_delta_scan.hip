@@ -19,7 +19,7 @@ namespace {
 constexpr int LDT = 72;      // row stride of an LDS array of 64 steps
 
 template <int DT, int DKP, int NT, bool BWD>
-__global__ __launch_bounds__(512, 4) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
+__global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int OO = OutOrder<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // S by columns
@@ -88,9 +88,9 @@ __global__ __launch_bounds__(512, 4) void scan_kernel(DeltaArgs a, uint32_t head
     Rows<DT> K(a.k, a.k_s, sq, hk, (a.Dk + 7) & ~7, c0), V(a.v, a.v_s, sq, h, a.Dv, c0);
     Piece<uint16_t> W(a.W, kDeltaMatrix, a.Hv, ch0);
     Piece<float> D(a.dec, kDeltaDec, a.Hv, ch0);
-    Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0), Ro(a.R, 64 * (int64_t)a.Dvp, a.Hv, ch0);
-    const uint32_t od = (16 * w + 4 * g4) * 4, ldv = 4 * a.Dvp;
-    const uint32_t os = (16 * MT * w + 4 * g4) * ldv + (dv0 + r) * 4, on = (16 * w + 4 * g4) * ldv + (dv0 + r) * 4;
+    Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0);
+    const uint32_t od = (16 * w + 4 * g4) * 4;
+    const uint32_t os = ((slice * NT * (DKP / 16) + MT * w) * 64 + l) * 16, on = ((slice * NT * 4 + w) * 64 + l) * 16;
     RowTile<DT, DKP, LDK> kt(w, l, K.stride, a.Dk);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -152,30 +152,23 @@ __global__ __launch_bounds__(512, 4) void scan_kernel(DeltaArgs a, uint32_t head
       }
       load_gates(nn);
       // beta R
-      f32x4 R[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const f32x4 x = ks[j].total();
+        f32x4 R;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) R[j][e] = __builtin_fmaf(-gt.gam[e], x[e], widen<DT>(xv[j][e]));
-        put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, R[j] * gt.beta);
+        for (int e = 0; e < 4; ++e) R[e] = __builtin_fmaf(-gt.gam[e], x[e], widen<DT>(xv[j][e]));
+        put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, R * gt.beta);
       }
       load_V(nn);
       lds_barrier();
       if constexpr (BWD) {
-        const __amdgpu_buffer_rsrc_t sb = So.piece(true), rb = Ro.piece(true);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(sb, os + (16 * m + e) * ldv + 64 * j, S[m][j][e]);
+        const __amdgpu_buffer_rsrc_t sb = So.piece(true);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(rb, on + e * ldv + 64 * j, R[j][e]);
+          for (int m = 0; m < MT; ++m) buf_store_f4(sb, os + (j * (DKP / 16) + m) * 1024, S[m][j]);
         So.at += So.step;
-        Ro.at += Ro.step;
       }
 
       // N = W (beta R); W is lower triangular
@@ -198,9 +191,7 @@ __global__ __launch_bounds__(512, 4) void scan_kernel(DeltaArgs a, uint32_t head
       if constexpr (BWD) {
         const __amdgpu_buffer_rsrc_t nb = No.piece(true);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) buf_store1<CCV_DT_F32>(nb, on + e * ldv + 64 * j, N[j][e]);
+        for (int j = 0; j < NT; ++j) buf_store_f4(nb, on + j * 4096, N[j]);
         No.at += No.step;
       }
 

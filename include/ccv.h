@@ -418,7 +418,7 @@ int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream);
  * value heads that share a key head included, so results repeat bit for bit.
  * dinitial_state may be dfinal_state itself, with the same strides; other outputs may be
  * no input and no other output (CCV_E_ALIAS).  The workspace holds the states at
- * both ends of every group of 64 steps: about (2 Dk + 352) Dv fp32 values a group and head, with
+ * both ends of every group of 64 steps: about (2 Dk + 288) Dv fp32 values a group and head, with
  * Dk rounded up to 64 or 128 and Dv to a multiple of 32 (for 128 and 128: 0.3 MB). */
 typedef struct ccv_delta_bwd_args {
   int64_t struct_size;          /* = sizeof(ccv_delta_bwd_args_t) */
