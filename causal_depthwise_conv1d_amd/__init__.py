@@ -41,6 +41,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -775,22 +776,89 @@ def causal_conv1d_fn(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
                                  final_states_out, activation)
 
 
+# ---- calls of the layer's operators ------------------------------------------------------------
+#
+# A small call's cost is the host's, so these fill their args struct in one go: the values, in
+# the order of the struct's fields, packed to its layout, which the library takes by address.
+
+_FORMAT = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", _I64x2: "2q", _I64x3: "3q"}
+
+
+class _Call:
+    """One C entry point with its packed args."""
+
+    def __init__(self, name):
+        self.name = name
+        args_t, self.workspace = _LAYER_CALLS[name]
+        self.pack = struct.Struct("@" + "".join(_FORMAT[t] for _, t in args_t._fields_)).pack
+        self.size = ctypes.sizeof(args_t)
+        self.fn = self.ws_fn = None
+
+    def bind(self):
+        L = lib()
+        fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, ctypes.c_void_p)((self.name, L))
+        if self.workspace:
+            self.ws_fn = ctypes.CFUNCTYPE(ctypes.c_int64, ctypes.c_char_p)((self.name + "_workspace_size", L))
+        self.fn = fn
+
+    def __call__(self, device, *values):
+        """Enqueue on the device's current stream; the workspace, which follows the values in
+        the struct, is allocated here, through torch."""
+        if self.fn is None:
+            self.bind()
+        if self.workspace:
+            ws = self.ws_fn(self.pack(self.size, *values, 0, 0))
+            if ws < 0:
+                _raise(int(ws), self.name)
+            buf = torch.empty(ws or 16, dtype=torch.uint8, device=device)
+            values += (buf.data_ptr(), buf.numel())
+        args = self.pack(self.size, *values)
+        index = device.index
+        if index == torch.cuda.current_device():
+            st = self.fn(args, _raw_stream(index))
+        else:
+            with torch.cuda.device(device):
+                st = self.fn(args, _raw_stream(index))
+        if st:
+            _raise(st, self.name)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_CALLS = {name: _Call(name) for name in _LAYER_CALLS}
+
+
+def _p(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _at(t):
+    """A tensor's address and its three leading strides, as consecutive values."""
+    if t is None:
+        return (0, 0, 0, 0)
+    s = t.stride()
+    return (t.data_ptr(), s[0], s[1], s[2])
+
+
 # ---- the gated delta rule ------------------------------------------------------------------
 
 def _same_device(x, **others):
     if not x.is_cuda:
         raise ValueError("tensors must be on a GPU (there is no CPU path)")
+    d = x.device
     for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} must be on {x.device}")
+        if t is not None and t.device != d:
+            raise ValueError(f"{name} must be on {d}")
+    return d
 
 
 def _delta_sizes(q, k, v, g, beta):
     """(B, L, Hk, Hv, Dk, Dv) of the five inputs, checked against each other."""
-    if q.dim() != 4 or k.shape != q.shape or v.dim() != 4 or v.shape[:2] != q.shape[:2]:
+    qs, vs = q.shape, v.shape
+    if len(qs) != 4 or k.shape != qs or len(vs) != 4 or vs[:2] != qs[:2]:
         raise ValueError("expected q and k [B, L, Hk, Dk] and v [B, L, Hv, Dv]")
-    B, L, Hk, Dk = q.shape
-    Hv, Dv = v.shape[2:]
+    B, L, Hk, Dk = qs
+    Hv, Dv = vs[2], vs[3]
     if Hk < 1 or Hv < 1 or Hv % Hk:
         raise ValueError("the value heads must be a multiple of the key heads")
     if not 1 <= Dk <= 128 or Dv < 1:
@@ -798,7 +866,7 @@ def _delta_sizes(q, k, v, g, beta):
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype")
     for name, t in (("g", g), ("beta", beta)):
-        if tuple(t.shape) != (B, L, Hv):
+        if t.shape != (B, L, Hv):
             raise ValueError(f"{name} must be [B, L, Hv]")
     for name, t in (("q", q), ("g", g), ("beta", beta)):
         if t.dtype not in DTYPE_CODE:
@@ -817,40 +885,16 @@ def _delta_states(name, t, shape):
     return t
 
 
-def _put(a, name, stride, t):
-    """A tensor's pointer and leading strides into fields of an args struct."""
-    if t is not None:
-        setattr(a, name, t.data_ptr())
-        setattr(a, stride, _I64x3(*t.stride()[:3]))
-
-
-def _delta_args(a, q, k, v, g, beta, scale):
-    a.B, a.L = q.shape[:2]
-    a.Hk, a.Dk = q.shape[2:]
-    a.Hv, a.Dv = v.shape[2:]
-    a.x_dtype, a.g_dtype, a.beta_dtype = DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype]
-    a.scale = q.shape[3] ** -0.5 if scale is None else scale
-    for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
-        _put(a, name, name + "_stride", t)
-    return a
-
-
-def _delta_sequences(a, cu_seqlens, B):
-    """The packed sequences into the args; returns how many sequences have states."""
+def _delta_sequences(cu_seqlens, B):
+    """(packed sequences, sequences that have states)."""
     if cu_seqlens is None:
-        return B
+        return 0, B
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous int32 [N + 1]")
     if B != 1:
         raise ValueError("packed sequences (cu_seqlens) need B = 1")
-    a.N = cu_seqlens.numel() - 1
-    a.cu_seqlens = cu_seqlens.data_ptr()
-    return a.N
-
-
-def _workspace(size, where, device):
-    _raise(int(size) if size < 0 else 0, where)
-    return torch.empty(max(int(size), 16), dtype=torch.uint8, device=device)
+    N = cu_seqlens.numel() - 1
+    return N, N
 
 
 def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -874,35 +918,30 @@ def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     if final_state_out is not None and not return_final_state:
         raise ValueError("final_state_out given but return_final_state is False")
     B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
-    _same_device(q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
-                 final_state_out=final_state_out, out=out)
-    given = {"q": q, "k": k, "v": v, "initial_state": initial_state}
+    device = _same_device(q, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                          final_state_out=final_state_out, out=out)
+    given = (("q", q), ("k", k), ("v", v), ("initial_state", initial_state))
     q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
-    a = _delta_args(ccv_delta_fwd_args_t(), q, k, v, g, beta, scale)
-    shape = (_delta_sequences(a, cu_seqlens, B), Hv, Dk, Dv)
+    N, seqs = _delta_sequences(cu_seqlens, B)
+    shape = (seqs, Hv, Dk, Dv)
     if _delta_states("initial_state", initial_state, shape) is not None:
         initial_state = _unit_heads(initial_state)
     if out is None:
-        out = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=v.device)
+        out = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=device)
     elif out.dtype != v.dtype or tuple(out.shape) != (B, L, Hv, Dv) or (out.stride(-1) != 1 and Dv > 1):
         raise ValueError("out must be [B, L, Hv, Dv] in v's dtype with unit stride in its last dimension")
     ht = None
     if return_final_state:
-        ht = torch.empty(shape, dtype=torch.float32, device=v.device) if final_state_out is None else final_state_out
+        ht = torch.empty(shape, dtype=torch.float32, device=device) if final_state_out is None else final_state_out
         _delta_states("final_state_out", ht, shape)
         if ht.stride(-1) != 1 and Dv > 1:
             raise ValueError("final_state_out must have unit stride in its last dimension")
-    _put(a, "initial_state", "init_stride", initial_state)
-    _put(a, "final_state", "final_stride", ht)
-    _put(a, "out", "out_stride", out)
-    ws = _workspace(ccv_delta_fwd_workspace_size(a), "ccv_delta_fwd", v.device)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    with torch.cuda.device(v.device):
-        st = ccv_delta_fwd(a)
-    _raise(st, "ccv_delta_fwd")
+    _CALLS["ccv_delta_fwd"](device, B, L, N, Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype],
+                            Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v), *_at(g), *_at(beta),
+                            _p(cu_seqlens), *_at(initial_state), *_at(ht), *_at(out))
     if info is not None:
-        now = {"q": q, "k": k, "v": v, "initial_state": initial_state}
-        info["copied"] = [n for n in given if given[n] is not now[n]]
+        now = (q, k, v, initial_state)
+        info["copied"] = [name for (name, t), u in zip(given, now) if t is not u]
     return (out, ht) if return_final_state else out
 
 
@@ -917,31 +956,25 @@ def gated_delta_rule_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     only with return_dinitial_state, which needs initial_state.
     """
     B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
-    _same_device(q, k=k, v=v, g=g, beta=beta, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state,
-                 dfinal_state=dfinal_state)
+    device = _same_device(q, k=k, v=v, g=g, beta=beta, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                          dfinal_state=dfinal_state)
     if dout.dtype != v.dtype or dout.shape != v.shape:
         raise ValueError("dout must be [B, L, Hv, Dv] in v's dtype")
     if return_dinitial_state and initial_state is None:
         raise ValueError("dinitial_state needs initial_state")
     q, k, v, dout = _unit_heads(q), _unit_heads(k), _unit_heads(v), _unit_heads(dout)
-    a = _delta_args(ccv_delta_bwd_args_t(), q, k, v, g, beta, scale)
-    shape = (_delta_sequences(a, cu_seqlens, B), Hv, Dk, Dv)
+    N, seqs = _delta_sequences(cu_seqlens, B)
+    shape = (seqs, Hv, Dk, Dv)
     if _delta_states("initial_state", initial_state, shape) is not None:
         initial_state = _unit_heads(initial_state)
     if _delta_states("dfinal_state", dfinal_state, shape) is not None:
         dfinal_state = _unit_heads(dfinal_state)
-    dq, dk, dv, dg, db = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v, g, beta))
-    dh = torch.empty(shape, dtype=torch.float32, device=v.device) if return_dinitial_state else None
-    for name, stride, t in (("initial_state", "init_stride", initial_state), ("dout", "dout_stride", dout),
-                            ("dfinal_state", "dfinal_stride", dfinal_state), ("dq", "dq_stride", dq),
-                            ("dk", "dk_stride", dk), ("dv", "dv_stride", dv), ("dg", "dg_stride", dg),
-                            ("dbeta", "dbeta_stride", db), ("dinitial_state", "dinit_stride", dh)):
-        _put(a, name, stride, t)
-    ws = _workspace(ccv_delta_bwd_workspace_size(a), "ccv_delta_bwd", v.device)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    with torch.cuda.device(v.device):
-        st = ccv_delta_bwd(a)
-    _raise(st, "ccv_delta_bwd")
+    dq, dk, dv, dg, db = (torch.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v, g, beta))
+    dh = torch.empty(shape, dtype=torch.float32, device=device) if return_dinitial_state else None
+    _CALLS["ccv_delta_bwd"](device, B, L, N, Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype],
+                            Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v), *_at(g), *_at(beta),
+                            _p(cu_seqlens), *_at(initial_state), *_at(dout), *_at(dfinal_state), *_at(dq), *_at(dk),
+                            *_at(dv), *_at(dg), *_at(db), *_at(dh))
     return dq, dk, dv, dg, db, dh
 
 
@@ -992,31 +1025,26 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     if one:
         q, k, v, g, beta = (t.unsqueeze(1) for t in (q, k, v, g, beta))
     B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
-    _same_device(q, k=k, v=v, g=g, beta=beta, state=state, state_indices=state_indices, out=out)
-    if state.dtype != torch.float32 or state.dim() != 4 or tuple(state.shape[1:]) != (Hv, Dk, Dv):
+    device = _same_device(q, k=k, v=v, g=g, beta=beta, state=state, state_indices=state_indices, out=out)
+    if state.dtype != torch.float32 or state.dim() != 4 or state.shape[1:] != (Hv, Dk, Dv):
         raise ValueError("state must be float32 [slots, Hv, Dk, Dv]")
     if state.stride(-1) != 1 and Dv > 1:
         raise ValueError("state must have unit stride in its last dimension")
-    if state_indices is not None and (state_indices.dtype != torch.int32 or tuple(state_indices.shape) != (B,)
+    if state_indices is not None and (state_indices.dtype != torch.int32 or state_indices.shape != (B,)
                                       or not state_indices.is_contiguous()):
         raise ValueError("state_indices must be contiguous int32 [B]")
     if state_indices is None and B > state.shape[0]:
         raise ValueError("more rows than states")
     q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
     if out is None:
-        o = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=v.device)
+        o = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=device)
     else:
         o = out.unsqueeze(1) if one else out
         if o.dtype != v.dtype or tuple(o.shape) != (B, L, Hv, Dv) or (o.stride(-1) != 1 and Dv > 1):
             raise ValueError("out must have v's shape and dtype with unit stride in its last dimension")
-    a = _delta_args(ccv_delta_update_args_t(), q, k, v, g, beta, scale)
-    a.slots = state.shape[0]
-    a.state_indices = _ptr(state_indices)
-    _put(a, "state", "state_stride", state)
-    _put(a, "out", "out_stride", o)
-    with torch.cuda.device(v.device):
-        st = ccv_delta_update(a)
-    _raise(st, "ccv_delta_update")
+    _CALLS["ccv_delta_update"](device, B, L, state.shape[0], Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype],
+                               DTYPE_CODE[beta.dtype], Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v),
+                               *_at(g), *_at(beta), _p(state_indices), *_at(state), *_at(o))
     return o.squeeze(1) if one else o
 
 
@@ -1029,7 +1057,9 @@ def _norm_rows(x):
         raise ValueError("x needs a last dimension to be normalised")
     if x.shape[-1] > 1 and x.stride(-1) != 1:
         x = x.contiguous()
-    if x.dim() <= 3:
+    if x.dim() == 3:
+        return x
+    if x.dim() < 3:
         return x[(None,) * (3 - x.dim())]
     try:
         return x.view(-1, x.shape[-2], x.shape[-1])
@@ -1039,13 +1069,18 @@ def _norm_rows(x):
 
 def _norm_weights(x, weight, bias):
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and (tuple(t.shape) != (x.shape[-1],) or t.dtype not in DTYPE_CODE):
+        if t is not None and (t.shape != x.shape[-1:] or t.dtype not in DTYPE_CODE):
             raise ValueError(f"{name} must be [width] in float32, float16 or bfloat16")
     if weight is not None and bias is not None and bias.dtype != weight.dtype:
         raise ValueError("bias must have the weight's dtype")
     if x.dtype not in DTYPE_CODE:
         raise ValueError(f"x must be float32, float16 or bfloat16, not {x.dtype}")
-    return (t if t is None else t.contiguous() for t in (weight, bias))
+    return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous())
+
+
+def _rows_of(out, shape):
+    """The row strides of a contiguous tensor seen as [n0, n1, width]."""
+    return shape[1] * shape[2], shape[2]
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -1057,27 +1092,20 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [...].
     """
     weight, bias = _norm_weights(x, weight, bias)
-    _same_device(x, weight=weight, bias=bias, out=out)
+    device = _same_device(x, weight=weight, bias=bias, out=out)
     rows = _norm_rows(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
     elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous with x's shape and dtype")
-    o = out.view(rows.shape) if out.numel() else out.reshape(rows.shape)
-    stats = [torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2)] if return_stats else [None] * 2
-    a = ccv_norm_fwd_args_t()
-    a.n0, a.n1, a.width = rows.shape
-    a.x_dtype = DTYPE_CODE[x.dtype]
-    a.w_dtype = DTYPE_CODE[(weight if weight is not None else bias if bias is not None else x).dtype]
-    a.eps = eps
-    a.x, a.x_stride = rows.data_ptr(), _I64x2(*rows.stride()[:2])
-    a.weight, a.bias = _ptr(weight), _ptr(bias)
-    a.out, a.out_stride = o.data_ptr(), _I64x2(*o.stride()[:2])
-    a.mean, a.rstd = _ptr(stats[0]), _ptr(stats[1])
-    with torch.cuda.device(x.device):
-        st = ccv_norm_fwd(a)
-    _raise(st, "ccv_norm_fwd")
-    return (out, *stats) if return_stats else out
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
+    w = weight if weight is not None else bias if bias is not None else x
+    s = rows.stride()
+    _CALLS["ccv_norm_fwd"](device, *rows.shape, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], eps, 0, rows.data_ptr(), s[0], s[1],
+                           _p(weight), _p(bias), out.data_ptr(), *_rows_of(out, rows.shape), _p(mean), _p(rstd))
+    return (out, mean, rstd) if return_stats else out
 
 
 def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.Tensor, mean: torch.Tensor,
@@ -1090,7 +1118,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.
     in a fixed order.
     """
     weight, _ = _norm_weights(x, weight, None)
-    _same_device(x, weight=weight, dout=dout, mean=mean, rstd=rstd)
+    device = _same_device(x, weight=weight, dout=dout, mean=mean, rstd=rstd)
     if dout.dtype != x.dtype or dout.shape != x.shape:
         raise ValueError("dout must have x's shape and dtype")
     for name, t in (("mean", mean), ("rstd", rstd)):
@@ -1100,24 +1128,13 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.
     if wd not in DTYPE_CODE:
         raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
     rows, drows = _norm_rows(x), _norm_rows(dout)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
-    dw = torch.empty(x.shape[-1], dtype=wd, device=x.device) if want_dweight else None
-    db = torch.empty(x.shape[-1], dtype=wd, device=x.device) if want_dbias else None
-    a = ccv_norm_bwd_args_t()
-    a.n0, a.n1, a.width = rows.shape
-    a.x_dtype, a.w_dtype = DTYPE_CODE[x.dtype], DTYPE_CODE[wd]
-    a.x, a.x_stride = rows.data_ptr(), _I64x2(*rows.stride()[:2])
-    a.dout, a.dout_stride = drows.data_ptr(), _I64x2(*drows.stride()[:2])
-    a.weight, a.mean, a.rstd = _ptr(weight), mean.data_ptr(), rstd.data_ptr()
-    if dx is not None:
-        o = dx.view(rows.shape) if dx.numel() else dx.reshape(rows.shape)
-        a.dx, a.dx_stride = o.data_ptr(), _I64x2(*o.stride()[:2])
-    a.dweight, a.dbias = _ptr(dw), _ptr(db)
-    ws = _workspace(ccv_norm_bwd_workspace_size(a), "ccv_norm_bwd", x.device)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    with torch.cuda.device(x.device):
-        st = ccv_norm_bwd(a)
-    _raise(st, "ccv_norm_bwd")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=device) if want_dx else None
+    dw = torch.empty(x.shape[-1], dtype=wd, device=device) if want_dweight else None
+    db = torch.empty(x.shape[-1], dtype=wd, device=device) if want_dbias else None
+    s, d = rows.stride(), drows.stride()
+    _CALLS["ccv_norm_bwd"](device, *rows.shape, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], rows.data_ptr(), s[0], s[1], _p(weight),
+                           drows.data_ptr(), d[0], d[1], mean.data_ptr(), rstd.data_ptr(), _p(dx), *_rows_of(dx, rows.shape),
+                           _p(dw), _p(db))
     return dx, dw, db
 
 
@@ -1161,13 +1178,10 @@ def sequence_tables(lengths: torch.Tensor, total: int):
         raise ValueError("lengths must be contiguous int32 [N]")
     if total < 0:
         raise ValueError("total must not be negative")
-    _same_device(lengths)
-    cu = torch.empty(lengths.numel() + 1, dtype=torch.int32, device=lengths.device)
-    seq, pos = (torch.empty(1, total, dtype=torch.int32, device=lengths.device) for _ in range(2))
-    a = ccv_seq_tables_args_t()
-    a.N, a.total = lengths.numel(), total
-    a.lengths, a.cu_seqlens, a.seq_idx, a.positions = _ptr(lengths), cu.data_ptr(), seq.data_ptr(), pos.data_ptr()
-    with torch.cuda.device(lengths.device):
-        st = ccv_seq_tables(a)
-    _raise(st, "ccv_seq_tables")
+    device = _same_device(lengths)
+    n = lengths.numel()
+    cu = torch.empty(n + 1, dtype=torch.int32, device=device)
+    seq = torch.empty(1, total, dtype=torch.int32, device=device)
+    pos = torch.empty(1, total, dtype=torch.int32, device=device)
+    _CALLS["ccv_seq_tables"](device, n, total, lengths.data_ptr(), cu.data_ptr(), seq.data_ptr(), pos.data_ptr())
     return cu, seq, pos

@@ -394,15 +394,8 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   for (int n = 0; n < TK; ++n) dq[n] = dk[n] = f32x4{0, 0, 0, 0};
 
   if (k.seq < a.nseq) {
-    if (half) {
-      RowTile<DT, DKP, LDK> x(w, l, (uint32_t)(a.k_s[1] * ES), a.Dk);
-      x.load(chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7));
-      x.store(&Kl[0][0][0], 64 * LDK);
-    } else {
-      RowTile<DT, DKP, LDK> x(w, l, (uint32_t)(a.q_s[1] * ES), a.Dk);
-      x.load(chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7));
-      x.store(&Ql[0][0][0], 64 * LDK);
-    }
+    RowTile<DT, DKP, LDK> kq(w, l, (uint32_t)((half ? a.k_s[1] : a.q_s[1]) * ES), a.Dk);
+    kq.load(half ? chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7) : chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7));
     // what a thread moves of 32 values: RS times 4 keys of one value of S and dS', 4 steps of one
     // value of N and Y, and 8 values of one step of dO
     constexpr int RS = DKP / 64, kLanesO = 4;
@@ -429,7 +422,9 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         if constexpr (TWO)
           o4 = buf16(ob, orow < 64 && v0 + oc < a.Dv ? orow * (uint32_t)(a.do_s[1] * ES) + (v0 + oc) * ES : kNowhere);
       };
+      load(0);
       if (tid < 64) G[tid] = reinterpret_cast<const double*>(dec + 192)[tid];
+      if (hg == 0) kq.store(half ? &Kl[0][0][0] : &Ql[0][0][0], 64 * LDK);
       f32x4 zq[TK], zy[TK], zn[TK], pr[4];
       float dot = 0;
 #pragma unroll
@@ -437,7 +432,6 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int n = 0; n < 4; ++n) pr[n] = f32x4{0, 0, 0, 0};
 
-      load(0);
       for (int v0 = 0; v0 < a.Dvp; v0 += 32) {
         lds_barrier();
         // 1 KB tiles [lane][4 rows]: tile (16 values, 16 keys) of S, (16 values, 16 steps) of N and Y
@@ -585,10 +579,11 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         }
         g -= cc;
         const float* part = a.part + ch * a.slices * kDeltaPart;
-        for (int i = 0; i < a.slices; ++i, part += kDeltaPart) {
-          g += part[l] + part[128 + l];
-          b += part[64 + l];
-          cj += part[192 + l];
+#pragma unroll 8
+        for (int i = 0; i < a.slices; ++i) {       // loads of eight slices under way together
+          g += part[i * kDeltaPart + l] + part[i * kDeltaPart + 128 + l];
+          b += part[i * kDeltaPart + 64 + l];
+          cj += part[i * kDeltaPart + 192 + l];
         }
         if (l >= k.n - 1) cj = 0;      // the last step's decay to the end is 1, whatever its g
         float tot = cj;
