@@ -166,6 +166,7 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
     w.take(&a->dS, heads, (int64_t)a->Dkp * a->Dvp);
     w.take(&a->N, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->Y, heads, 64 * (int64_t)a->Dvp);
+    w.take(&a->pairs, heads, kDeltaPairs);
     w.take(&a->part, heads, a->Dvp / 16 * kDeltaPart);
   }
   const int64_t steps = z.B * z.L, wk = z.Hk * round_up(z.Dk, 8), wv = z.Hv * round_up(z.Dv, 8);

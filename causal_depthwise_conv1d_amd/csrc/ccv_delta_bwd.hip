@@ -373,8 +373,9 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   constexpr int kStage = (TWO ? 2 : 1) * kS + 2 * kN + kO, kPair = 2 * OP * 64 * LDT;
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
   __shared__ __bf16 un[kStage > kPair ? kStage : kPair];
-  __shared__ double G[64];
+  __shared__ __align__(16) float gates[kDeltaDec];  // e^G, e^(G63 - G), beta, and G as doubles
   __shared__ float rows[64], cols[8][64], dots[8];
+  const double* G = reinterpret_cast<const double*>(gates + 192);
   __bf16* St = un;                                  // [OP][32][LDK]
   __bf16* Dt = TWO ? St + kS : St;
   __bf16* Nt = Dt + kS;                             // [3][32][LDT]
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           o4 = buf16(ob, orow < 64 && v0 + oc < a.Dv ? orow * (uint32_t)(a.do_s[1] * ES) + (v0 + oc) * ES : kNowhere);
       };
       load(0);
-      if (tid < 64) G[tid] = reinterpret_cast<const double*>(dec + 192)[tid];
+      if (tid < kDeltaDec) gates[tid] = dec[tid];
       if (hg == 0) kq.store(half ? &Kl[0][0][0] : &Ql[0][0][0], 64 * LDK);
       f32x4 zq[TK], zy[TK], zn[TK], pr[4];
       float dot = 0;
@@ -492,7 +493,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
       if (l == 0) dots[w8] = dot;
-      const float gam = dec[t], del = dec[64 + t], bet = dec[128 + t];
+      const float gam = gates[t], del = gates[64 + t], bet = gates[128 + t];
 #pragma unroll
       for (int n = 0; n < TK; ++n) {
         dq[n] += zq[n] * (a.scale * gam);
@@ -507,7 +508,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         Gi[e] = G[16 * w + 4 * g4 + e];
-        bi[e] = half ? -dec[128 + 16 * w + 4 * g4 + e] : a.scale;
+        bi[e] = half ? -gates[128 + 16 * w + 4 * g4 + e] : a.scale;
       }
       __bf16* Pt = half ? Et : Ft;
 #pragma unroll
@@ -571,46 +572,16 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
         }
       }
       if (w8 == 0) {                                          // a step a lane
-        float g = rows[l], b = 0, cj = 0, cc = 0, sd = 0;
+        float g = rows[l], sd = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          cc += cols[i][l];
+          g -= cols[i][l];
           sd += dots[i];
         }
-        g -= cc;
-        const float* part = a.part + ch * a.slices * kDeltaPart;
-#pragma unroll 8
-        for (int i = 0; i < a.slices; ++i) {       // loads of eight slices under way together
-          g += part[i * kDeltaPart + l] + part[i * kDeltaPart + 128 + l];
-          b += part[i * kDeltaPart + 64 + l];
-          cj += part[i * kDeltaPart + 192 + l];
-        }
-        if (l >= k.n - 1) cj = 0;      // the last step's decay to the end is 1, whatever its g
-        float tot = cj;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) tot += __shfl_xor(tot, d);
-        g -= cj;
-        if (l == 63) g += tot + dec[63] * sd;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const float o = __shfl_down(g, d);
-          if (l + d < 64) g += o;
-        }
-        const int begin = a.packed ? a.cstart[a.nseq + 2 + k.seq] : 0;
-        if (l == 0 && k.t0 == begin && !a.h0) g = 0;
-        if (l < k.n) {
-          const int64_t s = (int64_t)k.t0 + l;
-          store_gate(a.dg, a.g_dtype, k.row * a.dg_s[0] + s * a.dg_s[1] + h * a.dg_s[2], g);
-          store_gate(a.dbeta, a.b_dtype, k.row * a.db_s[0] + s * a.db_s[1] + h * a.db_s[2], b / dec[128 + l]);
-        }
+        a.pairs[ch * kDeltaPairs + l] = g;
+        if (l == 0) a.pairs[ch * kDeltaPairs + 64] = sd;
       }
       lds_barrier();      // before the next head writes what is read here
-    }
-  } else if (tid < 64 && tid < k.n) {
-    for (int h = hk * group; h < (hk + 1) * group; ++h) {
-      const int64_t s = (int64_t)k.t0 + tid;
-      store_gate(a.dg, a.g_dtype, k.row * a.dg_s[0] + s * a.dg_s[1] + h * a.dg_s[2], 0.0f);
-      store_gate(a.dbeta, a.b_dtype, k.row * a.db_s[0] + s * a.db_s[1] + h * a.db_s[2], 0.0f);
     }
   }
   if (live) {
@@ -622,6 +593,50 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
       store4<DT>(dqp + d * ES, dq[n], a.Dk - d, a.vec_dqk);
       store4<DT>(dkp + d * ES, dk[n], a.Dk - d, a.vec_dqk);
     }
+  }
+}
+
+// dg and dbeta of a chunk and head, a step a lane of one wave: the slices' sums and the pairs'
+// joined, then the running sum from the chunk's end.
+__global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) {
+  const int64_t ch = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (ch >= items) return;
+  const int c = (int)(ch / a.Hv), h = (int)(ch - (int64_t)c * a.Hv), l = threadIdx.x & 63;
+  const Chunk k = chunk_at(a, c);
+  if (k.n <= 0) return;
+  float g = 0, b = 0;
+  if (k.seq < a.nseq) {
+    const float* part = a.part + ch * a.slices * kDeltaPart;
+    const float* pairs = a.pairs + ch * kDeltaPairs;
+    const float* dec = a.dec + ch * kDeltaDec;
+    const float beta = dec[128 + l], last = dec[63], dot = pairs[64];
+    float cj = 0;
+    g = pairs[l];
+#pragma unroll 4
+    for (int i = 0; i < a.slices; ++i) {
+      g += part[i * kDeltaPart + l] + part[i * kDeltaPart + 128 + l];
+      b += part[i * kDeltaPart + 64 + l];
+      cj += part[i * kDeltaPart + 192 + l];
+    }
+    if (l >= k.n - 1) cj = 0;      // the last step's decay to the end is 1, whatever its g
+    float tot = cj;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) tot += __shfl_xor(tot, d);
+    g -= cj;
+    if (l == 63) g += tot + last * dot;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float o = __shfl_down(g, d);
+      if (l + d < 64) g += o;
+    }
+    const int begin = a.packed ? a.cstart[a.nseq + 2 + k.seq] : 0;
+    if (l == 0 && k.t0 == begin && !a.h0) g = 0;
+    b /= beta;
+  }
+  if (l < k.n) {
+    const int64_t t = (int64_t)k.t0 + l;
+    store_gate(a.dg, a.g_dtype, k.row * a.dg_s[0] + t * a.dg_s[1] + h * a.dg_s[2], g);
+    store_gate(a.dbeta, a.b_dtype, k.row * a.db_s[0] + t * a.db_s[1] + h * a.db_s[2], b);
   }
 }
 
@@ -665,6 +680,10 @@ int launch_delta_grads(const DeltaArgs& a, void* stream) {
   if (a.x_dtype == CCV_DT_F32) launch_grads<CCV_DT_F32>(a, st);
   else if (a.x_dtype == CCV_DT_F16) launch_grads<CCV_DT_F16>(a, st);
   else launch_grads<CCV_DT_BF16>(a, st);
+  const int e = (int)hipGetLastError();
+  if (e) return e;
+  const int64_t items = (int64_t)a.nchunks * a.Hv;
+  gates_kernel<<<(uint32_t)((items + 3) / 4), 256, 0, st>>>(a, items);
   return (int)hipGetLastError();
 }
 

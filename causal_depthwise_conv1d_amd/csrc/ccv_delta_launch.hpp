@@ -10,6 +10,7 @@ constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 1
 constexpr int kDeltaMatrix = 3 * 64 * 64;   // elements of a chunk's W or P
 constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
 constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, Y.N, Y.N - dv.v, c
+constexpr int kDeltaPairs = 128;      // fp32 values: 64 of dG, one dot product, and room
 constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
 
 // One forward or backward call.  Strides are in elements: (row, step, head), unit inside
@@ -47,6 +48,7 @@ struct DeltaArgs {
   float *S, *dS;                                // [ch][Dvp / 16][Dkp / 16] tiles: state at a chunk's start, gradient at its end
   float *N, *Y;                                 // [ch][Dvp / 16][4] tiles
   float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
+  float* pairs;                                 // backward: [ch][kDeltaPairs] dG by pairs of steps; <S, dS'>
   int32_t Dkp, slices;
 };
 
