@@ -3,11 +3,15 @@
 //   n = (x - mean) rstd,  out = n w + b;     a = dout w,
 //   dx = rstd (a - mean(a) - n mean(a n)),   dw = sum over rows of dout n,   db = sum of dout.
 // Bound by memory: x in, out out; in the backward x and dout in, dx out.  A row is read
-// once into registers, `lanes` threads a row (16 for a head's width, up to 512), and the
+// once into registers, `LANES` threads a row (16 for a head's width, up to 512), and the
 // variance is summed from the deviations there, in fp32.  Workgroups walk rows at a
-// stride, so a thread always has the same columns: the weights stay in registers, and in
-// the backward so do the thread's sums of dw and db.  Each workgroup leaves one partial
-// row, and a second kernel adds the partial rows in a fixed order.
+// stride, with the next row's loads under way while a row's sums pass through LDS; a thread
+// always has the same columns, so the weights stay in registers, and in the backward so do
+// the thread's sums of dw and db.  Each workgroup leaves one partial row, and a second
+// kernel adds the partial rows in a fixed order.
+// Every access is 16 bytes at any alignment.  Where the width is no multiple of that, a
+// row's last vector starts where it ends with the row; the elements that it shares with
+// the vector before it are left out of sums and written twice, with the same value.
 #include "ccv_delta_device.hpp"
 #include "ccv_norm_launch.hpp"
 
@@ -64,145 +68,218 @@ __device__ inline void load_weights(const void* p, int dtype, int col, int width
   for (int e = 0; e < V; ++e) w[e] = p && col + e < width ? load_param(p, dtype, col + e) : other;
 }
 
-// Sum over the `LANES` threads of a row; every one of them gets it.  Rows of more than a
-// wave: through `red`, two rows of it in turn, so that one barrier a sum suffices.
-template <int LANES>
-__device__ inline float row_sum(float v, float (*red)[8], int& turn) {
-  v = sum16(v);
-  if constexpr (LANES >= 64) v = sum4rows(v);
+// Sums over the `LANES` threads of a row of N values; every one of them gets them.  Rows of more
+// than a wave: through `red`, two pieces of it in turn, so that one barrier suffices.
+template <int LANES, int N>
+__device__ inline f32x2 row_sums(f32x2 v, float (*red)[2][8], int& turn) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float s = sum16(v[n]);
+    if constexpr (LANES >= 64) s = sum4rows(s);
+    v[n] = s;
+  }
   if constexpr (LANES > 64) {
     const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[turn][w] = v;
-    __syncthreads();
-    v = 0;
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int i = 0; i < LANES / 64; ++i) v += red[turn][i];
+      for (int n = 0; n < N; ++n) red[turn][n][w] = v[n];
+    lds_barrier();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float s = 0;
+#pragma unroll
+      for (int i = 0; i < LANES / 64; ++i) s += red[turn][n][i];
+      v[n] = s;
+    }
     turn ^= 1;
   }
   return v;
 }
 
-template <int DT>
-__device__ inline const char* norm_row(const void* p, const int64_t* s, int64_t r, int64_t n1) {
-  const int64_t i = r / n1;
-  return static_cast<const char*>(p) + (i * s[0] + (r - i * n1) * s[1]) * (DT == CCV_DT_F32 ? 4 : 2);
+// Row r of a view; rows that follow each other at one stride need no division (n1 is then 0).
+__device__ inline int64_t row_at(const int64_t* s, int64_t r, uint32_t n1) {
+  if (n1 == 0) return r * s[1];
+  const uint32_t i = (uint32_t)r / n1;
+  return i * s[0] + ((uint32_t)r - i * n1) * s[1];
 }
 template <int DT>
-__device__ inline char* norm_row(void* p, const int64_t* s, int64_t r, int64_t n1) {
-  const int64_t i = r / n1;
-  return static_cast<char*>(p) + (i * s[0] + (r - i * n1) * s[1]) * (DT == CCV_DT_F32 ? 4 : 2);
+__device__ inline const char* norm_row(const void* p, const int64_t* s, int64_t r, uint32_t n1) {
+  return static_cast<const char*>(p) + row_at(s, r, n1) * (DT == CCV_DT_F32 ? 4 : 2);
+}
+template <int DT>
+__device__ inline char* norm_row(void* p, const int64_t* s, int64_t r, uint32_t n1) {
+  return static_cast<char*>(p) + row_at(s, r, n1) * (DT == CCV_DT_F32 ? 4 : 2);
 }
 
 template <int LANES> constexpr int kThreads = LANES > 256 ? LANES : 256;
 
-template <int DT, int LANES, int NV>
-__global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(NormArgs a) {
-  constexpr int V = Vec<DT>::n, TH = kThreads<LANES>, RW = TH / LANES, ES = DT == CCV_DT_F32 ? 4 : 2;
-  __shared__ float red[2][8];
-  int turn = 0;
-  const int lane = threadIdx.x % LANES;
-  float w[NV][V], b[NV][V];
+// A thread's vectors of a row.
+template <int DT, int LANES, int NV, bool FULL>
+struct Columns {
+  static constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  int col[NV], skip[NV];                 // first element; elements that belong to another thread (V: all)
+  __device__ inline Columns(int width) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * LANES + lane) * V;
-    load_weights<V>(a.w, a.w_dtype, col, a.width, a.vec_w, 1.0f, w[i]);
-    load_weights<V>(a.b, a.w_dtype, col, a.width, a.vec_w, 0.0f, b[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LANES + (int)(threadIdx.x % LANES)) * V;
+      col[i] = FULL || c + V <= width ? c : width - V;
+      skip[i] = FULL ? 0 : c >= width ? V : c - col[i];
+    }
   }
+  __device__ inline bool mine(int i, int e) const { return FULL || e >= skip[i]; }
+  __device__ inline void load(u32x4 (&raw)[NV], const char* row) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      raw[i] = gload<u32x4>(pick(FULL || skip[i] < V, reinterpret_cast<uintptr_t>(row) + (uint32_t)col[i] * ES,
+                                 reinterpret_cast<uintptr_t>(kZeroSrc)));
+  }
+  __device__ static inline void unpack(u32x4 raw, float* x) {
+    if constexpr (DT == CCV_DT_F32) F32::unpack(raw, x);
+    else if constexpr (DT == CCV_DT_BF16) BF16::unpack(raw, x);
+    else F16::unpack(raw, x);
+  }
+  __device__ inline void store(char* row, int i, const float* y) const {
+    if (!FULL && skip[i] >= V) return;
+    char* p = row + (uint32_t)col[i] * ES;
+    if constexpr (DT == CCV_DT_F32) store16(p, F32::pack(y));
+    else if constexpr (DT == CCV_DT_BF16) store16(p, BF16::pack(y));
+    else store16(p, F16::pack(y));
+  }
+  __device__ inline void weights(float (&w)[NV][V], const void* p, int dtype, float other) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (!p || (!FULL && skip[i] >= V)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[i][e] = other;
+      } else if (dtype == CCV_DT_F32) {
+#pragma unroll
+        for (int e = 0; e < V; e += 4) F32::unpack(load16(static_cast<const float*>(p) + col[i] + e), w[i] + e);
+      } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + col[i];
+#pragma unroll
+        for (int e = 0; e < V; e += 4) {
+          const u32x2 d = gload<u32x2>(reinterpret_cast<uintptr_t>(q + e));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t two = d[j / 2];
+            const uint16_t h = (uint16_t)(two >> (16 * (j % 2)));
+            w[i][e + j] = dtype == CCV_DT_BF16 ? BF16::to_f(h) : F16::to_f(h);
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int DT, int LANES, int NV, bool FULL>
+__global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(NormArgs a) {
+  constexpr int V = Vec<DT>::n, RW = kThreads<LANES> / LANES;
+  __shared__ float red[2][2][8];
+  int turn = 0;
+  const Columns<DT, LANES, NV, FULL> cols(a.width);
+  float w[NV][V], b[NV][V];
+  cols.weights(w, a.w, a.w_dtype, 1.0f);
+  cols.weights(b, a.b, a.w_dtype, 0.0f);
   const float inv = 1.0f / (float)a.width;
-  // the trip count is the same for every thread of a workgroup whose rows share barriers
-  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += (int64_t)gridDim.x * RW) {
-    const int64_t row = base + threadIdx.x / LANES;
-    const bool live = row < a.rows;
-    const char* xp = norm_row<DT>(a.x, a.x_s, live ? row : 0, a.n1);
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / LANES;
+  u32x4 raw[NV];
+  cols.load(raw, norm_row<DT>(a.x, a.x_s, row < a.rows ? row : a.rows - 1, a.n1));
+  // the trip count is the same for all threads of a workgroup; rows past the last are read as it
+  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += step, row += step) {
     float x[NV][V], s = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * LANES + lane) * V;
-      load_vec<DT>(xp + col * ES, live ? a.width - col : 0, a.vec, x[i]);
+      cols.unpack(raw[i], x[i]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += cols.mine(i, e) ? x[i][e] : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) s += x[i][e];
-    const float mean = row_sum<LANES>(s, red, turn) * inv;
+    if (base + step < a.rows) cols.load(raw, norm_row<DT>(a.x, a.x_s, row + step < a.rows ? row + step : a.rows - 1, a.n1));
+    const float mean = row_sums<LANES, 1>(f32x2{s, 0}, red, turn)[0] * inv;
     float q = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const int col = (i * LANES + lane) * V + e;
-        x[i][e] = col < a.width ? x[i][e] - mean : 0.0f;
-        q = __builtin_fmaf(x[i][e], x[i][e], q);
+        x[i][e] -= mean;
+        const float d = cols.mine(i, e) ? x[i][e] : 0.0f;
+        q = __builtin_fmaf(d, d, q);
       }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<LANES>(q, red, turn) * inv + a.eps);
-    if (!live) continue;
-    if (lane == 0) {
+    const float rstd = 1.0f / __builtin_sqrtf(row_sums<LANES, 1>(f32x2{q, 0}, red, turn)[0] * inv + a.eps);
+    if (row >= a.rows) continue;
+    if (threadIdx.x % LANES == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
     char* op = norm_row<DT>(a.out, a.o_s, row, a.n1);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * LANES + lane) * V;
       float y[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) y[e] = __builtin_fmaf(x[i][e] * rstd, w[i][e], b[i][e]);
-      store_vec<DT>(op + col * ES, a.width - col, a.vec, y);
+      cols.store(op, i, y);
     }
   }
 }
 
-template <int DT, int LANES, int NV>
+template <int DT, int LANES, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
-  constexpr int V = Vec<DT>::n, TH = kThreads<LANES>, RW = TH / LANES, ES = DT == CCV_DT_F32 ? 4 : 2;
-  __shared__ float red[2][8];
+  constexpr int V = Vec<DT>::n, TH = kThreads<LANES>, RW = TH / LANES;
+  __shared__ float red[2][2][8];
   __shared__ float sums[RW > 1 ? TH * V : 1];
   int turn = 0;
   const int lane = threadIdx.x % LANES;
+  const Columns<DT, LANES, NV, FULL> cols(a.width);
   float w[NV][V], dw[NV][V], db[NV][V];
+  cols.weights(w, a.w, a.w_dtype, 1.0f);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load_weights<V>(a.w, a.w_dtype, (i * LANES + lane) * V, a.width, a.vec_w, 1.0f, w[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
-  }
   const float inv = 1.0f / (float)a.width;
-  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += (int64_t)gridDim.x * RW) {
-    const int64_t row = base + threadIdx.x / LANES;
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int64_t row = (int64_t)blockIdx.x * RW + threadIdx.x / LANES;
+  u32x4 xr[NV], dr[NV];
+  float mean, rstd;
+  const auto load = [&](int64_t r) {
+    r = r < a.rows ? r : a.rows - 1;
+    cols.load(xr, norm_row<DT>(a.x, a.x_s, r, a.n1));
+    cols.load(dr, norm_row<DT>(a.dout, a.do_s, r, a.n1));
+    mean = a.mean[r];
+    rstd = a.rstd[r];
+  };
+  load(row);
+  for (int64_t base = (int64_t)blockIdx.x * RW; base < a.rows; base += step, row += step) {
     const bool live = row < a.rows;
-    const char* xp = norm_row<DT>(a.x, a.x_s, live ? row : 0, a.n1);
-    const char* dp = norm_row<DT>(a.dout, a.do_s, live ? row : 0, a.n1);
+    const float mu = mean, rs = rstd;
     float x[NV][V], d[NV][V];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int col = (i * LANES + lane) * V;
-      load_vec<DT>(xp + col * ES, live ? a.width - col : 0, a.vec, x[i]);
-      load_vec<DT>(dp + col * ES, live ? a.width - col : 0, a.vec, d[i]);
-    }
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
     float s1 = 0, s2 = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      cols.unpack(xr[i], x[i]);
+      cols.unpack(dr[i], d[i]);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const bool in = (i * LANES + lane) * V + e < a.width;
-        x[i][e] = in ? (x[i][e] - mean) * rstd : 0.0f;
-        dw[i][e] = __builtin_fmaf(d[i][e], x[i][e], dw[i][e]);
-        db[i][e] += d[i][e];
+        x[i][e] = (x[i][e] - mu) * rs;
+        const float dd = cols.mine(i, e) && live ? d[i][e] : 0.0f;
+        dw[i][e] = __builtin_fmaf(dd, x[i][e], dw[i][e]);
+        db[i][e] += dd;
         d[i][e] *= w[i][e];
-        s1 += d[i][e];
-        s2 = __builtin_fmaf(d[i][e], x[i][e], s2);
+        const float aa = FULL ? d[i][e] : cols.mine(i, e) ? d[i][e] : 0.0f;
+        s1 += aa;
+        s2 = __builtin_fmaf(aa, x[i][e], s2);
       }
-    const float m1 = row_sum<LANES>(s1, red, turn) * inv, m2 = row_sum<LANES>(s2, red, turn) * inv;
+    }
+    if (base + step < a.rows) load(row + step);
+    const f32x2 m = row_sums<LANES, 2>(f32x2{s1, s2}, red, turn) * inv;
     if (!live || !a.dx) continue;
     char* op = norm_row<DT>(a.dx, a.dx_s, row, a.n1);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * LANES + lane) * V;
       float y[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = rstd * (d[i][e] - m1 - x[i][e] * m2);
-      store_vec<DT>(op + col * ES, a.width - col, a.vec, y);
+      for (int e = 0; e < V; ++e) y[e] = rs * (d[i][e] - m[0] - x[i][e] * m[1]);
+      cols.store(op, i, y);
     }
   }
   if (!a.part) return;
@@ -212,7 +289,6 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * LANES + lane) * V;
       float* src = side ? db[i] : dw[i];
       if constexpr (RW > 1) {
         __syncthreads();
@@ -224,13 +300,13 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
           for (int e = 0; e < V; ++e) {
             float s = 0;
             for (int r = 0; r < RW; ++r) s += sums[(r * LANES + lane) * V + e];
-            if (col + e < a.width) part[side * (int64_t)a.width + col + e] = s;
+            src[e] = s;
           }
-      } else {
+      }
+      if (threadIdx.x < LANES)
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (col + e < a.width) part[side * (int64_t)a.width + col + e] = src[e];
-      }
+          if (cols.mine(i, e)) part[side * (int64_t)a.width + cols.col[i] + e] = src[e];
     }
 }
 
@@ -243,6 +319,7 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
   if (!out) return;
   float s = 0;
   if (col < a.width)
+#pragma unroll 8
     for (int r = g; r < a.groups; r += 32) s += a.part[((int64_t)r * 2 + side) * a.width + col];
   t[g][c] = s;
   __syncthreads();
@@ -253,7 +330,7 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
   if (g == 0 && col < a.width) store_gate(out, a.w_dtype, col, t[0][c]);
 }
 
-// ---- rows wider than 512 threads hold: walked again for each sum (they stay in L2) ------
+// ---- rows wider than 512 threads hold (walked again for each sum; they stay in L2), or narrower than a vector ----
 
 __device__ inline float block_sum(float v, float* red) {
   v = sum4rows(sum16(v));
@@ -363,8 +440,12 @@ int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
 
 template <int DT, int LANES, int NV>
 void go(const NormArgs& a, bool bwd, int grid, hipStream_t st) {
-  if (bwd) bwd_kernel<DT, LANES, NV><<<grid, kThreads<LANES>, 0, st>>>(a);
-  else fwd_kernel<DT, LANES, NV><<<grid, kThreads<LANES>, 0, st>>>(a);
+  constexpr int T = kThreads<LANES>;
+  const bool full = a.width == LANES * NV * Vec<DT>::n;
+  if (bwd && full) bwd_kernel<DT, LANES, NV, true><<<grid, T, 0, st>>>(a);
+  else if (bwd) bwd_kernel<DT, LANES, NV, false><<<grid, T, 0, st>>>(a);
+  else if (full) fwd_kernel<DT, LANES, NV, true><<<grid, T, 0, st>>>(a);
+  else fwd_kernel<DT, LANES, NV, false><<<grid, T, 0, st>>>(a);
 }
 template <int DT, int LANES>
 void go(const NormArgs& a, bool bwd, int nv, int grid, hipStream_t st) {

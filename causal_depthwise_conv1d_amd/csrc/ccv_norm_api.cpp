@@ -37,8 +37,12 @@ int check_common(int64_t n0, int64_t n1, int64_t width, int x_dtype, int w_dtype
   if (x_dtype < 0 || x_dtype > 2 || w_dtype < 0 || w_dtype > 2) return CCV_E_DTYPE;
   if (!(eps >= 0.0f) || isinf(eps)) return CCV_E_UNSUPPORTED;
   int64_t rows;
-  return __builtin_mul_overflow(n0, n1, &rows) ? CCV_E_SHAPE : CCV_OK;
+  return __builtin_mul_overflow(n0, n1, &rows) || rows > INT32_MAX ? CCV_E_SHAPE : CCV_OK;
 }
+
+// Whether row (i, j) lies at (i n1 + j) s[1], as far as there are such rows; one group of rows, or
+// groups of one, then take the stride that counts.
+bool flat(const int64_t s[2], int64_t n0, int64_t n1) { return n0 <= 1 || n1 <= 1 || s[0] == n1 * s[1]; }
 
 int validate_fwd(const ccv_norm_fwd_args_t* p, NormArgs* a) {
   if (!p) return CCV_E_NULL;
@@ -66,7 +70,14 @@ int validate_fwd(const ccv_norm_fwd_args_t* p, NormArgs* a) {
     a->o_s[i] = p->out_stride[i];
   }
   a->rows = p->n0 * p->n1;
-  a->n1 = p->n1;
+  a->n1 = (uint32_t)p->n1;
+  if (flat(a->x_s, p->n0, p->n1) && flat(a->o_s, p->n0, p->n1)) {
+    a->n1 = 0;
+    if (p->n1 == 1) {
+      a->x_s[1] = a->x_s[0];
+      a->o_s[1] = a->o_s[0];
+    }
+  }
   a->width = (int32_t)p->width;
   a->x_dtype = p->x_dtype;
   a->w_dtype = p->w_dtype;
@@ -119,7 +130,15 @@ int validate_bwd(const ccv_norm_bwd_args_t* p, NormArgs* a, int64_t* bytes, bool
     a->dx_s[i] = p->dx_stride[i];
   }
   a->rows = rows;
-  a->n1 = p->n1 > 0 ? p->n1 : 1;
+  a->n1 = p->n1 > 0 ? (uint32_t)p->n1 : 1;
+  if (flat(a->x_s, p->n0, p->n1) && flat(a->do_s, p->n0, p->n1) && (!p->dx || flat(a->dx_s, p->n0, p->n1))) {
+    a->n1 = 0;
+    if (p->n1 == 1) {
+      a->x_s[1] = a->x_s[0];
+      a->do_s[1] = a->do_s[0];
+      a->dx_s[1] = a->dx_s[0];
+    }
+  }
   a->width = (int32_t)p->width;
   a->x_dtype = p->x_dtype;
   a->w_dtype = p->w_dtype;

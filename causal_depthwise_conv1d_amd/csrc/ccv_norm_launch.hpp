@@ -7,26 +7,28 @@
 namespace ccv {
 
 // Rows are numbered r = i * n1 + j, row (i, j) of x starting at i * s[0] + j * s[1]
-// elements; elements of a row are unit-stride.
+// elements (n1 = 0: row r at r * s[1], in every view); elements of a row are unit-stride.
 struct NormArgs {
   const void *x, *w, *b, *dout;
   void *out, *dx, *dw, *db;
   int64_t x_s[2], o_s[2], do_s[2], dx_s[2];
   float *mean, *rstd;                 // [rows]; written by the forward when wanted, read by the backward
-  int64_t rows, n1;
+  int64_t rows;
+  uint32_t n1;
   int32_t width, x_dtype, w_dtype;
-  int32_t vec, vec_w;                 // rows / weights may move as whole 16-byte vectors
+  int32_t vec, vec_w;                 // lanes 0: rows / weights may move as whole 16-byte vectors
   float eps;
   float* part;                        // backward: [groups][2][width] partial sums of dw, db
   int32_t groups;                     // workgroups of the backward's first kernel
 };
 
 // How a call is laid out: `lanes` threads a row, each holding `nv` 16-byte vectors of it;
-// lanes 0: rows too wide for that, walked in pieces.
+// lanes 0: rows too wide for that or narrower than a vector, walked in pieces.
 struct NormShape { int32_t lanes, nv; };
 
 inline NormShape norm_shape(int64_t width, int elt) {
   const int64_t v = 16 / elt;
+  if (width < v) return {0, 0};
   for (int32_t lanes : {16, 64, 256, 512})
     for (int32_t nv : {1, 2, 4})
       if (width <= lanes * nv * v) return {lanes, nv};

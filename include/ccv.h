@@ -475,7 +475,7 @@ int ccv_delta_update(const ccv_delta_update_args_t* args, void* hip_stream);
 
 /* ---- layer norm -------------------------------------------------------------------------
  *
- * Over the last dimension of x [n0, n1, width], row (i, j) at i s[0] + j s[1] elements:
+ * Over the last dimension of x [n0, n1, width] (n0 n1 below 2^31), row (i, j) at i s[0] + j s[1] elements:
  *
  *   mean = sum x / width;  rstd = (sum (x - mean)^2 / width + eps)^-1/2;  n = (x - mean) rstd
  *   out  = n weight + bias
