@@ -291,10 +291,15 @@ def test_reference_tables():
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-def test_rounded_reference_is_within_the_limits(dtype):
-    """The 64-bit results, rounded once to the type, pass the limits that the kernels are held to."""
-    q, k, v, g, beta, h0 = ref.delta_inputs(2, 70, 1, 2, 64, 32, dtype, seed=1)
-    out, _ = ref.delta_reference(q, k, v, g, beta, None, None, h0)
-    ref.assert_near("out", out.to(ref.DT[dtype]), out)
+@pytest.mark.parametrize("L", [1, 2, 70])
+def test_rounded_reference_is_within_the_limits(dtype, L):
+    """The 64-bit results, rounded once to the type, pass the limits that the kernels are held to,
+    whatever the number of elements; results one spacing off do not."""
+    q, k, v, g, beta, h0 = ref.delta_inputs(2, L, 1, 2, 64, 32, dtype, seed=L)
+    want = ref.delta_gradients(q, k, v, g, beta, v, None, None, h0)
+    for name in ("out", "dq", "dk", "dv", "dg", "dbeta"):
+        ref.assert_near(name, want[name].to(ref.DT[dtype]), want[name])
     with pytest.raises(AssertionError):
-        ref.assert_near("out", (out * (1 + 2.0 ** -7)).to(ref.DT[dtype]), out)
+        ref.assert_near("out", (want["out"] * (1 + 2.0 ** -7)).to(ref.DT[dtype]), want["out"])
+    tiny = torch.linspace(-1e-5, 1e-5, 999, dtype=torch.float64)
+    assert bool(((tiny.to(ref.DT[dtype]).double() - tiny).abs() <= ref.half_spacing(ref.DT[dtype], tiny)).all())
