@@ -149,13 +149,16 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   groups = round_up(groups, 8);
   if (groups * (a->Dvp / 16) > INT32_MAX) return CCV_E_SHAPE;
   a->nchunks = (int32_t)nch;
-  *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
+  const bool wide = z.x_dtype != CCV_F32;
+  a->waves = wide && !bwd && groups * (a->Dvp / 16) >= 1024;
+  *nt = !wide || a->waves || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
   a->slices = a->Dvp / (16 * *nt);
 
   Pieces w{static_cast<char*>(ws), 0, false};
   if (packed) {
     w.take(&a->table, nch, 4);
     w.take(&a->cstart, a->nseq + 2, 2);
+    w.take(&a->order, a->nseq + 1, 1);
   }
   w.take(&a->W, heads, kDeltaMatrix);
   w.take(&a->P, heads, kDeltaMatrix);

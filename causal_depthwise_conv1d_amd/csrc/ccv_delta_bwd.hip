@@ -31,7 +31,7 @@ constexpr int LDT = 72;
 // by lane, so it takes one 16-byte LDS access a tile and needs no other order than the
 // three barriers.
 template <int DT, int DKP, int NT>
-__global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
+__global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // dS by columns
@@ -42,9 +42,9 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
   __shared__ f32x4 Pd[NT][4][64];          // scale P^T dO; then del (K dS'), from the lane that read it
   __shared__ f32x4 Ud[MT][NT][4][64];      // Q^T (scale gam dO); then Y in its first tile, likewise
-  const uint32_t hs = blockIdx.x % heads_pad, slice = blockIdx.x / heads_pad;
+  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
   if (hs >= heads) return;
-  const int seq = hs / a.Hv, h = hs - seq * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
   const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // steps of no sequence have no gradient
@@ -643,8 +643,9 @@ __global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) 
 template <int DT, int DKP, int NT>
 void launch_rev(const DeltaArgs& a, hipStream_t st) {
   const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
-  const dim3 grid(pad * ((a.Dvp + 16 * NT - 1) / (16 * NT)));
-  reverse_kernel<DT, DKP, NT><<<grid, 512, 0, st>>>(a, heads, pad);
+  const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
+  const dim3 grid(pad * slices);
+  reverse_kernel<DT, DKP, NT><<<grid, 512, 0, st>>>(a, heads, slices);
 }
 template <int DT>
 void launch_rev(const DeltaArgs& a, int nt, hipStream_t st) {

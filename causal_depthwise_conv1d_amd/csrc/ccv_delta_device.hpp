@@ -344,6 +344,9 @@ __device__ inline Sequence sequence_at(const DeltaArgs& a, int s) {
   return q;
 }
 
+// The i-th sequence that a pass over the chunks takes.
+__device__ inline int in_order(const DeltaArgs& a, int i) { return a.packed ? __builtin_amdgcn_readfirstlane(a.order[i]) : i; }
+
 template <int DT>
 __device__ inline const char* row_ptr(const void* base, const int64_t* s, int row, int64_t t, int h) {
   return static_cast<const char*>(base) + (row * s[0] + t * s[1] + h * s[2]) * (DT == CCV_DT_F32 ? 4 : 2);
@@ -458,6 +461,120 @@ struct RowTile {
 // order in which a wave's lanes hold it as fragments, so that they load it in a row.
 __device__ inline int fragment_at(int m, int k) {
   return (((m >> 4) * 2 + (k >> 5)) * 64 + ((k >> 3) & 3) * 16 + (m & 15)) * 8;
+}
+
+// ---- products that stay in a wave's registers ------------------------------------------------
+//
+// A wave that holds 16 columns of a product to the full height can use it as the next product's
+// right-hand side without an exchange: the accumulator's lane (g4, r) holds rows 4 g4 + e of
+// column r, the right-hand side's wants rows 8 g4 .. 8 g4 + 7 of 32.  So the left-hand side's rows
+// are taken in another order: row 16 (2 s + o) + 4 q + e of the product is row 32 s + 8 q + 4 o + e of
+// the matrix, and the tiles 2 s and 2 s + 1 joined are the right-hand side's fragment s.
+__host__ __device__ constexpr int joined(int t) {      // matrix row t's place in that order
+  return (t & 32) | ((t & 4) << 2) | ((t >> 1) & 12) | (t & 3);
+}
+__device__ inline f32x8 join(f32x4 a, f32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// A 16-bit input is one operand as it is stored; what it meets is fp32, in planes of the same type.
+// In fp16 two planes keep 22 bits of an element, and 2^-39 of its column's largest: a column is scaled by a
+// power of two that brings its largest value to 2^14 .. 2^15.
+template <int DT> struct Cut { static constexpr int n = DT == CCV_DT_F16 ? 2 : 3; u32x4 p[n]; };
+
+template <int DT>
+__device__ inline f32x4 mfma16(u32x4 x, u32x4 y, f32x4 acc) {
+  if constexpr (DT == CCV_DT_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc, 0, 0, 0);
+}
+// The exponent that a column's values are taken relative to (0 in bf16, whose range is fp32's).
+template <int DT, int N>
+__device__ inline int column_exponent(const f32x4 (&x)[N]) {
+  if constexpr (DT != CCV_DT_F16) return 0;
+  float m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(x[i][e]));
+  m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+  m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+  return __builtin_amdgcn_frexp_expf(m) - 15;
+}
+template <int DT>
+__device__ inline float scaled(float x, int exponent) { return DT == CCV_DT_F16 ? __builtin_ldexpf(x, exponent) : x; }
+template <int DT>
+__device__ inline f32x4 scaled(f32x4 x, int exponent) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = scaled<DT>(x[e], exponent);
+  return x;
+}
+template <int DT>
+__device__ inline Cut<DT> cut(f32x8 x, int exponent) {
+  Cut<DT> c;
+  if constexpr (DT == CCV_DT_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f32x2 y = {__builtin_ldexpf(x[2 * i], -exponent), __builtin_ldexpf(x[2 * i + 1], -exponent)};
+      const f16x2 hi = __builtin_convertvector(y, f16x2);
+      y = {y[0] - (float)hi[0], y[1] - (float)hi[1]};
+      c.p[0][i] = __builtin_bit_cast(uint32_t, hi);
+      c.p[1][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, f16x2));
+    }
+  } else {
+    const Frag<3> f = split8<3>(x);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c.p[i] = __builtin_bit_cast(u32x4, f.p[i]);
+  }
+  return c;
+}
+
+// The value, computed anew where it is used: kept out of the loop's registers.
+__device__ inline uint32_t anew(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A chunk's 64 rows of 16-bit elements into LDS as they are, shared between NW waves; JOINED: in the
+// order above.
+template <int DKP, int LD, int NW, bool JOINED>
+struct RowCopy {
+  static constexpr int kLanes = DKP / 8, kEach = 64 / kLanes, kLoads = kLanes / NW;
+  u32x4 raw[kLoads];
+  uint32_t off, next;
+  int at;
+  __device__ inline RowCopy(int w, int l, uint32_t stride, int width) {
+    const int row = w * (64 / NW) + l / kLanes, c = l % kLanes * 8;
+    off = c < width ? row * stride + c * 2 : kNowhere;
+    next = c < width ? kEach * stride : 0;
+    at = (JOINED ? joined(row) : row) * LD + c;
+  }
+  __device__ inline void load(__amdgpu_buffer_rsrc_t b) {
+    uint32_t o = anew(off);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i, o += next) raw[i] = buf16(b, o);
+  }
+  __device__ inline void store(uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)      // joined() moves bits, and these of the row lie apart from the lane's and the wave's
+      *reinterpret_cast<u32x4*>(lds + at + (JOINED ? joined(i * kEach) : i * kEach) * LD) = raw[i];
+  }
+};
+
+// Matrix instructions and memory accesses stay on their side of this line.  A wave alone on its SIMD has
+// nothing to cover a load with but its own matrix instructions; left alone, the compiler moves a load down to
+// where its value is used, which saves registers that such a wave has.
+__device__ inline void keep_order() { __builtin_amdgcn_sched_barrier(0x0002 | 0x0004); }
+
+// The transposed fragment of a joined LDS array: lane (g4, r) gets steps 32 s + 8 g4 .. + 7 of column
+// 32 c + 8 (r / 4) + 4 o + r % 4 (columns in the joined order too).
+template <int LD>
+__device__ inline u32x4 get_joined_t(const uint16_t* lds, int s, int c, int o, int lane) {
+  const int r = lane & 15;
+  const uint16_t* at = lds + (32 * s + 4 * (lane >> 4) + (r >> 2)) * LD + 32 * c + 4 * o + 8 * (r & 3);
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 16 * LD));
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 }  // namespace ccv

@@ -39,6 +39,7 @@ struct DeltaArgs {
   // workspace (element counts below), ch = chunk * Hv + head
   int32_t* table;                               // packed: [nchunks] x (sequence, first step, steps, -)
   int32_t* cstart;                              // packed: [nseq + 2] first chunk of each sequence
+  int32_t* order;                               // packed: [nseq + 1] the sequences, longest first
   uint16_t* W;                                  // [ch][3][64 x 64, fragment_at]: (1 + A)^-1 as bf16 planes
   uint16_t* P;                                  // likewise, kDeltaMatrix a chunk and head; the backward holds it transposed
   uint16_t* WT;                                 // backward: W transposed
@@ -50,6 +51,7 @@ struct DeltaArgs {
   float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
   float* pairs;                                 // backward: [ch][kDeltaPairs] dG by pairs of steps; <S, dS'>
   int32_t Dkp, slices;
+  int32_t waves;                                // the forward pass runs on whole columns a wave, W's rows in joined() order
 };
 
 // Single steps against states in a cache.

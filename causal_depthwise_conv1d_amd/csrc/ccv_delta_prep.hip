@@ -73,8 +73,29 @@ __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
     csum += s1;
   }
   if (tid == 0) a.cstart[0] = 0;
+  mx[tid] = 0;
   __threadfence_block();
   __syncthreads();
+  // the order in which the passes over the chunks take the sequences: longest first, so that no long one
+  // starts when the others are done (which of two of one length comes first changes no result)
+  const auto bucket = [&](int s) {
+    const int n = a.cstart[s + 1] - a.cstart[s];
+    return n < 1023 ? 1023 - n : 0;
+  };
+  for (int s = tid; s < a.nseq; s += 1024) atomicAdd(&mx[bucket(s)], 1);
+  __syncthreads();
+  sm[tid] = mx[tid];
+  __syncthreads();
+  for (int d = 1; d < 1024; d <<= 1) {
+    const int o = tid >= d ? sm[tid - d] : 0;
+    __syncthreads();
+    sm[tid] += o;
+    __syncthreads();
+  }
+  sm[tid] -= mx[tid];
+  __syncthreads();
+  for (int s = tid; s < a.nseq; s += 1024) a.order[atomicAdd(&sm[bucket(s)], 1)] = s;
+  if (tid == 0) a.order[a.nseq] = a.nseq;
   for (int c = tid; c < a.nchunks; c += 1024) {
     int s = a.nseq, t0 = 0, len = 0;
     if (c < csum) {
@@ -244,7 +265,7 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   }
   __syncthreads();
   // out as planes: a thread takes 8 consecutive elements of two rows (columns when transposed)
-  const auto write = [&](uint16_t* out, const float (*m)[LDA], auto nplanes, bool transposed) {
+  const auto write = [&](uint16_t* out, const float (*m)[LDA], auto nplanes, bool transposed, bool join = false) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = i * 256 + tid, ro = transposed ? e & 63 : e >> 3, co = 8 * (transposed ? e >> 6 : e & 7);
@@ -254,10 +275,10 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
       const auto f = split8<nplanes.value>(x);
 #pragma unroll
       for (int p = 0; p < nplanes.value; ++p)
-        *reinterpret_cast<bf16x8*>(out + (int64_t)ch * kDeltaMatrix + p * 4096 + fragment_at(ro, co)) = f.p[p];
+        *reinterpret_cast<bf16x8*>(out + (int64_t)ch * kDeltaMatrix + p * 4096 + fragment_at(join ? joined(ro) : ro, co)) = f.p[p];
     }
   };
-  write(a.W, Wl, std::integral_constant<int, 3>(), false);
+  write(a.W, Wl, std::integral_constant<int, 3>(), false, a.waves);
   if constexpr (BWD) {
     write(a.WT, Wl, std::integral_constant<int, 3>(), true);
     write(a.P, Pl, std::integral_constant<int, 3>(), true);

@@ -19,7 +19,7 @@ namespace {
 constexpr int LDT = 72;      // row stride of an LDS array of 64 steps
 
 template <int DT, int DKP, int NT, bool BWD>
-__global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t heads_pad) {
+__global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int OO = OutOrder<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // S by columns
@@ -34,9 +34,9 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
   auto& Ql = qn.q;
   auto& Np = qn.n.p;
   auto& Nd = qn.n.d;
-  const uint32_t hs = blockIdx.x % heads_pad, slice = blockIdx.x / heads_pad;
+  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
   if (hs >= heads) return;
-  const int seq = hs / a.Hv, h = hs - seq * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
   const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // the steps of a packed row that belong to no sequence
@@ -324,18 +324,317 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
   }
 }
 
+// ---- 16-bit inputs: 16 columns a wave --------------------------------------------------------
+//
+// A wave holds 16 columns of the state to their full height, so that all of the chain above stays
+// in its registers (see joined()): K S is R's rows, R the right-hand side of W R, N that of
+// K^T (del N) and the left-hand side of P N.  What the waves share are K and Q, which are needed
+// by rows and, K, by columns: a chunk's rows lie in LDS, two chunks in turn, one barrier a chunk.
+constexpr int NW = 4;        // waves that share them
+
+template <int DT, int DKP, bool BWD>
+__global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
+  constexpr int KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
+  __shared__ uint16_t Kl[2][64][LDK], Ql[2][64][LDK];
+  __shared__ float Gl[2][3][64];            // gam, del, beta
+  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
+  if (hs >= heads) return;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk);
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
+  if (seq >= a.nseq) {                     // the steps of a packed row that belong to no sequence
+    if constexpr (!BWD) {
+      const int32_t* begin = a.cstart + (a.nseq + 2);
+      for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 64 * NW) {
+        const int64_t t = i / CB;
+        const int d = (int)slice * CB + (int)(i - t * CB);
+        if (d < a.Dv) store1<DT>(row_ptr<DT>(a.out, a.o_s, 0, t, h) + d * 2, 0.0f);
+      }
+    }
+    return;
+  }
+  const int ct = slice * NW + w, dv0 = 16 * ct, dv = dv0 + r;      // this wave's columns, and the lane's
+  const Sequence sq = sequence_at(a, seq);
+  const int c0 = sq.first, c1 = sq.end;
+  const int64_t ch0 = (int64_t)c0 * a.Hv + h;
+
+  f32x4 S[2 * KS];                         // tile 2 s + o: keys 32 s + 8 g4 + 4 o + e
+#pragma unroll
+  for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int dk = 16 * (m & ~1) + 8 * g4 + 4 * (m & 1) + e;
+      S[m][e] = a.h0 && dk < a.Dk && dv < a.Dv ? a.h0[seq * a.h0_s[0] + h * a.h0_s[1] + dk * a.h0_s[2] + dv] : 0.0f;
+    }
+  Rows<DT> K(a.k, a.k_s, sq, hk, (a.Dk + 7) & ~7, c0), Q(a.q, a.q_s, sq, hk, (a.Dk + 7) & ~7, c0), V(a.v, a.v_s, sq, h, a.Dv, c0);
+  Rows<DT> O(BWD ? a.dout : a.out, BWD ? a.do_s : a.o_s, sq, h, BWD ? (a.Dv + 7) & ~7 : a.Dv, c0);
+  Piece<uint16_t> W(a.W, kDeltaMatrix, a.Hv, ch0), P(a.P, kDeltaMatrix, a.Hv, ch0);
+  Piece<float> D(a.dec, kDeltaDec, a.Hv, ch0);
+  Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0);
+  const float scale = a.scale;
+  const bool vec = a.vec_o;
+  const int dleft = a.Dv - dv0 - 4 * g4;
+  const uint32_t oo = dleft > 0 ? r * O.stride + (dv0 + 4 * g4) * 2 : kNowhere, onext = dleft > 0 ? 16 * O.stride : 0;
+  const uint32_t ov = dv < a.Dv ? 8 * g4 * V.stride + dv * 2 : kNowhere, vnext = dv < a.Dv ? V.stride : 0;
+  // tiles as the workspace has them: row 32 s + 8 g4 + 4 o + e is element e of lane group 2 (g4 % 2) + o of tile 2 s + g4 / 2
+  const uint32_t to = ((g4 >> 1) * 64 + 2 * (g4 & 1) * 16 + r) * 16;
+  const uint32_t os = ct * (DKP / 16) * 1024 + to, on = ct * 4096 + to;
+
+  RowCopy<DKP, LDK, NW, true> kt(w, l, K.stride, a.Dk);
+  RowCopy<DKP, LDK, NW, false> qt(w, l, Q.stride, a.Dk);
+  Frag<3> xW[6];
+  Frag<2> xP[6];
+  uint16_t xv[4][4];
+  Raw4<DT> xd[4];
+  float gates;                             // one of a chunk's gam, del, beta, on the way to LDS
+  int64_t left = sq.len;                   // steps from the chunk at hand on
+  const auto ahead = [&](int chunks) {     // steps of a chunk further on, 0 past the last
+    const int64_t n = left - chunks * kDeltaChunk;
+    return n <= 0 ? 0 : n < kDeltaChunk ? (int)n : kDeltaChunk;
+  };
+  const auto load_rows = [&](int n) {
+    kt.load(K.rows(n));
+    qt.load(Q.rows(n));
+    gates = buf1<CCV_DT_F32>(D.piece(n > 0), tid < 192 ? tid * 4 : kNowhere);
+    K.at += K.step;
+    Q.at += Q.step;
+    D.at += D.step;
+  };
+  const auto store_rows = [&](int b) {
+    kt.store(&Kl[b][0][0]);
+    qt.store(&Ql[b][0][0]);
+    if (tid < 192) Gl[b][0][tid] = gates;
+  };
+  const auto load_V = [&](int n) {
+    const __amdgpu_buffer_rsrc_t b = V.rows(n);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      uint32_t o = anew(ov) + (32 * (it >> 1) + 4 * (it & 1)) * vnext;
+#pragma unroll
+      for (int e = 0; e < 4; ++e, o += vnext) xv[it][e] = buf_raw<DT>(b, o);
+    }
+    V.at += V.step;
+  };
+  const auto load_W = [&](int n) {
+    const __amdgpu_buffer_rsrc_t b = W.piece(n > 0);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) xW[i] = buf_planes<3>(b, ((i < 4 ? 2 * i : 2 * i - 3) * 64 + l) * 16, 8192);
+    W.at += W.step;
+  };
+  const auto load_P = [&](int n) {
+    if constexpr (BWD) {
+      const __amdgpu_buffer_rsrc_t b = O.rows(n);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) xd[t] = buf_raw4<DT>(b, anew(oo) + t * onext);
+      O.at += O.step;
+    } else {
+      const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
+#pragma unroll
+      for (int i = 0; i < 6; ++i) xP[i] = buf_planes<2>(b, ((i < 4 ? 2 * i : 2 * i - 3) * 64 + l) * 16, 8192);
+      P.at += P.step;
+    }
+  };
+  if (c0 < c1) {
+    load_rows(ahead(0));
+    store_rows(0);
+    load_rows(ahead(1));                   // in the loop's order: the waits of both have to agree
+    load_V(ahead(0));
+  }
+  for (int c = c0; c < c1; ++c) {
+    const int b = (c - c0) & 1, n = ahead(0), nn = ahead(1);
+    const uint16_t *Kb = &Kl[b][0][0], *Qb = &Ql[b][0][0];
+    const auto gate = [&](int which, int it) {
+      return *reinterpret_cast<const f32x4*>(&Gl[b][which][32 * (it >> 1) + 4 * (it & 1) + 8 * g4]);
+    };
+    lds_barrier();
+    // K S, and (Q S)^T; the next 32 keys' fragments are read before these are multiplied
+    f32x4 hi[4] = {}, lo[4] = {}, qs[4] = {};
+    const int es = column_exponent<DT>(S);
+    u32x4 kf[1][4], qf[1][4];
+    const auto read_rows = [&](int s) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        kf[0][t] = *reinterpret_cast<const u32x4*>(Kb + (16 * t + r) * LDK + 32 * s + 8 * g4);
+        qf[0][t] = *reinterpret_cast<const u32x4*>(Qb + (16 * t + r) * LDK + 32 * s + 8 * g4);
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      read_rows(s);
+      
+      const Cut<DT> x = cut<DT>(join(S[2 * s], S[2 * s + 1]), es);
+#pragma unroll
+      for (int p = PS - 1; p > 0; --p)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          lo[t] = mfma16<DT>(kf[0][t], x.p[p], lo[t]);
+          if (BWD || p < 2) qs[t] = mfma16<DT>(x.p[p], qf[0][t], qs[t]);
+        }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        hi[t] = mfma16<DT>(kf[0][t], x.p[0], hi[t]);
+        qs[t] = mfma16<DT>(x.p[0], qf[0][t], qs[t]);
+      }
+      
+    }
+    load_W(n);
+    
+    store_rows(b ^ 1);                     // its readers were done at the barrier
+    load_rows(ahead(2));
+    
+    if constexpr (BWD) {
+      const __amdgpu_buffer_rsrc_t sb = So.piece(true);
+#pragma unroll
+      for (int m = 0; m < 2 * KS; ++m) buf_store_f4(sb, os + (m >> 1) * 2048 + (m & 1) * 256, S[m]);
+      So.at += So.step;
+    }
+    // beta R
+    Frag<3> rf[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 R[2];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int it = 2 * s + o;
+        const f32x4 x = scaled<DT>(hi[it] + lo[it], es), gam = gate(0, it), beta = gate(2, it);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) R[o][e] = __builtin_fmaf(-gam[e], x[e], widen<DT>(xv[it][e])) * beta[e];
+      }
+      rf[s] = split8<3>(join(R[0], R[1]));
+    }
+    load_V(nn);
+    
+    u32x4 tf[1][2][2];
+    const auto read_columns = [&](int c) {
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) tf[0][o][s] = get_joined_t<LDK>(Kb, s, c, o, l);
+    };
+    // N = W (beta R); W is lower triangular
+    f32x4 N[4] = {};
+#pragma unroll
+    for (int q = 2; q >= 0; --q)
+#pragma unroll
+      for (int i = 0; i <= q; ++i)
+#pragma unroll
+        for (int x = 0; x < 6; ++x) {        // row tiles 0 1 2 3 2 3, steps 0 0 0 0 32 32 ..
+          const int it = x < 4 ? x : x - 2, s = x / 4;
+          N[it] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xW[x].p[i], rf[s].p[q - i], N[it], 0, 0, 0);
+        }
+    load_P(n);
+    
+    if constexpr (BWD) {
+      const __amdgpu_buffer_rsrc_t nb = No.piece(true);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) buf_store_f4(nb, on + (it >> 1) * 2048 + (it & 1) * 256, N[it]);
+      No.at += No.step;
+    }
+    // the state at the chunk's end
+    {
+      f32x4 y[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) y[it] = N[it] * gate(1, it);
+      const int ey = column_exponent<DT>(y);
+      const float last = Gl[b][0][63];
+      Cut<DT> yf[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) yf[s] = cut<DT>(join(y[2 * s], y[2 * s + 1]), ey);
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        read_columns(c);
+        
+        f32x4 t[2] = {};
+#pragma unroll
+        for (int p = PS - 1; p >= 0; --p)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) t[o] = mfma16<DT>(tf[0][o][s], yf[s].p[p], t[o]);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          t[o] = scaled<DT>(t[o], ey);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[2 * c + o][e] = __builtin_fmaf(S[2 * c + o][e], last, t[o][e]);
+        }
+        
+      }
+    }
+    int er[4] = {};                        // the rows of (Q S)^T are columns of S
+    if constexpr (DT == CCV_DT_F16) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) er[e] = __shfl(es, 4 * g4 + e);
+    }
+    if constexpr (BWD) {
+      // scale gam dO . (Q S): the part of dG that comes by the state
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 d = widen4<DT>(xd[t]);
+        float dot = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], scaled<DT>(qs[t][e], er[e]), dot);
+        dot = sum4rows(dot) * Gl[b][0][16 * t + r] * scale;
+        if (g4 == 0 && ct < a.slices) a.part[(((int64_t)c * a.Hv + h) * a.slices + ct) * kDeltaPart + 16 * t + r] = dot;
+      }
+    } else {
+      // the outputs: step 16 t + r, four consecutive values a lane
+      const __amdgpu_buffer_rsrc_t ob = O.rows(n);
+      Frag<2> nf[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) nf[s] = split8<2>(join(N[2 * s], N[2 * s + 1]));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float gam = Gl[b][0][16 * t + r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qs[t][e] = scaled<DT>(qs[t][e], er[e]) * gam;
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q)            // planes 0 1, 1 0, 0 0
+#pragma unroll
+        for (int x = 0; x < 6; ++x) {
+          const int t = x < 4 ? x : x - 2, s = x / 4;
+          qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[s].p[q == 1], xP[x].p[q == 0], qs[t], 0, 0, 0);
+        }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) buf_store4<DT>(ob, anew(oo) + t * onext, qs[t] * scale, dleft, vec);
+      O.at += O.step;
+    }
+    left -= kDeltaChunk;
+  }
+  if (a.ht) {
+#pragma unroll
+    for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int dk = 16 * (m & ~1) + 8 * g4 + 4 * (m & 1) + e;
+        if (dk < a.Dk && dv < a.Dv) a.ht[seq * a.ht_s[0] + h * a.ht_s[1] + dk * a.ht_s[2] + dv] = S[m][e];
+      }
+  }
+}
+
+template <int DT, int DKP>
+void launch_waves(const DeltaArgs& a, bool bwd, hipStream_t st) {
+  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t slices = (a.Dvp + 16 * NW - 1) / (16 * NW);
+  const dim3 grid(pad * slices);
+  if (bwd) wave_kernel<DT, DKP, true><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
+  else wave_kernel<DT, DKP, false><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
+}
 template <int DT, int DKP, int NT>
 void launch(const DeltaArgs& a, bool bwd, hipStream_t st) {
   const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv;
   // slices of one head lie 8 k workgroups apart: on one XCD, whose L2 then holds the
   // chunk's K, Q, W and P once for all of them
   const uint32_t pad = (heads + 7) / 8 * 8;
-  const dim3 grid(pad * ((a.Dvp + 16 * NT - 1) / (16 * NT)));
-  if (bwd) scan_kernel<DT, DKP, NT, true><<<grid, 512, 0, st>>>(a, heads, pad);
-  else scan_kernel<DT, DKP, NT, false><<<grid, 512, 0, st>>>(a, heads, pad);
+  const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
+  const dim3 grid(pad * slices);
+  if (bwd) scan_kernel<DT, DKP, NT, true><<<grid, 512, 0, st>>>(a, heads, slices);
+  else scan_kernel<DT, DKP, NT, false><<<grid, 512, 0, st>>>(a, heads, slices);
 }
 template <int DT>
 void launch(const DeltaArgs& a, bool bwd, int nt, hipStream_t st) {
+  if constexpr (DT != CCV_DT_F32) {
+    if (a.waves) return a.Dkp == 64 ? launch_waves<DT, 64>(a, bwd, st) : launch_waves<DT, 128>(a, bwd, st);
+  }
   if (a.Dkp == 64) {
     if (nt == 1) launch<DT, 64, 1>(a, bwd, st);
     else launch<DT, 64, 2>(a, bwd, st);

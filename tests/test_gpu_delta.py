@@ -91,6 +91,62 @@ def test_many_heads_take_the_wider_slices(dtype):
     check_bwd(q, k, v, g, beta, h0, what="144 heads")
 
 
+# rows, key heads, value heads, widths: at least 1024 blocks of 16 values, where 16-bit inputs take whole
+# columns a wave
+WAVES = [(16, 4, 16, 64, 64), (16, 16, 16, 128, 50), (11, 4, 16, 72, 96), (64, 1, 8, 1, 17), (4, 16, 32, 128, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(WAVES)))
+@pytest.mark.parametrize("L", [1, 64, 130])
+def test_whole_columns(dtype, i, L):
+    B, Hk, Hv, Dk, Dv = WAVES[i]
+    q, k, v, g, beta, h0 = ref.delta_inputs(B, L, Hk, Hv, Dk, Dv, dtype, "f32", "bf16", seed=i)
+    check_fwd(q, k, v, g, beta, h0, what="columns")
+    check_bwd(q, k, v, g, beta, h0 if L > 1 else None, what="columns")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("few", [False, True])
+def test_columns_of_different_size(dtype, few):
+    """Values and states of 1e-5 to 3e4 side by side: each column keeps its own precision."""
+    B, H = (1, 2) if few else (16, 16)
+    q, k, v, g, beta, h0 = ref.delta_inputs(B, 100, H, H, 64, 64, dtype, seed=5)
+    size = 10.0 ** torch.linspace(-3 if dtype == "f16" else -5, 4, 64)
+    v, h0 = (v.float() * size).to(v.dtype), h0 * size
+    dout = torch.randn(v.shape, generator=torch.Generator().manual_seed(1)).to(v.dtype)
+    out, ht = ccv.gated_delta_rule_fwd(*gpu(q, k, v, g, beta), initial_state=h0.cuda(), return_final_state=True)
+    got = ccv.gated_delta_rule_bwd(*gpu(q, k, v, g, beta, dout), initial_state=h0.cuda(), return_dinitial_state=True)
+    want = ref.delta_gradients(q, k, v, g, beta, dout, None, None, h0)
+    for c in range(0, 64, 9):
+        ref.assert_near("out", out[..., c], want["out"][..., c], 1, f"column {c}")
+        ref.assert_near("final_state", ht[..., c], want["ht"][..., c], 1, f"column {c}")
+        ref.assert_near("dv", got[2][..., c], want["dv"][..., c], 2, f"column {c}")
+        ref.assert_near("dh0", got[5][..., c], want["dh0"][..., c], 2, f"column {c}")
+
+
+def test_nan_stays_in_its_column_of_values():
+    q, k, v, g, beta, h0 = ref.delta_inputs(16, 70, 16, 16, 64, 64, "f16", seed=6)
+    clean, _ = ccv.gated_delta_rule_fwd(*gpu(q, k, v, g, beta), initial_state=h0.cuda(), return_final_state=True)
+    v[3, 20, 5, 7], v[2, 20, 5, 8] = NAN, float("inf")
+    out, _ = ccv.gated_delta_rule_fwd(*gpu(q, k, v, g, beta), initial_state=h0.cuda(), return_final_state=True)
+    same = torch.ones(16, 70, 16, 64, dtype=torch.bool)
+    same[3, :, 5, 7] = same[2, :, 5, 8] = False
+    assert torch.equal(out.cpu()[same], clean.cpu()[same])
+    assert torch.isnan(out[3, 20:, 5, 7]).all() and not torch.isfinite(out[2, 20:, 5, 8]).any()
+
+
+def test_many_sequences_of_one_row():
+    """Packed rows of whole-column waves: 130 sequences, longest first whatever their order."""
+    gen = torch.Generator().manual_seed(3)
+    lengths = torch.randint(0, 40, (130,), generator=gen).tolist()
+    lengths[17], lengths[100] = 200, 129
+    for dtype in ("f16", "bf16"):
+        q, k, v, g, beta, h0 = ref.delta_inputs(1, sum(lengths), 1, 2, 64, 64, dtype, seed=4, seqs=130)
+        check_fwd(q, k, v, g, beta, h0, lengths, what="130 sequences")
+        check_bwd(q, k, v, g, beta, h0, lengths, what="130 sequences")
+
+
 PACKED = [[5, 0, 64, 1, 130], [0, 0, 7], [64, 64], [200], [0], [1] * 20, [65, 0]]
 
 
