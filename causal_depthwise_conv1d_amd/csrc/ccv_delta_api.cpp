@@ -149,10 +149,11 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   groups = round_up(groups, 8);
   if (groups * (a->Dvp / 16) > INT32_MAX) return CCV_E_SHAPE;
   a->nchunks = (int32_t)nch;
-  const bool wide = z.x_dtype != CCV_F32;
-  a->waves = wide && !bwd && groups * (a->Dvp / 16) >= 1024;
-  *nt = !wide || a->waves || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
+  a->waves = z.x_dtype != CCV_F32 && groups * (a->Dvp / 16) >= 1024;
+  a->waves_back = a->waves && z.x_dtype == CCV_F16;
+  *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
   a->slices = a->Dvp / (16 * *nt);
+  a->qslices = a->waves ? a->Dvp / 16 : a->slices;
 
   Pieces w{static_cast<char*>(ws), 0, false};
   if (packed) {
@@ -170,7 +171,8 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
     w.take(&a->N, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->Y, heads, 64 * (int64_t)a->Dvp);
     w.take(&a->pairs, heads, kDeltaPairs);
-    w.take(&a->part, heads, a->Dvp / 16 * kDeltaPart);
+    w.take(&a->part, heads, a->slices * kDeltaPart);
+    w.take(&a->qpart, heads, a->qslices * 64);
   }
   const int64_t steps = z.B * z.L, wk = z.Hk * round_up(z.Dk, 8), wv = z.Hv * round_up(z.Dv, 8);
   char* p[4] = {};

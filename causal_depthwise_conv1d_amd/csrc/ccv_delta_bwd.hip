@@ -346,13 +346,286 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       for (int e = 0; e < 4; ++e) {
         const float b = sum16(bs[e]), g = sum16(gs[e]), q = sum16(cs[e]);
         if (r == 0) {
-          part[64 + e] = b;
-          part[128 + e] = b - g;
-          part[192 + e] = q;
+          part[e] = b;
+          part[64 + e] = b - g;
+          part[128 + e] = q;
         }
       }
       lds_barrier();
     }
+  }
+}
+
+// The same for fp16 and many heads, as the forward's wave_kernel has it: 16 columns a wave, the chain
+//   K dS', P^T dO -> dN,  W^T dN = Y,  Q^T (scale gam dO) and K^T (gam beta Y) -> dS
+// in its registers, K and Q shared through LDS; both have their rows in the joined order.
+template <int DT, int DKP>
+__global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
+  constexpr int NW = kColumnWaves, NA = InPlanes<DT>::n, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
+  __shared__ uint16_t Kl[2][64][LDK], Ql[2][64][LDK];
+  __shared__ float Gl[2][3][64];           // gam, del, beta
+  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
+  if (hs >= heads) return;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk);
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
+  if (seq >= a.nseq) {                     // steps of no sequence have no gradient
+    const int32_t* begin = a.cstart + (a.nseq + 2);
+    for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 64 * NW) {
+      const int64_t t = i / CB;
+      const int d = (int)slice * CB + (int)(i - t * CB);
+      if (d < a.Dv) store1<DT>(row_ptr<DT>(a.dv, a.dv_s, 0, t, h) + d * 2, 0.0f);
+    }
+    return;
+  }
+  const int ct = slice * NW + w, dv = 16 * ct + r;
+  const Sequence sq = sequence_at(a, seq);
+  const int c0 = sq.first, c1 = sq.end;
+  const int64_t chl = (int64_t)(c1 - 1) * a.Hv + h;
+
+  f32x4 S[2 * KS];                         // dS': tile 2 s + o: keys 32 s + 8 g4 + 4 o + e
+#pragma unroll
+  for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int dk = 16 * (m & ~1) + 8 * g4 + 4 * (m & 1) + e;
+      S[m][e] = a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
+    }
+  Rows<DT> K(a.k, a.k_s, sq, hk, (a.Dk + 7) & ~7, c1 - 1), Q(a.q, a.q_s, sq, hk, (a.Dk + 7) & ~7, c1 - 1), V(a.v, a.v_s, sq, h, a.Dv, c1 - 1),
+      O(a.dout, a.do_s, sq, h, a.Dv, c1 - 1), dV(a.dv, a.dv_s, sq, h, a.Dv, c1 - 1);
+  Piece<uint16_t> W(a.WT, kDeltaMatrix, a.Hv, chl), P(a.P, kDeltaMatrix, a.Hv, chl);
+  Piece<float> D(a.dec, kDeltaDec, a.Hv, chl), So(a.dS, (int64_t)DKP * a.Dvp, a.Hv, chl);
+  Piece<float> Ni(a.N, 64 * (int64_t)a.Dvp, a.Hv, chl), Yo(a.Y, 64 * (int64_t)a.Dvp, a.Hv, chl),
+      Po(a.part, (int64_t)a.slices * kDeltaPart, a.Hv, chl);
+  const float scale = a.scale;
+  const bool in = dv < a.Dv;
+  const uint32_t ov = in ? 8 * g4 * V.stride + dv * 2 : kNowhere, vnext = V.stride;
+  const uint32_t oo = in ? 8 * g4 * O.stride + dv * 2 : kNowhere, onext = O.stride;
+  const uint32_t odv = in ? 8 * g4 * dV.stride + dv * 2 : kNowhere, dnext = dV.stride;
+  // tiles as the workspace has them: row 32 s + 8 g4 + 4 o + e is element e of lane group 2 (g4 % 2) + o of tile 2 s + g4 / 2
+  const uint32_t to = ((g4 >> 1) * 64 + 2 * (g4 & 1) * 16 + r) * 16;
+  const uint32_t os = ct * (DKP / 16) * 1024 + to, on = ct * 4096 + to;
+  const uint32_t op = r == 0 ? (ct * kDeltaPart + 8 * g4) * 4 : kNowhere;      // past the slices: out of bounds too
+
+  RowCopy<DKP, LDK, NW, true> kt(w, l, K.stride, a.Dk), qt(w, l, Q.stride, a.Dk);
+  float gates;
+  uint16_t xd[4][4];
+  const auto steps_of = [&](int c) {       // 0 before the first chunk
+    if (c < c0) return 0;
+    const int64_t left = sq.len - (int64_t)(c - c0) * kDeltaChunk;
+    return left < kDeltaChunk ? (int)left : kDeltaChunk;
+  };
+  const auto load_rows = [&](int n) {
+    kt.load(K.rows(n));
+    qt.load(Q.rows(n));
+    gates = buf1<CCV_DT_F32>(D.piece(n > 0), tid < 192 ? tid * 4 : kNowhere);
+    K.at -= K.step;
+    Q.at -= Q.step;
+    D.at -= D.step;
+  };
+  const auto store_rows = [&](int b) {
+    kt.store(&Kl[b][0][0]);
+    qt.store(&Ql[b][0][0]);
+    if (tid < 192) Gl[b][0][tid] = gates;
+  };
+  const auto load_dO = [&](int n) {
+    const __amdgpu_buffer_rsrc_t b = O.rows(n);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      uint32_t o = anew(oo) + (32 * (it >> 1) + 4 * (it & 1)) * onext;
+#pragma unroll
+      for (int e = 0; e < 4; ++e, o += onext) xd[it][e] = buf_raw<DT>(b, o);
+    }
+    O.at -= O.step;
+  };
+  // an upper triangular matrix in joined rows: row tiles 0 1 by steps 0 .., 0 1 2 3 by steps 32 ..
+  const auto load_upper = [&](Frag<3> (&x)[6], Piece<uint16_t>& m) {
+    const __amdgpu_buffer_rsrc_t b = m.piece(true);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = buf_planes<3>(b, ((i < 2 ? 2 * i : 2 * i - 3) * 64 + l) * 16, 8192);
+    m.at -= m.step;
+  };
+  if (c0 < c1) {
+    load_rows(steps_of(c1 - 1));
+    store_rows(0);
+    load_rows(steps_of(c1 - 2));           // in the loop's order: the waits of both have to agree
+    load_dO(steps_of(c1 - 1));
+  }
+  for (int c = c1 - 1; c >= c0; --c) {
+    const int b = (c1 - 1 - c) & 1, n = steps_of(c);
+    const uint16_t *Kb = &Kl[b][0][0], *Qb = &Ql[b][0][0];
+    const auto gate = [&](int which, int it) {
+      return *reinterpret_cast<const f32x4*>(&Gl[b][which][32 * (it >> 1) + 4 * (it & 1) + 8 * g4]);
+    };
+    lds_barrier();
+    // K dS'
+    f32x4 hi[4] = {}, lo[4] = {}, dN[4];
+    const int es = column_exponent<DT>(S);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const Cut<DT> x = cut<DT>(join(S[2 * s], S[2 * s + 1]), es);
+      u32x4 kf[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) kf[t] = *reinterpret_cast<const u32x4*>(Kb + (16 * t + r) * LDK + 32 * s + 8 * g4);
+#pragma unroll
+      for (int p = PS - 1; p > 0; --p)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) lo[t] = mfma16<DT>(kf[t], x.p[p], lo[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) hi[t] = mfma16<DT>(kf[t], x.p[0], hi[t]);
+      keep_order();
+    }
+    {
+      const __amdgpu_buffer_rsrc_t sb = So.piece(true);
+#pragma unroll
+      for (int m = 0; m < 2 * KS; ++m) buf_store_f4(sb, os + (m >> 1) * 2048 + (m & 1) * 256, S[m]);
+      So.at -= So.step;
+    }
+    f32x4 x[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) x[it] = scaled<DT>(hi[it] + lo[it], es) * gate(1, it);
+    Frag<3> xP[6], xW[6];
+    __builtin_amdgcn_sched_barrier(0);
+    load_upper(xP, P);
+    store_rows(b ^ 1);                     // its readers were done at the barrier
+    load_rows(steps_of(c - 2));
+    // P^T dO, and scale gam dO for the state
+    f32x4 pd[4] = {};
+    uint32_t two[4][2];                    // dO, two steps a dword
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) two[it][i] = xd[it][2 * i] | (uint32_t)xd[it][2 * i + 1] << 16;
+    const auto dO = [&](int it) {
+      return f32x4{widen<DT>((uint16_t)two[it][0]), widen<DT>((uint16_t)(two[it][0] >> 16)), widen<DT>((uint16_t)two[it][1]),
+                   widen<DT>((uint16_t)(two[it][1] >> 16))};
+    };
+    {
+      Frag<NA> of[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) of[s] = split8<NA>(join(dO(2 * s), dO(2 * s + 1)));
+#pragma unroll
+      for (int q = 2; q >= 0; --q)
+#pragma unroll
+        for (int j = 0; j < NA && j <= q; ++j)
+#pragma unroll
+          for (int x = 0; x < 6; ++x) {
+            const int it = x < 2 ? x : x - 2, s = x < 2 ? 0 : 1;
+            pd[it] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xP[x].p[q - j], of[s].p[j], pd[it], 0, 0, 0);
+          }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_upper(xW, W);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) dN[it] = pd[it] * scale + x[it];
+    // Y = W^T dN
+    f32x4 Y[4] = {};
+    {
+      Frag<3> df[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) df[s] = split8<3>(join(dN[2 * s], dN[2 * s + 1]));
+#pragma unroll
+      for (int q = 2; q >= 0; --q)
+#pragma unroll
+        for (int i = 0; i <= q; ++i)
+#pragma unroll
+          for (int x = 0; x < 6; ++x) {
+            const int it = x < 2 ? x : x - 2, s = x < 2 ? 0 : 1;
+            Y[it] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xW[x].p[i], df[s].p[q - i], Y[it], 0, 0, 0);
+          }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 xN[4];
+    uint16_t xv[4][4];
+    {
+      const __amdgpu_buffer_rsrc_t nb = Ni.piece(true), vb = V.rows(n);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        xN[it] = buf_f4(nb, on + (it >> 1) * 2048 + (it & 1) * 256);
+        uint32_t o = anew(ov) + (32 * (it >> 1) + 4 * (it & 1)) * vnext;
+#pragma unroll
+        for (int e = 0; e < 4; ++e, o += vnext) xv[it][e] = buf_raw<DT>(vb, o);
+      }
+      Ni.at -= Ni.step;
+      V.at -= V.step;
+    }
+    // gam63 dS' + Q^T (scale gam dO), then - K^T (gam beta Y)
+    const auto add_to_state = [&](const uint16_t* rows, const f32x4 (&y)[4], float last) {
+      const int ey = column_exponent<DT>(y);
+      Cut<DT> yf[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) yf[s] = cut<DT>(join(y[2 * s], y[2 * s + 1]), ey);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        f32x4 t[2] = {};
+        u32x4 f[2][2];
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) f[o][s] = get_joined_t<LDK>(rows, s, k, o, l);
+#pragma unroll
+        for (int p = PS - 1; p >= 0; --p)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) t[o] = mfma16<DT>(f[o][s], yf[s].p[p], t[o]);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          t[o] = scaled<DT>(t[o], ey);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[2 * k + o][e] = __builtin_fmaf(S[2 * k + o][e], last, t[o][e]);
+        }
+        keep_order();
+      }
+    };
+    keep_order();
+    {
+      f32x4 gd[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) gd[it] = dO(it) * gate(0, it) * scale;
+      add_to_state(Qb, gd, Gl[b][0][63]);
+    }
+    const __amdgpu_buffer_rsrc_t part = Po.piece(true);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      f32x4 q;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = sum16(x[it][e] * xN[it][e]);
+      buf_store_f4(part, op + (128 + 32 * (it >> 1) + 4 * (it & 1)) * 4, q);
+    }
+    {
+      const __amdgpu_buffer_rsrc_t yb = Yo.piece(true), vb = dV.rows(n);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const f32x4 dR = Y[it] * gate(2, it);
+        uint32_t o = anew(odv) + (32 * (it >> 1) + 4 * (it & 1)) * dnext;
+        f32x4 bs, bg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e, o += dnext) {
+          buf_store1<DT>(vb, o, dR[e]);
+          bs[e] = sum16(Y[it][e] * xN[it][e]);
+          bg[e] = bs[e] - sum16(dR[e] * widen<DT>(xv[it][e]));
+        }
+        buf_store_f4(yb, on + (it >> 1) * 2048 + (it & 1) * 256, Y[it]);
+        buf_store_f4(part, op + (32 * (it >> 1) + 4 * (it & 1)) * 4, bs);
+        buf_store_f4(part, op + (64 + 32 * (it >> 1) + 4 * (it & 1)) * 4, bg);
+        Y[it] = dR * -gate(0, it);
+      }
+      Yo.at -= Yo.step;
+      dV.at -= dV.step;
+      Po.at -= Po.step;
+    }
+    keep_order();
+    load_dO(steps_of(c - 1));
+    add_to_state(Kb, Y, 1.0f);
+  }
+  if (a.dh0) {
+#pragma unroll
+    for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int dk = 16 * (m & ~1) + 8 * g4 + 4 * (m & 1) + e;
+        if (dk < a.Dk && dv < a.Dv) a.dh0[seq * a.dh0_s[0] + h * a.dh0_s[1] + dk * a.dh0_s[2] + dv] = S[m][e];
+      }
   }
 }
 
@@ -614,10 +887,13 @@ __global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) 
     g = pairs[l];
 #pragma unroll 4
     for (int i = 0; i < a.slices; ++i) {
-      g += part[i * kDeltaPart + l] + part[i * kDeltaPart + 128 + l];
-      b += part[i * kDeltaPart + 64 + l];
-      cj += part[i * kDeltaPart + 192 + l];
+      b += part[i * kDeltaPart + l];
+      g += part[i * kDeltaPart + 64 + l];
+      cj += part[i * kDeltaPart + 128 + l];
     }
+    const float* by_state = a.qpart + ch * a.qslices * 64;
+#pragma unroll 4
+    for (int i = 0; i < a.qslices; ++i) g += by_state[i * 64 + l];
     if (l >= k.n - 1) cj = 0;      // the last step's decay to the end is 1, whatever its g
     float tot = cj;
 #pragma unroll
@@ -647,8 +923,17 @@ void launch_rev(const DeltaArgs& a, hipStream_t st) {
   const dim3 grid(pad * slices);
   reverse_kernel<DT, DKP, NT><<<grid, 512, 0, st>>>(a, heads, slices);
 }
+template <int DT, int DKP>
+void launch_rev_waves(const DeltaArgs& a, hipStream_t st) {
+  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t slices = (a.Dvp + 16 * kColumnWaves - 1) / (16 * kColumnWaves);
+  reverse_wave_kernel<DT, DKP><<<dim3(pad * slices), 64 * kColumnWaves, 0, st>>>(a, heads, slices);
+}
 template <int DT>
 void launch_rev(const DeltaArgs& a, int nt, hipStream_t st) {
+  if constexpr (DT == CCV_DT_F16) {
+    if (a.waves_back) return a.Dkp == 64 ? launch_rev_waves<DT, 64>(a, st) : launch_rev_waves<DT, 128>(a, st);
+  }
   if constexpr (DT == CCV_DT_BF16) {       // 32 columns of two or three planes of K and Q exceed the LDS
     if (nt == 2) {
       if (a.Dkp == 64) launch_rev<DT, 64, 2>(a, st);

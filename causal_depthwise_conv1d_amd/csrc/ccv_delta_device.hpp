@@ -534,6 +534,8 @@ __device__ inline uint32_t anew(uint32_t x) {
   return x;
 }
 
+constexpr int kColumnWaves = 4;        // waves of a workgroup whose waves hold whole columns
+
 // A chunk's 64 rows of 16-bit elements into LDS as they are, shared between NW waves; JOINED: in the
 // order above.
 template <int DKP, int LD, int NW, bool JOINED>
@@ -545,7 +547,7 @@ struct RowCopy {
   __device__ inline RowCopy(int w, int l, uint32_t stride, int width) {
     const int row = w * (64 / NW) + l / kLanes, c = l % kLanes * 8;
     off = c < width ? row * stride + c * 2 : kNowhere;
-    next = c < width ? kEach * stride : 0;
+    next = kEach * stride;       // the same in every lane: kNowhere and 63 steps stay above any bound and below 2^32
     at = (JOINED ? joined(row) : row) * LD + c;
   }
   __device__ inline void load(__amdgpu_buffer_rsrc_t b) {

@@ -9,7 +9,7 @@ namespace ccv {
 constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 16-row matrix tiles
 constexpr int kDeltaMatrix = 3 * 64 * 64;   // elements of a chunk's W or P
 constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
-constexpr int kDeltaPart = 256;       // fp32 sums of a chunk and slice: 64 each of dG by the state, Y.N, Y.N - dv.v, c
+constexpr int kDeltaPart = 192;       // fp32 sums of a chunk and slice: 64 each of Y.N, Y.N - dv.v, c
 constexpr int kDeltaPairs = 128;      // fp32 values: 64 of dG, one dot product, and room
 constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
 
@@ -49,9 +49,11 @@ struct DeltaArgs {
   float *S, *dS;                                // [ch][Dvp / 16][Dkp / 16] tiles: state at a chunk's start, gradient at its end
   float *N, *Y;                                 // [ch][Dvp / 16][4] tiles
   float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
+  float* qpart;                                 // backward: [ch][qslices][64] dG by the state, likewise
   float* pairs;                                 // backward: [ch][kDeltaPairs] dG by pairs of steps; <S, dS'>
-  int32_t Dkp, slices;
-  int32_t waves;                                // the forward pass runs on whole columns a wave, W's rows in joined() order
+  int32_t Dkp, slices, qslices;                 // value slices of the pass from the end, and of the forward one
+  int32_t waves;                                // the forward pass holds whole columns a wave; W has its rows in joined() order
+  int32_t waves_back;                           // the backward's pass likewise, W and P transposed
 };
 
 // Single steps against states in a cache.

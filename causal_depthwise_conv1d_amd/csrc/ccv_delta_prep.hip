@@ -280,8 +280,8 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   };
   write(a.W, Wl, std::integral_constant<int, 3>(), false, a.waves);
   if constexpr (BWD) {
-    write(a.WT, Wl, std::integral_constant<int, 3>(), true);
-    write(a.P, Pl, std::integral_constant<int, 3>(), true);
+    write(a.WT, Wl, std::integral_constant<int, 3>(), true, a.waves_back);
+    write(a.P, Pl, std::integral_constant<int, 3>(), true, a.waves_back);
   } else {
     write(a.P, Pl, std::integral_constant<int, OP>(), false);
   }

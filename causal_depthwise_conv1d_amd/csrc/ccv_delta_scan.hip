@@ -299,7 +299,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
         }
         load_P(nn);
         dot = sum4rows(dot) * gam * scale;
-        if (g4 == 0) a.part[(((int64_t)c * a.Hv + h) * a.slices + slice) * kDeltaPart + i] = dot;
+        if (g4 == 0) a.qpart[(((int64_t)c * a.Hv + h) * a.qslices + slice) * 64 + i] = dot;
         lds_barrier();
       } else {
         f32x4 o[NT];
@@ -330,11 +330,9 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
 // in its registers (see joined()): K S is R's rows, R the right-hand side of W R, N that of
 // K^T (del N) and the left-hand side of P N.  What the waves share are K and Q, which are needed
 // by rows and, K, by columns: a chunk's rows lie in LDS, two chunks in turn, one barrier a chunk.
-constexpr int NW = 4;        // waves that share them
-
 template <int DT, int DKP, bool BWD>
-__global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
-  constexpr int KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
+__global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
+  constexpr int NW = kColumnWaves, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
   __shared__ uint16_t Kl[2][64][LDK], Ql[2][64][LDK];
   __shared__ float Gl[2][3][64];            // gam, del, beta
   const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
@@ -369,15 +367,17 @@ __global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t 
   Rows<DT> O(BWD ? a.dout : a.out, BWD ? a.do_s : a.o_s, sq, h, BWD ? (a.Dv + 7) & ~7 : a.Dv, c0);
   Piece<uint16_t> W(a.W, kDeltaMatrix, a.Hv, ch0), P(a.P, kDeltaMatrix, a.Hv, ch0);
   Piece<float> D(a.dec, kDeltaDec, a.Hv, ch0);
-  Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0);
+  Piece<float> So(a.S, (int64_t)DKP * a.Dvp, a.Hv, ch0), No(a.N, 64 * (int64_t)a.Dvp, a.Hv, ch0),
+      Po(a.qpart, (int64_t)a.qslices * 64, a.Hv, ch0);
   const float scale = a.scale;
   const bool vec = a.vec_o;
   const int dleft = a.Dv - dv0 - 4 * g4;
-  const uint32_t oo = dleft > 0 ? r * O.stride + (dv0 + 4 * g4) * 2 : kNowhere, onext = dleft > 0 ? 16 * O.stride : 0;
-  const uint32_t ov = dv < a.Dv ? 8 * g4 * V.stride + dv * 2 : kNowhere, vnext = dv < a.Dv ? V.stride : 0;
+  const uint32_t oo = dleft > 0 ? r * O.stride + (dv0 + 4 * g4) * 2 : kNowhere, onext = 16 * O.stride;
+  const uint32_t ov = dv < a.Dv ? 8 * g4 * V.stride + dv * 2 : kNowhere, vnext = V.stride;
   // tiles as the workspace has them: row 32 s + 8 g4 + 4 o + e is element e of lane group 2 (g4 % 2) + o of tile 2 s + g4 / 2
   const uint32_t to = ((g4 >> 1) * 64 + 2 * (g4 & 1) * 16 + r) * 16;
   const uint32_t os = ct * (DKP / 16) * 1024 + to, on = ct * 4096 + to;
+  const uint32_t op = g4 == 0 ? (ct * 64 + r) * 4 : kNowhere;      // past the slices: out of bounds too
 
   RowCopy<DKP, LDK, NW, true> kt(w, l, K.stride, a.Dk);
   RowCopy<DKP, LDK, NW, false> qt(w, l, Q.stride, a.Dk);
@@ -566,6 +566,7 @@ __global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t 
     }
     if constexpr (BWD) {
       // scale gam dO . (Q S): the part of dG that comes by the state
+      const __amdgpu_buffer_rsrc_t part = Po.piece(true);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f32x4 d = widen4<DT>(xd[t]);
@@ -573,8 +574,9 @@ __global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t 
 #pragma unroll
         for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], scaled<DT>(qs[t][e], er[e]), dot);
         dot = sum4rows(dot) * Gl[b][0][16 * t + r] * scale;
-        if (g4 == 0 && ct < a.slices) a.part[(((int64_t)c * a.Hv + h) * a.slices + ct) * kDeltaPart + 16 * t + r] = dot;
+        buf_store1<CCV_DT_F32>(part, op + 64 * t, dot);
       }
+      Po.at += Po.step;
     } else {
       // the outputs: step 16 t + r, four consecutive values a lane
       const __amdgpu_buffer_rsrc_t ob = O.rows(n);
@@ -613,6 +615,7 @@ __global__ __launch_bounds__(64 * NW, 2) void wave_kernel(DeltaArgs a, uint32_t 
 
 template <int DT, int DKP>
 void launch_waves(const DeltaArgs& a, bool bwd, hipStream_t st) {
+  constexpr int NW = kColumnWaves;
   const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
   const uint32_t slices = (a.Dvp + 16 * NW - 1) / (16 * NW);
   const dim3 grid(pad * slices);
