@@ -110,7 +110,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
     const auto load_W = [&](int n) {
       const __amdgpu_buffer_rsrc_t b = W.piece(n > 0);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, !s && w >= 2 ? kNowhere : om + 1024 * s, 8192);
       W.at -= W.step;
     };
     if (c0 < c1) {
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
     const auto load_P = [&](int n) {
       const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) xP[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      for (int s = 0; s < 2; ++s) xP[s] = buf_planes<3>(b, !s && w >= 2 ? kNowhere : om + 1024 * s, 8192);
       P.at -= P.step;
     };
     const auto load_NV = [&](int n) {

@@ -125,12 +125,13 @@ __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
 // matrix instruction, whose accumulator layout is the next product's operand.
 template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
-  constexpr int NA = InPlanes<DT>::n, LDK = DKP + 8, LDA = 68, ES = DT == CCV_DT_F32 ? 4 : 2;
+  // 16-bit rows go through LDS as they are, and are multiplied in their own type: exact products
+  constexpr int RT = DT == CCV_DT_F32 ? DT : CCV_DT_BF16, NA = InPlanes<RT>::n, LDK = DKP + 8, LDA = 68, ES = DT == CCV_DT_F32 ? 4 : 2;
   constexpr int OP = OutOrder<DT>::n + 1;
-  __shared__ union { __bf16 k[NA][64][LDK]; float p[64][LDA]; } kp;    // K's planes, then P
-  auto& Kp = kp.k;
-  auto& Pl = kp.p;
-  __shared__ float Al[64][LDA], Wl[64][LDA];
+  __shared__ union { __bf16 k[NA][64][LDK]; float w[64][LDA]; } kw;    // K's planes, then W
+  auto& Kp = kw.k;
+  auto& Wl = kw.w;
+  __shared__ float Al[64][LDA];                                        // A, then P
   __shared__ double G[64];
   __shared__ float bt[64];
   const int ch = blockIdx.x, c = ch / a.Hv, h = ch - c * a.Hv, hk = h / (a.Hv / a.Hk);
@@ -171,7 +172,7 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   const int row = 16 * w + r;
   Frag<NA> qf[DKP / 32];
   {
-    RowTile<DT, DKP, LDK> kt(w, l, (uint32_t)(a.k_s[1] * ES), a.Dk), qt(w, l, (uint32_t)(a.q_s[1] * ES), a.Dk);
+    RowTile<RT, DKP, LDK> kt(w, l, (uint32_t)(a.k_s[1] * ES), a.Dk), qt(w, l, (uint32_t)(a.q_s[1] * ES), a.Dk);
     kt.load(chunk_rows<DT>(a.k, a.k_s, k, hk, (a.Dk + 7) & ~7));
     qt.load(chunk_rows<DT>(a.q, a.q_s, k, hk, (a.Dk + 7) & ~7));
     qt.store(&Kp[0][0][0], 64 * LDK);          // each wave's own rows
@@ -179,7 +180,6 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     for (int s = 0; s < DKP / 32; ++s) qf[s] = get8<NA>(&Kp[0][row][32 * s + 8 * g4], 64 * LDK);
     kt.store(&Kp[0][0][0], 64 * LDK);
   }
-  for (int i = tid; i < 64 * LDA / 4; i += 256) reinterpret_cast<f32x4*>(&Wl[0][0])[i] = f32x4{0, 0, 0, 0};
   __syncthreads();
 
   f32x4 pv[4];
@@ -199,8 +199,14 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
       for (int s = 0; s < DKP / 32; ++s) {
         const Frag<NA> bf = get8<NA>(&Kp[0][j][32 * s + 8 * g4], 64 * LDK);
         const Frag<NA> af = get8<NA>(&Kp[0][row][32 * s + 8 * g4], 64 * LDK);
-        kk = mma<2>(af, bf, kk);
-        qk = mma<2>(qf[s], bf, qk);
+        if constexpr (DT == CCV_DT_F32) {
+          kk = mma<2>(af, bf, kk);
+          qk = mma<2>(qf[s], bf, qk);
+        } else {
+          const u32x4 y = __builtin_bit_cast(u32x4, bf.p[0]);
+          kk = mfma16<DT>(__builtin_bit_cast(u32x4, af.p[0]), y, kk);
+          qk = mfma16<DT>(__builtin_bit_cast(u32x4, qf[s].p[0]), y, qk);
+        }
       }
     }
 #pragma unroll
@@ -212,11 +218,10 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     }
   }
   __syncthreads();
-  // P over K's planes
+  // what of W's rows lies right of the diagonal blocks
 #pragma unroll
-  for (int jb = 0; jb < 4; ++jb)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) Pl[16 * w + 4 * g4 + e][16 * jb + r] = pv[jb][e];
+  for (int jb = 1; jb < 4; ++jb)
+    if (jb > w) *reinterpret_cast<f32x4*>(&Wl[16 * w + r][16 * jb + 4 * g4]) = f32x4{0, 0, 0, 0};
 
   // diagonal blocks: column r of block w, the four groups of lanes alike
   {
@@ -264,11 +269,17 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     for (int e = 0; e < 4; ++e) Wl[32 + 16 * rb + 4 * g4 + e][16 * cb + r] = -y[e];
   }
   __syncthreads();
+#pragma unroll
+  for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Al[16 * w + 4 * g4 + e][16 * jb + r] = pv[jb][e];
+  __syncthreads();
   // out as planes: a thread takes 8 consecutive elements of two rows (columns when transposed)
   const auto write = [&](uint16_t* out, const float (*m)[LDA], auto nplanes, bool transposed, bool join = false) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = i * 256 + tid, ro = transposed ? e & 63 : e >> 3, co = 8 * (transposed ? e >> 6 : e & 7);
+      if (transposed ? ro >= 32 && co < 32 : ro < 32 && co >= 32) continue;      // the zero quarter: nobody reads it
       f32x8 x;
 #pragma unroll
       for (int q = 0; q < 8; ++q) x[q] = transposed ? m[co + q][ro] : m[ro][co + q];
@@ -281,9 +292,9 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   write(a.W, Wl, std::integral_constant<int, 3>(), false, a.waves);
   if constexpr (BWD) {
     write(a.WT, Wl, std::integral_constant<int, 3>(), true, a.waves_back);
-    write(a.P, Pl, std::integral_constant<int, 3>(), true, a.waves_back);
+    write(a.P, Al, std::integral_constant<int, 3>(), true, a.waves_back);
   } else {
-    write(a.P, Pl, std::integral_constant<int, OP>(), false);
+    write(a.P, Al, std::integral_constant<int, OP>(), false);
   }
 }
 

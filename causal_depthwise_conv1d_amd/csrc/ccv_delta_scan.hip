@@ -122,7 +122,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
     const auto load_W = [&](int n) {
       const __amdgpu_buffer_rsrc_t b = W.piece(n > 0);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, om + 1024 * s, 8192);
+      for (int s = 0; s < 2; ++s) xW[s] = buf_planes<3>(b, s && w < 2 ? kNowhere : om + 1024 * s, 8192);
       W.at += W.step;
     };
     const auto ahead = [&](int chunks) {       // steps of a chunk further on, 0 past the last
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
       } else {
         const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) xP[s] = buf_planes<OO + 1>(b, om + 1024 * s, 8192);
+        for (int s = 0; s < 2; ++s) xP[s] = buf_planes<OO + 1>(b, s && w < 2 ? kNowhere : om + 1024 * s, 8192);
         P.at += P.step;
       }
     };

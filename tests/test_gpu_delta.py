@@ -481,3 +481,19 @@ def test_graph_replays_equal_eager():
         for t, u in zip(got, work()):
             assert torch.equal(t, u), r
         assert torch.equal(after, cache)
+
+
+@pytest.mark.parametrize("heads", [2, 256])
+def test_fp16_subnormals(heads):
+    """Keys below fp16's normal range count in every product."""
+    gen = torch.Generator().manual_seed(2)
+    q, k, v, g, beta, h0 = ref.delta_inputs(1, 70, heads, heads, 64, 64, "f16", seed=3)
+    k = (torch.randint(-60, 60, k.shape, generator=gen) * 2.0 ** -24).to(torch.float16)
+    q = (q.float() * 3e4).to(torch.float16)
+    check_fwd(q, k, v, g, beta, None, what="subnormal keys")
+    check_fwd(k, q * 2.0 ** -15, v, g, beta, h0 * 2.0 ** -18, what="subnormal queries and small states")
+    dout = (torch.randint(-60, 60, v.shape, generator=gen) * 2.0 ** -24).to(torch.float16)
+    got = ccv.gated_delta_rule_bwd(*gpu(q, k, v, g, beta, dout), initial_state=h0.cuda(), return_dinitial_state=True)
+    want = ref.delta_gradients(q, k, v, g, beta, dout, None, None, h0)
+    for name, t in (("dq", got[0]), ("dg", got[3]), ("dbeta", got[4]), ("dh0", got[5])):
+        ref.assert_near(name, t, want[name], 2)
