@@ -152,6 +152,17 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   a->waves = z.x_dtype != CCV_F32 && groups * (a->Dvp / 16) >= 1024;
   a->waves_back = a->waves && z.x_dtype == CCV_F16;
   *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
+  // Few heads: a sequence in parts that run side by side, once for the map of the state that each is and
+  // once from the states that these give.  A chunk of the chain costs the same in both, so parts pay
+  // where a sequence is several times twice its part.
+  const int64_t blocks = z.Hv * (a->Dvp / 16), side = std::max<int64_t>(1, 256 / blocks);
+  const int64_t each = std::max<int64_t>(4, (nch + side - 1) / side);
+  if (!a->waves && a->nseq > 0 && nch >= 4 * each * a->nseq) {
+    a->part_chunks = (int32_t)each;
+    a->parts_per_row = packed ? 0 : (int32_t)((a->chunks_per_row + each - 1) / each);
+    a->parts = packed ? (int32_t)(nch / each + z.N + 1) : a->nseq * a->parts_per_row;
+    *nt = 1;
+  }
   a->slices = a->Dvp / (16 * *nt);
   a->qslices = a->waves ? a->Dvp / 16 : a->slices;
 
@@ -160,7 +171,12 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
     w.take(&a->table, nch, 4);
     w.take(&a->cstart, a->nseq + 2, 2);
     w.take(&a->order, a->nseq + 1, 1);
+    if (a->part_chunks) {
+      w.take(&a->pstart, a->nseq + 2, 1);
+      w.take(&a->ptable, a->parts, 2);
+    }
   }
+  if (a->part_chunks) w.take(&a->carry, (int64_t)a->parts * z.Hv, (int64_t)a->Dkp * (a->Dkp + a->Dvp));
   w.take(&a->W, heads, kDeltaMatrix);
   w.take(&a->P, heads, kDeltaMatrix);
   w.take(&a->dec, heads, kDeltaDec);
@@ -451,6 +467,7 @@ int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream) {
     if (pack(&w, hip_stream) != 0) return CCV_E_HIP;
     if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_prep(w.a, false, hip_stream) != 0) return CCV_E_HIP;
+    if (w.a.part_chunks && launch_delta_carry(w.a, hip_stream) != 0) return CCV_E_HIP;
   }
   return launch_delta_scan(w.a, false, w.nt, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
 }
@@ -475,6 +492,7 @@ int ccv_delta_bwd(const ccv_delta_bwd_args_t* args, void* hip_stream) {
     if (pack(&w, hip_stream) != 0) return CCV_E_HIP;
     if (w.a.packed && launch_delta_table(w.a, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_prep(w.a, true, hip_stream) != 0) return CCV_E_HIP;
+    if (w.a.part_chunks && launch_delta_carry(w.a, hip_stream) != 0) return CCV_E_HIP;
     if (launch_delta_scan(w.a, true, w.nt, hip_stream) != 0) return CCV_E_HIP;
   }
   if (launch_delta_reverse(w.a, w.nt, hip_stream) != 0) return CCV_E_HIP;

@@ -30,7 +30,8 @@ constexpr int LDT = 72;
 // values, dv and Y to memory).  Both sides of such an exchange hold the same elements lane
 // by lane, so it takes one 16-byte LDS access a tile and needs no other order than the
 // three barriers.
-template <int DT, int DKP, int NT>
+// MAP: what a part of a sequence makes of a gradient of zero at its end; no more than the chain.
+template <int DT, int DKP, int NT, bool MAP>
 __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
@@ -44,10 +45,13 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
   __shared__ f32x4 Ud[MT][NT][4][64];      // Q^T (scale gam dO); then Y in its first tile, likewise
   const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
   if (hs >= heads) return;
-  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
+  const Part part = part_at(a, sh);
+  const int seq = part.seq;
   const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // steps of no sequence have no gradient
+    if (MAP || seq > a.nseq) return;
     const int32_t* begin = a.cstart + (a.nseq + 2);
     for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 512) {
       const int64_t t = i / CB;
@@ -56,7 +60,8 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
     }
     return;
   }
-  const Sequence sq = sequence_at(a, seq);
+  if (MAP && part.k == 0) return;          // nothing lies before it
+  const Sequence sq = part.sq;
   const int c0 = sq.first, c1 = sq.end;
   const int64_t chl = (int64_t)(c1 - 1) * a.Hv + h;
   const uint32_t om = (2 * w * 64 + l) * 16, od = (16 * w + 4 * g4) * 4;
@@ -70,14 +75,19 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
   if (w8 < 4) {
     // ---- dS: rows 16 (MT w + m) + 4 g4 + e, column 16 j + r ------------------------------
     f32x4 S[MT][NT];
+    const f32x4* start = MAP ? nullptr : start_tiles(a, part, h, 1);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
+        if (start) {
+          S[m][j] = start[((slice * NT + j) * (DKP / 16) + MT * w + m) * 64 + l];
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-          S[m][j][e] = a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
+          for (int e = 0; e < 4; ++e) {
+            const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
+            S[m][j][e] = !MAP && a.dht && dk < a.Dk && dv < a.Dv ? a.dht[seq * a.dht_s[0] + h * a.dht_s[1] + dk * a.dht_s[2] + dv] : 0.0f;
+          }
         }
     const auto put_state = [&]() {
 #pragma unroll
@@ -141,7 +151,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            buf_store_f4(sb, os + (j * (DKP / 16) + m) * 1024, S[m][j]);
+            if constexpr (!MAP) buf_store_f4(sb, os + (j * (DKP / 16) + m) * 1024, S[m][j]);
             S[m][j] = S[m][j] * gt.last + Ud[m][j][w][l];
           }
         So.at -= So.step;
@@ -150,7 +160,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       for (int j = 0; j < NT; ++j) {
         const f32x4 x = kd[j].total() * gt.del;
         put4<3>(&Rp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, Pd[j][w][l] + x);
-        Pd[j][w][l] = x;
+        if constexpr (!MAP) Pd[j][w][l] = x;
       }
       lds_barrier();
 
@@ -167,7 +177,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       for (int j = 0; j < NT; ++j) {
         const f32x4 y = ys[j].total();
         put4<3>(&Yp[0][16 * j + r][16 * w + 4 * g4], CB * LDT, y * gt.beta * -gt.gam);
-        Ud[0][j][w][l] = y;
+        if constexpr (!MAP) Ud[0][j][w][l] = y;
       }
       lds_barrier();
 
@@ -192,7 +202,13 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       put_state();
       lds_barrier();
     }
-    if (a.dh0) {
+    if constexpr (MAP) {
+      f32x4* to = reinterpret_cast<f32x4*>(part_map(a, sh, h) + DKP * DKP);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) to[((slice * NT + j) * (DKP / 16) + MT * w + m) * 64 + l] = S[m][j];
+    } else if (a.dh0 && part.k == 0) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -299,7 +315,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
     if (c0 < c1) {
       load_QD(steps_of(c1 - 1));
       load_P(steps_of(c1 - 1));
-      load_NV(steps_of(c1 - 1));
+      if constexpr (!MAP) load_NV(steps_of(c1 - 1));
       stage();
       load_QD(steps_of(c1 - 2));
     }
@@ -317,6 +333,12 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       lds_barrier();
       products();
       load_P(steps_of(c - 2));
+      if constexpr (MAP) {
+        lds_barrier();
+        hand_over();
+        lds_barrier();
+        continue;
+      }
       f32x4 cs = {0, 0, 0, 0}, bs = {0, 0, 0, 0}, gs = {0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -918,10 +940,16 @@ __global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) 
 
 template <int DT, int DKP, int NT>
 void launch_rev(const DeltaArgs& a, hipStream_t st) {
-  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t heads = (a.part_chunks ? (uint32_t)a.parts : (uint32_t)(a.nseq + (a.packed ? 1 : 0))) * a.Hv, pad = (heads + 7) / 8 * 8;
   const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
   const dim3 grid(pad * slices);
-  reverse_kernel<DT, DKP, NT><<<grid, 512, 0, st>>>(a, heads, slices);
+  if constexpr (NT == 1) {
+    if (a.part_chunks) {
+      reverse_kernel<DT, DKP, 1, true><<<grid, 512, 0, st>>>(a, heads, slices);
+      join_kernel<DKP, true><<<dim3((uint32_t)a.nseq * a.Hv, a.Dvp / 16), 256, 0, st>>>(a);
+    }
+  }
+  reverse_kernel<DT, DKP, NT, false><<<grid, 512, 0, st>>>(a, heads, slices);
 }
 template <int DT, int DKP>
 void launch_rev_waves(const DeltaArgs& a, hipStream_t st) {

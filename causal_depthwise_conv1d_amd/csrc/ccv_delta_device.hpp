@@ -347,6 +347,55 @@ __device__ inline Sequence sequence_at(const DeltaArgs& a, int s) {
 // The i-th sequence that a pass over the chunks takes.
 __device__ inline int in_order(const DeltaArgs& a, int i) { return a.packed ? __builtin_amdgcn_readfirstlane(a.order[i]) : i; }
 
+// What a workgroup of such a pass takes: a sequence, or a part of one.
+struct Part {
+  int seq, k, first;      // the sequence (nseq: the steps of none; above: nothing), which part of it, the number of its part 0
+  bool last;
+  Sequence sq;
+};
+__device__ inline Part part_at(const DeltaArgs& a, int s) {
+  Part p{};
+  if (!a.part_chunks) {
+    p.seq = in_order(a, s);
+    p.last = true;
+    if (p.seq < a.nseq) p.sq = sequence_at(a, p.seq);
+    return p;
+  }
+  if (a.packed) {
+    p.seq = __builtin_amdgcn_readfirstlane(a.ptable[2 * s]);
+    p.k = __builtin_amdgcn_readfirstlane(a.ptable[2 * s + 1]);
+  } else {
+    p.seq = s / a.parts_per_row;
+    p.k = s - p.seq * a.parts_per_row;
+  }
+  p.first = s - p.k;
+  if (p.seq >= a.nseq) return p;
+  p.sq = sequence_at(a, p.seq);
+  const int64_t skip = (int64_t)p.k * a.part_chunks * kDeltaChunk, most = (int64_t)a.part_chunks * kDeltaChunk;
+  p.sq.first += p.k * a.part_chunks;
+  p.sq.t0 += (int)skip;
+  p.last = p.sq.end <= p.sq.first + a.part_chunks;
+  if (!p.last) p.sq.end = p.sq.first + a.part_chunks;
+  p.sq.len = p.sq.len - skip < most ? p.sq.len - skip : most;
+  return p;
+}
+
+// A part's map of the state in the workspace: T as right-to-left fragments (map_at), then B in 16 x 16 tiles as a
+// wave's accumulators hold them, tiles of one 16 values together.
+__device__ inline float* part_map(const DeltaArgs& a, int part, int h) {
+  return a.carry + ((int64_t)part * a.Hv + h) * a.Dkp * (a.Dkp + a.Dvp);
+}
+template <int DKP>
+__device__ inline int map_at(int row, int col) {       // element of T: a lane's 8 columns of a row lie together
+  return (((row >> 4) * (DKP / 32) + (col >> 5)) * 64 + ((col >> 3) & 3) * 16 + (row & 15)) * 8 + (col & 7);
+}
+// The state that a part starts from where that is not the sequence's own: what the part next to it (step: -1 before, 1
+// after) leaves, as the join left it in B's place.
+__device__ inline const f32x4* start_tiles(const DeltaArgs& a, const Part& p, int h, int step) {
+  if (step < 0 ? p.k == 0 : p.last) return nullptr;
+  return reinterpret_cast<const f32x4*>(part_map(a, p.first + p.k + step, h) + a.Dkp * a.Dkp);
+}
+
 template <int DT>
 __device__ inline const char* row_ptr(const void* base, const int64_t* s, int row, int64_t t, int h) {
   return static_cast<const char*>(base) + (row * s[0] + t * s[1] + h * s[2]) * (DT == CCV_DT_F32 ? 4 : 2);
@@ -577,6 +626,80 @@ __device__ inline u32x4 get_joined_t(const uint16_t* lds, int s, int c, int o, i
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at));
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 16 * LD));
   return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// ---- parts of sequences -----------------------------------------------------------------------
+//
+// The states at the parts' starts (BACK: the gradients at their ends), from the sequence's own and the parts'
+// maps: S <- T S + B part by part, or S <- T^T S + B from the last on, each left where B was.  A workgroup
+// takes 16 values of one sequence and head; a map is loaded while the one before it is applied.
+template <int DKP, bool BACK>
+__global__ __launch_bounds__(256, 1) void join_kernel(DeltaArgs a) {
+  constexpr int KS = DKP / 32, MT = DKP / 64, LDK = DKP + 16;
+  __shared__ __bf16 Sp[3][16][LDK];
+  const int seq = blockIdx.x / a.Hv, h = blockIdx.x - seq * a.Hv, dv0 = 16 * blockIdx.y;
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r = l & 15, g4 = l >> 4;
+  const int first = a.packed ? a.pstart[seq] : seq * a.parts_per_row, maps = (a.packed ? a.pstart[seq + 1] - first : a.parts_per_row) - 1;
+  const int64_t each = (BACK ? -1 : 1) * (int64_t)a.Hv * DKP * (DKP + a.Dvp);
+  float* map = part_map(a, first + (BACK ? maps : 0), h);
+  f32x4* tiles = reinterpret_cast<f32x4*>(map + DKP * DKP) + (blockIdx.y * (DKP / 16) + MT * w) * 64 + l;
+  struct Map {
+    f32x8 T[MT][KS];
+    f32x4 B[MT];
+  } x, y;
+  const auto load = [&](Map& t, int p) {
+    if (p >= maps) return;
+    const float* at = map + p * each;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = 16 * (MT * w + m) + r;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int k = 32 * s + 8 * g4;
+        if constexpr (BACK) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t.T[m][s][e] = at[map_at<DKP>(k + e, row)];
+        } else {
+          t.T[m][s] = *reinterpret_cast<const f32x8*>(at + map_at<DKP>(row, k));
+        }
+      }
+      t.B[m] = tiles[p * each / 4 + m * 64];
+    }
+  };
+  const float* own = BACK ? a.dht : a.h0;
+  const int64_t* os = BACK ? a.dht_s : a.h0_s;
+  f32x4 S[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + r;
+      S[m][e] = own && dk < a.Dk && dv < a.Dv ? own[seq * os[0] + h * os[1] + dk * os[2] + dv] : 0.0f;
+    }
+  const auto apply = [&](Map& t, int p) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) put4<3>(&Sp[0][r][16 * (MT * w + m) + 4 * g4], 16 * LDK, S[m]);
+    lds_barrier();
+    Sums<2> ts[MT];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const Frag<3> sf = get8<3>(&Sp[0][r][32 * s + 8 * g4], 16 * LDK);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) ts[m].add(split8<3>(t.T[m][s]), sf);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) S[m] = ts[m].total() + t.B[m];
+    load(t, p + 2);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tiles[p * each / 4 + m * 64] = S[m];
+    lds_barrier();
+  };
+  load(x, 0);
+  load(y, 1);
+  for (int p = 0; p < maps; p += 2) {
+    apply(x, p);
+    if (p + 1 < maps) apply(y, p + 1);
+  }
 }
 
 }  // namespace ccv

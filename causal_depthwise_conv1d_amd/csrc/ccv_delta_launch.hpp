@@ -40,6 +40,11 @@ struct DeltaArgs {
   int32_t* table;                               // packed: [nchunks] x (sequence, first step, steps, -)
   int32_t* cstart;                              // packed: [nseq + 2] first chunk of each sequence
   int32_t* order;                               // packed: [nseq + 1] the sequences, longest first
+  // few heads: the passes over the chunks take parts of `part_chunks` chunks (0: whole sequences)
+  int32_t part_chunks, parts, parts_per_row;    // parts: upper bound over all sequences
+  int32_t* pstart;                              // packed: [nseq + 2] first part of each sequence
+  int32_t* ptable;                              // packed: [parts] x (sequence, part of it)
+  float* carry;                                 // [part][head]: the map of the state over a part, S -> T S + B: Dkp x Dkp of T, Dkp x Dvp of B
   uint16_t* W;                                  // [ch][3][64 x 64, fragment_at]: (1 + A)^-1 as bf16 planes
   uint16_t* P;                                  // likewise, kDeltaMatrix a chunk and head; the backward holds it transposed
   uint16_t* WT;                                 // backward: W transposed
@@ -82,6 +87,7 @@ struct DeltaPackArgs {
 int launch_delta_pack(const DeltaPackArgs& a, void* stream);
 int launch_delta_table(const DeltaArgs& a, void* stream);
 int launch_delta_prep(const DeltaArgs& a, bool backward, void* stream);
+int launch_delta_carry(const DeltaArgs& a, void* stream);
 int launch_delta_scan(const DeltaArgs& a, bool backward, int nt, void* stream);
 int launch_delta_reverse(const DeltaArgs& a, int nt, void* stream);
 int launch_delta_grads(const DeltaArgs& a, void* stream);

@@ -96,6 +96,36 @@ __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
   __syncthreads();
   for (int s = tid; s < a.nseq; s += 1024) a.order[atomicAdd(&sm[bucket(s)], 1)] = s;
   if (tid == 0) a.order[a.nseq] = a.nseq;
+  if (a.part_chunks) {      // the parts of each sequence, one at least
+    int psum = 0;
+    for (int base = 0; base < n; base += 1024) {
+      const int i = base + tid, c = i < a.nseq ? (a.cstart[i + 1] - a.cstart[i] + a.part_chunks - 1) / a.part_chunks : 1;
+      __syncthreads();
+      sm[tid] = i < n ? (c > 1 ? c : 1) : 0;
+      __syncthreads();
+      for (int d = 1; d < 1024; d <<= 1) {
+        const int o = tid >= d ? sm[tid - d] : 0;
+        __syncthreads();
+        sm[tid] += o;
+        __syncthreads();
+      }
+      if (i < n) a.pstart[i + 1] = psum + sm[tid];
+      psum += sm[1023];
+    }
+    if (tid == 0) a.pstart[0] = 0;
+    __threadfence_block();
+    __syncthreads();
+    for (int p = tid; p < a.parts; p += 1024) {
+      int lo = 0, hi = a.nseq;                       // the last sequence whose first part is <= p
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (a.pstart[m] <= p) lo = m;
+        else hi = m - 1;
+      }
+      a.ptable[2 * p] = p < psum ? lo : n;
+      a.ptable[2 * p + 1] = p < psum ? p - a.pstart[lo] : 0;
+    }
+  }
   for (int c = tid; c < a.nchunks; c += 1024) {
     int s = a.nseq, t0 = 0, len = 0;
     if (c < csum) {

@@ -16,17 +16,22 @@
 namespace ccv {
 namespace {
 
-constexpr int LDT = 72;      // row stride of an LDS array of 64 steps
+constexpr int LDT = 80;      // row stride of an LDS array of 64 steps
 
-template <int DT, int DKP, int NT, bool BWD>
-__global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
-  constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 8;
+// kMap: what a part of a sequence makes of any state, S -> T S + B: the columns of T are the chain's result from
+// those of the identity, without values, and those of B from zeros; only the waves of the state.
+enum Mode { kForward, kBackward, kMap };
+
+template <int DT, int DKP, int NT, Mode MODE>
+__global__ __launch_bounds__(MODE == kMap ? 256 : 512, DT == CCV_DT_BF16 && NT == 1 && MODE == kForward ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
+  constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 16;
+  constexpr bool BWD = MODE == kBackward;
   constexpr int OO = OutOrder<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // S by columns
   __shared__ __bf16 Rp[3][CB][LDT];        // beta R by columns
   __shared__ __bf16 Kl[NA][64][LDK];
   __shared__ union {                       // Q until the first barrier of a chunk, N from then on
-    __bf16 q[NA][64][LDK];
+    __bf16 q[MODE == kMap ? 1 : NA][MODE == kMap ? 1 : 64][LDK];
     struct {
       __bf16 p[OO + 1][CB][LDT], d[3][CB][LDT];      // N, del N
     } n;
@@ -36,11 +41,14 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
   auto& Nd = qn.n.d;
   const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
   if (hs >= heads) return;
-  const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
+  const int sh = hs / a.Hv, h = hs - sh * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB - (MODE == kMap ? DKP : 0);
+  const Part part = part_at(a, sh);
+  const int seq = part.seq;
   const int tid = threadIdx.x, w8 = __builtin_amdgcn_readfirstlane(tid >> 6), w = w8 & 3, l = tid & 63, r = l & 15, g4 = l >> 4;
 
   if (seq >= a.nseq) {                     // the steps of a packed row that belong to no sequence
-    if constexpr (!BWD) {
+    if constexpr (MODE == kForward) {
+      if (seq > a.nseq) return;
       const int32_t* begin = a.cstart + (a.nseq + 2);
       for (int64_t i = (int64_t)begin[a.nseq] * CB + tid; i < a.L * CB; i += 512) {
         const int64_t t = i / CB;
@@ -50,7 +58,8 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
     }
     return;
   }
-  const Sequence sq = sequence_at(a, seq);
+  if (MODE == kMap && part.last && (!a.dS || !part.k || dv0 >= 0)) return;   // its T serves the backward only, its B nobody
+  const Sequence sq = part.sq;
   const int c0 = sq.first, c1 = sq.end;
   const int64_t ch0 = (int64_t)c0 * a.Hv + h;
   const int i = 16 * w + r;                // the step whose row of K, Q, W, P this lane holds
@@ -61,14 +70,20 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
   if (w8 < 4) {
     // ---- the state: rows 16 (MT w + m) + 4 g4 + e, column 16 j + r ----------------------
     f32x4 S[MT][NT];
+    const f32x4* start = MODE == kMap ? nullptr : start_tiles(a, part, h, -1);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
+        if (start) {
+          S[m][j] = start[((slice * NT + j) * (DKP / 16) + MT * w + m) * 64 + l];
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
-          S[m][j][e] = a.h0 && dk < a.Dk && dv < a.Dv ? a.h0[seq * a.h0_s[0] + h * a.h0_s[1] + dk * a.h0_s[2] + dv] : 0.0f;
+          for (int e = 0; e < 4; ++e) {
+            const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + 16 * j + r;
+            if constexpr (MODE == kMap) S[m][j][e] = dk == dv + DKP ? 1.0f : 0.0f;
+            else S[m][j][e] = a.h0 && dk < a.Dk && dv < a.Dv ? a.h0[seq * a.h0_s[0] + h * a.h0_s[1] + dk * a.h0_s[2] + dv] : 0.0f;
+          }
         }
     const auto put_state = [&]() {
 #pragma unroll
@@ -97,7 +112,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int dv = dv0 + 16 * j + r;
-        ov[j][e] = dv < a.Dv ? (16 * w + 4 * g4 + e) * V.stride + dv * ES : kNowhere;
+        ov[j][e] = dv >= 0 && dv < a.Dv ? (16 * w + 4 * g4 + e) * V.stride + dv * ES : kNowhere;
       }
     const auto load_K = [&](int n) {
       kt.load(K.rows(n));
@@ -185,7 +200,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
       for (int j = 0; j < NT; ++j) {
         N[j] = ws[j].total();
         put4<3>(&Nd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j] * gt.del);
-        if constexpr (!BWD) put4<OO + 1>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
+        if constexpr (MODE == kForward) put4<OO + 1>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
       }
       lds_barrier();
       if constexpr (BWD) {
@@ -221,7 +236,20 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
       left -= kDeltaChunk;
       lds_barrier();
     }
-    if (a.ht) {
+    if constexpr (MODE == kMap) {
+      float* to = part_map(a, sh, h);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if (dv0 < 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[map_at<DKP>(16 * (MT * w + m) + 4 * g4 + e, slice * CB + 16 * j + r)] = S[m][j][e];
+          } else {
+            reinterpret_cast<f32x4*>(to + DKP * DKP)[((dv0 / 16 + j) * (DKP / 16) + MT * w + m) * 64 + l] = S[m][j];
+          }
+        }
+    } else if (a.ht && part.last) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -232,7 +260,7 @@ __global__ __launch_bounds__(512, DT == CCV_DT_BF16 && NT == 1 && !BWD ? 4 : 2) 
             if (dk < a.Dk && dv < a.Dv) a.ht[seq * a.ht_s[0] + h * a.ht_s[1] + dk * a.ht_s[2] + dv] = S[m][j][e];
           }
     }
-  } else {
+  } else if constexpr (MODE != kMap) {
     // ---- the outputs: step i, four consecutive values 16 j + 4 g4 a lane; the same barriers ----
     Frag<OO + 1> xP[2];
     Raw4<DT> xd[NT];
@@ -622,32 +650,52 @@ void launch_waves(const DeltaArgs& a, bool bwd, hipStream_t st) {
   if (bwd) wave_kernel<DT, DKP, true><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
   else wave_kernel<DT, DKP, false><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
 }
+uint32_t parts_of(const DeltaArgs& a) { return a.part_chunks ? (uint32_t)a.parts : (uint32_t)(a.nseq + (a.packed ? 1 : 0)); }
+
+template <int DT, int DKP>
+void launch_map(const DeltaArgs& a, hipStream_t st) {
+  const uint32_t heads = (uint32_t)a.parts * a.Hv, pad = (heads + 7) / 8 * 8, slices = (DKP + a.Dvp) / 16;
+  scan_kernel<DT, DKP, 1, kMap><<<dim3(pad * slices), 256, 0, st>>>(a, heads, slices);
+  join_kernel<DKP, false><<<dim3((uint32_t)a.nseq * a.Hv, a.Dvp / 16), 256, 0, st>>>(a);
+}
+template <int DT>
+void launch_map(const DeltaArgs& a, hipStream_t st) {
+  if (a.Dkp == 64) launch_map<DT, 64>(a, st);
+  else launch_map<DT, 128>(a, st);
+}
+
 template <int DT, int DKP, int NT>
 void launch(const DeltaArgs& a, bool bwd, hipStream_t st) {
-  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv;
+  const uint32_t heads = parts_of(a) * a.Hv;
   // slices of one head lie 8 k workgroups apart: on one XCD, whose L2 then holds the
   // chunk's K, Q, W and P once for all of them
   const uint32_t pad = (heads + 7) / 8 * 8;
   const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
   const dim3 grid(pad * slices);
-  if (bwd) scan_kernel<DT, DKP, NT, true><<<grid, 512, 0, st>>>(a, heads, slices);
-  else scan_kernel<DT, DKP, NT, false><<<grid, 512, 0, st>>>(a, heads, slices);
+  if (bwd) scan_kernel<DT, DKP, NT, kBackward><<<grid, 512, 0, st>>>(a, heads, slices);
+  else scan_kernel<DT, DKP, NT, kForward><<<grid, 512, 0, st>>>(a, heads, slices);
 }
 template <int DT>
 void launch(const DeltaArgs& a, bool bwd, int nt, hipStream_t st) {
   if constexpr (DT != CCV_DT_F32) {
     if (a.waves) return a.Dkp == 64 ? launch_waves<DT, 64>(a, bwd, st) : launch_waves<DT, 128>(a, bwd, st);
   }
-  if (a.Dkp == 64) {
-    if (nt == 1) launch<DT, 64, 1>(a, bwd, st);
-    else launch<DT, 64, 2>(a, bwd, st);
-  } else {
-    if (nt == 1) launch<DT, 128, 1>(a, bwd, st);
-    else launch<DT, 128, 2>(a, bwd, st);
+  if constexpr (DT != CCV_DT_F32) {
+    if (nt == 2) return a.Dkp == 64 ? launch<DT, 64, 2>(a, bwd, st) : launch<DT, 128, 2>(a, bwd, st);
   }
+  if (a.Dkp == 64) launch<DT, 64, 1>(a, bwd, st);
+  else launch<DT, 128, 1>(a, bwd, st);
 }
 
 }  // namespace
+
+int launch_delta_carry(const DeltaArgs& a, void* stream) {
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.x_dtype == CCV_DT_F32) launch_map<CCV_DT_F32>(a, st);
+  else if (a.x_dtype == CCV_DT_F16) launch_map<CCV_DT_F16>(a, st);
+  else launch_map<CCV_DT_BF16>(a, st);
+  return (int)hipGetLastError();
+}
 
 int launch_delta_scan(const DeltaArgs& a, bool backward, int nt, void* stream) {
   const hipStream_t st = static_cast<hipStream_t>(stream);

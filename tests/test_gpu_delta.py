@@ -147,6 +147,37 @@ def test_many_sequences_of_one_row():
         check_bwd(q, k, v, g, beta, h0, lengths, what="130 sequences")
 
 
+# few heads and many chunks: the passes take the sequences in parts
+LONG = [(1, 1, 64, 64, [1030]), (1, 2, 128, 40, [2048]), (2, 4, 72, 33, [1500]), (1, 1, 64, 64, [1100, 0, 3, 1500]),
+        (1, 3, 20, 130, [0, 64, 2500, 0]), (1, 2, 64, 64, [4096 + 64])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("i", range(len(LONG)))
+def test_long_sequences_of_few_heads(dtype, i):
+    Hk, Hv, Dk, Dv, lengths = LONG[i]
+    one = len(lengths) == 1
+    q, k, v, g, beta, h0 = ref.delta_inputs(1, sum(lengths) + (0 if one else 7), Hk, Hv, Dk, Dv, dtype, seed=i, seqs=len(lengths),
+                                            decay=0.01)
+    check_fwd(q, k, v, g, beta, h0, None if one else lengths, what="long")
+    check_bwd(q, k, v, g, beta, h0, None if one else lengths, what="long")
+    g[:, 700] = -float("inf")
+    g[:, 64:300] = 0.01
+    check_fwd(q, k, v, g.clamp(min=-1e4), beta, None, None if one else lengths, what="long, forgotten", views=gpu(q, k, v, g, beta))
+
+
+def test_nan_in_a_part_stays_behind_it():
+    q, k, v, g, beta, _ = ref.delta_inputs(1, 2048, 1, 2, 64, 64, "bf16", seed=1)
+    clean = ccv.gated_delta_rule_fwd(*gpu(q, k, v, g, beta))
+    v[0, 1000, 1, 5], k[0, 1500, 0, 3] = NAN, NAN
+    out = ccv.gated_delta_rule_fwd(*gpu(q, k, v, g, beta))
+    same = torch.ones(1, 2048, 2, 64, dtype=torch.bool)
+    same[0, 960:, 1, 5] = False             # from its chunk on
+    same[0, 1472:] = False
+    assert torch.equal(out.cpu()[same], clean.cpu()[same])
+    assert torch.isnan(out[0, 1000:, 1, 5]).all() and torch.isnan(out[0, 1500:]).all()
+
+
 PACKED = [[5, 0, 64, 1, 130], [0, 0, 7], [64, 64], [200], [0], [1] * 20, [65, 0]]
 
 
