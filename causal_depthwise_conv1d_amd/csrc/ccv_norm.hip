@@ -20,54 +20,6 @@ namespace {
 
 template <int DT> struct Vec { static constexpr int n = DT == CCV_DT_F32 ? 4 : 8; };
 
-// 16 bytes of a row, widened; zeros past the first `left` elements.
-template <int DT>
-__device__ inline void load_vec(const void* p, int left, bool vec, float* x) {
-  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
-  if (vec && left >= V) {
-    const u32x4 d = load16(p);
-    if constexpr (DT == CCV_DT_F32) F32::unpack(d, x);
-    else if constexpr (DT == CCV_DT_BF16) BF16::unpack(d, x);
-    else F16::unpack(d, x);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = i < left ? load1<DT>(static_cast<const char*>(p) + i * ES) : 0.0f;
-}
-template <int DT>
-__device__ inline void store_vec(void* p, int left, bool vec, const float* y) {
-  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
-  if (vec && left >= V) {
-    if constexpr (DT == CCV_DT_F32) store16(p, F32::pack(y));
-    else if constexpr (DT == CCV_DT_BF16) store16(p, BF16::pack(y));
-    else store16(p, F16::pack(y));
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < left) store1<DT>(static_cast<char*>(p) + i * ES, y[i]);
-}
-
-// Vec<DT>::n weights from element `col`; `other` past the width or where there are none.
-template <int V>
-__device__ inline void load_weights(const void* p, int dtype, int col, int width, bool vec, float other, float* w) {
-  if (p && vec && col + V <= width) {
-    if (dtype == CCV_DT_F32) {
-#pragma unroll
-      for (int i = 0; i < V; i += 4) F32::unpack(load16(static_cast<const float*>(p) + col + i), w + i);
-      return;
-    }
-    if constexpr (V == 8) {
-      const u32x4 d = load16(static_cast<const uint16_t*>(p) + col);
-      if (dtype == CCV_DT_BF16) BF16::unpack(d, w);
-      else F16::unpack(d, w);
-      return;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) w[e] = p && col + e < width ? load_param(p, dtype, col + e) : other;
-}
-
 // Sums over the `LANES` threads of a row of N values; every one of them gets them.  Rows of more
 // than a wave: through `red`, two pieces of it in turn, so that one barrier suffices.
 template <int LANES, int N>
@@ -228,7 +180,6 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
   __shared__ float red[2][2][8];
   __shared__ float sums[RW > 1 ? TH * V : 1];
   int turn = 0;
-  const int lane = threadIdx.x % LANES;
   const Columns<DT, LANES, NV, FULL> cols(a.width);
   float w[NV][V], dw[NV][V], db[NV][V];
   cols.weights(w, a.w, a.w_dtype, 1.0f);
@@ -289,24 +240,24 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float* src = side ? db[i] : dw[i];
+      const float* src = side ? db[i] : dw[i];
       if constexpr (RW > 1) {
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < V; ++e) sums[threadIdx.x * V + e] = src[e];
         __syncthreads();
-        if (threadIdx.x < LANES)
+        for (int o = threadIdx.x; o < LANES * V; o += TH) {
+          const int c = (i * LANES + o / V) * V, col = FULL || c + V <= a.width ? c : a.width - V, e = o % V;
+          float s = 0;
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            float s = 0;
-            for (int r = 0; r < RW; ++r) s += sums[(r * LANES + lane) * V + e];
-            src[e] = s;
-          }
-      }
-      if (threadIdx.x < LANES)
+          for (int r = 0; r < RW; ++r) s += sums[r * LANES * V + o];
+          if (FULL || (c < a.width && e >= c - col)) part[side * (int64_t)a.width + col + e] = s;
+        }
+      } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
           if (cols.mine(i, e)) part[side * (int64_t)a.width + cols.col[i] + e] = src[e];
+      }
     }
 }
 
@@ -342,25 +293,64 @@ __device__ inline float block_sum(float v, float* red) {
   return v;
 }
 
+// A vector of such a row: the last one ends with the row; what it shares with the one before is not its own.
+// Rows narrower than a vector are one vector, element by element.
+template <int DT>
+struct Piece16 {
+  static constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  int col, skip, n;
+  __device__ inline Piece16(int i, int width)
+      : col(i + V <= width ? i : width < V ? 0 : width - V), skip(i - col), n(width < V ? width : V) {}
+  __device__ inline bool mine(int e) const { return e >= skip && e < n; }
+  __device__ inline void load(const char* row, float* x) const {
+    if (n == V) Columns<DT, 16, 1, false>::unpack(gload<u32x4>(reinterpret_cast<uintptr_t>(row) + (uint32_t)col * ES), x);
+    else
+      for (int e = 0; e < V; ++e) x[e] = e < n ? load1<DT>(row + e * ES) : 0.0f;
+  }
+  __device__ inline void store(char* row, const float* y) const {
+    char* p = row + (uint32_t)col * ES;
+    if (n < V) {
+      for (int e = 0; e < n; ++e) store1<DT>(p + e * ES, y[e]);
+    } else if constexpr (DT == CCV_DT_F32) {
+      store16(p, F32::pack(y));
+    } else if constexpr (DT == CCV_DT_BF16) {
+      store16(p, BF16::pack(y));
+    } else {
+      store16(p, F16::pack(y));
+    }
+  }
+  __device__ inline void weights(const void* p, int dtype, float other, float* w) const {
+    if (p && n == V && dtype == CCV_DT_F32) {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) F32::unpack(gload<u32x4>(reinterpret_cast<uintptr_t>(p) + ((uint32_t)col + e) * 4), w + e);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = p && e < n ? load_param(p, dtype, col + e) : other;
+    }
+  }
+};
+
 template <int DT>
 __global__ __launch_bounds__(1024) void wide_fwd_kernel(NormArgs a) {
-  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  constexpr int V = Vec<DT>::n;
   __shared__ float red[16];
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char* xp = norm_row<DT>(a.x, a.x_s, row, a.n1);
     char* op = norm_row<DT>(a.out, a.o_s, row, a.n1);
     float s = 0, q = 0, x[V], w[V], b[V];
     for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
-      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+      const Piece16<DT> p(i, a.width);
+      p.load(xp, x);
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += x[e];
+      for (int e = 0; e < V; ++e) s += p.mine(e) ? x[e] : 0.0f;
     }
     const float mean = block_sum(s, red) / (float)a.width;
     for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
-      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
+      const Piece16<DT> p(i, a.width);
+      p.load(xp, x);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float d = i + e < a.width ? x[e] - mean : 0.0f;
+        const float d = p.mine(e) ? x[e] - mean : 0.0f;
         q = __builtin_fmaf(d, d, q);
       }
     }
@@ -370,19 +360,20 @@ __global__ __launch_bounds__(1024) void wide_fwd_kernel(NormArgs a) {
       if (a.rstd) a.rstd[row] = rstd;
     }
     for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
-      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
-      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
-      load_weights<V>(a.b, a.w_dtype, i, a.width, a.vec_w, 0.0f, b);
+      const Piece16<DT> p(i, a.width);
+      p.load(xp, x);
+      p.weights(a.w, a.w_dtype, 1.0f, w);
+      p.weights(a.b, a.w_dtype, 0.0f, b);
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] = __builtin_fmaf((x[e] - mean) * rstd, w[e], b[e]);
-      store_vec<DT>(op + (int64_t)i * ES, a.width - i, a.vec, x);
+      p.store(op, x);
     }
   }
 }
 
 template <int DT>
 __global__ __launch_bounds__(1024) void wide_dx_kernel(NormArgs a) {
-  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  constexpr int V = Vec<DT>::n;
   __shared__ float red[16];
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const char* xp = norm_row<DT>(a.x, a.x_s, row, a.n1);
@@ -391,24 +382,26 @@ __global__ __launch_bounds__(1024) void wide_dx_kernel(NormArgs a) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s1 = 0, s2 = 0, x[V], d[V], w[V];
     for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
-      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
-      load_vec<DT>(dp + (int64_t)i * ES, a.width - i, a.vec, d);
-      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
+      const Piece16<DT> p(i, a.width);
+      p.load(xp, x);
+      p.load(dp, d);
+      p.weights(a.w, a.w_dtype, 1.0f, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float n = i + e < a.width ? (x[e] - mean) * rstd : 0.0f, y = d[e] * w[e];
+        const float y = p.mine(e) ? d[e] * w[e] : 0.0f;
         s1 += y;
-        s2 = __builtin_fmaf(y, n, s2);
+        s2 += p.mine(e) ? y * ((x[e] - mean) * rstd) : 0.0f;
       }
     }
     const float m1 = block_sum(s1, red) / (float)a.width, m2 = block_sum(s2, red) / (float)a.width;
     for (int i = threadIdx.x * V; i < a.width; i += 1024 * V) {
-      load_vec<DT>(xp + (int64_t)i * ES, a.width - i, a.vec, x);
-      load_vec<DT>(dp + (int64_t)i * ES, a.width - i, a.vec, d);
-      load_weights<V>(a.w, a.w_dtype, i, a.width, a.vec_w, 1.0f, w);
+      const Piece16<DT> p(i, a.width);
+      p.load(xp, x);
+      p.load(dp, d);
+      p.weights(a.w, a.w_dtype, 1.0f, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) x[e] = rstd * (d[e] * w[e] - m1 - (x[e] - mean) * rstd * m2);
-      store_vec<DT>(op + (int64_t)i * ES, a.width - i, a.vec, x);
+      p.store(op, x);
     }
   }
 }
@@ -416,13 +409,15 @@ __global__ __launch_bounds__(1024) void wide_dx_kernel(NormArgs a) {
 // Partial sums of dw and db: a thread has one vector of columns, blockIdx.y its rows.
 template <int DT>
 __global__ __launch_bounds__(256) void wide_sums_kernel(NormArgs a) {
-  constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
-  const int64_t col = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-  if (col >= a.width) return;
+  constexpr int V = Vec<DT>::n;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+  if (i >= a.width) return;
+  const Piece16<DT> p((int)i, a.width);
   float dw[V] = {}, db[V] = {}, x[V], d[V];
+#pragma unroll 4
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    load_vec<DT>(norm_row<DT>(a.dout, a.do_s, row, a.n1) + col * ES, a.width - (int)col, a.vec, d);
-    load_vec<DT>(norm_row<DT>(a.x, a.x_s, row, a.n1) + col * ES, a.width - (int)col, a.vec, x);
+    p.load(norm_row<DT>(a.dout, a.do_s, row, a.n1), d);
+    p.load(norm_row<DT>(a.x, a.x_s, row, a.n1), x);
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -430,10 +425,12 @@ __global__ __launch_bounds__(256) void wide_sums_kernel(NormArgs a) {
       db[e] += d[e];
     }
   }
-  for (int e = 0; e < V && col + e < a.width; ++e) {
-    a.part[((int64_t)blockIdx.y * 2) * a.width + col + e] = dw[e];
-    a.part[((int64_t)blockIdx.y * 2 + 1) * a.width + col + e] = db[e];
-  }
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (p.mine(e)) {
+      a.part[((int64_t)blockIdx.y * 2) * a.width + p.col + e] = dw[e];
+      a.part[((int64_t)blockIdx.y * 2 + 1) * a.width + p.col + e] = db[e];
+    }
 }
 
 int64_t min64(int64_t x, int64_t y) { return x < y ? x : y; }
@@ -449,9 +446,9 @@ void go(const NormArgs& a, bool bwd, int grid, hipStream_t st) {
 }
 template <int DT, int LANES>
 void go(const NormArgs& a, bool bwd, int nv, int grid, hipStream_t st) {
-  if (nv == 1) go<DT, LANES, 1>(a, bwd, grid, st);
-  else if (nv == 2) go<DT, LANES, 2>(a, bwd, grid, st);
-  else go<DT, LANES, 4>(a, bwd, grid, st);
+  if (nv == 1) return go<DT, LANES, 1>(a, bwd, grid, st);
+  if constexpr (LANES == 16) return go<DT, LANES, 2>(a, bwd, grid, st);
+  else return nv == 2 ? go<DT, LANES, 2>(a, bwd, grid, st) : go<DT, LANES, 4>(a, bwd, grid, st);
 }
 template <int DT>
 void go(const NormArgs& a, bool bwd, int cus, hipStream_t st) {

@@ -28,10 +28,6 @@ int check_rows(const Rows& r, int64_t n0, int64_t n1, int64_t width, int es, boo
   return !written || non_overlapping(n, s) ? CCV_OK : CCV_E_LAYOUT;
 }
 
-bool vectors(const Rows& r, int64_t n0, int64_t n1, int es) {
-  return aligned16(r.p) && stride_ok16(n0, r.s[0], es) && stride_ok16(n1, r.s[1], es);
-}
-
 int check_common(int64_t n0, int64_t n1, int64_t width, int x_dtype, int w_dtype, float eps) {
   if (n0 < 0 || n1 < 0 || width < 0 || width > INT32_MAX / 2) return CCV_E_SHAPE;
   if (x_dtype < 0 || x_dtype > 2 || w_dtype < 0 || w_dtype > 2) return CCV_E_DTYPE;
@@ -82,8 +78,6 @@ int validate_fwd(const ccv_norm_fwd_args_t* p, NormArgs* a) {
   a->x_dtype = p->x_dtype;
   a->w_dtype = p->w_dtype;
   a->eps = p->eps;
-  a->vec = vectors(x, p->n0, p->n1, es) && vectors(o, p->n0, p->n1, es);
-  a->vec_w = aligned16(p->weight) && aligned16(p->bias);
   return CCV_OK;
 }
 
@@ -102,10 +96,8 @@ int validate_bwd(const ccv_norm_bwd_args_t* p, NormArgs* a, int64_t* bytes, bool
     const Rows x{p->x, p->x_stride}, d{p->dout, p->dout_stride}, o{p->dx, p->dx_stride};
     if ((st = check_rows(x, p->n0, p->n1, p->width, es, false)) != CCV_OK) return st;
     if ((st = check_rows(d, p->n0, p->n1, p->width, es, false)) != CCV_OK) return st;
-    a->vec = vectors(x, p->n0, p->n1, es) && vectors(d, p->n0, p->n1, es);
     if (p->dx) {
       if ((st = check_rows(o, p->n0, p->n1, p->width, es, true)) != CCV_OK) return st;
-      a->vec = a->vec && vectors(o, p->n0, p->n1, es);
     }
   }
   const void* written[] = {p->dx, p->dweight, p->dbias};
@@ -142,7 +134,6 @@ int validate_bwd(const ccv_norm_bwd_args_t* p, NormArgs* a, int64_t* bytes, bool
   a->width = (int32_t)p->width;
   a->x_dtype = p->x_dtype;
   a->w_dtype = p->w_dtype;
-  a->vec_w = aligned16(p->weight);
   if (p->dweight || p->dbias) {
     const NormShape s = norm_shape(p->width, es);
     const int64_t per = s.lanes && s.lanes < 256 ? 256 / s.lanes : 1, need = (rows + per - 1) / per;
