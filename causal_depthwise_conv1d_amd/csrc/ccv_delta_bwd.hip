@@ -29,7 +29,8 @@ constexpr int LDT = 72;
 // behind them with what nothing waits for (the sums of Y.N, dv.v and c over this slice's
 // values, dv and Y to memory).  Both sides of such an exchange hold the same elements lane
 // by lane, so it takes one 16-byte LDS access a tile and needs no other order than the
-// three barriers.
+// three barriers.  Bound by the chain, as the forward: 2 x 4096 steps, 16 heads of 128 in bf16, 210 us, 3.3 us a
+// chunk.
 // MAP: what a part of a sequence makes of a gradient of zero at its end; no more than the chain.
 template <int DT, int DKP, int NT, bool MAP>
 __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
@@ -380,7 +381,9 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
 
 // The same for fp16 and many heads, as the forward's wave_kernel has it: 16 columns a wave, the chain
 //   K dS', P^T dO -> dN,  W^T dN = Y,  Q^T (scale gam dO) and K^T (gam beta Y) -> dS
-// in its registers, K and Q shared through LDS; both have their rows in the joined order.
+// in its registers, K and Q shared through LDS; both have their rows in the joined order.  8 x 2048 steps, 32 heads
+// of 128 in fp16: 630 us, 2.1 GB at 3.3 TB/s, against 1004 of reverse_kernel, 16 heads 455 against 510.  In bf16
+// reverse_kernel has LDS for 32 columns a workgroup and needs no more (633 and 325 us).
 template <int DT, int DKP>
 __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NW = kColumnWaves, NA = InPlanes<DT>::n, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
@@ -658,7 +661,8 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(Delt
 // w % 4; waves 0..3 the first half of the keys' columns and F, waves 4..7 the other half
 // and E.  Contractions over the values go through LDS 32 values at a time, the next 32
 // under way in registers; S, dS', N and Y lie there by values, and the transposing read
-// makes fragments of them.
+// makes fragments of them.  Bound by that staging and its waits, one workgroup a CU: 2 x 4096 steps, 16 heads of
+// 128 in bf16, 188 us, 557 MB at 3.0 TB/s.
 template <int DT, int DKP>
 __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   constexpr int NA = InPlanes<DT>::n, OO = OutOrder<DT>::n, OP = OO + 1, KS = DKP / 32, LDK = DKP + 8, LDO = 40;
@@ -892,7 +896,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 }
 
 // dg and dbeta of a chunk and head, a step a lane of one wave: the slices' sums and the pairs'
-// joined, then the running sum from the chunk's end.
+// joined, then the running sum from the chunk's end (2048 chunks and heads: 9 us).
 __global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) {
   const int64_t ch = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (ch >= items) return;

@@ -3,6 +3,11 @@
 // For the 64 steps of a chunk and one value head, with G the running sum of g inside the
 // chunk:   A_ij = beta_i e^(G_i - G_j) k_i.k_j  (i > j),   P_ij = e^(G_i - G_j) q_i.k_j  (i >= j),
 //          W = (1 + A)^-1.
+// Bound by memory, and by the latency of a chunk's few steps one after the other: 35 KB of LDS let four
+// workgroups of 16-bit inputs share a CU.  W goes out as three bf16 planes (fp32 states need them), P as
+// two where the outputs are 16-bit, both without the quarter above the diagonal blocks of 32, which is
+// zero.  4 x 4096 steps, 16 heads of 128 in bf16: 62 us, 260 MB at 4.2 TB/s; with whole planes and K's
+// and W's LDS apart it took 78.  65536 packed steps, 10 key and 20 value heads in fp16: 295 us.
 // G is summed in 64 bits, so that differences of steps that lie far down a strongly
 // decaying chunk keep 32 bits.  A decay of g < -2000 (and -inf, a forgotten state) counts
 // as -2000: e^-2000 is 0 in fp32 with room to spare, and no inf - inf arises.
@@ -29,7 +34,7 @@ __global__ __launch_bounds__(256) void pack_kernel(DeltaPackArgs a) {
 // Sequence s holds the steps [cu[s], cu[s + 1]); the offsets count as their running maximum,
 // clamped to [0, L], so that no table can lead outside the row.  The steps past the last
 // sequence are sequence `nseq`, whose outputs are zeros.  One workgroup: the longest part
-// is a binary search a chunk.
+// is a binary search a chunk (64 sequences of 65536 steps: 11 us, 7 of 3011 steps: 7 us).
 __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
   __shared__ int mx[1024], sm[1024];
   const int tid = threadIdx.x, n = a.nseq + 1, L = (int)a.L;

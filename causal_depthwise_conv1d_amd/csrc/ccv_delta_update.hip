@@ -7,7 +7,9 @@
 // One wave takes 32 values of a head (a 128-byte line of each of the state's rows): lane l
 // holds values 4 (l % 8) .. + 3 of RPT consecutive rows, RPT = 8 or 16 for up to 64 or 128
 // keys, the sums over rows finish across the wave's eight row groups, and no LDS or
-// barrier is needed.  The state stays in registers over the call's steps.
+// barrier is needed.  The state stays in registers over the call's steps.  Bound by the state's way in
+// and out: 256 rows of 32 heads of 128 x 128, 1.08 GB, 204 us, 5.3 TB/s; 5 rows of 20 heads are one round
+// trip to memory and the launch, 8.6 us.
 #include "ccv_delta_device.hpp"
 
 namespace ccv {

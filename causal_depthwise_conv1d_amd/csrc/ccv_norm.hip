@@ -9,6 +9,9 @@
 // always has the same columns, so the weights stay in registers, and in the backward so do
 // the thread's sums of dw and db.  Each workgroup leaves one partial row, and a second
 // kernel adds the partial rows in a fixed order.
+// 32768 rows of 4096 in bf16: forward 99 us, 0.54 GB at 5.4 TB/s; backward 170 us, 0.81 GB at 4.7, and
+// 8.5 us for the 1024 partial rows (2048 of them cost more than the shorter walks gain: 182 and 164 us
+// for 65536 x 2048).  65536 x 20 rows of 128 in fp16: 131, 211 and 5 us.
 // Every access is 16 bytes at any alignment.  Where the width is no multiple of that, a
 // row's last vector starts where it ends with the row; the elements that it shares with
 // the vector before it are left out of sums and written twice, with the same value.
@@ -282,6 +285,7 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
 }
 
 // ---- rows wider than 512 threads hold (walked again for each sum; they stay in L2), or narrower than a vector ----
+// 6700 rows of 20000 in bf16: forward 190 us, 2.8 TB/s of the row in and out; backward 405 us.
 
 __device__ inline float block_sum(float v, float* red) {
   v = sum4rows(sum16(v));

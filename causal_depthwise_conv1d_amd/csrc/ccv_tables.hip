@@ -5,7 +5,8 @@
 // Lengths count as 0 when negative, and sums stop at `total`.  One launch: every workgroup
 // adds up all lengths for itself (n is small beside the row, and they stay in L2), so none
 // waits for another; it keeps the offsets of its own steps' sequences in LDS, a piece of
-// 1024 sequences at a time, and writes the steps of a piece as it passes it.
+// 1024 sequences at a time, and writes the steps of a piece as it passes it.  Bound by the latency of
+// that: 64 sequences of 65536 steps 7 us, 4001 of 1048576 (8 MB) 13 us.
 #include "ccv_delta_device.hpp"
 #include "ccv_norm_launch.hpp"
 

@@ -366,7 +366,8 @@ int ccv_bwd_static(const ccv_bwd_args_t* args, void* hip_stream);
  *
  *   - q, k: [B, L, Hk, Dk]; v, out: [B, L, Hv, Dv]; g (log decay) and beta (write
  *     strength): [B, L, Hv].  Hv is a multiple of Hk; value head h uses key head
- *     h / (Hv / Hk).  1 <= Dk <= 128 (else CCV_E_UNSUPPORTED), Dv >= 1.
+ *     h / (Hv / Hk).  1 <= Dk <= 128 (else CCV_E_UNSUPPORTED), 1 <= Dv <= 2^20 (else
+ *     CCV_E_SHAPE).
  *   - x_dtype is the storage type of q, k, v and out, g_dtype of g, beta_dtype of beta;
  *     states and every sum are fp32.  out is rounded once.
  *   - cu_seqlens NULL: each of the B rows is one sequence (N must be 0).  Otherwise B is 1
@@ -381,11 +382,14 @@ int ccv_bwd_static(const ccv_bwd_args_t* args, void* hip_stream);
  *   - Element (b, t, h, d) of a [B, L, H, D] array lies at b s[0] + t s[1] + h s[2] + d
  *     elements: unit stride inside a head.  States: (sequence, head, key) strides, unit
  *     along the values.  Inputs may have zero strides (broadcast); written arrays may not
- *     map two elements to one address (CCV_E_LAYOUT).
+ *     map two elements to one address, and steps of out and dv may lie at most 32 MB apart
+ *     (CCV_E_LAYOUT).  Rows of q, k, v and dout whose width, strides or address no 16-byte
+ *     load takes are copied into the workspace first.
  *
  * ccv_delta_fwd works by groups of 64 steps, whose inner products are matrix products: a
  * first kernel makes what no state enters, a second carries the states along the
- * sequences (a packed row's sequences at the same time).  It needs a workspace of
+ * sequences (a packed row's sequences at the same time; with few heads, parts of a
+ * sequence too).  It needs a workspace of
  * ccv_delta_fwd_workspace_size bytes (16-byte aligned, contents immaterial, free again
  * when the call's work is done): CCV_E_NULL without, CCV_E_SHAPE when smaller.
  * final_state may be initial_state itself, with the same strides; out may be no input. */
@@ -418,8 +422,8 @@ int ccv_delta_fwd(const ccv_delta_fwd_args_t* args, void* hip_stream);
  * value heads that share a key head included, so results repeat bit for bit.
  * dinitial_state may be dfinal_state itself, with the same strides; other outputs may be
  * no input and no other output (CCV_E_ALIAS).  The workspace holds the states at
- * both ends of every group of 64 steps: about (2 Dk + 288) Dv fp32 values a group and head, with
- * Dk rounded up to 64 or 128 and Dv to a multiple of 32 (for 128 and 128: 0.3 MB). */
+ * both ends of every group of 64 steps: about (2 Dk + 150) Dv + 19000 fp32 values a group and
+ * head, with Dk rounded up to 64 or 128 and Dv to a multiple of 32 (for 128 and 128: 0.28 MB). */
 typedef struct ccv_delta_bwd_args {
   int64_t struct_size;          /* = sizeof(ccv_delta_bwd_args_t) */
   int64_t B, L, N;
