@@ -34,14 +34,48 @@ __global__ __launch_bounds__(256) void pack_kernel(DeltaPackArgs a) {
 // Sequence s holds the steps [cu[s], cu[s + 1]); the offsets count as their running maximum,
 // clamped to [0, L], so that no table can lead outside the row.  The steps past the last
 // sequence are sequence `nseq`, whose outputs are zeros.  One workgroup: the longest part
-// is a binary search a chunk (64 sequences of 65536 steps: 11 us, 7 of 3011 steps: 7 us).
+// is a binary search a chunk (64 sequences of 65536 steps: 7 us, 7 of 3011 steps: 4 us).
+struct Most { static __device__ inline int of(int x, int y) { return x > y ? x : y; } };
+struct Sum { static __device__ inline int of(int x, int y) { return x + y; } };
+
+// Running results over the workgroup's 1024 threads of values that are not negative, from `from` on, which becomes
+// the result of all.  `wave` may be used again after the next barrier.
+template <class OP>
+__device__ inline int running(int x, int& from, int (&wave)[16]) {
+  const auto row = [](int v, auto ctrl, auto rows) {
+    return OP::of(v, __builtin_amdgcn_update_dpp(0, v, ctrl.value, rows.value, 0xf, false));
+  };
+  using std::integral_constant;
+  x = row(x, integral_constant<int, 0x111>(), integral_constant<int, 0xf>());      // rows of 16: 1, 2, 4, 8 lanes back
+  x = row(x, integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+  x = row(x, integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+  x = row(x, integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+  x = row(x, integral_constant<int, 0x142>(), integral_constant<int, 0xa>());      // a row's last lane to the next row
+  x = row(x, integral_constant<int, 0x143>(), integral_constant<int, 0xc>());      // lane 31 to the upper half
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 63) wave[w] = x;
+  __syncthreads();
+  int before = from, all = from;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if (k == w) before = all;
+    all = OP::of(all, wave[k]);
+  }
+  from = all;
+  return OP::of(before, x);
+}
+
 __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
-  __shared__ int mx[1024], sm[1024];
+  __shared__ int waves[3][16], count[1024], at[1024], ends[1024];
   const int tid = threadIdx.x, n = a.nseq + 1, L = (int)a.L;
   int32_t* begin = a.cstart + (a.nseq + 2);
-  int cmax = 0, csum = 0;
+  int last = 0, chunks = 0, parts = 0;
+  count[tid] = 0;
+  // the order in which the passes over the chunks take the sequences: longest first, so that no long one
+  // starts when the others are done (which of two of one length comes first changes no result)
+  const auto bucket = [](int chunks) { return chunks < 1023 ? 1023 - chunks : 0; };
   for (int base = 0; base < n; base += 1024) {
-    const int i = base + tid;
+    const int i = base + tid, before = last;
     int e = 0;
     if (i < a.nseq) {
       const int x = a.cu[i + 1];
@@ -49,98 +83,54 @@ __global__ __launch_bounds__(1024) void table_kernel(DeltaArgs a) {
     } else if (i == a.nseq) {
       e = L;
     }
-    mx[tid] = e;
+    const int end = running<Most>(e, last, waves[0]);
+    ends[tid] = end;
     __syncthreads();
-    for (int d = 1; d < 1024; d <<= 1) {
-      const int o = tid >= d ? mx[tid - d] : 0;
-      __syncthreads();
-      mx[tid] = mx[tid] > o ? mx[tid] : o;
-      __syncthreads();
-    }
-    const int end = mx[tid] > cmax ? mx[tid] : cmax;
-    const int before = tid ? (mx[tid - 1] > cmax ? mx[tid - 1] : cmax) : cmax;
-    sm[tid] = i < n ? (end - before + kDeltaChunk - 1) / kDeltaChunk : 0;
-    __syncthreads();
-    for (int d = 1; d < 1024; d <<= 1) {
-      const int o = tid >= d ? sm[tid - d] : 0;
-      __syncthreads();
-      sm[tid] += o;
-      __syncthreads();
-    }
+    const int t0 = tid ? ends[tid - 1] : before;
+    const int c = i < n ? (end - t0 + kDeltaChunk - 1) / kDeltaChunk : 0;
+    const int upto = running<Sum>(c, chunks, waves[1]);
     if (i < n) {
-      a.cstart[i + 1] = csum + sm[tid];
-      begin[i] = before;
+      a.cstart[i + 1] = upto;
+      begin[i] = t0;
       if (i == a.nseq) begin[n] = L;
+      else atomicAdd(&count[bucket(c)], 1);
     }
-    const int m1 = mx[1023], s1 = sm[1023];
+    if (a.part_chunks) {      // the parts of each sequence, one at least
+      const int p = i < a.nseq ? (c + a.part_chunks - 1) / a.part_chunks : 1;
+      const int up = running<Sum>(i < n ? (p > 1 ? p : 1) : 0, parts, waves[2]);
+      if (i < n) a.pstart[i + 1] = up;
+    }
     __syncthreads();
-    cmax = m1 > cmax ? m1 : cmax;
-    csum += s1;
   }
-  if (tid == 0) a.cstart[0] = 0;
-  mx[tid] = 0;
+  if (tid == 0) {
+    a.cstart[0] = 0;
+    if (a.part_chunks) a.pstart[0] = 0;
+    a.order[a.nseq] = a.nseq;
+  }
+  int zero = 0;
+  at[tid] = running<Sum>(count[tid], zero, waves[0]) - count[tid];
   __threadfence_block();
   __syncthreads();
-  // the order in which the passes over the chunks take the sequences: longest first, so that no long one
-  // starts when the others are done (which of two of one length comes first changes no result)
-  const auto bucket = [&](int s) {
-    const int n = a.cstart[s + 1] - a.cstart[s];
-    return n < 1023 ? 1023 - n : 0;
+  for (int s = tid; s < a.nseq; s += 1024) a.order[atomicAdd(&at[bucket(a.cstart[s + 1] - a.cstart[s])], 1)] = s;
+  // the last of the first `n` entries of an increasing table that is <= x
+  const auto find = [&](const int32_t* table, int x) {
+    int lo = 0, hi = a.nseq;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (table[m] <= x) lo = m;
+      else hi = m - 1;
+    }
+    return lo;
   };
-  for (int s = tid; s < a.nseq; s += 1024) atomicAdd(&mx[bucket(s)], 1);
-  __syncthreads();
-  sm[tid] = mx[tid];
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    const int o = tid >= d ? sm[tid - d] : 0;
-    __syncthreads();
-    sm[tid] += o;
-    __syncthreads();
-  }
-  sm[tid] -= mx[tid];
-  __syncthreads();
-  for (int s = tid; s < a.nseq; s += 1024) a.order[atomicAdd(&sm[bucket(s)], 1)] = s;
-  if (tid == 0) a.order[a.nseq] = a.nseq;
-  if (a.part_chunks) {      // the parts of each sequence, one at least
-    int psum = 0;
-    for (int base = 0; base < n; base += 1024) {
-      const int i = base + tid, c = i < a.nseq ? (a.cstart[i + 1] - a.cstart[i] + a.part_chunks - 1) / a.part_chunks : 1;
-      __syncthreads();
-      sm[tid] = i < n ? (c > 1 ? c : 1) : 0;
-      __syncthreads();
-      for (int d = 1; d < 1024; d <<= 1) {
-        const int o = tid >= d ? sm[tid - d] : 0;
-        __syncthreads();
-        sm[tid] += o;
-        __syncthreads();
-      }
-      if (i < n) a.pstart[i + 1] = psum + sm[tid];
-      psum += sm[1023];
-    }
-    if (tid == 0) a.pstart[0] = 0;
-    __threadfence_block();
-    __syncthreads();
-    for (int p = tid; p < a.parts; p += 1024) {
-      int lo = 0, hi = a.nseq;                       // the last sequence whose first part is <= p
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (a.pstart[m] <= p) lo = m;
-        else hi = m - 1;
-      }
-      a.ptable[2 * p] = p < psum ? lo : n;
-      a.ptable[2 * p + 1] = p < psum ? p - a.pstart[lo] : 0;
-    }
+  for (int p = tid; a.part_chunks && p < a.parts; p += 1024) {
+    const int s = find(a.pstart, p);
+    a.ptable[2 * p] = p < parts ? s : n;
+    a.ptable[2 * p + 1] = p < parts ? p - a.pstart[s] : 0;
   }
   for (int c = tid; c < a.nchunks; c += 1024) {
     int s = a.nseq, t0 = 0, len = 0;
-    if (c < csum) {
-      int lo = 0, hi = a.nseq;                       // the last sequence whose first chunk is <= c
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (a.cstart[m] <= c) lo = m;
-        else hi = m - 1;
-      }
-      s = lo;
+    if (c < chunks) {
+      s = find(a.cstart, c);
       t0 = begin[s] + (c - a.cstart[s]) * kDeltaChunk;
       len = begin[s + 1] - t0;
       len = len < kDeltaChunk ? len : kDeltaChunk;

@@ -5,6 +5,8 @@ elements, then by a tree: the statistics are within 2^-20 of the row's largest d
 2^-22 of its mean (rounding of x - mean), so an fp32 element is within 2^-18 (|n w| + |w|), and
 rounds once more in 16 bits.  dx has three such terms with |dout w rstd| as their scale; column
 sums over r rows are within 2^-20 sqrt(r) of the largest term, plus their own rounding."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -225,3 +227,19 @@ def test_tables_of_a_random_row():
         cu, seq, pos = ccv.sequence_tables(torch.from_numpy(lengths).cuda(), total)
         for got, w in zip((cu, seq[0], pos[0]), ref.tables_reference(lengths.tolist(), total)):
             assert np.array_equal(got.cpu().numpy(), w), (n, total)
+
+
+def test_tables_at_any_address():
+    """The low-level call with outputs 4 bytes off a 16-byte boundary."""
+    lengths = torch.tensor([70, 0, 5000, 3, 4096], dtype=torch.int32).cuda()
+    total = 9300
+    buf = [torch.full((total + 8,), -7, dtype=torch.int32, device="cuda") for _ in range(3)]
+    a = ccv.ccv_seq_tables_args_t(struct_size=ctypes.sizeof(ccv.ccv_seq_tables_args_t), N=5, total=total, lengths=lengths.data_ptr(),
+                                  cu_seqlens=buf[0].data_ptr() + 4, seq_idx=buf[1].data_ptr() + 4, positions=buf[2].data_ptr() + 12)
+    assert ccv.ccv_seq_tables(a) == 0
+    torch.cuda.synchronize()
+    cu, seq, pos = ref.tables_reference(lengths.tolist(), total)
+    for t, at, w in ((buf[0], 1, cu), (buf[1], 1, seq), (buf[2], 3, pos)):
+        got = t.cpu().numpy()
+        assert np.array_equal(got[at:at + len(w)], w)
+        assert (got[:at] == -7).all() and (got[at + len(w):] == -7).all()
