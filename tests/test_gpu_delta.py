@@ -528,3 +528,84 @@ def test_fp16_subnormals(heads):
     want = ref.delta_gradients(q, k, v, g, beta, dout, None, None, h0)
     for name, t in (("dq", got[0]), ("dg", got[3]), ("dbeta", got[4]), ("dh0", got[5])):
         ref.assert_near(name, t, want[name], 2)
+
+
+# the same calls where 16-bit inputs take whole columns a wave, and where a sequence runs in parts
+FORMS = [("columns", 16, 64, [5, 0, 64, 1, 130]), ("parts", 1, 2, [1100, 0, 1500])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_padding_of_either_form(dtype, form):
+    """Steps behind the last sequence are not looked at, and give zeros."""
+    what, Hk, Hv, lengths = FORMS[form]
+    live = sum(lengths)
+    q, k, v, g, beta, h0 = ref.delta_inputs(1, live + 70, Hk, Hv, 64, 48, dtype, seed=form, seqs=len(lengths), decay=0.05)
+    dout = torch.randn(v.shape, generator=torch.Generator().manual_seed(1)).to(v.dtype)
+    bad = [t.clone() for t in (q, k, v, g, beta, dout)]
+    for t in bad:
+        t[:, live:] = NAN
+    cu = ref.cu_of(lengths).cuda()
+    out, ht = ccv.gated_delta_rule_fwd(*gpu(*bad[:5]), cu_seqlens=cu, initial_state=h0.cuda(), return_final_state=True)
+    got = ccv.gated_delta_rule_bwd(*gpu(*bad), cu_seqlens=cu, initial_state=h0.cuda(), return_dinitial_state=True)
+    want = ref.delta_gradients(q, k, v, g, beta, dout, None, lengths, h0)
+    ref.assert_near("out", out, want["out"], 1, what)
+    ref.assert_near("final_state", ht, want["ht"], 1, what)
+    for name, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got):
+        ref.assert_near(name, t, want[name], 2, what)
+        if name != "dh0":
+            assert not t[:, live:].any(), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,L,Hk,Hv", [(16, 70, 8, 16), (1, 1100, 1, 2)])
+def test_strides_of_either_form(dtype, B, L, Hk, Hv):
+    """Views of one wider buffer at odd offsets, heads first, outputs with a stride of their own, in place states."""
+    Dk, Dv = 64, 61
+    q, k, v, g, beta, h0 = ref.delta_inputs(B, L, Hk, Hv, Dk, Dv, dtype, seed=4, decay=0.05)
+    off = 3
+    buf = torch.full((B, L, off + 2 * Hk * Dk + Hv * Dv + 1), NAN, dtype=q.dtype, device="cuda")
+    a, b = off + Hk * Dk, off + 2 * Hk * Dk
+    views = [buf[..., off:a].unflatten(2, (Hk, Dk)), buf[..., a:b].unflatten(2, (Hk, Dk)), buf[..., b:b + Hv * Dv].unflatten(2, (Hv, Dv))]
+    for view, t in zip(views, (q, k, v)):
+        view.copy_(t)
+    check_fwd(q, k, v, g, beta, h0, what="fused", views=views + gpu(g, beta))
+    check_bwd(q, k, v, g, beta, h0, what="fused", views=views + gpu(g, beta))
+    views = [t.cuda().transpose(1, 2).contiguous().transpose(1, 2) for t in (q, k, v, g, beta)]
+    check_bwd(q, k, v, g, beta, h0, what="heads first", views=views)
+    state = h0.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    out, s = ccv.gated_delta_rule_fwd(*views, initial_state=state, return_final_state=True, final_state_out=state)
+    want, wht = ref.delta_reference(q, k, v, g, beta, None, None, h0)
+    ref.assert_near("out", out, want)
+    ref.assert_near("final_state", state, wht)
+
+
+@pytest.mark.parametrize("B,L,H", [(16, 130, 16), (1, 1300, 1)])
+def test_either_form_repeats_and_replays(B, L, H):
+    """Bit for bit: again, on another stream, and in a graph replayed with new inputs."""
+    first = ref.delta_inputs(B, L, H, H, 64, 64, "f16", seed=30, decay=0.05)
+    a = gpu(*first)
+    dout = torch.ones_like(a[2])
+
+    def work():
+        o, s = ccv.gated_delta_rule_fwd(*a[:5], initial_state=a[5], return_final_state=True)
+        return [o, s, *ccv.gated_delta_rule_bwd(*a[:5], dout, initial_state=a[5], return_dinitial_state=True)]
+
+    once = work()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for t, u in zip(once, work()):
+            assert torch.equal(t, u)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        static = work()
+    for r in range(3):
+        for t, n in zip(a, ref.delta_inputs(B, L, H, H, 64, 64, "f16", seed=31 + r, decay=0.05)):
+            t.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, u in zip([t.clone() for t in static], work()):
+            assert torch.equal(t, u), r
