@@ -489,41 +489,37 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
       return *reinterpret_cast<const f32x4*>(&Gl[b][which][32 * (it >> 1) + 4 * (it & 1) + 8 * g4]);
     };
     lds_barrier();
-    // K S, and (Q S)^T; the next 32 keys' fragments are read before these are multiplied
+    // K S, and (Q S)^T
     f32x4 hi[4] = {}, lo[4] = {}, qs[4] = {};
     const int es = column_exponent<DT>(S);
-    u32x4 kf[1][4], qf[1][4];
+    u32x4 kf[4], qf[4];
     const auto read_rows = [&](int s) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        kf[0][t] = *reinterpret_cast<const u32x4*>(Kb + (16 * t + r) * LDK + 32 * s + 8 * g4);
-        qf[0][t] = *reinterpret_cast<const u32x4*>(Qb + (16 * t + r) * LDK + 32 * s + 8 * g4);
+        kf[t] = *reinterpret_cast<const u32x4*>(Kb + (16 * t + r) * LDK + 32 * s + 8 * g4);
+        qf[t] = *reinterpret_cast<const u32x4*>(Qb + (16 * t + r) * LDK + 32 * s + 8 * g4);
       }
     };
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       read_rows(s);
-      
       const Cut<DT> x = cut<DT>(join(S[2 * s], S[2 * s + 1]), es);
 #pragma unroll
       for (int p = PS - 1; p > 0; --p)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          lo[t] = mfma16<DT>(kf[0][t], x.p[p], lo[t]);
-          if (BWD || p < 2) qs[t] = mfma16<DT>(x.p[p], qf[0][t], qs[t]);
+          lo[t] = mfma16<DT>(kf[t], x.p[p], lo[t]);
+          if (BWD || p < 2) qs[t] = mfma16<DT>(x.p[p], qf[t], qs[t]);
         }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        hi[t] = mfma16<DT>(kf[0][t], x.p[0], hi[t]);
-        qs[t] = mfma16<DT>(x.p[0], qf[0][t], qs[t]);
+        hi[t] = mfma16<DT>(kf[t], x.p[0], hi[t]);
+        qs[t] = mfma16<DT>(x.p[0], qf[t], qs[t]);
       }
-      
     }
     load_W(n);
-    
     store_rows(b ^ 1);                     // its readers were done at the barrier
     load_rows(ahead(2));
-    
     if constexpr (BWD) {
       const __amdgpu_buffer_rsrc_t sb = So.piece(true);
 #pragma unroll
@@ -545,13 +541,12 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
       rf[s] = split8<3>(join(R[0], R[1]));
     }
     load_V(nn);
-    
-    u32x4 tf[1][2][2];
+    u32x4 tf[2][2];
     const auto read_columns = [&](int c) {
 #pragma unroll
       for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) tf[0][o][s] = get_joined_t<LDK>(Kb, s, c, o, l);
+        for (int s = 0; s < 2; ++s) tf[o][s] = get_joined_t<LDK>(Kb, s, c, o, l);
     };
     // N = W (beta R); W is lower triangular
     f32x4 N[4] = {};
@@ -565,7 +560,6 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
           N[it] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xW[x].p[i], rf[s].p[q - i], N[it], 0, 0, 0);
         }
     load_P(n);
-    
     if constexpr (BWD) {
       const __amdgpu_buffer_rsrc_t nb = No.piece(true);
 #pragma unroll
@@ -585,21 +579,19 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         read_columns(c);
-        
         f32x4 t[2] = {};
 #pragma unroll
         for (int p = PS - 1; p >= 0; --p)
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int o = 0; o < 2; ++o) t[o] = mfma16<DT>(tf[0][o][s], yf[s].p[p], t[o]);
+            for (int o = 0; o < 2; ++o) t[o] = mfma16<DT>(tf[o][s], yf[s].p[p], t[o]);
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           t[o] = scaled<DT>(t[o], ey);
 #pragma unroll
           for (int e = 0; e < 4; ++e) S[2 * c + o][e] = __builtin_fmaf(S[2 * c + o][e], last, t[o][e]);
         }
-        
       }
     }
     int er[4] = {};                        // the rows of (Q S)^T are columns of S
