@@ -840,6 +840,12 @@ def _at(t):
     return (t.data_ptr(), s[0], s[1], s[2])
 
 
+def _step_at(t):
+    """The same of a tensor without the dimension of steps."""
+    s = t.stride()
+    return (t.data_ptr(), s[0], 0, s[1])
+
+
 # ---- the gated delta rule ------------------------------------------------------------------
 
 def _same_device(x, **others):
@@ -852,13 +858,16 @@ def _same_device(x, **others):
     return d
 
 
-def _delta_sizes(q, k, v, g, beta):
-    """(B, L, Hk, Hv, Dk, Dv) of the five inputs, checked against each other."""
+def _delta_sizes(q, k, v, g, beta, one=False):
+    """(B, L, Hk, Hv, Dk, Dv) of the five inputs, checked against each other; one: a single step
+    without its dimension."""
     qs, vs = q.shape, v.shape
-    if len(qs) != 4 or k.shape != qs or len(vs) != 4 or vs[:2] != qs[:2]:
+    lead = 1 if one else 2
+    if len(qs) != lead + 2 or k.shape != qs or len(vs) != lead + 2 or vs[:lead] != qs[:lead]:
         raise ValueError("expected q and k [B, L, Hk, Dk] and v [B, L, Hv, Dv]")
-    B, L, Hk, Dk = qs
-    Hv, Dv = vs[2], vs[3]
+    Hk, Dk = qs[lead:]
+    Hv, Dv = vs[lead:]
+    B, L = qs[0], 1 if one else qs[1]
     if Hk < 1 or Hv < 1 or Hv % Hk:
         raise ValueError("the value heads must be a multiple of the key heads")
     if not 1 <= Dk <= 128 or Dv < 1:
@@ -866,7 +875,7 @@ def _delta_sizes(q, k, v, g, beta):
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must have one dtype")
     for name, t in (("g", g), ("beta", beta)):
-        if t.shape != (B, L, Hv):
+        if t.shape != vs[:-1]:
             raise ValueError(f"{name} must be [B, L, Hv]")
     for name, t in (("q", q), ("g", g), ("beta", beta)):
         if t.dtype not in DTYPE_CODE:
@@ -927,7 +936,7 @@ def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     if _delta_states("initial_state", initial_state, shape) is not None:
         initial_state = _unit_heads(initial_state)
     if out is None:
-        out = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=device)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     elif out.dtype != v.dtype or tuple(out.shape) != (B, L, Hv, Dv) or (out.stride(-1) != 1 and Dv > 1):
         raise ValueError("out must be [B, L, Hv, Dv] in v's dtype with unit stride in its last dimension")
     ht = None
@@ -969,7 +978,7 @@ def gated_delta_rule_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
         initial_state = _unit_heads(initial_state)
     if _delta_states("dfinal_state", dfinal_state, shape) is not None:
         dfinal_state = _unit_heads(dfinal_state)
-    dq, dk, dv, dg, db = (torch.empty(t.shape, dtype=t.dtype, device=device) for t in (q, k, v, g, beta))
+    dq, dk, dv, dg, db = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v, g, beta))
     dh = torch.empty(shape, dtype=torch.float32, device=device) if return_dinitial_state else None
     _CALLS["ccv_delta_bwd"](device, B, L, N, Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype],
                             Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v), *_at(g), *_at(beta),
@@ -1022,9 +1031,7 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     its outputs are zeros.  Two rows may not use one slot.  Returns out with v's shape.
     """
     one = q.dim() == 3
-    if one:
-        q, k, v, g, beta = (t.unsqueeze(1) for t in (q, k, v, g, beta))
-    B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta)
+    B, L, Hk, Hv, Dk, Dv = _delta_sizes(q, k, v, g, beta, one)
     device = _same_device(q, k=k, v=v, g=g, beta=beta, state=state, state_indices=state_indices, out=out)
     if state.dtype != torch.float32 or state.dim() != 4 or state.shape[1:] != (Hv, Dk, Dv):
         raise ValueError("state must be float32 [slots, Hv, Dk, Dv]")
@@ -1037,50 +1044,41 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
         raise ValueError("more rows than states")
     q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
     if out is None:
-        o = torch.empty(B, L, Hv, Dv, dtype=v.dtype, device=device)
-    else:
-        o = out.unsqueeze(1) if one else out
-        if o.dtype != v.dtype or tuple(o.shape) != (B, L, Hv, Dv) or (o.stride(-1) != 1 and Dv > 1):
-            raise ValueError("out must have v's shape and dtype with unit stride in its last dimension")
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+    elif out.dtype != v.dtype or out.shape != v.shape or (out.stride(-1) != 1 and Dv > 1):
+        raise ValueError("out must have v's shape and dtype with unit stride in its last dimension")
+    at = _step_at if one else _at
     _CALLS["ccv_delta_update"](device, B, L, state.shape[0], Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype],
-                               DTYPE_CODE[beta.dtype], Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v),
-                               *_at(g), *_at(beta), _p(state_indices), *_at(state), *_at(o))
-    return o.squeeze(1) if one else o
+                               DTYPE_CODE[beta.dtype], Dk ** -0.5 if scale is None else scale, *at(q), *at(k), *at(v),
+                               *at(g), *at(beta), _p(state_indices), *_at(state), *at(out))
+    return out
 
 
 # ---- layer norm ------------------------------------------------------------------------------
 
 def _norm_rows(x):
-    """x as [n0, n1, width] with unit stride along the width, copied only where its strides
-    allow no such view."""
+    """(x, (n0, n1, width), strides of the first two): x as [n0, n1, width] with unit stride along
+    the width, copied only where its strides allow no such view."""
     if x.dim() < 1:
         raise ValueError("x needs a last dimension to be normalised")
     if x.shape[-1] > 1 and x.stride(-1) != 1:
         x = x.contiguous()
-    if x.dim() == 3:
-        return x
-    if x.dim() < 3:
-        return x[(None,) * (3 - x.dim())]
-    try:
-        return x.view(-1, x.shape[-2], x.shape[-1])
-    except RuntimeError:
-        return x.contiguous().view(-1, x.shape[-2], x.shape[-1])
+    dim = x.dim()
+    if dim > 3:
+        x = x.flatten(0, dim - 3)
+    return (x, (1,) * (3 - dim) + tuple(x.shape), (0,) * (3 - dim) + x.stride()[:-1])
 
 
 def _norm_weights(x, weight, bias):
+    width = x.shape[-1:]
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and (t.shape != x.shape[-1:] or t.dtype not in DTYPE_CODE):
+        if t is not None and (t.shape != width or t.dtype not in DTYPE_CODE):
             raise ValueError(f"{name} must be [width] in float32, float16 or bfloat16")
     if weight is not None and bias is not None and bias.dtype != weight.dtype:
         raise ValueError("bias must have the weight's dtype")
     if x.dtype not in DTYPE_CODE:
         raise ValueError(f"x must be float32, float16 or bfloat16, not {x.dtype}")
     return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous())
-
-
-def _rows_of(out, shape):
-    """The row strides of a contiguous tensor seen as [n0, n1, width]."""
-    return shape[1] * shape[2], shape[2]
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -1093,18 +1091,17 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     """
     weight, bias = _norm_weights(x, weight, bias)
     device = _same_device(x, weight=weight, bias=bias, out=out)
-    rows = _norm_rows(x)
+    rows, shape, s = _norm_rows(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous with x's shape and dtype")
     mean = rstd = None
     if return_stats:
         mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
     w = weight if weight is not None else bias if bias is not None else x
-    s = rows.stride()
-    _CALLS["ccv_norm_fwd"](device, *rows.shape, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], eps, 0, rows.data_ptr(), s[0], s[1],
-                           _p(weight), _p(bias), out.data_ptr(), *_rows_of(out, rows.shape), _p(mean), _p(rstd))
+    _CALLS["ccv_norm_fwd"](device, *shape, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], eps, 0, rows.data_ptr(), s[0], s[1],
+                           _p(weight), _p(bias), out.data_ptr(), shape[1] * shape[2], shape[2], _p(mean), _p(rstd))
     return (out, mean, rstd) if return_stats else out
 
 
@@ -1127,13 +1124,12 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.
     wd = weight.dtype if weight is not None else weight_dtype or x.dtype
     if wd not in DTYPE_CODE:
         raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
-    rows, drows = _norm_rows(x), _norm_rows(dout)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=device) if want_dx else None
+    (rows, shape, s), (drows, _, d) = _norm_rows(x), _norm_rows(dout)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
     dw = torch.empty(x.shape[-1], dtype=wd, device=device) if want_dweight else None
     db = torch.empty(x.shape[-1], dtype=wd, device=device) if want_dbias else None
-    s, d = rows.stride(), drows.stride()
-    _CALLS["ccv_norm_bwd"](device, *rows.shape, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], rows.data_ptr(), s[0], s[1], _p(weight),
-                           drows.data_ptr(), d[0], d[1], mean.data_ptr(), rstd.data_ptr(), _p(dx), *_rows_of(dx, rows.shape),
+    _CALLS["ccv_norm_bwd"](device, *shape, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], rows.data_ptr(), s[0], s[1], _p(weight),
+                           drows.data_ptr(), d[0], d[1], mean.data_ptr(), rstd.data_ptr(), _p(dx), shape[1] * shape[2], shape[2],
                            _p(dw), _p(db))
     return dx, dw, db
 
@@ -1180,8 +1176,6 @@ def sequence_tables(lengths: torch.Tensor, total: int):
         raise ValueError("total must not be negative")
     device = _same_device(lengths)
     n = lengths.numel()
-    cu = torch.empty(n + 1, dtype=torch.int32, device=device)
-    seq = torch.empty(1, total, dtype=torch.int32, device=device)
-    pos = torch.empty(1, total, dtype=torch.int32, device=device)
+    cu, seq, pos = lengths.new_empty(n + 1), lengths.new_empty((1, total)), lengths.new_empty((1, total))
     _CALLS["ccv_seq_tables"](device, n, total, lengths.data_ptr(), cu.data_ptr(), seq.data_ptr(), pos.data_ptr())
     return cu, seq, pos
