@@ -149,6 +149,9 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   groups = round_up(groups, 8);
   if (groups * (a->Dvp / 16) > INT32_MAX) return CCV_E_SHAPE;
   a->nchunks = (int32_t)nch;
+  // key heads enough for the chip's eight dies to get as many each
+  a->share = (int64_t)a->nseq * z.Hk >= 64 ? (int32_t)(z.Hv / z.Hk) : 1;
+  a->share_prep = nch * z.Hk >= 64 ? (int32_t)(z.Hv / z.Hk) : 1;
   // Which kernels: both sides of each bound stand measured beside the kernels (ccv_delta_scan.hip, ccv_delta_bwd.hip).
   a->waves = z.x_dtype != CCV_F32 && groups * (a->Dvp / 16) >= 1024;
   a->waves_back = a->waves && z.x_dtype == CCV_F16;

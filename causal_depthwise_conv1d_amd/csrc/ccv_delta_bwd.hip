@@ -44,8 +44,8 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
   __shared__ f32x4 Pd[NT][4][64];          // scale P^T dO; then del (K dS'), from the lane that read it
   __shared__ f32x4 Ud[MT][NT][4][64];      // Q^T (scale gam dO); then Y in its first tile, likewise
-  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
-  if (hs >= heads) return;
+  uint32_t hs, slice;
+  if (!place(a.share, heads, slices, &hs, &slice)) return;
   const int sh = hs / a.Hv, h = hs - sh * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB;
   const Part part = part_at(a, sh);
   const int seq = part.seq;
@@ -389,8 +389,8 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(Delt
   constexpr int NW = kColumnWaves, NA = InPlanes<DT>::n, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
   __shared__ uint16_t Kl[2][64][LDK], Ql[2][64][LDK];
   __shared__ float Gl[2][3][64];           // gam, del, beta
-  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
-  if (hs >= heads) return;
+  uint32_t hs, slice;
+  if (!place(a.share, heads, slices, &hs, &slice)) return;
   const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk);
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
   if (seq >= a.nseq) {                     // steps of no sequence have no gradient
@@ -944,9 +944,9 @@ __global__ __launch_bounds__(256) void gates_kernel(DeltaArgs a, int64_t items) 
 
 template <int DT, int DKP, int NT>
 void launch_rev(const DeltaArgs& a, hipStream_t st) {
-  const uint32_t heads = (a.part_chunks ? (uint32_t)a.parts : (uint32_t)(a.nseq + (a.packed ? 1 : 0))) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t heads = (a.part_chunks ? (uint32_t)a.parts : (uint32_t)(a.nseq + (a.packed ? 1 : 0))) * a.Hv;
   const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
-  const dim3 grid(pad * slices);
+  const dim3 grid(places(a.share, heads, slices));
   if constexpr (NT == 1) {
     if (a.part_chunks) {
       reverse_kernel<DT, DKP, 1, true><<<grid, 512, 0, st>>>(a, heads, slices);
@@ -957,9 +957,9 @@ void launch_rev(const DeltaArgs& a, hipStream_t st) {
 }
 template <int DT, int DKP>
 void launch_rev_waves(const DeltaArgs& a, hipStream_t st) {
-  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv;
   const uint32_t slices = (a.Dvp + 16 * kColumnWaves - 1) / (16 * kColumnWaves);
-  reverse_wave_kernel<DT, DKP><<<dim3(pad * slices), 64 * kColumnWaves, 0, st>>>(a, heads, slices);
+  reverse_wave_kernel<DT, DKP><<<dim3(places(a.share, heads, slices)), 64 * kColumnWaves, 0, st>>>(a, heads, slices);
 }
 template <int DT>
 void launch_rev(const DeltaArgs& a, int nt, hipStream_t st) {

@@ -56,6 +56,7 @@ struct DeltaArgs {
   float* part;                                  // backward: [ch][slices][kDeltaPart] sums over a slice's values
   float* qpart;                                 // backward: [ch][qslices][64] dG by the state, likewise
   float* pairs;                                 // backward: [ch][kDeltaPairs] dG by pairs of steps; <S, dS'>
+  int32_t share, share_prep;                    // value heads of one key head that go to one die together, or 1
   int32_t Dkp, slices, qslices;                 // value slices of the pass from the end, and of the forward one
   int32_t waves;                                // the forward pass holds whole columns a wave; W has its rows in joined() order
   int32_t waves_back;                           // the backward's pass likewise, W and P transposed

@@ -7,7 +7,7 @@
 // workgroups of 16-bit inputs share a CU.  W goes out as three bf16 planes (fp32 states need them), P as
 // two where the outputs are 16-bit, both without the quarter above the diagonal blocks of 32, which is
 // zero.  4 x 4096 steps, 16 heads of 128 in bf16: 62 us, 260 MB at 4.2 TB/s; with whole planes and K's
-// and W's LDS apart it took 78.  65536 packed steps, 10 key and 20 value heads in fp16: 295 us.
+// and W's LDS apart it took 78.  65536 packed steps, 10 key and 20 value heads in fp16: 285 us.
 // G is summed in 64 bits, so that differences of steps that lie far down a strongly
 // decaying chunk keep 32 bits.  A decay of g < -2000 (and -inf, a forgotten state) counts
 // as -2000: e^-2000 is 0 in fp32 with room to spare, and no inf - inf arises.
@@ -159,7 +159,9 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   __shared__ float Al[64][LDA];                                        // A, then P
   __shared__ double G[64];
   __shared__ float bt[64];
-  const int ch = blockIdx.x, c = ch / a.Hv, h = ch - c * a.Hv, hk = h / (a.Hv / a.Hk);
+  uint32_t item, slice;
+  if (!place(a.share_prep, (uint32_t)a.nchunks * a.Hv, 1, &item, &slice)) return;
+  const int ch = item, c = ch / a.Hv, h = ch - c * a.Hv, hk = h / (a.Hv / a.Hk);
   const Chunk k = chunk_at(a, c);
   if (k.n <= 0 || k.seq >= a.nseq) return;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
@@ -325,7 +327,7 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
 
 template <int DT, int DKP>
 void launch_prep(const DeltaArgs& a, bool bwd, hipStream_t st) {
-  const dim3 grid((uint32_t)((int64_t)a.nchunks * a.Hv));
+  const dim3 grid(places(a.share_prep, (int64_t)a.nchunks * a.Hv, 1));
   if (bwd) prep_kernel<DT, DKP, true><<<grid, 256, 0, st>>>(a);
   else prep_kernel<DT, DKP, false><<<grid, 256, 0, st>>>(a);
 }

@@ -47,8 +47,8 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
   auto& Ql = qn.q;
   auto& Np = qn.n.p;
   auto& Nd = qn.n.d;
-  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
-  if (hs >= heads) return;
+  uint32_t hs, slice;
+  if (!place(a.share, heads, slices, &hs, &slice)) return;
   const int sh = hs / a.Hv, h = hs - sh * a.Hv, hk = h / (a.Hv / a.Hk), dv0 = slice * CB - (MODE == kMap ? DKP : 0);
   const Part part = part_at(a, sh);
   const int seq = part.seq;
@@ -378,8 +378,8 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
   constexpr int NW = kColumnWaves, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;
   __shared__ uint16_t Kl[2][64][LDK], Ql[2][64][LDK];
   __shared__ float Gl[2][3][64];            // gam, del, beta
-  const uint32_t hs = blockIdx.x / (8 * slices) * 8 + blockIdx.x % 8, slice = blockIdx.x / 8 % slices;
-  if (hs >= heads) return;
+  uint32_t hs, slice;
+  if (!place(a.share, heads, slices, &hs, &slice)) return;
   const int sh = hs / a.Hv, h = hs - sh * a.Hv, seq = in_order(a, sh), hk = h / (a.Hv / a.Hk);
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, r = l & 15, g4 = l >> 4;
   if (seq >= a.nseq) {                     // the steps of a packed row that belong to no sequence
@@ -651,9 +651,9 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
 template <int DT, int DKP>
 void launch_waves(const DeltaArgs& a, bool bwd, hipStream_t st) {
   constexpr int NW = kColumnWaves;
-  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv, pad = (heads + 7) / 8 * 8;
+  const uint32_t heads = (uint32_t)(a.nseq + (a.packed ? 1 : 0)) * a.Hv;
   const uint32_t slices = (a.Dvp + 16 * NW - 1) / (16 * NW);
-  const dim3 grid(pad * slices);
+  const dim3 grid(places(a.share, heads, slices));
   if (bwd) wave_kernel<DT, DKP, true><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
   else wave_kernel<DT, DKP, false><<<grid, 64 * NW, 0, st>>>(a, heads, slices);
 }
@@ -661,8 +661,8 @@ uint32_t parts_of(const DeltaArgs& a) { return a.part_chunks ? (uint32_t)a.parts
 
 template <int DT, int DKP>
 void launch_map(const DeltaArgs& a, hipStream_t st) {
-  const uint32_t heads = (uint32_t)a.parts * a.Hv, pad = (heads + 7) / 8 * 8, slices = (DKP + a.Dvp) / 16;
-  scan_kernel<DT, DKP, 1, kMap><<<dim3(pad * slices), 256, 0, st>>>(a, heads, slices);
+  const uint32_t heads = (uint32_t)a.parts * a.Hv, slices = (DKP + a.Dvp) / 16;
+  scan_kernel<DT, DKP, 1, kMap><<<dim3(places(a.share, heads, slices)), 256, 0, st>>>(a, heads, slices);
   join_kernel<DKP, false><<<dim3((uint32_t)a.nseq * a.Hv, a.Dvp / 16), 256, 0, st>>>(a);
 }
 template <int DT>
@@ -674,11 +674,8 @@ void launch_map(const DeltaArgs& a, hipStream_t st) {
 template <int DT, int DKP, int NT>
 void launch(const DeltaArgs& a, bool bwd, hipStream_t st) {
   const uint32_t heads = parts_of(a) * a.Hv;
-  // slices of one head lie 8 k workgroups apart: on one XCD, whose L2 then holds the
-  // chunk's K, Q, W and P once for all of them
-  const uint32_t pad = (heads + 7) / 8 * 8;
   const uint32_t slices = (a.Dvp + 16 * NT - 1) / (16 * NT);
-  const dim3 grid(pad * slices);
+  const dim3 grid(places(a.share, heads, slices));
   if (bwd) scan_kernel<DT, DKP, NT, kBackward><<<grid, 512, 0, st>>>(a, heads, slices);
   else scan_kernel<DT, DKP, NT, kForward><<<grid, 512, 0, st>>>(a, heads, slices);
 }
