@@ -138,7 +138,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       kt.store(&Kl[0][0][0], 64 * LDK);
       load_K(nn);
       // dN = scale P^T dO + del (K dS')
-      Sums<2> kd[NT];
+      Sums kd[NT];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const Frag<NA> kf = get8<NA>(&Kl[0][16 * w + r][32 * s + 8 * g4], 64 * LDK);
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       lds_barrier();
 
       // Y = W^T dN; W^T is upper triangular
-      Sums<2> ys[NT];
+      Sums ys[NT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (2 * s + 1 < w) continue;
@@ -183,7 +183,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       lds_barrier();
 
       // dS at the chunk's start
-      Sums<2> sn[MT][NT];
+      Sums sn[MT][NT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Frag<3> yf[NT];
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
     };
     f32x4 pd[NT], ud[MT][NT];
     const auto products = [&]() {
-      Sums<2> ps[NT], us[MT][NT];
+      Sums ps[NT], us[MT][NT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (2 * s + 1 < w) continue;           // P^T is upper triangular
@@ -665,7 +665,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(Delt
 // 128 in bf16, 188 us, 557 MB at 3.0 TB/s.
 template <int DT, int DKP>
 __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
-  constexpr int NA = InPlanes<DT>::n, OO = OutOrder<DT>::n, OP = OO + 1, KS = DKP / 32, LDK = DKP + 8, LDO = 40;
+  constexpr int NA = InPlanes<DT>::n, OP = kOrder + 1, KS = DKP / 32, LDK = DKP + 8, LDO = 40;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2, TK = DKP / 32;       // TK: a wave's 16-column tiles of the keys
   constexpr bool TWO = DT != CCV_DT_F32;                            // LDS for S and dS' at once
   constexpr int kS = OP * 32 * LDK, kN = 3 * 32 * LDT, kO = TWO ? NA * 64 * LDO : 0;
@@ -770,23 +770,23 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
         for (int n = 0; n < TK; ++n) {
           const Frag<OP> sf = get8t<OP>(St + 16 * (TK * half + n), LDK, 32 * LDK, l);
-          zq[n] = mma<OO>(sf, of, zq[n]);
-          zy[n] = mma<OO>(sf, yf, zy[n]);
-          if constexpr (TWO) zn[n] = mma<OO>(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
+          zq[n] = mma(sf, of, zq[n]);
+          zy[n] = mma(sf, yf, zy[n]);
+          if constexpr (TWO) zn[n] = mma(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           if (n > w) continue;
           const Frag<3> nf = get8t<3>(Nt + 16 * n, LDT, 32 * LDT, l);
-          if (half) pr[n] = mma<2>(yf, nf, pr[n]);
-          else pr[n] = mma<2>(of, nf, pr[n]);
+          if (half) pr[n] = mma(yf, nf, pr[n]);
+          else pr[n] = mma(of, nf, pr[n]);
         }
         if constexpr (!TWO) {
           lds_barrier();
           put_S(Dt, later);
           lds_barrier();
 #pragma unroll
-          for (int n = 0; n < TK; ++n) zn[n] = mma<OO>(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
+          for (int n = 0; n < TK; ++n) zn[n] = mma(get8t<OP>(Dt + 16 * (TK * half + n), LDK, 32 * LDK, l), nown, zn[n]);
         }
       }
 #pragma unroll
@@ -819,7 +819,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
           f32x4 x = {0, 0, 0, 0};
 #pragma unroll
           for (int s = 0; s < KS; ++s)
-            x = mma<2>(half ? get8<NA>(&Kl[0][t][32 * s + 8 * g4], 64 * LDK) : get8<NA>(&Ql[0][t][32 * s + 8 * g4], 64 * LDK),
+            x = mma(half ? get8<NA>(&Kl[0][t][32 * s + 8 * g4], 64 * LDK) : get8<NA>(&Ql[0][t][32 * s + 8 * g4], 64 * LDK),
                        get8<NA>(&Kl[0][j][32 * s + 8 * g4], 64 * LDK), x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -847,26 +847,23 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const bool lo = 2 * s <= w, up = 2 * s + 1 >= w;      // rows i >= j; rows j <= i
-        Frag<OP> fr, er, fc, ec;
-        if (lo) {
-          fr = get8t<OP>(Ft + 32 * s * LDT + 16 * w, LDT, 64 * LDT, l);
-          er = get8t<OP>(Et + 32 * s * LDT + 16 * w, LDT, 64 * LDT, l);
-        }
-        if (up) {
-          fc = get8<OP>(Ft + t * LDT + 32 * s + 8 * g4, 64 * LDT);
-          ec = get8<OP>(Et + t * LDT + 32 * s + 8 * g4, 64 * LDT);
-        }
+        // F's fragments, then E's: both at once would not stay in registers
 #pragma unroll
-        for (int n = 0; n < TK; ++n) {
-          const Frag<NA> kt = get8t<NA>(&Kl[0][32 * s][16 * (TK * half + n)], LDK, 64 * LDK, l);
-          const Frag<NA> qt = get8t<NA>(&Ql[0][32 * s][16 * (TK * half + n)], LDK, 64 * LDK, l);
-          if (lo) {
-            dq[n] = mma<OO>(kt, fr, dq[n]);
-            dk[n] = mma<OO>(kt, er, dk[n]);
-          }
-          if (up) {
-            dk[n] = mma<OO>(qt, fc, dk[n]);
-            dk[n] = mma<OO>(kt, ec, dk[n]);
+        for (int e = 0; e < 2; ++e) {
+          const __bf16* Mt = e ? Et : Ft;
+          Frag<OP> mr, mc;
+          if (lo) mr = get8t<OP>(Mt + 32 * s * LDT + 16 * w, LDT, 64 * LDT, l);
+          if (up) mc = get8<OP>(Mt + t * LDT + 32 * s + 8 * g4, 64 * LDT);
+#pragma unroll
+          for (int n = 0; n < TK; ++n) {
+            const Frag<NA> kt = get8t<NA>(&Kl[0][32 * s][16 * (TK * half + n)], LDK, 64 * LDK, l);
+            if (e) {
+              if (lo) dk[n] = mma(kt, mr, dk[n]);
+              if (up) dk[n] = mma(kt, mc, dk[n]);
+            } else {
+              if (lo) dq[n] = mma(kt, mr, dq[n]);
+              if (up) dk[n] = mma(get8t<NA>(&Ql[0][32 * s][16 * (TK * half + n)], LDK, 64 * LDK, l), mc, dk[n]);
+            }
           }
         }
       }

@@ -2,11 +2,12 @@
 //
 // Every product runs on the bf16 matrix instruction 16x16x32.  An fp32 value is held as a
 // sum of bf16 planes, hi + mid + lo (8 significant bits each, 24 together), and a product
-// of two such values is the sum of the plane products whose indexes add up to at most
-// `ORDER`: order 2 keeps about 2^-23 of the result, which is what fp32 outputs (states,
-// gate gradients) need; order 1 about 2^-16, enough for a 16-bit output.  An fp32 product
-// through three planes takes 6 instructions where the fp32 matrix instruction takes the
-// time of 16.  bf16 inputs are one plane, exactly; fp16 inputs are two, exactly.
+// of two such values is the sum of the six plane products whose indexes add up to at most
+// 2, which keeps about 2^-23 of the result: 6 instructions where the fp32 matrix
+// instruction takes the time of 16.  Results that are rounded to 16 bits are computed so
+// too: with two planes, 16 bits, of S, N and P in place of 24, three times as many of them come
+// out on the other side of a rounding as of 32-bit sums (in the 2-norm, 1.2e-4 from the rounded
+// 64-bit result in bf16).  bf16 inputs are one plane, exactly; fp16 inputs are two, exactly.
 #pragma once
 
 #include "ccv_device.hpp"
@@ -25,8 +26,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 
 // planes of an input element
 template <int DT> struct InPlanes { static constexpr int n = DT == CCV_DT_BF16 ? 1 : DT == CCV_DT_F16 ? 2 : 3; };
-// order of products whose results are rounded to the input's type
-template <int DT> struct OutOrder { static constexpr int n = DT == CCV_DT_F32 ? 2 : 1; };
+constexpr int kOrder = 2;      // of the plane products that are kept
 
 template <int P> struct Frag { bf16x8 p[P]; };
 
@@ -55,10 +55,10 @@ __device__ inline Frag<P> split8(f32x8 x) {
 }
 
 // acc += a b over 32 steps of the contraction; the small terms first.
-template <int ORDER, int PA, int PB>
+template <int PA, int PB>
 __device__ inline f32x4 mma(const Frag<PA>& a, const Frag<PB>& b, f32x4 acc) {
 #pragma unroll
-  for (int s = ORDER; s >= 0; --s)
+  for (int s = kOrder; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < PA; ++i)
       if (s - i >= 0 && s - i < PB) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], acc, 0, 0, 0);
@@ -66,11 +66,11 @@ __device__ inline f32x4 mma(const Frag<PA>& a, const Frag<PB>& b, f32x4 acc) {
 }
 
 // The same with a sum for each size of term: chains of dependent instructions a third as long.
-template <int ORDER> struct Sums {
-  f32x4 s[ORDER + 1];
+struct Sums {
+  f32x4 s[kOrder + 1];
   __device__ inline Sums() {
 #pragma unroll
-    for (int i = 0; i <= ORDER; ++i) s[i] = f32x4{0, 0, 0, 0};
+    for (int i = 0; i <= kOrder; ++i) s[i] = f32x4{0, 0, 0, 0};
   }
   template <int PA, int PB>
   __device__ inline void add(const Frag<PA>& a, const Frag<PB>& b) {
@@ -78,12 +78,12 @@ template <int ORDER> struct Sums {
     for (int i = 0; i < PA; ++i)
 #pragma unroll
       for (int j = 0; j < PB; ++j)
-        if (i + j <= ORDER) s[i + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], s[i + j], 0, 0, 0);
+        if (i + j <= kOrder) s[i + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], s[i + j], 0, 0, 0);
   }
   __device__ inline f32x4 total() const {
-    f32x4 t = s[ORDER];
+    f32x4 t = s[kOrder];
 #pragma unroll
-    for (int i = ORDER - 1; i >= 0; --i) t += s[i];
+    for (int i = kOrder - 1; i >= 0; --i) t += s[i];
     return t;
   }
 };
@@ -696,7 +696,7 @@ __global__ __launch_bounds__(256, 1) void join_kernel(DeltaArgs a) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) put4<3>(&Sp[0][r][16 * (MT * w + m) + 4 * g4], 16 * LDK, S[m]);
     lds_barrier();
-    Sums<2> ts[MT];
+    Sums ts[MT];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       const Frag<3> sf = get8<3>(&Sp[0][r][32 * s + 8 * g4], 16 * LDK);

@@ -4,9 +4,8 @@
 // chunk:   A_ij = beta_i e^(G_i - G_j) k_i.k_j  (i > j),   P_ij = e^(G_i - G_j) q_i.k_j  (i >= j),
 //          W = (1 + A)^-1.
 // Bound by memory, and by the latency of a chunk's few steps one after the other: 35 KB of LDS let four
-// workgroups of 16-bit inputs share a CU.  W goes out as three bf16 planes (fp32 states need them), P as
-// two where the outputs are 16-bit, both without the quarter above the diagonal blocks of 32, which is
-// zero.  4 x 4096 steps, 16 heads of 128 in bf16: 62 us, 260 MB at 4.2 TB/s; with whole planes and K's
+// workgroups of 16-bit inputs share a CU.  W and P go out as three bf16 planes, both without the quarter
+// above the diagonal blocks of 32, which is zero.  4 x 4096 steps, 16 heads of 128 in bf16: 62 us, 260 MB at 4.2 TB/s; with whole planes and K's
 // and W's LDS apart it took 78.  65536 packed steps, 10 key and 20 value heads in fp16: 285 us.
 // G is summed in 64 bits, so that differences of steps that lie far down a strongly
 // decaying chunk keep 32 bits.  A decay of g < -2000 (and -inf, a forgotten state) counts
@@ -152,7 +151,6 @@ template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   // 16-bit rows go through LDS as they are, and are multiplied in their own type: exact products
   constexpr int RT = DT == CCV_DT_F32 ? DT : CCV_DT_BF16, NA = InPlanes<RT>::n, LDK = DKP + 8, LDA = 68, ES = DT == CCV_DT_F32 ? 4 : 2;
-  constexpr int OP = OutOrder<DT>::n + 1;
   __shared__ union { __bf16 k[NA][64][LDK]; float w[64][LDA]; } kw;    // K's planes, then W
   auto& Kp = kw.k;
   auto& Wl = kw.w;
@@ -227,8 +225,8 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
         const Frag<NA> bf = get8<NA>(&Kp[0][j][32 * s + 8 * g4], 64 * LDK);
         const Frag<NA> af = get8<NA>(&Kp[0][row][32 * s + 8 * g4], 64 * LDK);
         if constexpr (DT == CCV_DT_F32) {
-          kk = mma<2>(af, bf, kk);
-          qk = mma<2>(qf[s], bf, qk);
+          kk = mma(af, bf, kk);
+          qk = mma(qf[s], bf, qk);
         } else {
           const u32x4 y = __builtin_bit_cast(u32x4, bf.p[0]);
           kk = mfma16<DT>(__builtin_bit_cast(u32x4, af.p[0]), y, kk);
@@ -321,7 +319,7 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     write(a.WT, Wl, std::integral_constant<int, 3>(), true, a.waves_back);
     write(a.P, Al, std::integral_constant<int, 3>(), true, a.waves_back);
   } else {
-    write(a.P, Al, std::integral_constant<int, OP>(), false);
+    write(a.P, Al, std::integral_constant<int, 3>(), false);
   }
 }
 

@@ -34,14 +34,14 @@ template <int DT, int DKP, int NT, Mode MODE>
 __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == CCV_DT_BF16 && NT == 1 && MODE == kForward ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 16;
   constexpr bool BWD = MODE == kBackward;
-  constexpr int OO = OutOrder<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
+  constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
   __shared__ __bf16 Sp[3][CB][LDK];        // S by columns
   __shared__ __bf16 Rp[3][CB][LDT];        // beta R by columns
   __shared__ __bf16 Kl[NA][64][LDK];
   __shared__ union {                       // Q until the first barrier of a chunk, N from then on
     __bf16 q[MODE == kMap ? 1 : NA][MODE == kMap ? 1 : 64][LDK];
     struct {
-      __bf16 p[OO + 1][CB][LDT], d[3][CB][LDT];      // N, del N
+      __bf16 p[3][CB][LDT], d[3][CB][LDT];      // N, del N
     } n;
   } qn;
   auto& Ql = qn.q;
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       kt.store(&Kl[0][0][0], 64 * LDK);
       load_K(nn);
       // K S (rows: steps)
-      Sums<2> ks[NT];
+      Sums ks[NT];
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const Frag<NA> kf = get8<NA>(&Kl[0][i][32 * s + 8 * g4], 64 * LDK);
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       }
 
       // N = W (beta R); W is lower triangular
-      Sums<2> ws[NT];
+      Sums ws[NT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (2 * s > w) continue;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       for (int j = 0; j < NT; ++j) {
         N[j] = ws[j].total();
         put4<3>(&Nd[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j] * gt.del);
-        if constexpr (MODE == kForward) put4<OO + 1>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
+        if constexpr (MODE == kForward) put4<3>(&Np[0][16 * j + r][16 * w + 4 * g4], CB * LDT, N[j]);
       }
       lds_barrier();
       if constexpr (BWD) {
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int j = 0; j < NT; ++j) S[m][j] *= gt.last;
-      Sums<2> sn[MT][NT];
+      Sums sn[MT][NT];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         Frag<3> nf[NT];
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
     }
   } else if constexpr (MODE != kMap) {
     // ---- the outputs: step i, four consecutive values 16 j + 4 g4 a lane; the same barriers ----
-    Frag<OO + 1> xP[2];
+    Frag<3> xP[2];
     Raw4<DT> xd[NT];
     float gam, gam_next;
     uint32_t oo[NT];
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       } else {
         const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) xP[s] = buf_planes<OO + 1>(b, s && w < 2 ? kNowhere : om + 1024 * s, 8192);
+        for (int s = 0; s < 2; ++s) xP[s] = buf_planes<3>(b, s && w < 2 ? kNowhere : om + 1024 * s, 8192);
         P.at += P.step;
       }
     };
@@ -315,12 +315,12 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
       const int nn = left > 0 ? steps(left) : 0;
       gam = gam_next;
       qt.store(&Ql[0][0][0], 64 * LDK);      // this wave's own rows: no barrier
-      Sums<BWD ? 2 : OO> qs[NT];      // S^T Q^T (columns: steps)
+      Sums qs[NT];      // S^T Q^T (columns: steps)
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const Frag<NA> qf = get8<NA>(&Ql[0][i][32 * s + 8 * g4], 64 * LDK);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) qs[j].add(get8<BWD ? 3 : OO + 1>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK), qf);
+        for (int j = 0; j < NT; ++j) qs[j].add(get8<3>(&Sp[0][16 * j + r][32 * s + 8 * g4], CB * LDK), qf);
       }
       load_Q(nn);
       lds_barrier();
@@ -342,12 +342,12 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] = qs[j].total() * gam;
         lds_barrier();
-        Sums<OO> ps[NT];
+        Sums ps[NT];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (2 * s > w) continue;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) ps[j].add(get8<OO + 1>(&Np[0][16 * j + r][32 * s + 8 * g4], CB * LDT), xP[s]);
+          for (int j = 0; j < NT; ++j) ps[j].add(get8<3>(&Np[0][16 * j + r][32 * s + 8 * g4], CB * LDT), xP[s]);
         }
         load_P(nn);
         const __amdgpu_buffer_rsrc_t b = O.rows(n);
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
   RowCopy<DKP, LDK, NW, true> kt(w, l, K.stride, a.Dk);
   RowCopy<DKP, LDK, NW, false> qt(w, l, Q.stride, a.Dk);
   Frag<3> xW[6];
-  Frag<2> xP[6];
+  Frag<3> xP[6];
   uint16_t xv[4][4];
   Raw4<DT> xd[4];
   float gates;                             // one of a chunk's gam, del, beta, on the way to LDS
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
     } else {
       const __amdgpu_buffer_rsrc_t b = P.piece(n > 0);
 #pragma unroll
-      for (int i = 0; i < 6; ++i) xP[i] = buf_planes<2>(b, ((i < 4 ? 2 * i : 2 * i - 3) * 64 + l) * 16, 8192);
+      for (int i = 0; i < 6; ++i) xP[i] = buf_planes<3>(b, ((i < 4 ? 2 * i : 2 * i - 3) * 64 + l) * 16, 8192);
       P.at += P.step;
     }
   };
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           lo[t] = mfma16<DT>(kf[t], x.p[p], lo[t]);
-          if (BWD || p < 2) qs[t] = mfma16<DT>(x.p[p], qf[t], qs[t]);
+          qs[t] = mfma16<DT>(x.p[p], qf[t], qs[t]);
         }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -615,22 +615,25 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a,
     } else {
       // the outputs: step 16 t + r, four consecutive values a lane
       const __amdgpu_buffer_rsrc_t ob = O.rows(n);
-      Frag<2> nf[2];
+      Frag<3> nf[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) nf[s] = split8<2>(join(N[2 * s], N[2 * s + 1]));
+      for (int s = 0; s < 2; ++s) nf[s] = split8<3>(join(N[2 * s], N[2 * s + 1]));
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float gam = Gl[b][0][16 * t + r];
 #pragma unroll
         for (int e = 0; e < 4; ++e) qs[t][e] = scaled<DT>(qs[t][e], er[e]) * gam;
       }
+      // the low planes last: they arrive last (65536 packed steps, 20 heads in fp16: 920 us, 1015 with them first)
 #pragma unroll
-      for (int q = 0; q < 3; ++q)            // planes 0 1, 1 0, 0 0
+      for (int q = 0; q <= kOrder; ++q)
 #pragma unroll
-        for (int x = 0; x < 6; ++x) {
-          const int t = x < 4 ? x : x - 2, s = x / 4;
-          qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[s].p[q == 1], xP[x].p[q == 0], qs[t], 0, 0, 0);
-        }
+        for (int i = q; i >= 0; --i)
+#pragma unroll
+          for (int x = 0; x < 6; ++x) {
+            const int t = x < 4 ? x : x - 2, s = x / 4;
+            qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf[s].p[i], xP[x].p[q - i], qs[t], 0, 0, 0);
+          }
 #pragma unroll
       for (int t = 0; t < 4; ++t) buf_store4<DT>(ob, anew(oo) + t * onext, qs[t] * scale, dleft, vec);
       O.at += O.step;
