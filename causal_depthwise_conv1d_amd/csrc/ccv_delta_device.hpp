@@ -365,6 +365,7 @@ __device__ inline int in_order(const DeltaArgs& a, int i) { return a.packed ? __
 // What a workgroup of such a pass takes: a sequence, or a part of one.
 struct Part {
   int seq, k, first;      // the sequence (nseq: the steps of none; above: nothing), which part of it, the number of its part 0
+  int end;                // and of the part after its last
   bool last;
   Sequence sq;
 };
@@ -385,6 +386,7 @@ __device__ inline Part part_at(const DeltaArgs& a, int s) {
   }
   p.first = s - p.k;
   if (p.seq >= a.nseq) return p;
+  p.end = a.packed ? __builtin_amdgcn_readfirstlane(a.pstart[p.seq + 1]) : p.first + a.parts_per_row;
   p.sq = sequence_at(a, p.seq);
   const int64_t skip = (int64_t)p.k * a.part_chunks * kDeltaChunk, most = (int64_t)a.part_chunks * kDeltaChunk;
   p.sq.first += p.k * a.part_chunks;
@@ -404,11 +406,14 @@ template <int DKP>
 __device__ inline int map_at(int row, int col) {       // element of T: a lane's 8 columns of a row lie together
   return (((row >> 4) * (DKP / 32) + (col >> 5)) * 64 + ((col >> 3) & 3) * 16 + (row & 15)) * 8 + (col & 7);
 }
-// The state that a part starts from where that is not the sequence's own: what the part next to it (step: -1 before, 1
-// after) leaves, as the join left it in B's place.
+// The state that a part starts from, as the join left it in B's place: what the part next to it (step: -1 before, 1
+// after) leaves.  Forward, the first of several parts takes the sequence's own from the last part's place, which has no
+// B: the caller may have the final state written over the initial one, and the last part may be done before the
+// first begins.  Null for a part that is a whole sequence: it reads what itself writes.
 __device__ inline const f32x4* start_tiles(const DeltaArgs& a, const Part& p, int h, int step) {
-  if (step < 0 ? p.k == 0 : p.last) return nullptr;
-  return reinterpret_cast<const f32x4*>(part_map(a, p.first + p.k + step, h) + a.Dkp * a.Dkp);
+  if (step < 0 ? p.k == 0 && p.last : p.last) return nullptr;
+  const int from = step < 0 && p.k == 0 ? p.end - 1 : p.first + p.k + step;
+  return reinterpret_cast<const f32x4*>(part_map(a, from, h) + a.Dkp * a.Dkp);
 }
 
 template <int DT>
@@ -692,6 +697,10 @@ __global__ __launch_bounds__(256, 1) void join_kernel(DeltaArgs a) {
       const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + r;
       S[m][e] = own && dk < a.Dk && dv < a.Dv ? own[seq * os[0] + h * os[1] + dk * os[2] + dv] : 0.0f;
     }
+  if (!BACK && maps) {      // for the first part (start_tiles)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tiles[maps * each / 4 + m * 64] = S[m];
+  }
   const auto apply = [&](Map& t, int p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) put4<3>(&Sp[0][r][16 * (MT * w + m) + 4 * g4], 16 * LDK, S[m]);
