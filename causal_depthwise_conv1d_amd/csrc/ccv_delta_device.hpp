@@ -407,12 +407,13 @@ __device__ inline int map_at(int row, int col) {       // element of T: a lane's
   return (((row >> 4) * (DKP / 32) + (col >> 5)) * 64 + ((col >> 3) & 3) * 16 + (row & 15)) * 8 + (col & 7);
 }
 // The state that a part starts from, as the join left it in B's place: what the part next to it (step: -1 before, 1
-// after) leaves.  Forward, the first of several parts takes the sequence's own from the last part's place, which has no
-// B: the caller may have the final state written over the initial one, and the last part may be done before the
-// first begins.  Null for a part that is a whole sequence: it reads what itself writes.
+// after) leaves.  The first of several parts, from the end the last, takes the sequence's own from the place of the
+// part at the other end, which has no B: the caller may have the result written over the state that it came from, and
+// the part that writes it may be done before the one that starts from it begins.  Null for a part that is a whole
+// sequence: it reads what itself writes.
 __device__ inline const f32x4* start_tiles(const DeltaArgs& a, const Part& p, int h, int step) {
-  if (step < 0 ? p.k == 0 && p.last : p.last) return nullptr;
-  const int from = step < 0 && p.k == 0 ? p.end - 1 : p.first + p.k + step;
+  if (p.k == 0 && p.last) return nullptr;
+  const int from = step < 0 ? (p.k == 0 ? p.end - 1 : p.first + p.k - 1) : p.last ? p.first : p.first + p.k + 1;
   return reinterpret_cast<const f32x4*>(part_map(a, from, h) + a.Dkp * a.Dkp);
 }
 
@@ -697,7 +698,7 @@ __global__ __launch_bounds__(256, 1) void join_kernel(DeltaArgs a) {
       const int dk = 16 * (MT * w + m) + 4 * g4 + e, dv = dv0 + r;
       S[m][e] = own && dk < a.Dk && dv < a.Dv ? own[seq * os[0] + h * os[1] + dk * os[2] + dv] : 0.0f;
     }
-  if (!BACK && maps) {      // for the first part (start_tiles)
+  if (maps) {      // for the first part, or the last (start_tiles)
 #pragma unroll
     for (int m = 0; m < MT; ++m) tiles[maps * each / 4 + m * 64] = S[m];
   }
