@@ -152,16 +152,19 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   // key heads enough for the chip's eight dies to get as many each
   a->share = (int64_t)a->nseq * z.Hk >= 64 ? (int32_t)(z.Hv / z.Hk) : 1;
   a->share_prep = nch * z.Hk >= 64 ? (int32_t)(z.Hv / z.Hk) : 1;
-  // Which kernels: both sides of each bound stand measured beside the kernels (ccv_delta_scan.hip, ccv_delta_bwd.hip).
-  a->waves = z.x_dtype != CCV_F32 && groups * (a->Dvp / 16) >= 1024;
-  a->waves_back = a->waves && z.x_dtype == CCV_F16;
-  *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || groups * (a->Dvp / 32) < 256 ? 1 : 2;
+  // Which kernels, by the blocks of 16 values that there are: 32 values a workgroup once 16 would be more workgroups
+  // than the chip's 256 CUs, whole columns a wave once 32 would be, and in the pass from the end once 16 would be three
+  // rounds of them.  Both sides of each bound stand measured beside the kernels (ccv_delta_scan.hip, ccv_delta_bwd.hip).
+  const int64_t blocks = (int64_t)a->nseq * z.Hv * (a->Dvp / 16);
+  a->waves = z.x_dtype != CCV_F32 && blocks > 512;
+  a->waves_back = z.x_dtype == CCV_F16 && blocks > 768;
+  *nt = z.x_dtype == CCV_F32 || (bwd && z.x_dtype != CCV_BF16) || blocks <= 256 ? 1 : 2;
   // Few heads: a sequence in parts that run side by side, once for the map of the state that each is and
   // once from the states that these give.  A chunk of the chain costs the same in both, so parts pay
   // where a sequence is several times twice its part: forward, fp32 1 x 2048, one head of 64, parts of 4
   // chunks: 30 us against 57 of the chain; bf16 1 x 8192, 2 heads of 128, parts of 8: 78 against 243;
   // 1 x 32768, 8 heads, parts of 128: 553 against 970.
-  const int64_t blocks = z.Hv * (a->Dvp / 16), side = std::max<int64_t>(1, 256 / blocks);
+  const int64_t side = std::max<int64_t>(1, 256 / (z.Hv * (a->Dvp / 16)));
   const int64_t each = std::max<int64_t>(4, (nch + side - 1) / side);
   if (!a->waves && a->nseq > 0 && nch >= 4 * each * a->nseq) {
     a->part_chunks = (int32_t)each;

@@ -381,9 +381,10 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
 
 // The same for fp16 and many heads, as the forward's wave_kernel has it: 16 columns a wave, the chain
 //   K dS', P^T dO -> dN,  W^T dN = Y,  Q^T (scale gam dO) and K^T (gam beta Y) -> dS
-// in its registers, K and Q shared through LDS; both have their rows in the joined order.  8 x 2048 steps, 32 heads
-// of 128 in fp16: 630 us, 2.1 GB at 3.3 TB/s, against 1004 of reverse_kernel, 16 heads 455 against 510.  In bf16
-// reverse_kernel has LDS for 32 columns a workgroup and needs no more (633 and 325 us).
+// in its registers, K and Q shared through LDS; both have their rows in the joined order.  1 x 2048 steps of 256
+// heads of 128 in fp16: 592 us against 904 of reverse_kernel, 104 heads 413 against 441, 96 heads, three rounds of
+// reverse_kernel's workgroups, 411 against 356.  In bf16 reverse_kernel has LDS for 32 columns a workgroup and needs
+// no more (554 and 278 us).
 template <int DT, int DKP>
 __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NW = kColumnWaves, NA = InPlanes<DT>::n, KS = DKP / 32, LDK = DKP + 8, CB = 16 * NW, PS = Cut<DT>::n;

@@ -13,10 +13,10 @@
 // which nothing else can shorten, holds no work of theirs.
 //
 // What bounds it is that chain: 4 x 4096 steps, 16 heads of 128 in bf16 take 196 us, 3.1 us (6700 cycles) a
-// chunk, of which the matrix units are busy 24 % and LDS 60 %.  NT is 2 where that leaves a workgroup for
-// every CU, since K, Q, W and P are then staged for 32 columns at once, and 1 below: 64 heads
-// forward, backward's forward pass and pass from the end: 196, 256, 307 us with 2, 216, 340, 432 with 1;
-// 32 heads: 173, 218, 254 with 2, 120, 163, 210 with 1.  fp32, and the backward's passes in fp16, have LDS
+// chunk, of which the matrix units are busy 24 % and LDS 60 %.  NT is 2 where blocks of 16 columns are more
+// than the CUs, since K, Q, W and P are then staged for 32 columns at once, and 1 below: 1 x 2048 steps of 34 heads of
+// 128 in bf16, forward, backward's forward pass and pass from the end: 94, 102, 127 us with 2, 97, 126, 173 with 1;
+// 32 heads: 93, 99, 117 with 2, 63, 70, 94 with 1.  fp32, and the backward's passes in fp16, have LDS
 // for 1 only.  The forward with NT 1 in bf16 is held to 128 registers, so that two
 // workgroups share a CU: 120 us, 128 without.
 #include "ccv_delta_device.hpp"
@@ -368,10 +368,11 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
 // by rows and, K, by columns: a chunk's rows lie in LDS, two chunks in turn, one barrier a chunk.
 //
 // A chunk takes longer so (4.8 us: all of a column's 132 to 182 matrix instructions in one wave) but costs
-// the CU less: nothing is exchanged, and K and Q are staged once for 64 columns.  It pays from four waves a
-// CU on: 8 x 2048 steps of 16 heads of 128, 1024 waves: 178 us against 211 (bf16) and 249 (fp16) of scan_kernel,
-// 32 heads: 272 against 425 and 491; 4 x 4096, 16 heads, 512 waves: 308 against 196.  65536 packed steps, 64
-// sequences, 20 heads in fp16: 720 to 850 us against 1370.  Bound by the instructions of two waves a SIMD and the
+// the CU less: nothing is exchanged, and K and Q are staged once for 64 columns.  It pays once scan_kernel's
+// workgroups of 32 columns are more than the CUs: 1 x 2048 steps of 72 heads of 128, 576 waves, forward and the
+// backward's forward pass: 148 and 186 us against 176 and 215 (bf16), 153 and 179 against 230 and 260 (fp16); 64 heads:
+// 146 and 177 against 94 and 120, 150 and 170 against 128 and 182; 256 heads: 271 against 371 and 482 forward.  65536
+// packed steps, 64 sequences, 20 heads in fp16: 840 to 980 us.  Bound by the instructions of two waves a SIMD and the
 // loads of W and P between them; 256 registers a wave leave no room to fetch those a chunk ahead.
 template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
