@@ -846,6 +846,30 @@ def _step_at(t):
     return (t.data_ptr(), s[0], 0, s[1])
 
 
+class _FirstOrder(torch.autograd.Function):
+    """Gradients made by a C call, passed on as they are: nothing records how they depend on the
+    inputs, so differentiating them again has to raise, where they would pass for constants."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tuple(t.view_as(t) for t in tensors[count:])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no second derivative: its gradients cannot be differentiated again")
+
+
+def _first_order(name, inputs, grads):
+    """A backward's gradients (some None) of what `inputs` hold; under create_graph=True marked so
+    that they can be used, but not differentiated."""
+    given = [t for t in inputs if t is not None and t.requires_grad] if torch.is_grad_enabled() else []
+    if not given:
+        return grads
+    marked = iter(_FirstOrder.apply(name, len(given), *given, *(g for g in grads if g is not None)))
+    return tuple(None if g is None else next(marked) for g in grads)
+
+
 # ---- the gated delta rule ------------------------------------------------------------------
 
 def _same_device(x, **others):
@@ -1006,8 +1030,10 @@ class _GatedDeltaRuleFn(torch.autograd.Function):
         dht = rest[0] if ctx.return_final_state and rest else None
         dout = torch.zeros_like(v) if dout is None else dout.to(v.dtype)
         want_dh = initial_state is not None and ctx.needs_input_grad[7]
-        dq, dk, dv, dg, db, dh = gated_delta_rule_bwd(q, k, v, g, beta, dout, ctx.scale, cu_seqlens, initial_state,
-                                                      None if dht is None else dht.float(), want_dh)
+        with torch.no_grad():
+            grads = gated_delta_rule_bwd(q, k, v, g, beta, dout, ctx.scale, cu_seqlens, initial_state,
+                                         None if dht is None else dht.float(), want_dh)
+        dq, dk, dv, dg, db, dh = _first_order("gated_delta_rule_fn", (q, k, v, g, beta, initial_state, dout, dht), grads)
         return dq, dk, dv, dg, db, None, None, dh, None
 
 
@@ -1015,7 +1041,8 @@ def gated_delta_rule_fn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: to
                         scale: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
                         initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False):
     """Differentiable gated delta rule (gated_delta_rule_fwd, with gradients for q, k, v, g,
-    beta and initial_state through gated_delta_rule_bwd)."""
+    beta and initial_state through gated_delta_rule_bwd).  Differentiable once: a second
+    derivative raises."""
     return _GatedDeltaRuleFn.apply(q, k, v, g, beta, scale, cu_seqlens, initial_state, return_final_state)
 
 
@@ -1148,14 +1175,15 @@ class _LayerNormFn(torch.autograd.Function):
     def backward(ctx, dout):
         x, weight, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dw, db = layer_norm_bwd(x, weight, dout.to(x.dtype), mean, rstd, need[0], need[1], need[2], ctx.bias_dtype)
-        return dx, dw, db, None
+        with torch.no_grad():
+            grads = layer_norm_bwd(x, weight, dout.to(x.dtype), mean, rstd, need[0], need[1], need[2], ctx.bias_dtype)
+        return *_first_order("layer_norm_fn", (x, weight, dout), grads), None
 
 
 def layer_norm_fn(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                   eps: float = 1e-5) -> torch.Tensor:
     """Differentiable layer norm (layer_norm_fwd, with gradients for x, weight and bias
-    through layer_norm_bwd)."""
+    through layer_norm_bwd).  Differentiable once: a second derivative raises."""
     return _LayerNormFn.apply(x, weight, bias, eps)
 
 
