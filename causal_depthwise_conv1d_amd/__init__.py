@@ -840,6 +840,12 @@ def _at(t):
     return (t.data_ptr(), s[0], s[1], s[2])
 
 
+def _written(*given):
+    """Tells autograd that a call wrote the caller's own tensors, which it does by address: a backward
+    that has kept one of them then raises, as after torch's in-place operators."""
+    torch.autograd.graph.increment_version([t for t in given if t is not None])
+
+
 def _step_at(t):
     """The same of a tensor without the dimension of steps."""
     s = t.stride()
@@ -959,6 +965,7 @@ def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     shape = (seqs, Hv, Dk, Dv)
     if _delta_states("initial_state", initial_state, shape) is not None:
         initial_state = _unit_heads(initial_state)
+    written = (out, final_state_out)
     if out is None:
         out = torch.empty_like(v, memory_format=torch.contiguous_format)
     elif out.dtype != v.dtype or tuple(out.shape) != (B, L, Hv, Dv) or (out.stride(-1) != 1 and Dv > 1):
@@ -972,6 +979,7 @@ def gated_delta_rule_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     _CALLS["ccv_delta_fwd"](device, B, L, N, Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype], DTYPE_CODE[beta.dtype],
                             Dk ** -0.5 if scale is None else scale, *_at(q), *_at(k), *_at(v), *_at(g), *_at(beta),
                             _p(cu_seqlens), *_at(initial_state), *_at(ht), *_at(out))
+    _written(*written)
     if info is not None:
         now = (q, k, v, initial_state)
         info["copied"] = [name for (name, t), u in zip(given, now) if t is not u]
@@ -1070,6 +1078,7 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     if state_indices is None and B > state.shape[0]:
         raise ValueError("more rows than states")
     q, k, v = _unit_heads(q), _unit_heads(k), _unit_heads(v)
+    written = (state, out)
     if out is None:
         out = torch.empty_like(v, memory_format=torch.contiguous_format)
     elif out.dtype != v.dtype or out.shape != v.shape or (out.stride(-1) != 1 and Dv > 1):
@@ -1078,6 +1087,7 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     _CALLS["ccv_delta_update"](device, B, L, state.shape[0], Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype],
                                DTYPE_CODE[beta.dtype], Dk ** -0.5 if scale is None else scale, *at(q), *at(k), *at(v),
                                *at(g), *at(beta), _p(state_indices), *_at(state), *at(out))
+    _written(*written)
     return out
 
 
@@ -1119,6 +1129,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     weight, bias = _norm_weights(x, weight, bias)
     device = _same_device(x, weight=weight, bias=bias, out=out)
     rows, shape, s = _norm_rows(x)
+    written = out
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous():
@@ -1129,6 +1140,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     w = weight if weight is not None else bias if bias is not None else x
     _CALLS["ccv_norm_fwd"](device, *shape, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], eps, 0, rows.data_ptr(), s[0], s[1],
                            _p(weight), _p(bias), out.data_ptr(), shape[1] * shape[2], shape[2], _p(mean), _p(rstd))
+    _written(written)
     return (out, mean, rstd) if return_stats else out
 
 

@@ -91,3 +91,72 @@ def test_second_derivatives_of_layer_norm_are_refused(monkeypatch, states):
 @pytest.mark.parametrize("make", [delta, norm])
 def test_second_derivatives_on_the_gpu(make, states):
     check_second_derivative(make("cuda", states), states)
+
+
+def step_inputs(x, state):
+    """One step's q, k, v, g, beta of the sequences' inputs, and the state."""
+    return [*(t.detach()[:, 0].contiguous() for t in x[:5]), state]
+
+
+def calls_do_nothing(monkeypatch):
+    monkeypatch.setattr(ccv, "_same_device", lambda x, **others: x.device)
+    for name in ("ccv_delta_fwd", "ccv_delta_update", "ccv_norm_fwd"):
+        monkeypatch.setitem(ccv._CALLS, name, lambda *values: None)
+
+
+def test_written_tensors_have_new_versions(monkeypatch):
+    calls_do_nothing(monkeypatch)
+    q, k, v, g, beta, h0 = ref.delta_inputs(1, 6, 1, 2, 8, 8)
+    out, one = torch.empty_like(v), torch.empty_like(v[:, 0])
+    given = {"state": h0, "out": out, "one": one, "q": q}
+    before = {n: t._version for n, t in given.items()}
+    ccv.gated_delta_rule_fwd(q, k, v, g, beta, initial_state=h0, return_final_state=True)
+    ccv.gated_delta_rule_fwd(q, k, v, g, beta, initial_state=h0)
+    assert {n: t._version for n, t in given.items()} == before
+    ccv.gated_delta_rule_fwd(q, k, v, g, beta, initial_state=h0, return_final_state=True, final_state_out=h0, out=out)
+    assert h0._version > before["state"] and out._version > before["out"]
+    at = h0._version
+    ccv.gated_delta_rule_update(*step_inputs((q, k, v, g, beta), h0), out=one)
+    assert h0._version > at and one._version > before["one"] and q._version == before["q"]
+    y = torch.empty(3, 8)
+    at = y._version
+    ccv.layer_norm_fwd(torch.ones(3, 8), out=y)
+    assert y._version > at
+    with torch.inference_mode():
+        ccv.gated_delta_rule_update(*step_inputs((q, k, v, g, beta), torch.zeros(1, 2, 8, 8)))
+
+
+def check_advanced_state(x, advance):
+    """A cache that was the initial state of a differentiable call, advanced before its backward: torch raises."""
+    leaves, cache = x[:5], x[5].detach().clone()
+    loss = ccv.gated_delta_rule_fn(*leaves, initial_state=cache).sum()
+    advance(leaves, cache)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def by_update(leaves, cache):
+    ccv.gated_delta_rule_update(*step_inputs(leaves, cache))
+
+
+def by_prefill(leaves, cache):
+    with torch.no_grad():
+        ccv.gated_delta_rule_fwd(*leaves, initial_state=cache, return_final_state=True, final_state_out=cache)
+
+
+def test_a_state_advanced_before_the_backward(monkeypatch):
+    calls_do_nothing(monkeypatch)
+    for advance in (by_update, by_prefill):
+        leaves, _ = delta()
+        forward = ccv.gated_delta_rule_fwd
+        with monkeypatch.context() as m:
+            delta_by_reference(m)
+            reference = ccv.gated_delta_rule_fwd
+            m.setattr(ccv, "gated_delta_rule_fwd", lambda *a, **kw: (forward if "final_state_out" in kw else reference)(*a, **kw))
+            check_advanced_state(leaves, advance)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("advance", [by_update, by_prefill])
+def test_a_state_advanced_before_the_backward_on_the_gpu(advance):
+    check_advanced_state(delta("cuda")[0], advance)
