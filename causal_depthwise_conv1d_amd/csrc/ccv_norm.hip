@@ -271,11 +271,15 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
   const int side = blockIdx.y, c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
   void* out = side ? a.db : a.dw;
   if (!out) return;
-  float s = 0;
-  if (col < a.width)
+  float all = 0;
+  for (int r = g; col < a.width && r < a.groups;) {
+    const int end = min(a.groups, r + 32 * kNormRun);
+    float s = 0;
 #pragma unroll 8
-    for (int r = g; r < a.groups; r += 32) s += a.part[((int64_t)r * 2 + side) * a.width + col];
-  t[g][c] = s;
+    for (; r < end; r += 32) s += a.part[((int64_t)r * 2 + side) * a.width + col];
+    all += s;
+  }
+  t[g][c] = all;
   __syncthreads();
   for (int h = 16; h; h >>= 1) {
     if (g < h) t[g][c] += t[g + h][c];
@@ -417,23 +421,32 @@ __global__ __launch_bounds__(256) void wide_sums_kernel(NormArgs a) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
   if (i >= a.width) return;
   const Piece16<DT> p((int)i, a.width);
-  float dw[V] = {}, db[V] = {}, x[V], d[V];
+  float dws[V] = {}, dbs[V] = {}, x[V], d[V];
+  for (int64_t row = blockIdx.y; row < a.rows;) {
+    const int64_t run = (int64_t)kNormRun * gridDim.y, end = a.rows - row > run ? row + run : a.rows;
+    float dw[V] = {}, db[V] = {};
 #pragma unroll 4
-  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    p.load(norm_row<DT>(a.dout, a.do_s, row, a.n1), d);
-    p.load(norm_row<DT>(a.x, a.x_s, row, a.n1), x);
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    for (; row < end; row += gridDim.y) {
+      p.load(norm_row<DT>(a.dout, a.do_s, row, a.n1), d);
+      p.load(norm_row<DT>(a.x, a.x_s, row, a.n1), x);
+      const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        dw[e] = __builtin_fmaf(d[e], (x[e] - mean) * rstd, dw[e]);
+        db[e] += d[e];
+      }
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      dw[e] = __builtin_fmaf(d[e], (x[e] - mean) * rstd, dw[e]);
-      db[e] += d[e];
+      dws[e] += dw[e];
+      dbs[e] += db[e];
     }
   }
 #pragma unroll
   for (int e = 0; e < V; ++e)
     if (p.mine(e)) {
-      a.part[((int64_t)blockIdx.y * 2) * a.width + p.col + e] = dw[e];
-      a.part[((int64_t)blockIdx.y * 2 + 1) * a.width + p.col + e] = db[e];
+      a.part[((int64_t)blockIdx.y * 2) * a.width + p.col + e] = dws[e];
+      a.part[((int64_t)blockIdx.y * 2 + 1) * a.width + p.col + e] = dbs[e];
     }
 }
 

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "ccv.h"
 #include "ccv_checks.hpp"
 #include "ccv_launch.hpp"
@@ -14,7 +16,7 @@ namespace {
 using namespace ccv;
 using namespace ccv::checks;
 
-constexpr int64_t kGroups = 1024;    // workgroups, and so partial rows, of the backward at the most
+constexpr int64_t kGroups = 1024;    // workgroups, and so partial rows, of the backward, unless it has very many rows
 
 struct Rows {
   const void* p;
@@ -137,8 +139,8 @@ int validate_bwd(const ccv_norm_bwd_args_t* p, NormArgs* a, int64_t* bytes, bool
   if (p->dweight || p->dbias) {
     const NormShape s = norm_shape(p->width, es);
     const int64_t per = s.lanes && s.lanes < 256 ? 256 / s.lanes : 1, need = (rows + per - 1) / per;
-    // rows walked by one workgroup share a partial row; the wide path's column sums take 64
-    const int64_t most = s.lanes ? kGroups : 64;
+    // rows walked by one workgroup share a partial row; the column sums of very wide rows take 64
+    const int64_t most = s.lanes ? std::max(kGroups, (need + kNormRows - 1) / kNormRows) : p->width * es < 16 ? kGroups : 64;
     a->groups = (int32_t)(need < most ? need : most);
     *bytes = (int64_t)a->groups * 2 * p->width * 4;
     if (with_ws && *bytes) {

@@ -21,6 +21,13 @@ struct NormArgs {
   int32_t groups;                     // workgroups of the backward's first kernel
 };
 
+// The terms of a column's sum that are added up one after the other before their sum joins those before it: with
+// millions of rows, one chain over all of a thread's would round each term to the whole sum's spacing.  Threads that
+// hold their rows in registers have no room for a second sum: there it is the workgroups that get more, beyond
+// kNormRows rows a thread (1024 of them are the fastest: 4194304 x 64 in fp32 takes 664 us, 710 with 2048).
+constexpr int kNormRun = 128;
+constexpr int kNormRows = 1024;
+
 // How a call is laid out: `lanes` threads a row, each holding `nv` 16-byte vectors of it;
 // lanes 0: rows too wide for that or narrower than a vector, walked in pieces.  Four vectors
 // in each of 16 threads would need a workgroup to have 16 rows' sums of dw and db in 200
