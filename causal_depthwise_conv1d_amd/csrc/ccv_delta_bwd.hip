@@ -114,7 +114,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
       const __amdgpu_buffer_rsrc_t d = D.piece(n > 0);
       gn.gam = buf_f4(d, od);
       gn.del = buf_f4(d, od + 256);
-      gn.beta = buf_f4(d, od + 512);
+      gn.beta = buf_f4(d, od + kDeltaBeta * 4);
       gn.last = buf1<CCV_DT_F32>(d, 4 * 63);
       D.at -= D.step;
     };
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(512, 2) void reverse_kernel(DeltaArgs a, uint32_t h
 #pragma unroll
         for (int e = 0; e < 4; ++e) xv[j][e] = buf_raw<DT>(vb, ov[j] == kNowhere ? kNowhere : ov[j] + e * V.stride);
       }
-      beta = buf_f4(Db.piece(n > 0), od + 512);
+      beta = buf_f4(Db.piece(n > 0), od + kDeltaBeta * 4);
       Ni.at -= Ni.step;
       V.at -= V.step;
       Db.at -= Db.step;
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(Delt
   const auto load_rows = [&](int n) {
     kt.load(K.rows(n));
     qt.load(Q.rows(n));
-    gates = buf1<CCV_DT_F32>(D.piece(n > 0), tid < 192 ? tid * 4 : kNowhere);
+    gates = buf1<CCV_DT_F32>(D.piece(n > 0), tid < 128 ? tid * 4 : tid < 192 ? (kDeltaBeta - 128 + tid) * 4 : kNowhere);
     K.at -= K.step;
     Q.at -= Q.step;
     D.at -= D.step;
@@ -673,7 +673,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   constexpr int kStage = (TWO ? 2 : 1) * kS + 2 * kN + kO, kPair = 2 * OP * 64 * LDT;
   __shared__ __bf16 Kl[NA][64][LDK], Ql[NA][64][LDK];
   __shared__ __bf16 un[kStage > kPair ? kStage : kPair];
-  __shared__ __align__(16) float gates[kDeltaDec];  // e^G, e^(G63 - G), beta, and G as doubles
+  __shared__ __align__(16) float gates[kDeltaDec];  // e^G, e^(G63 - G), -, G as doubles, beta
   __shared__ float rows[64], cols[8][64], dots[8];
   const double* G = reinterpret_cast<const double*>(gates + 192);
   __bf16* St = un;                                  // [OP][32][LDK]
@@ -793,7 +793,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
       if (l == 0) dots[w8] = dot;
-      const float gam = gates[t], del = gates[64 + t], bet = gates[128 + t];
+      const float gam = gates[t], del = gates[64 + t], bet = gates[kDeltaBeta + t];
 #pragma unroll
       for (int n = 0; n < TK; ++n) {
         dq[n] += zq[n] * (a.scale * gam);
@@ -808,7 +808,7 @@ __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         Gi[e] = G[16 * w + 4 * g4 + e];
-        bi[e] = half ? -gates[128 + 16 * w + 4 * g4 + e] : a.scale;
+        bi[e] = half ? -gates[kDeltaBeta + 16 * w + 4 * g4 + e] : a.scale;
       }
       __bf16* Pt = half ? Et : Ft;
 #pragma unroll

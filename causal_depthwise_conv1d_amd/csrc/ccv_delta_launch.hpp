@@ -8,7 +8,8 @@ namespace ccv {
 
 constexpr int kDeltaChunk = 64;       // steps a chunk: one wave's lanes, four 16-row matrix tiles
 constexpr int kDeltaMatrix = 3 * 64 * 64;   // elements of a chunk's W or P
-constexpr int kDeltaDec = 320;        // fp32 values of a chunk's gates in the workspace
+constexpr int kDeltaDec = 384;        // fp32 values of a chunk's gates in the workspace
+constexpr int kDeltaBeta = 320;       // where beta as given stands among them
 constexpr int kDeltaPart = 192;       // fp32 sums of a chunk and slice: 64 each of Y.N, Y.N - dv.v, c
 constexpr int kDeltaPairs = 128;      // fp32 values: 64 of dG, one dot product, and room
 constexpr int kDeltaMaxDk = 128;      // key width (the state's rows are spread over a workgroup's registers)
@@ -48,7 +49,7 @@ struct DeltaArgs {
   uint16_t* W;                                  // [ch][3][64 x 64, fragment_at]: (1 + A)^-1 as bf16 planes
   uint16_t* P;                                  // likewise, kDeltaMatrix a chunk and head; the backward holds it transposed
   uint16_t* WT;                                 // backward: W transposed
-  float* dec;                                   // [ch][kDeltaDec]: e^G, e^(G63 - G), beta, and G log2(e) as 64 doubles
+  float* dec;                                   // [ch][kDeltaDec]: e^G, e^(G63 - G), N's beta (ccv_delta_prep.hip), G log2(e) as 64 doubles, beta
   // backward, in 16 x 16 tiles as a wave's accumulators hold them, [tile][lane][4 rows], tiles of
   // one 16 values together:
   float *S, *dS;                                // [ch][Dvp / 16][Dkp / 16] tiles: state at a chunk's start, gradient at its end

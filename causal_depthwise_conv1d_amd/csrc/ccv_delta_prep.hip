@@ -167,15 +167,16 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
   // gates: wave 0, a step a lane
   if (w == 0) {
     double g = 0;
-    float b = 0;
+    float b = 0, given = 0;
     if (l < k.n) {
       const int64_t t = k.t0 + l;
       float x = load_param(a.g, a.g_dtype, k.row * a.g_s[0] + t * a.g_s[1] + h * a.g_s[2]);
       x = x < -2000.0f ? -2000.0f : x;
       g = (double)x * 1.4426950408889634;
-      b = load_param(a.beta, a.b_dtype, k.row * a.b_s[0] + t * a.b_s[1] + h * a.b_s[2]);
-      // the backward divides N by beta (dbeta = Y . N / beta): a beta of 0 is there the smallest that
-      // keeps N / beta in fp32, and N stays below anything it is added to
+      b = given = load_param(a.beta, a.b_dtype, k.row * a.b_s[0] + t * a.b_s[1] + h * a.b_s[2]);
+      // the backward divides N by beta (dbeta = Y . N / beta): a beta of 0 is there, for N, the smallest that
+      // keeps N / beta in fp32, and N stays below anything it is added to; what is a multiple of beta itself,
+      // dv among it, takes beta as given
       if (BWD && __builtin_fabsf(b) < 1e-30f) b = __builtin_copysignf(1e-30f, b);
     }
 #pragma unroll
@@ -190,6 +191,7 @@ __global__ __launch_bounds__(256) void prep_kernel(DeltaArgs a) {
     dec[l] = __builtin_amdgcn_exp2f((float)g);
     dec[64 + l] = __builtin_amdgcn_exp2f((float)(last - g));
     dec[128 + l] = b;
+    dec[kDeltaBeta + l] = given;
     reinterpret_cast<double*>(dec + 192)[l] = g;
   }
 
