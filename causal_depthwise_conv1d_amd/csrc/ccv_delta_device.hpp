@@ -17,7 +17,6 @@ namespace ccv {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -216,26 +215,6 @@ __device__ inline void store4(void* p, f32x4 x, int left, bool vec) {
     if (i < left) store1<DT>(static_cast<char*>(p) + i * (DT == CCV_DT_F32 ? 4 : 2), x[i]);
 }
 
-// The first `left` of 4 consecutive elements at p, widened.
-template <int DT>
-__device__ inline f32x4 load4(const void* p, int left, bool vec) {
-  f32x4 x = {0, 0, 0, 0};
-  if (vec && left >= 4) {
-    if constexpr (DT == CCV_DT_F32) return *static_cast<const f32x4*>(p);
-    const u32x2 d = *static_cast<const u32x2*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint16_t h = (uint16_t)(d[i / 2] >> (16 * (i % 2)));
-      x[i] = DT == CCV_DT_BF16 ? BF16::to_f(h) : F16::to_f(h);
-    }
-    return x;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < left) x[i] = load1<DT>(static_cast<const char*>(p) + i * (DT == CCV_DT_F32 ? 4 : 2));
-  return x;
-}
-
 // Four fp32 values into P planes of an LDS array whose planes are `plane` elements apart.
 template <int P>
 __device__ inline void put4(__bf16* at, int plane, f32x4 x) {
@@ -334,10 +313,6 @@ __device__ inline Chunk chunk_at(const DeltaArgs& a, int c) {
 struct Sequence {
   int first, end, row, t0;
   int64_t len;
-  __device__ inline Chunk chunk(int seq, int c) const {
-    const int64_t left = len - (int64_t)(c - first) * kDeltaChunk;
-    return {seq, row, t0 + (c - first) * kDeltaChunk, left < kDeltaChunk ? (int)left : kDeltaChunk};
-  }
 };
 
 __device__ inline Sequence sequence_at(const DeltaArgs& a, int s) {
