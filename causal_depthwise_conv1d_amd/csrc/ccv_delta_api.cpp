@@ -439,9 +439,9 @@ int pack(Work* w, void* stream) {
     const int32_t Dp = (int32_t)round_up(D, 8);
     DeltaPackArgs p{*src, {s[0], s[1], s[2]}, dst, B * a.L * H, a.L, H, D, Dp, a.x_dtype};
     *src = dst;
-    s[2] = Dp;
-    s[1] = (int64_t)H * Dp;
-    s[0] = s[1] * a.L;
+    s[1] = Dp;
+    s[2] = a.L * Dp;
+    s[0] = s[2] * H;
     return launch_delta_pack(p, stream);
   };
   int e = 0;

@@ -76,8 +76,9 @@ struct DeltaStepArgs {
   float scale;
 };
 
-// A [B, L, H, D] array into a contiguous one of Dp >= D elements a head, zeros behind the D:
-// rows of odd widths, strides or addresses, made ready for 16-byte loads.
+// A [B, L, H, D] array into one of Dp >= D elements a head, zeros behind the D: rows of odd widths, strides or
+// addresses, made ready for 16-byte loads.  The copy is [B, H, L, Dp], so that its steps lie as near to each other as
+// the 32-bit offsets over 64 of them need, however many heads there are.
 struct DeltaPackArgs {
   const void* src; int64_t s[3];
   void* dst;

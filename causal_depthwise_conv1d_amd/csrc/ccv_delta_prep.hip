@@ -22,8 +22,8 @@ template <class T>
 __global__ __launch_bounds__(256) void pack_kernel(DeltaPackArgs a) {
   const int64_t n = a.rows * a.Dp;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / a.Dp, d = i - r * a.Dp, bl = r / a.H, b = bl / a.L;
-    const T* src = static_cast<const T*>(a.src) + b * a.s[0] + (bl - b * a.L) * a.s[1] + (r - bl * a.H) * a.s[2];
+    const int64_t r = i / a.Dp, d = i - r * a.Dp, bh = r / a.L, b = bh / a.H;
+    const T* src = static_cast<const T*>(a.src) + b * a.s[0] + (r - bh * a.L) * a.s[1] + (bh - b * a.H) * a.s[2];
     static_cast<T*>(a.dst)[i] = d < a.D ? src[d] : T{0};
   }
 }
