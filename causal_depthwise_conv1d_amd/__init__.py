@@ -840,10 +840,15 @@ def _at(t):
     return (t.data_ptr(), s[0], s[1], s[2])
 
 
+_new_version = torch.autograd.graph.increment_version
+
+
 def _written(*given):
     """Tells autograd that a call wrote the caller's own tensors, which it does by address: a backward
     that has kept one of them then raises, as after torch's in-place operators."""
-    torch.autograd.graph.increment_version([t for t in given if t is not None])
+    for t in given:
+        if t is not None:
+            _new_version(t)
 
 
 def _step_at(t):
