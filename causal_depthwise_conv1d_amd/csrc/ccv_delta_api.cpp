@@ -162,8 +162,8 @@ int plan(const Sizes& z, bool bwd, void* ws, Work* out, const bool (&pack)[4]) {
   // Few heads: a sequence in parts that run side by side, once for the map of the state that each is and
   // once from the states that these give.  A chunk of the chain costs the same in both, so parts pay
   // where a sequence is several times twice its part: forward, fp32 1 x 2048, one head of 64, parts of 4
-  // chunks: 30 us against 57 of the chain; bf16 1 x 8192, 2 heads of 128, parts of 8: 78 against 243;
-  // 1 x 32768, 8 heads, parts of 128: 553 against 970.
+  // chunks: 30 us against 58 of the chain; bf16 1 x 8192, 2 heads of 128, parts of 8: 80 against 216;
+  // 1 x 32768, 8 heads, parts of 128: 580 against 875.
   const int64_t side = std::max<int64_t>(1, 256 / (z.Hv * (a->Dvp / 16)));
   const int64_t each = std::max<int64_t>(4, (nch + side - 1) / side);
   if (!a->waves && a->nseq > 0 && nch >= 4 * each * a->nseq) {

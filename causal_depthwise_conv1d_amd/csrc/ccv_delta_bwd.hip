@@ -663,7 +663,7 @@ __global__ __launch_bounds__(64 * kColumnWaves, 2) void reverse_wave_kernel(Delt
 // and E.  Contractions over the values go through LDS 32 values at a time, the next 32
 // under way in registers; S, dS', N and Y lie there by values, and the transposing read
 // makes fragments of them.  Bound by that staging and its waits, one workgroup a CU: 2 x 4096 steps, 16 heads of
-// 128 in bf16, 188 us, 557 MB at 3.0 TB/s.
+// 128 in bf16, 218 us, 0.6 GB at 2.8 TB/s.
 template <int DT, int DKP>
 __global__ __launch_bounds__(512) void grads_kernel(DeltaArgs a) {
   constexpr int NA = InPlanes<DT>::n, OP = kOrder + 1, KS = DKP / 32, LDK = DKP + 8, LDO = 40;

@@ -277,7 +277,7 @@ __device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_b
 // Workgroups go to the eight dies in turn, each with an L2 of its own: the slices of a head lie
 // on one, whose L2 then holds the chunk's K, Q, W and P once for all of them, and where there are key
 // heads enough to fill the chip so do the value heads that share K and Q (65536 packed steps, 10 / 20 heads in
-// fp16: the matrices' kernel reads 0.42 GB instead of 0.75, the pass 1.44 instead of 1.78).
+// fp16: the matrices' kernel reads 0.42 GB instead of 0.76, the pass 1.57 instead of 1.92).
 __device__ inline bool place(uint32_t share, uint32_t items, uint32_t slices, uint32_t* item, uint32_t* slice) {
   const uint32_t each = slices * share, b = blockIdx.x, r = b / 8 % each, g = r / slices;
   *item = (b / (8 * each) * 8 + b % 8) * share + g;

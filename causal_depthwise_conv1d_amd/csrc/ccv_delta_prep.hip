@@ -5,8 +5,9 @@
 //          W = (1 + A)^-1.
 // Bound by memory, and by the latency of a chunk's few steps one after the other: 35 KB of LDS let four
 // workgroups of 16-bit inputs share a CU.  W and P go out as three bf16 planes, both without the quarter
-// above the diagonal blocks of 32, which is zero.  4 x 4096 steps, 16 heads of 128 in bf16: 62 us, 260 MB at 4.2 TB/s; with whole planes and K's
-// and W's LDS apart it took 78.  65536 packed steps, 10 key and 20 value heads in fp16: 285 us.
+// above the diagonal blocks of 32, which is zero.  4 x 4096 steps, 16 heads of 128 in bf16: 67 us, 300 MB at 4.5 TB/s
+// (with P in two planes 62, then 78 with whole planes and K's and W's LDS apart).  65536 packed steps, 10 key
+// and 20 value heads in fp16: 270 to 330 us.
 // G is summed in 64 bits, so that differences of steps that lie far down a strongly
 // decaying chunk keep 32 bits.  A decay of g < -2000 (and -inf, a forgotten state) counts
 // as -2000: e^-2000 is 0 in fp32 with room to spare, and no inf - inf arises.

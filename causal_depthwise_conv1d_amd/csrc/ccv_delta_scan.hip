@@ -12,13 +12,13 @@
 // four waves make the outputs from the same planes, so that the chain from state to state,
 // which nothing else can shorten, holds no work of theirs.
 //
-// What bounds it is that chain: 4 x 4096 steps, 16 heads of 128 in bf16 take 196 us, 3.1 us (6700 cycles) a
-// chunk, of which the matrix units are busy 24 % and LDS 60 %.  NT is 2 where blocks of 16 columns are more
+// What bounds it is that chain: 4 x 4096 steps, 16 heads of 128 in bf16 take 204 us, 3.2 us a chunk,
+// of which the matrix units are busy 24 % and LDS 52 %.  NT is 2 where blocks of 16 columns are more
 // than the CUs, since K, Q, W and P are then staged for 32 columns at once, and 1 below: 1 x 2048 steps of 34 heads of
 // 128 in bf16, forward, backward's forward pass and pass from the end: 94, 102, 127 us with 2, 97, 126, 173 with 1;
 // 32 heads: 93, 99, 117 with 2, 63, 70, 94 with 1.  fp32, and the backward's passes in fp16, have LDS
-// for 1 only.  The forward with NT 1 in bf16 is held to 128 registers, so that two
-// workgroups share a CU: 120 us, 128 without.
+// for 1 only.  Held to 128 registers, for two workgroups a CU, the forward with NT 1 in bf16 is slower: 2 x 4096
+// steps of 16 heads of 128 take 127 us, 124 without.
 #include "ccv_delta_device.hpp"
 
 namespace ccv {
@@ -31,7 +31,7 @@ constexpr int LDT = 80;      // row stride of an LDS array of 64 steps
 enum Mode { kForward, kBackward, kMap };
 
 template <int DT, int DKP, int NT, Mode MODE>
-__global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == CCV_DT_BF16 && NT == 1 && MODE == kForward ? 4 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
+__global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : 2) void scan_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {
   constexpr int NA = InPlanes<DT>::n, CB = 16 * NT, KS = DKP / 32, MT = DKP / 64, LDK = DKP + 16;
   constexpr bool BWD = MODE == kBackward;
   constexpr int ES = DT == CCV_DT_F32 ? 4 : 2;
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(MODE == kMap ? 256 : 512, MODE == kMap ? 1 : DT == 
 // workgroups of 32 columns are more than the CUs: 1 x 2048 steps of 72 heads of 128, 576 waves, forward and the
 // backward's forward pass: 148 and 186 us against 176 and 215 (bf16), 153 and 179 against 230 and 260 (fp16); 64 heads:
 // 146 and 177 against 94 and 120, 150 and 170 against 128 and 182; 256 heads: 271 against 371 and 482 forward.  65536
-// packed steps, 64 sequences, 20 heads in fp16: 840 to 980 us.  Bound by the instructions of two waves a SIMD and the
+// packed steps, 64 sequences, 20 heads in fp16: 840 to 1000 us.  Bound by the instructions of two waves a SIMD and the
 // loads of W and P between them; 256 registers a wave leave no room to fetch those a chunk ahead.
 template <int DT, int DKP, bool BWD>
 __global__ __launch_bounds__(64 * kColumnWaves, 2) void wave_kernel(DeltaArgs a, uint32_t heads, uint32_t slices) {

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
 }
 
 // ---- rows wider than 512 threads hold (walked again for each sum; they stay in L2), or narrower than a vector ----
-// 6700 rows of 20000 in bf16: forward 190 us, 2.8 TB/s of the row in and out; backward 405 us.
+// 6700 rows of 20000 in bf16: forward 190 to 205 us, 2.7 TB/s of the row in and out; backward 405 to 419 us.
 
 __device__ inline float block_sum(float v, float* red) {
   v = sum4rows(sum16(v));
