@@ -12,7 +12,8 @@ Low level (same names as the C ABI):
     ccv_bwd(args, stream=None), ccv_bwd_check(args), ccv_bwd_plan(args),
     ccv_bwd_workspace_size(args),
     ccv_status_str(code), ccv_abi_version()
-    ccv_delta_fwd, ccv_delta_bwd, ccv_delta_update, ccv_norm_fwd, ccv_norm_bwd and
+    ccv_delta_fwd, ccv_delta_bwd, ccv_delta_update, ccv_linrec_fwd, ccv_linrec_bwd,
+    ccv_linrec_update, ccv_norm_fwd, ccv_norm_bwd and
     ccv_seq_tables (args, stream=None), their ccv_*_check(args) and, where they need a
     workspace, ccv_*_workspace_size(args)
 High level (the full-sequence contract of Ch.4 "Dao interface and source map",
@@ -33,6 +34,11 @@ The operators of a gated linear-attention layer around the conv:
     gated_delta_rule_bwd(q, k, v, g, beta, dout, ...)
     gated_delta_rule_fn(...)            (differentiable)
     gated_delta_rule_update(q, k, v, g, beta, state, state_indices=None, ...)
+    gated_linear_recurrence_fwd(x, g, cu_seqlens=None, initial_state=None,
+                                return_final_state=False, normalize=False, ...)
+    gated_linear_recurrence_bwd(x, g, dout, ...)
+    gated_linear_recurrence_fn(...)     (differentiable)
+    gated_linear_recurrence_update(x, g, state, state_indices=None, normalize=False, ...)
     layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, ...), layer_norm_bwd(...),
     layer_norm_fn(...)                  (differentiable)
     sequence_tables(lengths, total)     -> (cu_seqlens, seq_idx, positions)
@@ -219,10 +225,43 @@ class ccv_seq_tables_args_t(_Args):
                 ("positions", ctypes.c_void_p)]
 
 
+_LINREC_SIZES = [("struct_size", ctypes.c_int64), ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("C", ctypes.c_int64)]
+_LINREC_TYPES = [("x_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32), ("normalize", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                 ("x", ctypes.c_void_p), ("x_stride", _I64x2), ("g", ctypes.c_void_p), ("g_stride", _I64x2)]
+
+
+class ccv_linrec_fwd_args_t(_Args):
+    """Mirror of ``ccv_linrec_fwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [*_LINREC_SIZES, ("N", ctypes.c_int64), *_LINREC_TYPES, ("cu_seqlens", ctypes.c_void_p),
+                ("initial_state", ctypes.c_void_p), ("init_stride", ctypes.c_int64),
+                ("final_state", ctypes.c_void_p), ("final_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", _I64x2), ("carries", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ccv_linrec_bwd_args_t(_Args):
+    """Mirror of ``ccv_linrec_bwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [*_LINREC_SIZES, ("N", ctypes.c_int64), *_LINREC_TYPES, ("cu_seqlens", ctypes.c_void_p),
+                ("initial_state", ctypes.c_void_p), ("init_stride", ctypes.c_int64),
+                ("dout", ctypes.c_void_p), ("dout_stride", _I64x2),
+                ("dfinal_state", ctypes.c_void_p), ("dfinal_stride", ctypes.c_int64), ("carries", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_stride", _I64x2), ("dg", ctypes.c_void_p), ("dg_stride", _I64x2),
+                ("dinitial_state", ctypes.c_void_p), ("dinit_stride", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class ccv_linrec_update_args_t(_Args):
+    """Mirror of ``ccv_linrec_update_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [*_LINREC_SIZES, ("slots", ctypes.c_int64), *_LINREC_TYPES, ("state_indices", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("state_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", _I64x2)]
+
+
 _LAYER_CALLS = {
     "ccv_delta_fwd": (ccv_delta_fwd_args_t, True), "ccv_delta_bwd": (ccv_delta_bwd_args_t, True),
     "ccv_delta_update": (ccv_delta_update_args_t, False), "ccv_norm_fwd": (ccv_norm_fwd_args_t, False),
     "ccv_norm_bwd": (ccv_norm_bwd_args_t, True), "ccv_seq_tables": (ccv_seq_tables_args_t, False),
+    "ccv_linrec_fwd": (ccv_linrec_fwd_args_t, True), "ccv_linrec_bwd": (ccv_linrec_bwd_args_t, True),
+    "ccv_linrec_update": (ccv_linrec_update_args_t, False),
 }
 
 
@@ -435,6 +474,43 @@ def ccv_seq_tables(args: ccv_seq_tables_args_t, stream=None) -> int:
 
 def ccv_seq_tables_check(args: ccv_seq_tables_args_t) -> int:
     return lib().ccv_seq_tables_check(ctypes.byref(args))
+
+
+def ccv_linrec_fwd(args: ccv_linrec_fwd_args_t, stream=None) -> int:
+    """Enqueue the gated linear recurrence's forward on `stream`; returns the status code."""
+    return lib().ccv_linrec_fwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_linrec_fwd_check(args: ccv_linrec_fwd_args_t) -> int:
+    return lib().ccv_linrec_fwd_check(ctypes.byref(args))
+
+
+def ccv_linrec_fwd_workspace_size(args: ccv_linrec_fwd_args_t) -> int:
+    """Workspace bytes the forward needs (>= 0), or a negative status."""
+    return lib().ccv_linrec_fwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_linrec_bwd(args: ccv_linrec_bwd_args_t, stream=None) -> int:
+    """Enqueue the gated linear recurrence's backward on `stream`; returns the status code."""
+    return lib().ccv_linrec_bwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_linrec_bwd_check(args: ccv_linrec_bwd_args_t) -> int:
+    return lib().ccv_linrec_bwd_check(ctypes.byref(args))
+
+
+def ccv_linrec_bwd_workspace_size(args: ccv_linrec_bwd_args_t) -> int:
+    """Workspace bytes the backward needs (>= 0), or a negative status."""
+    return lib().ccv_linrec_bwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_linrec_update(args: ccv_linrec_update_args_t, stream=None) -> int:
+    """Enqueue new steps against cached states on `stream`; returns the status code."""
+    return lib().ccv_linrec_update(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_linrec_update_check(args: ccv_linrec_update_args_t) -> int:
+    return lib().ccv_linrec_update_check(ctypes.byref(args))
 
 
 # ---- tensors -> args -------------------------------------------------------------------
@@ -781,6 +857,8 @@ def causal_conv1d_fn(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch
 # A small call's cost is the host's, so these fill their args struct in one go: the values, in
 # the order of the struct's fields, packed to its layout, which the library takes by address.
 
+CCV_LINREC_CHUNK = 128       # steps between the states that gated_linear_recurrence_fwd leaves for its backward
+
 _FORMAT = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", _I64x2: "2q", _I64x3: "3q"}
 
 
@@ -1092,6 +1170,181 @@ def gated_delta_rule_update(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g
     _CALLS["ccv_delta_update"](device, B, L, state.shape[0], Hk, Hv, Dk, Dv, DTYPE_CODE[q.dtype], DTYPE_CODE[g.dtype],
                                DTYPE_CODE[beta.dtype], Dk ** -0.5 if scale is None else scale, *at(q), *at(k), *at(v),
                                *at(g), *at(beta), _p(state_indices), *_at(state), *at(out))
+    _written(*written)
+    return out
+
+
+# ---- the gated linear recurrence -------------------------------------------------------------
+
+def _linrec_sizes(x, g, one=False):
+    """(B, L, C) of the inputs, checked against each other; one: a single step without its dimension."""
+    s = x.shape
+    if len(s) != (2 if one else 3) or g.shape != s:
+        raise ValueError("expected x and g [B, C]" if one else "expected x and g [B, L, C]")
+    for name, t in (("x", x), ("g", g)):
+        if t.dtype not in DTYPE_CODE:
+            raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    return s[0], 1 if one else s[1], s[-1]
+
+
+def _rows2(t):
+    """A tensor's address and its two leading strides, as consecutive values."""
+    if t is None:
+        return (0, 0, 0)
+    s = t.stride()
+    return (t.data_ptr(), s[0], s[1])
+
+
+def _state_at(t):
+    """The same of a tensor of states, which has one."""
+    return (0, 0) if t is None else (t.data_ptr(), t.stride(0))
+
+
+def gated_linear_recurrence_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                                initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False,
+                                normalize: bool = False, final_state_out: Optional[torch.Tensor] = None,
+                                out: Optional[torch.Tensor] = None, return_carries: bool = False,
+                                info: Optional[dict] = None):
+    """A gated linear recurrence over whole sequences on the GPU, one state a channel:
+    ``h <- e^g h + s x; out = h``, with s = 1, or ``normalize``: s = sqrt(1 - e^2g).
+
+    x [B, L, C] and g (log decay, at most 0) [B, L, C], each in any of the three dtypes.  Strided views
+    are used as they are when channels are unit-stride; others are copied (``info["copied"]``
+    lists them).  ``cu_seqlens`` (int32 [N + 1], on the GPU) packs N sequences in one row (B = 1).
+    States are float32 [sequences, C]; ``final_state_out`` may be ``initial_state`` itself.
+    Returns out [B, L, C] in x's dtype, then the final state if wanted, then with
+    ``return_carries`` the states that gated_linear_recurrence_bwd can start from (float32
+    [B, ceil(L / 128), C]).
+    """
+    if final_state_out is not None and not return_final_state:
+        raise ValueError("final_state_out given but return_final_state is False")
+    B, L, C = _linrec_sizes(x, g)
+    device = _same_device(x, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, final_state_out=final_state_out, out=out)
+    given = (("x", x), ("g", g), ("initial_state", initial_state))
+    x, g = _unit_heads(x), _unit_heads(g)
+    N, seqs = _delta_sequences(cu_seqlens, B)
+    if _delta_states("initial_state", initial_state, (seqs, C)) is not None:
+        initial_state = _unit_heads(initial_state)
+    written = (out, final_state_out)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype != x.dtype or tuple(out.shape) != (B, L, C) or (out.stride(-1) != 1 and C > 1):
+        raise ValueError("out must be [B, L, C] in x's dtype with unit stride in its last dimension")
+    ht = None
+    if return_final_state:
+        ht = torch.empty((seqs, C), dtype=torch.float32, device=device) if final_state_out is None else final_state_out
+        _delta_states("final_state_out", ht, (seqs, C))
+        if ht.stride(-1) != 1 and C > 1:
+            raise ValueError("final_state_out must have unit stride in its last dimension")
+    carries = None
+    if return_carries:
+        carries = torch.empty((B, -(-L // CCV_LINREC_CHUNK), C), dtype=torch.float32, device=device)
+    _CALLS["ccv_linrec_fwd"](device, B, L, C, N, DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], int(normalize), 0, *_rows2(x), *_rows2(g),
+                             _p(cu_seqlens), *_state_at(initial_state), *_state_at(ht), *_rows2(out), _p(carries))
+    _written(*written)
+    if info is not None:
+        info["copied"] = [name for (name, t), u in zip(given, (x, g, initial_state)) if t is not u]
+    res = (out,) + ((ht,) if return_final_state else ()) + ((carries,) if return_carries else ())
+    return res if len(res) > 1 else out
+
+
+def gated_linear_recurrence_bwd(x: torch.Tensor, g: torch.Tensor, dout: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                                initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                                normalize: bool = False, carries: Optional[torch.Tensor] = None,
+                                return_dinitial_state: bool = False):
+    """Gradients of gated_linear_recurrence_fwd: (dx, dg, dinitial_state).
+
+    dout [B, L, C] in x's dtype; dfinal_state float32 like the states, or None (zeros); carries:
+    what the forward call returned for these inputs, or None (made again, by another pass over x and g).  Each gradient
+    has its input's shape and dtype, contiguous; dinitial_state (float32) only with
+    return_dinitial_state, which needs initial_state.
+    """
+    B, L, C = _linrec_sizes(x, g)
+    device = _same_device(x, g=g, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state, dfinal_state=dfinal_state,
+                          carries=carries)
+    if dout.dtype != x.dtype or dout.shape != x.shape:
+        raise ValueError("dout must be [B, L, C] in x's dtype")
+    if return_dinitial_state and initial_state is None:
+        raise ValueError("dinitial_state needs initial_state")
+    if carries is not None and (carries.dtype != torch.float32 or tuple(carries.shape) != (B, -(-L // CCV_LINREC_CHUNK), C)
+                                or not carries.is_contiguous()):
+        raise ValueError("carries must be what gated_linear_recurrence_fwd returned for these inputs")
+    x, g, dout = _unit_heads(x), _unit_heads(g), _unit_heads(dout)
+    N, seqs = _delta_sequences(cu_seqlens, B)
+    if _delta_states("initial_state", initial_state, (seqs, C)) is not None:
+        initial_state = _unit_heads(initial_state)
+    if _delta_states("dfinal_state", dfinal_state, (seqs, C)) is not None:
+        dfinal_state = _unit_heads(dfinal_state)
+    dx, dg = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (x, g))
+    dh = torch.empty((seqs, C), dtype=torch.float32, device=device) if return_dinitial_state else None
+    _CALLS["ccv_linrec_bwd"](device, B, L, C, N, DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], int(normalize), 0, *_rows2(x), *_rows2(g),
+                             _p(cu_seqlens), *_state_at(initial_state), *_rows2(dout), *_state_at(dfinal_state), _p(carries),
+                             *_rows2(dx), *_rows2(dg), *_state_at(dh))
+    return dx, dg, dh
+
+
+class _GatedLinearRecurrenceFn(torch.autograd.Function):
+    """Forward and backward through the C ABI; saves the inputs and the states between chunks of steps."""
+
+    @staticmethod
+    def forward(ctx, x, g, cu_seqlens, initial_state, return_final_state, normalize):
+        *res, carries = gated_linear_recurrence_fwd(x, g, cu_seqlens, initial_state, return_final_state, normalize, return_carries=True)
+        ctx.save_for_backward(x, g, cu_seqlens, initial_state, carries)
+        ctx.normalize = normalize
+        ctx.set_materialize_grads(False)
+        return tuple(res) if return_final_state else res[0]
+
+    @staticmethod
+    def backward(ctx, dout, dht=None):
+        x, g, cu_seqlens, initial_state, carries = ctx.saved_tensors
+        dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype)
+        want_dh = initial_state is not None and ctx.needs_input_grad[3]
+        with torch.no_grad():
+            grads = gated_linear_recurrence_bwd(x, g, dout, cu_seqlens, initial_state, None if dht is None else dht.float(),
+                                                ctx.normalize, carries, want_dh)
+        dx, dg, dh = _first_order("gated_linear_recurrence_fn", (x, g, initial_state, dout, dht), grads)
+        return dx, dg, None, dh, None, None
+
+
+def gated_linear_recurrence_fn(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                               initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False,
+                               normalize: bool = False):
+    """Differentiable gated linear recurrence (gated_linear_recurrence_fwd, with gradients for x, g and
+    initial_state through gated_linear_recurrence_bwd).  Differentiable once: a second derivative raises."""
+    return _GatedLinearRecurrenceFn.apply(x, g, cu_seqlens, initial_state, return_final_state, normalize)
+
+
+def gated_linear_recurrence_update(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                                   state_indices: Optional[torch.Tensor] = None, normalize: bool = False,
+                                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """New steps of the gated linear recurrence against cached states, advanced in place.
+
+    x and g [B, C] (one step), or [B, L, C]; state float32 [slots, C].  Row b uses slot
+    ``state_indices[b]`` (int32, on the GPU), or slot b without; a row whose index is outside
+    [0, slots) is idle: its outputs are zeros.  Two rows may not use one slot.  Returns out
+    with x's shape.
+    """
+    one = x.dim() == 2
+    B, L, C = _linrec_sizes(x, g, one)
+    device = _same_device(x, g=g, state=state, state_indices=state_indices, out=out)
+    if state.dtype != torch.float32 or state.dim() != 2 or state.shape[1] != C:
+        raise ValueError("state must be float32 [slots, C]")
+    if state.stride(-1) != 1 and C > 1:
+        raise ValueError("state must have unit stride in its last dimension")
+    if state_indices is not None and (state_indices.dtype != torch.int32 or state_indices.shape != (B,)
+                                      or not state_indices.is_contiguous()):
+        raise ValueError("state_indices must be contiguous int32 [B]")
+    if state_indices is None and B > state.shape[0]:
+        raise ValueError("more rows than states")
+    x, g = _unit_heads(x), _unit_heads(g)
+    written = (state, out)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype != x.dtype or out.shape != x.shape or (out.stride(-1) != 1 and C > 1):
+        raise ValueError("out must have x's shape and dtype with unit stride in its last dimension")
+    at = (lambda t: (t.data_ptr(), t.stride(0), 0)) if one else _rows2
+    _CALLS["ccv_linrec_update"](device, B, L, C, state.shape[0], DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], int(normalize), 0,
+                                *at(x), *at(g), _p(state_indices), *_state_at(state), *at(out))
     _written(*written)
     return out
 

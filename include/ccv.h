@@ -553,6 +553,104 @@ typedef struct ccv_seq_tables_args {
 int ccv_seq_tables_check(const ccv_seq_tables_args_t* args);
 int ccv_seq_tables(const ccv_seq_tables_args_t* args, void* hip_stream);
 
+/* ---- gated linear recurrence --------------------------------------------------------------
+ *
+ * The recurrence of a layer that keeps one number a channel, over the conv's output:
+ *
+ *   h <- e^g[t] h + s[t] x[t];   out[t] = h;
+ *   s = 1, or with normalize = 1: s = sqrt(1 - e^2g), which keeps the size of h that of x
+ *
+ *   - x, g (log decay) and out: [B, L, C], element (b, t, c) at b s[0] + t s[1] + c elements: unit stride
+ *     along the channels; steps may lie at most 32 MB apart (CCV_E_LAYOUT).  Inputs may have zero strides;
+ *     written arrays may not map two elements to one address.  L below 2^31 - 8192, C at most 2^24.
+ *   - x_dtype is the storage type of x and out, g_dtype of g; states and sums are fp32, out is rounded once.
+ *   - g is meant to be at most 0 (-inf gives a decay of 0).  Greater ones grow as the formula says, as long
+ *     as the products of the decays of 4096 successive steps stay finite; s is then 0 and has no gradient.
+ *   - cu_seqlens NULL: each of the B rows is one sequence (N must be 0).  Otherwise B is 1 and the row packs N sequences: s
+ *     has the steps cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32, on the device, never read by the host).
+ *     Offsets count as their running maximum, clamped to [0, L], and the first as 0.  Steps past the last
+ *     sequence give zeros, in out and in every gradient, and their inputs are not looked at.  A sequence
+ *     may be empty: its final state is its initial state.
+ *   - States are fp32 [sequences, C], rows init_stride or final_stride elements apart.  A NaN or an infinity stays in
+ *     its own sequence and channel, in its step and later ones (in the gradients, in earlier ones too).
+ *
+ * carries, where wanted: fp32 [B, ceil(L / CCV_LINREC_CHUNK), C], contiguous: the state before each chunk of
+ * that many steps, for ccv_linrec_bwd (not looked at where a chunk begins with a sequence).
+ * One pass over the data: tiles of 128 steps and 64 channels whose workgroups pass their sums on
+ * through the workspace (ccv_linrec_fwd_workspace_size bytes, 16-byte aligned, contents immaterial, free again when the
+ * call's work is done; CCV_E_NULL without, CCV_E_SHAPE when smaller), in a fixed order: results repeat bit
+ * for bit.  final_state may be initial_state itself, with the same stride; out may be no input. */
+#define CCV_LINREC_CHUNK 128
+typedef struct ccv_linrec_fwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_linrec_fwd_args_t) */
+  int64_t B, L, C, N;
+  int32_t x_dtype, g_dtype;     /* ccv_dtype_t */
+  int32_t normalize;            /* 0 or 1 */
+  int32_t reserved;             /* 0 */
+  const void* x;                int64_t x_stride[2];      /* (row, step) */
+  const void* g;                int64_t g_stride[2];
+  const int32_t* cu_seqlens;    /* device [N + 1], or NULL */
+  const float* initial_state;   int64_t init_stride;      /* [sequences, C], or NULL: zeros */
+  float* final_state;           int64_t final_stride;     /* or NULL: not wanted */
+  void* out;                    int64_t out_stride[2];
+  float* carries;               /* or NULL: not wanted */
+  void* workspace;              int64_t workspace_bytes;
+} ccv_linrec_fwd_args_t;
+
+int64_t ccv_linrec_fwd_workspace_size(const ccv_linrec_fwd_args_t* args);
+int ccv_linrec_fwd_check(const ccv_linrec_fwd_args_t* args);
+int ccv_linrec_fwd(const ccv_linrec_fwd_args_t* args, void* hip_stream);
+
+/* The gradients, with D[t] = dout[t] + e^g[t+1] D[t+1] inside a sequence (dfinal_state joins at its last step):
+ *   dx = s D,  dg = e^g h[t-1] D - (normalize: e^2g / s x D, 0 where s is 0),  dinitial_state = e^g D at the first step
+ * dx in x_dtype, dg in g_dtype, dinitial_state fp32 (NULL: not wanted; needs initial_state, else
+ * CCV_E_UNSUPPORTED), from dout (x_dtype) and dfinal_state (fp32, NULL: zeros).  carries: what the forward call left for the
+ * same inputs, or NULL: they are then made again first, by another pass over x and g.
+ * dinitial_state may be dfinal_state itself, with the same stride; other outputs may be no input and no other
+ * output (CCV_E_ALIAS). */
+typedef struct ccv_linrec_bwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_linrec_bwd_args_t) */
+  int64_t B, L, C, N;
+  int32_t x_dtype, g_dtype;
+  int32_t normalize;
+  int32_t reserved;
+  const void* x;                int64_t x_stride[2];
+  const void* g;                int64_t g_stride[2];
+  const int32_t* cu_seqlens;
+  const float* initial_state;   int64_t init_stride;
+  const void* dout;             int64_t dout_stride[2];
+  const float* dfinal_state;    int64_t dfinal_stride;
+  const float* carries;         /* or NULL */
+  void* dx;                     int64_t dx_stride[2];
+  void* dg;                     int64_t dg_stride[2];
+  float* dinitial_state;        int64_t dinit_stride;
+  void* workspace;              int64_t workspace_bytes;
+} ccv_linrec_bwd_args_t;
+
+int64_t ccv_linrec_bwd_workspace_size(const ccv_linrec_bwd_args_t* args);
+int ccv_linrec_bwd_check(const ccv_linrec_bwd_args_t* args);
+int ccv_linrec_bwd(const ccv_linrec_bwd_args_t* args, void* hip_stream);
+
+/* Decoding: L new steps of B rows, one after the other, against fp32 states in a cache [slots, C], advanced in
+ * place.  Row b uses slot state_indices[b] (int32, device), or slot b when state_indices is NULL (then B <= slots, else
+ * CCV_E_SHAPE).  A row whose index lies outside [0, slots) is idle: its outputs are zeros and no state is
+ * touched.  Two rows may not use one slot in the same call.  Needs no workspace. */
+typedef struct ccv_linrec_update_args {
+  int64_t struct_size;          /* = sizeof(ccv_linrec_update_args_t) */
+  int64_t B, L, C, slots;
+  int32_t x_dtype, g_dtype;
+  int32_t normalize;
+  int32_t reserved;
+  const void* x;                int64_t x_stride[2];
+  const void* g;                int64_t g_stride[2];
+  const int32_t* state_indices; /* device [B], or NULL */
+  float* state;                 int64_t state_stride;     /* of slots */
+  void* out;                    int64_t out_stride[2];
+} ccv_linrec_update_args_t;
+
+int ccv_linrec_update_check(const ccv_linrec_update_args_t* args);
+int ccv_linrec_update(const ccv_linrec_update_args_t* args, void* hip_stream);
+
 /* Static, NUL-terminated name of a status code ("CCV_OK", ...). */
 const char* ccv_status_str(int status);
 

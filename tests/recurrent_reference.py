@@ -1,0 +1,113 @@
+"""Plain 64-bit forms of the gated linear recurrence, with bounds on the rounding errors of 32-bit ones.
+
+The recurrence runs step by step from its definition, each sequence by itself, and so do its gradients.
+The bounds follow the arithmetic (u = 2^-24, half a step of fp32 relative to a value): a term b[s] reaches h[t]
+through t - s decays, each off by at most 2 u (its own rounding and the polynomial's error, 1.4e-8 of
+something no larger), and through at most t - s + 24 roundings of products and sums, whatever way they are
+grouped (24: two for the weight's square root and product, the rest where a lane's, a tile's and a
+group's parts are joined).  So |error| <= sum over s of 3 u (t - s + 24) |decays b[s]|, which the recurrences
+M[t] = a M[t-1] + |b[t]| and K[t] = a (K[t-1] + M[t-1]) give as 3 u (K + 24 M).  Gradients are products of such
+values.  A weight sqrt(1 - a^2), from 1 - a good to 2 u, is good to 4 u, a reciprocal of it to 6 u; what has more
+roundings than that is counted with 24 u.  Outputs of 16 bits are rounded once more: half a spacing.
+"""
+import torch
+
+from layer_reference import DT, half_spacing  # noqa: F401
+
+U = 2.0 ** -24
+
+
+def spans_of(B, L, lengths):
+    """(row, first step, end) of every sequence."""
+    if lengths is None:
+        return [(b, 0, L) for b in range(B)]
+    out, at = [], 0
+    for n in lengths:
+        out.append((0, at, at + n))
+        at += n
+    return out
+
+
+def walk(a, b):
+    """h[t] = a[t] h[t-1] + b[t] from 0, with M and K of the module's text; first dimension: steps."""
+    h = m = k = torch.zeros_like(b[0])
+    hs, ms, ks = [], [], []
+    for t in range(a.shape[0]):
+        k = a[t] * (k + m)
+        m = a[t] * m + b[t].abs()
+        h = a[t] * h + b[t]
+        hs.append(h)
+        ms.append(m)
+        ks.append(k)
+    return torch.stack(hs), torch.stack(ms), torch.stack(ks)
+
+
+def linrec(x, g, lengths=None, h0=None, normalize=False, dout=None, dht=None):
+    """Results and bounds: {name: (value, bound)} of out, ht and, with dout, dx, dg, dh0."""
+    B, L, C = x.shape
+    x, g = x.double(), g.double()
+    spans = spans_of(B, L, lengths)
+    zero = lambda *s: torch.zeros(*s, dtype=torch.float64)  # noqa: E731
+    shapes = {"out": (B, L, C), "ht": (len(spans), C)}
+    if dout is not None:
+        shapes.update({"dx": (B, L, C), "dg": (B, L, C), "dh0": (len(spans), C)})
+    v, e = ({n: zero(*s) for n, s in shapes.items()} for _ in range(2))
+    for s, (r, t0, t1) in enumerate(spans):
+        start = zero(C) if h0 is None else h0[s].double()
+        if t0 == t1:
+            v["ht"][s] = start
+            if dout is not None and dht is not None:
+                v["dh0"][s] = dht[s].double()
+            continue
+        a, y = g[r, t0:t1].exp(), -torch.expm1(g[r, t0:t1])
+        w = torch.sqrt((y * (2 - y)).clamp(min=0)) if normalize else torch.ones_like(a)
+        xs = x[r, t0:t1]
+        b = w * xs
+        # the state before the first step as a step of its own, so that its bound is counted the same way
+        h, m, k = walk(torch.cat([torch.ones_like(a[:1]), a]), torch.cat([start[None], b]))
+        bound = 3 * U * (k + 24 * m)
+        v["out"][r, t0:t1], e["out"][r, t0:t1] = h[1:], bound[1:]
+        v["ht"][s], e["ht"][s] = h[-1], bound[-1]
+        if dout is None:
+            continue
+        d = dout[r, t0:t1].double().clone()
+        if dht is not None:
+            d[-1] += dht[s].double()
+        D, dm, dk = (q.flip(0) for q in walk(torch.cat([a[1:], torch.ones_like(a[:1])]).flip(0), d.flip(0)))
+        db = 3 * U * (dk + 24 * dm)
+        v["dx"][r, t0:t1], e["dx"][r, t0:t1] = w * D, w * (db + 24 * U * dm)
+        hp, mp, bp = h[:-1], m[:-1], bound[:-1]
+        v["dg"][r, t0:t1] = a * hp * D
+        e["dg"][r, t0:t1] = a * (bp * dm + mp * db + bp * db + 24 * U * mp * dm)
+        if normalize:
+            q = torch.where(w > 0, a * a / torch.where(w > 0, w, 1.0), 0.0) * xs.abs()
+            v["dg"][r, t0:t1] -= q * xs.sign() * D
+            e["dg"][r, t0:t1] += q * (db + 24 * U * dm)
+        v["dh0"][s], e["dh0"][s] = a[0] * D[0], a[0] * (db[0] + 24 * U * dm[0])
+    return {n: (v[n], e[n]) for n in v}
+
+
+def assert_within(name, got, want, what="", least=1e-37):
+    """Every element of `got` within its bound of the 64-bit value, and within half a spacing of its type more;
+    fp32 results below `least` may be flushed to zero."""
+    value, bound = want
+    x = got.detach().cpu().double()
+    assert x.shape == value.shape, (what, name, x.shape, value.shape)
+    over = (x - value).abs() - bound - half_spacing(got.dtype, value.abs() + bound) - least
+    assert bool(torch.isfinite(x).all()), f"{what} {name}: not finite"
+    if over.numel():
+        i = int(over.argmax())
+        assert float(over.max()) <= 0, (f"{what} {name}: element {i} of {tuple(x.shape)} is {float(x.flatten()[i]):.9g}, not "
+                                        f"{float(value.flatten()[i]):.9g} (bound {float(bound.flatten()[i]):.3g})")
+
+
+def inputs(B, L, C, dtype="f32", gate="f32", seed=0, seqs=None, states=True, slow=0.999, pad=0):
+    """x as it leaves the conv, log decays between a slow channel's and -8 a step (CPU)."""
+    gen = torch.Generator().manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    x = rand(B, L, C + pad).to(DT[dtype])[..., :C]
+    base = torch.log10(torch.tensor(1 - slow))
+    size = 10 ** (base + (0.9 - base) * torch.rand(C, generator=gen) ** 2)
+    g = (-size * torch.rand(B, L, C, generator=gen)).to(DT[gate])
+    n = B if seqs is None else seqs
+    return x, g, rand(n, C) if states else None
