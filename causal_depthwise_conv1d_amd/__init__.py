@@ -13,7 +13,7 @@ Low level (same names as the C ABI):
     ccv_bwd_workspace_size(args),
     ccv_status_str(code), ccv_abi_version()
     ccv_delta_fwd, ccv_delta_bwd, ccv_delta_update, ccv_linrec_fwd, ccv_linrec_bwd,
-    ccv_linrec_update, ccv_norm_fwd, ccv_norm_bwd and
+    ccv_linrec_update, ccv_norm_fwd, ccv_norm_bwd, ccv_group_norm_fwd, ccv_group_norm_bwd and
     ccv_seq_tables (args, stream=None), their ccv_*_check(args) and, where they need a
     workspace, ccv_*_workspace_size(args)
 High level (the full-sequence contract of Ch.4 "Dao interface and source map",
@@ -41,6 +41,8 @@ The operators of a gated linear-attention layer around the conv:
     gated_linear_recurrence_update(x, g, state, state_indices=None, normalize=False, ...)
     layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, ...), layer_norm_bwd(...),
     layer_norm_fn(...)                  (differentiable)
+    group_norm_fwd(x, num_groups, weight=None, bias=None, gate=None, activation=None, ...),
+    group_norm_bwd(...), group_norm_fn(...)     (differentiable)
     sequence_tables(lengths, total)     -> (cu_seqlens, seq_idx, positions)
 """
 from __future__ import annotations
@@ -256,12 +258,34 @@ class ccv_linrec_update_args_t(_Args):
                 ("state", ctypes.c_void_p), ("state_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", _I64x2)]
 
 
+class ccv_group_norm_fwd_args_t(_Args):
+    """Mirror of ``ccv_group_norm_fwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
+class ccv_group_norm_bwd_args_t(_Args):
+    """Mirror of ``ccv_group_norm_bwd_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("dout", ctypes.c_void_p), ("dout_stride", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64), ("dgate", ctypes.c_void_p), ("dgate_stride", ctypes.c_int64),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 _LAYER_CALLS = {
     "ccv_delta_fwd": (ccv_delta_fwd_args_t, True), "ccv_delta_bwd": (ccv_delta_bwd_args_t, True),
     "ccv_delta_update": (ccv_delta_update_args_t, False), "ccv_norm_fwd": (ccv_norm_fwd_args_t, False),
     "ccv_norm_bwd": (ccv_norm_bwd_args_t, True), "ccv_seq_tables": (ccv_seq_tables_args_t, False),
     "ccv_linrec_fwd": (ccv_linrec_fwd_args_t, True), "ccv_linrec_bwd": (ccv_linrec_bwd_args_t, True),
     "ccv_linrec_update": (ccv_linrec_update_args_t, False),
+    "ccv_group_norm_fwd": (ccv_group_norm_fwd_args_t, False), "ccv_group_norm_bwd": (ccv_group_norm_bwd_args_t, True),
 }
 
 
@@ -511,6 +535,29 @@ def ccv_linrec_update(args: ccv_linrec_update_args_t, stream=None) -> int:
 
 def ccv_linrec_update_check(args: ccv_linrec_update_args_t) -> int:
     return lib().ccv_linrec_update_check(ctypes.byref(args))
+
+
+def ccv_group_norm_fwd(args: ccv_group_norm_fwd_args_t, stream=None) -> int:
+    """Enqueue group norm on `stream`; returns the status code."""
+    return lib().ccv_group_norm_fwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_group_norm_fwd_check(args: ccv_group_norm_fwd_args_t) -> int:
+    return lib().ccv_group_norm_fwd_check(ctypes.byref(args))
+
+
+def ccv_group_norm_bwd(args: ccv_group_norm_bwd_args_t, stream=None) -> int:
+    """Enqueue group norm's backward on `stream`; returns the status code."""
+    return lib().ccv_group_norm_bwd(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_group_norm_bwd_check(args: ccv_group_norm_bwd_args_t) -> int:
+    return lib().ccv_group_norm_bwd_check(ctypes.byref(args))
+
+
+def ccv_group_norm_bwd_workspace_size(args: ccv_group_norm_bwd_args_t) -> int:
+    """Workspace bytes the backward needs (>= 0), or a negative status."""
+    return lib().ccv_group_norm_bwd_workspace_size(ctypes.byref(args))
 
 
 # ---- tensors -> args -------------------------------------------------------------------
@@ -1455,6 +1502,132 @@ def layer_norm_fn(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     """Differentiable layer norm (layer_norm_fwd, with gradients for x, weight and bias
     through layer_norm_bwd).  Differentiable once: a second derivative raises."""
     return _LayerNormFn.apply(x, weight, bias, eps)
+
+
+# ---- group norm ------------------------------------------------------------------------------
+
+def _flat_rows(t):
+    """t [..., C] as [rows, C] with unit stride along the channels, copied only where its strides allow no
+    such view."""
+    t = _unit_heads(t)
+    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+
+
+def _group_sizes(x, num_groups, activation, weight, bias, gate):
+    """(rows, groups, width, activation's code), checked."""
+    if x.dim() < 2:
+        raise ValueError("expected x [..., C]")
+    C = x.shape[-1]
+    if num_groups < 1 or C % num_groups:
+        raise ValueError("num_groups must divide the channels")
+    if activation not in (None, "silu", "swish"):
+        raise ValueError(f"activation must be None, 'silu' or 'swish', not {activation!r}")
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"x must be float32, float16 or bfloat16, not {x.dtype}")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (t.shape != (C,) or t.dtype not in DTYPE_CODE):
+            raise ValueError(f"{name} must be [C] in float32, float16 or bfloat16")
+    if weight is not None and bias is not None and bias.dtype != weight.dtype:
+        raise ValueError("bias must have the weight's dtype")
+    if gate is not None and (gate.shape != x.shape or gate.dtype != x.dtype):
+        raise ValueError("gate must have x's shape and dtype")
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, num_groups, C // num_groups, CCV_ACT_NONE if activation is None else CCV_ACT_SILU
+
+
+def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, activation: Optional[str] = None, eps: float = 1e-5,
+                   return_stats: bool = False, out: Optional[torch.Tensor] = None):
+    """Group norm of each step's channels on the GPU, with an activation or a gate behind it.
+
+    x [..., C], channels last; every row's C channels are normalised in ``num_groups`` groups of neighbours, each over
+    its own C / num_groups values (torch's group_norm of [rows, C]): no step sees another.  With
+    y = (x - mean) rstd weight + bias (weight and bias [C] or None) returns act(y), or with
+    ``gate`` (x's shape and dtype) y act(gate); activation None or "silu".  Strided rows are used
+    as they are when channels are unit-stride and the leading dimensions lie at one stride.
+    Returns out (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [..., num_groups].
+    """
+    rows, groups, width, act = _group_sizes(x, num_groups, activation, weight, bias, gate)
+    device = _same_device(x, weight=weight, bias=bias, gate=gate, out=out)
+    weight, bias = (None if t is None else t.contiguous() for t in (weight, bias))
+    written = out
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif out.dtype != x.dtype or out.shape != x.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous with x's shape and dtype")
+    C = x.shape[-1]
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = (torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=device) for _ in range(2))
+    w = weight if weight is not None else bias if bias is not None else x
+    x2, z2 = _flat_rows(x), None if gate is None else _flat_rows(gate)
+    _CALLS["ccv_group_norm_fwd"](device, rows, groups, width, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], act, eps, *_state_at(x2),
+                                 _p(weight), _p(bias), *_state_at(z2), out.data_ptr(), C, _p(mean), _p(rstd))
+    _written(written)
+    return (out, mean, rstd) if return_stats else out
+
+
+def group_norm_bwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                   dout: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                   activation: Optional[str] = None, want_dx: bool = True, want_dweight: bool = True,
+                   want_dbias: bool = True, want_dgate: bool = True, weight_dtype: Optional[torch.dtype] = None):
+    """Gradients of group_norm_fwd: (dx, dweight, dbias, dgate), None where not wanted (dgate: or without a gate).
+
+    dout has x's shape and dtype; mean and rstd are the forward's.  dweight and dbias come in
+    ``weight_dtype`` (the weight's dtype by default, the bias's or x's without one), summed in float32 in
+    a fixed order.
+    """
+    rows, groups, width, act = _group_sizes(x, num_groups, activation, weight, bias, gate)
+    device = _same_device(x, weight=weight, bias=bias, dout=dout, mean=mean, rstd=rstd, gate=gate)
+    if dout.dtype != x.dtype or dout.shape != x.shape:
+        raise ValueError("dout must have x's shape and dtype")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (*x.shape[:-1], groups) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 [..., num_groups]")
+    weight, bias = (None if t is None else t.contiguous() for t in (weight, bias))
+    wd = weight.dtype if weight is not None else bias.dtype if bias is not None else weight_dtype or x.dtype
+    if wd not in DTYPE_CODE:
+        raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
+    C = x.shape[-1]
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
+    dz = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dgate and gate is not None else None
+    dw = torch.empty(C, dtype=wd, device=device) if want_dweight else None
+    db = torch.empty(C, dtype=wd, device=device) if want_dbias else None
+    x2, d2, z2 = _flat_rows(x), _flat_rows(dout), None if gate is None else _flat_rows(gate)
+    _CALLS["ccv_group_norm_bwd"](device, rows, groups, width, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], act, 0, *_state_at(x2),
+                                 _p(weight), _p(bias), *_state_at(z2), *_state_at(d2), mean.data_ptr(), rstd.data_ptr(),
+                                 _p(dx), C, _p(dz), C, _p(dw), _p(db))
+    return dx, dw, db, dz
+
+
+class _GroupNormFn(torch.autograd.Function):
+    """Forward and backward through the C ABI; saves the inputs and the groups' statistics."""
+
+    @staticmethod
+    def forward(ctx, x, num_groups, weight, bias, gate, activation, eps):
+        out, mean, rstd = group_norm_fwd(x, num_groups, weight, bias, gate, activation, eps, return_stats=True)
+        ctx.save_for_backward(x, weight, bias, gate, mean, rstd)
+        ctx.num_groups, ctx.activation = num_groups, activation
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, bias, gate, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        with torch.no_grad():
+            grads = group_norm_bwd(x, ctx.num_groups, weight, bias, dout.to(x.dtype), mean, rstd, gate, ctx.activation,
+                                   need[0], need[2], need[3], need[4])
+        dx, dw, db, dz = _first_order("group_norm_fn", (x, weight, bias, gate, dout), grads)
+        return dx, None, dw, db, dz, None, None
+
+
+def group_norm_fn(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, activation: Optional[str] = None, eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable group norm (group_norm_fwd, with gradients for x, weight, bias and gate through
+    group_norm_bwd).  Differentiable once: a second derivative raises."""
+    return _GroupNormFn.apply(x, num_groups, weight, bias, gate, activation, eps)
 
 
 # ---- sequence tables -------------------------------------------------------------------------

@@ -15,41 +15,10 @@
 // Every access is 16 bytes at any alignment.  Where the width is no multiple of that, a
 // row's last vector starts where it ends with the row; the elements that it shares with
 // the vector before it are left out of sums and written twice, with the same value.
-#include "ccv_delta_device.hpp"
-#include "ccv_norm_launch.hpp"
+#include "ccv_norm_device.hpp"
 
 namespace ccv {
 namespace {
-
-template <int DT> struct Vec { static constexpr int n = DT == CCV_DT_F32 ? 4 : 8; };
-
-// Sums over the `LANES` threads of a row of N values; every one of them gets them.  Rows of more
-// than a wave: through `red`, two pieces of it in turn, so that one barrier suffices.
-template <int LANES, int N>
-__device__ inline f32x2 row_sums(f32x2 v, float (*red)[2][8], int& turn) {
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float s = sum16(v[n]);
-    if constexpr (LANES >= 64) s = sum4rows(s);
-    v[n] = s;
-  }
-  if constexpr (LANES > 64) {
-    const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-      for (int n = 0; n < N; ++n) red[turn][n][w] = v[n];
-    lds_barrier();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float s = 0;
-#pragma unroll
-      for (int i = 0; i < LANES / 64; ++i) s += red[turn][n][i];
-      v[n] = s;
-    }
-    turn ^= 1;
-  }
-  return v;
-}
 
 // Row r of a view; rows that follow each other at one stride need no division (n1 is then 0).
 __device__ inline int64_t row_at(const int64_t* s, int64_t r, uint32_t n1) {
@@ -65,66 +34,6 @@ template <int DT>
 __device__ inline char* norm_row(void* p, const int64_t* s, int64_t r, uint32_t n1) {
   return static_cast<char*>(p) + row_at(s, r, n1) * (DT == CCV_DT_F32 ? 4 : 2);
 }
-
-template <int LANES> constexpr int kThreads = LANES > 256 ? LANES : 256;
-
-// A thread's vectors of a row.
-template <int DT, int LANES, int NV, bool FULL>
-struct Columns {
-  static constexpr int V = Vec<DT>::n, ES = DT == CCV_DT_F32 ? 4 : 2;
-  int col[NV], skip[NV];                 // first element; elements that belong to another thread (V: all)
-  __device__ inline Columns(int width) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * LANES + (int)(threadIdx.x % LANES)) * V;
-      col[i] = FULL || c + V <= width ? c : width - V;
-      skip[i] = FULL ? 0 : c >= width ? V : c - col[i];
-    }
-  }
-  __device__ inline bool mine(int i, int e) const { return FULL || e >= skip[i]; }
-  __device__ inline void load(u32x4 (&raw)[NV], const char* row) const {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      raw[i] = gload<u32x4>(pick(FULL || skip[i] < V, reinterpret_cast<uintptr_t>(row) + (uint32_t)col[i] * ES,
-                                 reinterpret_cast<uintptr_t>(kZeroSrc)));
-  }
-  __device__ static inline void unpack(u32x4 raw, float* x) {
-    if constexpr (DT == CCV_DT_F32) F32::unpack(raw, x);
-    else if constexpr (DT == CCV_DT_BF16) BF16::unpack(raw, x);
-    else F16::unpack(raw, x);
-  }
-  __device__ inline void store(char* row, int i, const float* y) const {
-    if (!FULL && skip[i] >= V) return;
-    char* p = row + (uint32_t)col[i] * ES;
-    if constexpr (DT == CCV_DT_F32) store16(p, F32::pack(y));
-    else if constexpr (DT == CCV_DT_BF16) store16(p, BF16::pack(y));
-    else store16(p, F16::pack(y));
-  }
-  __device__ inline void weights(float (&w)[NV][V], const void* p, int dtype, float other) const {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!p || (!FULL && skip[i] >= V)) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) w[i][e] = other;
-      } else if (dtype == CCV_DT_F32) {
-#pragma unroll
-        for (int e = 0; e < V; e += 4) F32::unpack(load16(static_cast<const float*>(p) + col[i] + e), w[i] + e);
-      } else {
-        const uint16_t* q = static_cast<const uint16_t*>(p) + col[i];
-#pragma unroll
-        for (int e = 0; e < V; e += 4) {
-          const u32x2 d = gload<u32x2>(reinterpret_cast<uintptr_t>(q + e));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t two = d[j / 2];
-            const uint16_t h = (uint16_t)(two >> (16 * (j % 2)));
-            w[i][e + j] = dtype == CCV_DT_BF16 ? BF16::to_f(h) : F16::to_f(h);
-          }
-        }
-      }
-    }
-  }
-};
 
 template <int DT, int LANES, int NV, bool FULL>
 __global__ __launch_bounds__(kThreads<LANES>) void fwd_kernel(NormArgs a) {
@@ -264,29 +173,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void bwd_kernel(NormArgs a) {
     }
 }
 
-// Column sums of the partial rows: a workgroup has 32 columns of one side, 32 threads a
-// column, joined through LDS.
-__global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
-  __shared__ float t[32][33];
-  const int side = blockIdx.y, c = threadIdx.x & 31, g = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  void* out = side ? a.db : a.dw;
-  if (!out) return;
-  float all = 0;
-  for (int r = g; col < a.width && r < a.groups;) {
-    const int end = min(a.groups, r + 32 * kNormRun);
-    float s = 0;
-#pragma unroll 8
-    for (; r < end; r += 32) s += a.part[((int64_t)r * 2 + side) * a.width + col];
-    all += s;
-  }
-  t[g][c] = all;
-  __syncthreads();
-  for (int h = 16; h; h >>= 1) {
-    if (g < h) t[g][c] += t[g + h][c];
-    __syncthreads();
-  }
-  if (g == 0 && col < a.width) store_gate(out, a.w_dtype, col, t[0][c]);
-}
+__global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) { sum_partials(a.part, a.groups, a.width, a.dw, a.db, a.w_dtype); }
 
 // ---- rows wider than 512 threads hold (walked again for each sum; they stay in L2), or narrower than a vector ----
 // 6700 rows of 20000 in bf16: forward 190 to 205 us, 2.7 TB/s of the row in and out; backward 405 to 419 us.

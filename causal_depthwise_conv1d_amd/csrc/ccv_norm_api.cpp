@@ -1,6 +1,6 @@
-// ccv_norm_api.cpp -- C ABI of layer norm and of the sequence tables: argument checks and
-// launches.  The operations are stated in ccv.h beside ccv_norm_fwd, ccv_norm_bwd and
-// ccv_seq_tables.  Host code; nothing here touches a device except the launches.
+// ccv_norm_api.cpp -- C ABI of layer norm, of group norm and of the sequence tables: argument
+// checks and launches.  The operations are stated in ccv.h beside ccv_norm_fwd, ccv_norm_bwd,
+// ccv_group_norm_fwd, ccv_group_norm_bwd and ccv_seq_tables.  Host code; nothing here touches a device except the launches.
 #include <math.h>
 #include <stdint.h>
 
@@ -155,6 +155,134 @@ int validate_bwd(const ccv_norm_bwd_args_t* p, NormArgs* a, int64_t* bytes, bool
   return CCV_OK;
 }
 
+// ---- group norm
+
+int check_group_rows(const void* p, int64_t s, int64_t rows, int64_t C, int es, bool written) {
+  if (!p) return CCV_OK;
+  const int64_t st[2] = {0, s};
+  return check_rows(Rows{p, st}, 1, rows, C, es, written);
+}
+
+int check_group_common(int64_t rows, int64_t groups, int64_t width, int x_dtype, int w_dtype, int activation, float eps) {
+  if (rows < 0 || groups < 1 || width < 0 || rows > INT32_MAX || groups > (1 << 24) || width > (1 << 24) || groups * width > (1 << 24)) return CCV_E_SHAPE;
+  if (x_dtype < 0 || x_dtype > 2 || w_dtype < 0 || w_dtype > 2) return CCV_E_DTYPE;
+  if (activation != CCV_ACT_NONE && activation != CCV_ACT_SILU) return CCV_E_UNSUPPORTED;
+  return !(eps >= 0.0f) || isinf(eps) ? CCV_E_UNSUPPORTED : CCV_OK;
+}
+
+// Walkers of a group: with `slots` groups under way a workgroup and about `blocks` workgroups; `least` rows each.
+int32_t group_walkers(int64_t rows, int64_t groups, int64_t slots, int64_t blocks, int64_t least) {
+  const int64_t most = std::max<int64_t>(1, blocks * slots / groups), need = (rows + least - 1) / least;
+  return (int32_t)std::max<int64_t>(1, std::min(most, need));
+}
+
+int validate_group_fwd(const ccv_group_norm_fwd_args_t* p, GroupNormArgs* a) {
+  if (!p) return CCV_E_NULL;
+  if (p->struct_size != (int64_t)sizeof(ccv_group_norm_fwd_args_t)) return CCV_E_ABI;
+  int st = check_group_common(p->rows, p->groups, p->width, p->x_dtype, p->w_dtype, p->activation, p->eps);
+  if (st != CCV_OK) return st;
+  *a = GroupNormArgs{};
+  if (p->rows == 0 || p->width == 0) return CCV_OK;
+  if (!p->x || !p->out) return CCV_E_NULL;
+  const int es = elt_size(p->x_dtype);
+  const int64_t C = p->groups * p->width;
+  if ((st = check_group_rows(p->x, p->x_stride, p->rows, C, es, false)) != CCV_OK) return st;
+  if ((st = check_group_rows(p->gate, p->gate_stride, p->rows, C, es, false)) != CCV_OK) return st;
+  if ((st = check_group_rows(p->out, p->out_stride, p->rows, C, es, true)) != CCV_OK) return st;
+  const void* written[] = {p->out, p->mean, p->rstd};
+  for (int i = 0; i < 3; ++i) {
+    if (!written[i]) continue;
+    for (const void* q : {p->x, p->weight, p->bias, p->gate})
+      if (q == written[i]) return CCV_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (written[j] == written[i]) return CCV_E_ALIAS;
+  }
+  a->x = p->x;
+  a->w = p->weight;
+  a->b = p->bias;
+  a->z = p->gate;
+  a->out = p->out;
+  a->mean = p->mean;
+  a->rstd = p->rstd;
+  a->x_s = p->x_stride;
+  a->z_s = p->gate_stride;
+  a->o_s = p->out_stride;
+  a->rows = p->rows;
+  a->groups = (int32_t)p->groups;
+  a->width = (int32_t)p->width;
+  a->x_dtype = p->x_dtype;
+  a->w_dtype = p->w_dtype;
+  a->silu = p->activation == CCV_ACT_SILU;
+  a->eps = p->eps;
+  return CCV_OK;
+}
+
+int validate_group_bwd(const ccv_group_norm_bwd_args_t* p, GroupNormArgs* a, int64_t* bytes, bool with_ws) {
+  if (!p) return CCV_E_NULL;
+  if (p->struct_size != (int64_t)sizeof(ccv_group_norm_bwd_args_t)) return CCV_E_ABI;
+  int st = check_group_common(p->rows, p->groups, p->width, p->x_dtype, p->w_dtype, p->activation, 0.0f);
+  if (st != CCV_OK) return st;
+  *a = GroupNormArgs{};
+  *bytes = 0;
+  if (p->dgate && !p->gate && p->rows > 0) return CCV_E_UNSUPPORTED;
+  if (p->width == 0) return CCV_OK;
+  const int es = elt_size(p->x_dtype);
+  const int64_t C = p->groups * p->width;
+  if (p->rows > 0) {
+    if (!p->x || !p->dout || !p->mean || !p->rstd) return CCV_E_NULL;
+    if ((st = check_group_rows(p->x, p->x_stride, p->rows, C, es, false)) != CCV_OK) return st;
+    if ((st = check_group_rows(p->gate, p->gate_stride, p->rows, C, es, false)) != CCV_OK) return st;
+    if ((st = check_group_rows(p->dout, p->dout_stride, p->rows, C, es, false)) != CCV_OK) return st;
+    if ((st = check_group_rows(p->dx, p->dx_stride, p->rows, C, es, true)) != CCV_OK) return st;
+    if ((st = check_group_rows(p->dgate, p->dgate_stride, p->rows, C, es, true)) != CCV_OK) return st;
+  }
+  const void* written[] = {p->dx, p->dgate, p->dweight, p->dbias};
+  for (int i = 0; i < 4; ++i) {
+    if (!written[i]) continue;
+    for (const void* q : {p->x, p->weight, p->bias, p->gate, p->dout, (const void*)p->mean, (const void*)p->rstd})
+      if (q == written[i]) return CCV_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (written[j] == written[i]) return CCV_E_ALIAS;
+  }
+  a->x = p->x;
+  a->w = p->weight;
+  a->b = p->bias;
+  a->z = p->gate;
+  a->dout = p->dout;
+  a->dx = p->dx;
+  a->dz = p->dgate;
+  a->dw = p->dweight;
+  a->db = p->dbias;
+  a->mean = const_cast<float*>(p->mean);
+  a->rstd = const_cast<float*>(p->rstd);
+  a->x_s = p->x_stride;
+  a->z_s = p->gate_stride;
+  a->do_s = p->dout_stride;
+  a->dx_s = p->dx_stride;
+  a->dz_s = p->dgate_stride;
+  a->rows = p->rows;
+  a->groups = (int32_t)p->groups;
+  a->width = (int32_t)p->width;
+  a->x_dtype = p->x_dtype;
+  a->w_dtype = p->w_dtype;
+  a->silu = p->activation == CCV_ACT_SILU;
+  const NormShape s = group_norm_shape(p->width, es);
+  if (p->rows == 0) a->walkers = 0;
+  else if (s.lanes) a->walkers = std::max(group_walkers(p->rows, p->groups, 256 / s.lanes, kGroups, 4), (int32_t)((p->rows + kNormRows - 1) / kNormRows));
+  else a->walkers = (int32_t)std::min<int64_t>(p->rows, 64);
+  if ((int64_t)a->walkers * p->groups > INT32_MAX / 256) return CCV_E_SHAPE;      // of threads in a launch
+  if (p->dweight || p->dbias) {
+    *bytes = (int64_t)a->walkers * 2 * C * 4;
+    if (with_ws && *bytes) {
+      if (!p->workspace) return CCV_E_NULL;
+      if (!aligned16(p->workspace)) return CCV_E_LAYOUT;
+      if (p->workspace_bytes < *bytes) return CCV_E_SHAPE;
+    }
+    a->part = static_cast<float*>(p->workspace);
+  }
+  return CCV_OK;
+}
+
 int validate_tables(const ccv_seq_tables_args_t* p, TablesArgs* a) {
   if (!p) return CCV_E_NULL;
   if (p->struct_size != (int64_t)sizeof(ccv_seq_tables_args_t)) return CCV_E_ABI;
@@ -208,6 +336,44 @@ int ccv_norm_bwd(const ccv_norm_bwd_args_t* args, void* hip_stream) {
   if (st != CCV_OK || a.width == 0) return st;
   if (a.rows == 0 && !a.dw && !a.db) return CCV_OK;
   return launch_norm_bwd(a, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
+}
+
+int ccv_group_norm_fwd_check(const ccv_group_norm_fwd_args_t* args) {
+  GroupNormArgs a;
+  return validate_group_fwd(args, &a);
+}
+
+int ccv_group_norm_fwd(const ccv_group_norm_fwd_args_t* args, void* hip_stream) {
+  GroupNormArgs a;
+  const int st = validate_group_fwd(args, &a);
+  if (st != CCV_OK || a.rows == 0) return st;
+  const int cus = device_cu_count(hip_stream);
+  if (cus < 0) return CCV_E_HIP;
+  const NormShape s = group_norm_shape(a.width, elt_size(a.x_dtype));
+  if (s.lanes) a.walkers = group_walkers(a.rows, a.groups, 256 / s.lanes, (int64_t)cu_count(cus) * 8, 1);
+  return launch_group_norm_fwd(a, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
+}
+
+int ccv_group_norm_bwd_check(const ccv_group_norm_bwd_args_t* args) {
+  GroupNormArgs a;
+  int64_t bytes;
+  return validate_group_bwd(args, &a, &bytes, true);
+}
+
+int64_t ccv_group_norm_bwd_workspace_size(const ccv_group_norm_bwd_args_t* args) {
+  GroupNormArgs a;
+  int64_t bytes;
+  const int st = validate_group_bwd(args, &a, &bytes, false);
+  return st != CCV_OK ? st : bytes;
+}
+
+int ccv_group_norm_bwd(const ccv_group_norm_bwd_args_t* args, void* hip_stream) {
+  GroupNormArgs a;
+  int64_t bytes;
+  const int st = validate_group_bwd(args, &a, &bytes, true);
+  if (st != CCV_OK || a.width == 0) return st;
+  if (!a.dw && !a.db && (a.rows == 0 || (!a.dx && !a.dz))) return CCV_OK;
+  return launch_group_norm_bwd(a, hip_stream) == 0 ? CCV_OK : CCV_E_HIP;
 }
 
 int ccv_seq_tables_check(const ccv_seq_tables_args_t* args) {

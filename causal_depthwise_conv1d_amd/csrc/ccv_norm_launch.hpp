@@ -43,6 +43,30 @@ inline NormShape norm_shape(int64_t width, int elt) {
   return {0, 0};
 }
 
+// Group norm: row r of x starts at r * x_s elements and has `groups` groups of `width` channels; a
+// group of a row is walked by `lanes` threads with `nv` vectors each (lanes 0: element by element, by one thread where
+// it is narrower than a vector, else by a workgroup).
+struct GroupNormArgs {
+  const void *x, *w, *b, *z, *dout;
+  void *out, *dx, *dz, *dw, *db;
+  int64_t x_s, z_s, o_s, do_s, dx_s, dz_s;
+  float *mean, *rstd;                 // [rows, groups]
+  int64_t rows;
+  int32_t groups, width, x_dtype, w_dtype, silu;
+  float eps;
+  float* part;                        // backward: [walkers][2][groups * width] partial sums of dw, db
+  int32_t walkers;                    // each takes every walkers-th row
+};
+
+inline NormShape group_norm_shape(int64_t width, int elt) {
+  const int64_t v = 16 / elt;
+  if (width < v) return {0, 0};
+  for (int32_t lanes : {4, 16, 64, 256})
+    for (int32_t nv : {1, 2, 4})
+      if (width <= lanes * nv * v && (nv < 4 || lanes == 256)) return {lanes, nv};
+  return {0, 0};
+}
+
 struct TablesArgs {
   const int32_t* lengths;
   int32_t *cu, *seq, *pos;            // [n + 1], [total] or nullptr, [total] or nullptr
@@ -52,6 +76,8 @@ struct TablesArgs {
 // Each returns a hipError_t value (0 = success).
 int launch_norm_fwd(const NormArgs& a, int cus, void* stream);
 int launch_norm_bwd(const NormArgs& a, void* stream);
+int launch_group_norm_fwd(const GroupNormArgs& a, void* stream);
+int launch_group_norm_bwd(const GroupNormArgs& a, void* stream);
 int launch_tables(const TablesArgs& a, void* stream);
 
 }  // namespace ccv

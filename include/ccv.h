@@ -530,6 +530,68 @@ int64_t ccv_norm_bwd_workspace_size(const ccv_norm_bwd_args_t* args);
 int ccv_norm_bwd_check(const ccv_norm_bwd_args_t* args);
 int ccv_norm_bwd(const ccv_norm_bwd_args_t* args, void* hip_stream);
 
+/* ---- group norm -------------------------------------------------------------------------
+ *
+ * Over `groups` groups of `width` neighbouring channels of each row of x [rows, groups width], channels last: the statistics
+ * are of one row (a step of a sequence), as a causal layer needs them, with a weight and a bias a channel, and an
+ * activation or a gate behind them (a layer's heads leave a recurrence so):
+ *
+ *   mean = sum x / width;  rstd = (sum (x - mean)^2 / width + eps)^-1/2   over a group
+ *   y    = (x - mean) rstd weight + bias
+ *   out  = act(y), or with a gate [rows, groups width]: out = y act(gate)
+ *
+ * Row r of an array lies at r times its stride in elements; gate and out have x's dtype; weight and bias ([groups width],
+ * contiguous, w_dtype) may each be NULL (ones, zeros); mean and rstd (fp32 [rows, groups]) are written when not NULL.
+ * activation is CCV_ACT_NONE or CCV_ACT_SILU, eps >= 0 and finite (else CCV_E_UNSUPPORTED).  rows below
+ * 2^31, groups width at most 2^24.  out may be no input.  Statistics are fp32, the variance summed from the deviations. */
+typedef struct ccv_group_norm_fwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_group_norm_fwd_args_t) */
+  int64_t rows, groups, width;
+  int32_t x_dtype, w_dtype;
+  int32_t activation;           /* ccv_act_t */
+  float eps;
+  const void* x;                int64_t x_stride;
+  const void* weight;
+  const void* bias;
+  const void* gate;             int64_t gate_stride;      /* or NULL */
+  void* out;                    int64_t out_stride;
+  float* mean;
+  float* rstd;
+} ccv_group_norm_fwd_args_t;
+
+int ccv_group_norm_fwd_check(const ccv_group_norm_fwd_args_t* args);
+int ccv_group_norm_fwd(const ccv_group_norm_fwd_args_t* args, void* hip_stream);
+
+/* Its gradients, with n = (x - mean) rstd; dy = dout act'(y), or with a gate dy = dout act(gate); e = dy weight:
+ *   dx = rstd (e - mean(e) - n mean(e n)),  dgate = dout y act'(gate),  dweight = sum of dy n,  dbias = sum of dy
+ * from x, dout, the forward's mean and rstd, and its weight, bias and gate.  dx, dgate, dweight, dbias may each be
+ * NULL (not wanted; dgate without a gate: CCV_E_UNSUPPORTED); dweight and dbias are summed in fp32 over all rows, in a
+ * fixed order, and rounded once to w_dtype (zeros when there are no rows).  They need a workspace of
+ * ccv_group_norm_bwd_workspace_size bytes, 16-byte aligned. */
+typedef struct ccv_group_norm_bwd_args {
+  int64_t struct_size;          /* = sizeof(ccv_group_norm_bwd_args_t) */
+  int64_t rows, groups, width;
+  int32_t x_dtype, w_dtype;
+  int32_t activation;
+  int32_t reserved;             /* 0 */
+  const void* x;                int64_t x_stride;
+  const void* weight;
+  const void* bias;
+  const void* gate;             int64_t gate_stride;
+  const void* dout;             int64_t dout_stride;
+  const float* mean;
+  const float* rstd;
+  void* dx;                     int64_t dx_stride;
+  void* dgate;                  int64_t dgate_stride;
+  void* dweight;
+  void* dbias;
+  void* workspace;              int64_t workspace_bytes;
+} ccv_group_norm_bwd_args_t;
+
+int64_t ccv_group_norm_bwd_workspace_size(const ccv_group_norm_bwd_args_t* args);
+int ccv_group_norm_bwd_check(const ccv_group_norm_bwd_args_t* args);
+int ccv_group_norm_bwd(const ccv_group_norm_bwd_args_t* args, void* hip_stream);
+
 /* ---- sequence tables ----------------------------------------------------------------------
  *
  * A packed row's tables, made on the GPU from the lengths of its N sequences (int32, device;

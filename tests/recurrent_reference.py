@@ -111,3 +111,68 @@ def inputs(B, L, C, dtype="f32", gate="f32", seed=0, seqs=None, states=True, slo
     g = (-size * torch.rand(B, L, C, generator=gen)).to(DT[gate])
     n = B if seqs is None else seqs
     return x, g, rand(n, C) if states else None
+
+
+# ---- group norm -----------------------------------------------------------------------------------
+#
+# The bounds follow the formulas a value at a time: a sum of n terms made by threads is off by at most k u of the sum of
+# its terms' sizes, k the roundings of one thread's chain (at most 32 elements, or a 1024th of a wider group) and of the joins (at
+# most 16); sigmoid and exponential are off by the argument's rounding, 1.5 u of its size, and a few units, and
+# a sigmoid below fp32's smallest normal number, 2^-126, is 0: the value v sigmoid(v) is then off by 2^-126 |v|.
+
+def act(v, silu):
+    """act, act' and bounds on their rounding errors, for v exact."""
+    if not silu:
+        return v, torch.ones_like(v), 0 * v, 0 * v
+    s = 1 / (1 + torch.exp(-v))
+    eps = (1.5 * v.abs() + 10) * U
+    none = 2.0 ** -126
+    return v * s, s * (1 + v * (1 - s)), eps * (v * s).abs() + none * v.abs(), eps * (1 + v.abs()) + none * (1 + v.abs())
+
+
+def group_norm(x, groups, w, b, z, silu, eps, dout=None):
+    """{name: (value, bound)} of out, mean, rstd and, with dout, dx, dw, db, dz; x [rows, C]."""
+    rows, C = x.shape
+    x = x.double().unflatten(1, (groups, -1))
+    per = lambda t, other: (torch.full((C,), other, dtype=torch.float64) if t is None else t.double()).view(1, groups, -1)  # noqa: E731
+    w, b = per(w, 1.0), per(b, 0.0)
+    avg = lambda t: t.mean(-1, keepdim=True)  # noqa: E731
+    k = (48 + x.shape[-1] / 1024) * U
+    mu, emu = avg(x), k * avg(x.abs())
+    d = x - mu
+    ed = emu + U * d.abs()
+    var = avg(d * d)
+    rs = (var + eps) ** -0.5
+    rel = 0.5 * (avg(2 * d.abs() * ed + ed * ed) + k * var) / (var + eps) + 4 * U
+    n = d * rs
+    en = rs * ed + n.abs() * (rel + U)
+    y = n * w + b
+    ey = w.abs() * en + 3 * U * ((n * w).abs() + b.abs())
+    if z is None:
+        v, slope, ev, es = act(y, silu)
+        out, eo = v, 1.1 * ey + ev
+    else:
+        z = z.double().unflatten(1, (groups, -1))
+        v, slope, ev, es = act(z, silu)
+        out, eo = y * v, v.abs() * ey + y.abs() * ev + ey * ev + U * (y * v).abs()
+    flat = lambda t: t.flatten(1)  # noqa: E731
+    ans = {"out": (flat(out), flat(eo)), "mean": (mu[..., 0], emu[..., 0]), "rstd": (rs[..., 0], (rs * rel)[..., 0])}
+    if dout is None:
+        return ans
+    g = dout.double().unflatten(1, (groups, -1))
+    if z is None:
+        dy, edy = g * slope, g.abs() * ((0.5 if silu else 0) * ey + es + U * slope.abs())
+    else:
+        dy, edy = g * v, g.abs() * (ev + U * v.abs())
+        ans["dz"] = (flat(g * y * slope), flat(g.abs() * (slope.abs() * ey + (y.abs() + ey) * es) + 3 * U * (g * y * slope).abs()))
+    e = dy * w
+    ee = w.abs() * edy + U * e.abs()
+    m1, em1 = avg(e), avg(ee) + k * avg(e.abs())
+    m2, em2 = avg(e * n), avg(ee * n.abs() + e.abs() * en + ee * en) + k * avg((e * n).abs())
+    inner = e - m1 - n * m2
+    einner = ee + em1 + n.abs() * em2 + en * (m2.abs() + em2) + 4 * U * (e.abs() + m1.abs() + (n * m2).abs())
+    ans["dx"] = (flat(rs * inner), flat(rs * (einner + (rel + 2 * U) * inner.abs()) * (1 + rel)))
+    chain = min(rows, 1200) * U
+    ans["dw"] = ((dy * n).sum(0).flatten(), (edy * n.abs() + dy.abs() * en + edy * en + chain * (dy * n).abs()).sum(0).flatten())
+    ans["db"] = (dy.sum(0).flatten(), (edy + chain * dy.abs()).sum(0).flatten())
+    return ans
