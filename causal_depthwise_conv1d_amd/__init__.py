@@ -13,7 +13,8 @@ Low level (same names as the C ABI):
     ccv_bwd_workspace_size(args),
     ccv_status_str(code), ccv_abi_version()
     ccv_delta_fwd, ccv_delta_bwd, ccv_delta_update, ccv_linrec_fwd, ccv_linrec_bwd,
-    ccv_linrec_update, ccv_norm_fwd, ccv_norm_bwd, ccv_group_norm_fwd, ccv_group_norm_bwd and
+    ccv_linrec_update, ccv_norm_fwd, ccv_norm_bwd, ccv_group_norm_fwd, ccv_group_norm_bwd,
+    ccv_rotary and
     ccv_seq_tables (args, stream=None), their ccv_*_check(args) and, where they need a
     workspace, ccv_*_workspace_size(args)
 High level (the full-sequence contract of Ch.4 "Dao interface and source map",
@@ -43,11 +44,15 @@ The operators of a gated linear-attention layer around the conv:
     layer_norm_fn(...)                  (differentiable)
     group_norm_fwd(x, num_groups, weight=None, bias=None, gate=None, activation=None, ...),
     group_norm_bwd(...), group_norm_fn(...)     (differentiable)
+    rotary_fwd(q, k, positions, frequencies, interleaved=False, scale=1.0, ...),
+    rotary_fn(...)                      (differentiable)
+    rotary_frequencies(turned, base=10000.0, scaling=None, ...)     -> (frequencies, scale)
     sequence_tables(lengths, total)     -> (cu_seqlens, seq_idx, positions)
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from typing import Optional
@@ -279,6 +284,15 @@ class ccv_group_norm_bwd_args_t(_Args):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+class ccv_rotary_args_t(_Args):
+    """Mirror of ``ccv_rotary_args_t`` in include/ccv.h (field order and types)."""
+    _fields_ = [("struct_size", ctypes.c_int64), ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("turned", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("scale", ctypes.c_float),
+                *_strided(("q", "q_stride"), ("k", "k_stride")), ("positions", ctypes.c_void_p), ("pos_stride", _I64x2),
+                ("frequencies", ctypes.c_void_p), *_strided(("q_out", "q_out_stride"), ("k_out", "k_out_stride"))]
+
+
 _LAYER_CALLS = {
     "ccv_delta_fwd": (ccv_delta_fwd_args_t, True), "ccv_delta_bwd": (ccv_delta_bwd_args_t, True),
     "ccv_delta_update": (ccv_delta_update_args_t, False), "ccv_norm_fwd": (ccv_norm_fwd_args_t, False),
@@ -286,6 +300,7 @@ _LAYER_CALLS = {
     "ccv_linrec_fwd": (ccv_linrec_fwd_args_t, True), "ccv_linrec_bwd": (ccv_linrec_bwd_args_t, True),
     "ccv_linrec_update": (ccv_linrec_update_args_t, False),
     "ccv_group_norm_fwd": (ccv_group_norm_fwd_args_t, False), "ccv_group_norm_bwd": (ccv_group_norm_bwd_args_t, True),
+    "ccv_rotary": (ccv_rotary_args_t, False),
 }
 
 
@@ -558,6 +573,15 @@ def ccv_group_norm_bwd_check(args: ccv_group_norm_bwd_args_t) -> int:
 def ccv_group_norm_bwd_workspace_size(args: ccv_group_norm_bwd_args_t) -> int:
     """Workspace bytes the backward needs (>= 0), or a negative status."""
     return lib().ccv_group_norm_bwd_workspace_size(ctypes.byref(args))
+
+
+def ccv_rotary(args: ccv_rotary_args_t, stream=None) -> int:
+    """Enqueue rotary positions on `stream`; returns the status code."""
+    return lib().ccv_rotary(ctypes.byref(args), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def ccv_rotary_check(args: ccv_rotary_args_t) -> int:
+    return lib().ccv_rotary_check(ctypes.byref(args))
 
 
 # ---- tensors -> args -------------------------------------------------------------------
@@ -1630,6 +1654,133 @@ def group_norm_fn(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tenso
     return _GroupNormFn.apply(x, num_groups, weight, bias, gate, activation, eps)
 
 
+# ---- rotary positions ------------------------------------------------------------------------
+
+def rotary_frequencies(turned: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original_length: Optional[int] = None, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequencies, scale) for rotary_fwd: float64 [turned / 2], base^(-2i / turned) radians a position, and the
+    factor of the results.
+
+    ``scaling`` stretches them for contexts ``factor`` times as long as the ones a model was trained on:
+      "linear"  every position divided by the factor
+      "base"    the base raised by factor^(turned / (turned - 2)), so that the slowest pair is divided by the
+                factor and the fastest not at all
+      "parts"   pairs that make more than ``fast`` turns over ``original_length`` positions stay, those that make fewer
+                than ``slow`` are divided, with a ramp between; scale = 0.1 ln(factor) + 1
+    """
+    if turned < 2 or turned % 2:
+        raise ValueError("turned must be a positive even number")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', not {scaling!r}")
+    if not base > 1 or not factor >= 1 or not fast > slow > 0:
+        raise ValueError("base must be above 1, factor at least 1 and fast above slow above 0")
+    if scaling == "base":
+        base = base * factor ** (turned / max(turned - 2, 1))
+    i = torch.arange(turned // 2, dtype=torch.float64)
+    f = base ** (-2 * i / turned)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original_length is None or original_length < 1:
+            raise ValueError("scaling 'parts' needs original_length")
+        pair = lambda turns: turned * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), turned // 2 - 1)
+        whole = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f / factor * (1 - whole) + f * whole
+        scale = 0.1 * math.log(factor) + 1
+    return f.to(device), scale
+
+
+def _rotary_sizes(q, k, positions, frequencies):
+    """(B, L, Hq, Hk, D), checked; one step without its dimension where q is [B, Hq, D]."""
+    one = q.dim() == 3
+    lead = q.shape[:-2]
+    if q.dim() not in (3, 4):
+        raise ValueError("expected q [B, L, Hq, D] or [B, Hq, D]")
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != lead or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype):
+        raise ValueError("k must have q's dtype and sizes, but for its heads")
+    if q.dtype not in DTYPE_CODE:
+        raise ValueError(f"q must be float32, float16 or bfloat16, not {q.dtype}")
+    if positions.dtype != torch.int32 or positions.shape != lead:
+        raise ValueError("positions must be int32 [B, L] ([B] for one step)")
+    D = q.shape[-1]
+    if frequencies.dtype != torch.float64 or frequencies.dim() != 1 or 2 * frequencies.numel() > D:
+        raise ValueError("frequencies must be float64 [turned / 2], with turned at most D")
+    if not 1 <= D <= 2048:
+        raise ValueError("heads must be 1 to 2048 wide")
+    return lead[0], 1 if one else lead[1], q.shape[-2], 0 if k is None else k.shape[-2], D
+
+
+def rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, frequencies: torch.Tensor,
+               interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Queries and keys turned by their positions on the GPU, in one call.
+
+    q [B, L, Hq, D] and k [B, L, Hk, D] or None, in one dtype; positions int32 [B, L] (those of
+    sequence_tables, say; any strides); or one step, without the dimension of L.  frequencies: float64 [turned / 2],
+    radians a position (rotary_frequencies).  The first ``turned`` elements of a head make pairs, (i, i + turned / 2)
+    or with ``interleaved`` (2i, 2i + 1); a pair (u, v) becomes scale (u cos - v sin, v cos + u sin), the rest of the head
+    is copied.  ``inverse`` turns the other way (the scale stays).  q_out and k_out may be q and k
+    themselves.  Strided views are used as they are when a head's elements are unit-stride.  Returns (q', k'), k' None
+    without k.
+    """
+    B, L, Hq, Hk, D = _rotary_sizes(q, k, positions, frequencies)
+    device = _same_device(q, k=k, positions=positions, frequencies=frequencies, q_out=q_out, k_out=k_out)
+    if k is None and k_out is not None:
+        raise ValueError("k_out given without k")
+    written = (q_out, k_out)
+    one = q.dim() == 3
+    outs = []
+    for name, t, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if t is None:
+            outs.append(None)
+        elif o is None:
+            outs.append(torch.empty_like(t, memory_format=torch.contiguous_format))
+        elif o.dtype != t.dtype or o.shape != t.shape or (o.stride(-1) != 1 and D > 1):
+            raise ValueError(f"{name} must have its input's shape and dtype with unit stride in its last dimension")
+        else:
+            outs.append(o)
+    q, k = _unit_heads(q), None if k is None else _unit_heads(k)
+    at = _step_at if one else _at
+    none = (0, 0, 0, 0)
+    ps = positions.stride()
+    frequencies = frequencies.contiguous()
+    _CALLS["ccv_rotary"](device, B, L, Hq, Hk, D, 2 * frequencies.numel(), DTYPE_CODE[q.dtype], int(interleaved), int(inverse), scale,
+                         *at(q), *(none if k is None else at(k)), positions.data_ptr(), ps[0], 0 if one else ps[1],
+                         frequencies.data_ptr(), *at(outs[0]), *(none if k is None else at(outs[1])))
+    _written(*written)
+    return outs[0], outs[1]
+
+
+class _RotaryFn(torch.autograd.Function):
+    """Forward and backward through the C ABI; the backward turns the gradients the other way."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, frequencies, interleaved, scale):
+        ctx.save_for_backward(positions, frequencies)
+        ctx.how = interleaved, scale
+        ctx.set_materialize_grads(False)
+        return rotary_fwd(q, k, positions, frequencies, interleaved, scale)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        given = [t for t in (dq, dk) if t is not None]
+        if not given:
+            return (None,) * 6
+        with torch.no_grad():
+            turned = rotary_fwd(given[0], given[1] if len(given) > 1 else None, *ctx.saved_tensors, *ctx.how, inverse=True)
+        turned = iter(_first_order("rotary_fn", given, turned))
+        return next(turned) if dq is not None else None, next(turned) if dk is not None else None, None, None, None, None
+
+
+def rotary_fn(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, frequencies: torch.Tensor,
+              interleaved: bool = False, scale: float = 1.0):
+    """Differentiable rotary positions (rotary_fwd, with gradients for q and k by the inverse turn).
+    Differentiable once: a second derivative raises."""
+    return _RotaryFn.apply(q, k, positions, frequencies, interleaved, scale)
+
+
 # ---- sequence tables -------------------------------------------------------------------------
 
 def sequence_tables(lengths: torch.Tensor, total: int):
@@ -1637,7 +1788,8 @@ def sequence_tables(lengths: torch.Tensor, total: int):
     (int32 [N], on the GPU): (cu_seqlens [N + 1], seq_idx [1, total], positions [1, total]),
     all int32, made on the GPU without a look by the host.
 
-    seq_idx is what causal_conv1d_fwd takes and cu_seqlens what gated_delta_rule_fwd takes.
+    seq_idx is what causal_conv1d_fwd takes, cu_seqlens what gated_delta_rule_fwd and
+    gated_linear_recurrence_fwd take, positions what rotary_fwd takes.
     Steps past the last sequence have seq_idx -1 and position 0; lengths that do not fit
     are cut at ``total``, negative ones count as 0.
     """

@@ -31,9 +31,9 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", CSRC, "-I"
 
 KERNEL_SOURCES = ["ccv_cf.hip", "ccv_cl.hip", "ccv_update.hip", "ccv_bwd.hip", "ccv_bwd_static.hip",
                   "ccv_device_info.hip", "ccv_delta_prep.hip", "ccv_delta_scan.hip", "ccv_delta_bwd.hip",
-                  "ccv_delta_update.hip", "ccv_norm.hip", "ccv_tables.hip", "ccv_linrec.hip", "ccv_linrec_bwd.hip", "ccv_gnorm.hip", "ccv_gnorm_bwd.hip"]
+                  "ccv_delta_update.hip", "ccv_norm.hip", "ccv_tables.hip", "ccv_linrec.hip", "ccv_linrec_bwd.hip", "ccv_gnorm.hip", "ccv_gnorm_bwd.hip", "ccv_rotary.hip"]
 HOST_SOURCES = ["ccv_api.cpp", "ccv_update_api.cpp", "ccv_bwd_api.cpp", "ccv_delta_api.cpp", "ccv_norm_api.cpp",
-                "ccv_linrec_api.cpp"]
+                "ccv_linrec_api.cpp", "ccv_rotary_api.cpp"]
 CALIB_SOURCES = ["ccv_calib.hip"]
 
 

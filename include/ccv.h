@@ -601,8 +601,8 @@ int ccv_group_norm_bwd(const ccv_group_norm_bwd_args_t* args, void* hip_stream);
  *   seq_idx[t] = s and positions[t] = t - cu_seqlens[s] for t in sequence s;
  *   seq_idx[t] = -1 and positions[t] = 0 for cu_seqlens[N] <= t < total
  *
- * seq_idx is what the conv takes (as [1, total]), cu_seqlens what ccv_delta_fwd takes.
- * seq_idx and positions may be NULL. */
+ * seq_idx is what the conv takes (as [1, total]), cu_seqlens what ccv_delta_fwd and ccv_linrec_fwd take,
+ * positions what ccv_rotary takes.  seq_idx and positions may be NULL. */
 typedef struct ccv_seq_tables_args {
   int64_t struct_size;          /* = sizeof(ccv_seq_tables_args_t) */
   int64_t N, total;
@@ -712,6 +712,37 @@ typedef struct ccv_linrec_update_args {
 
 int ccv_linrec_update_check(const ccv_linrec_update_args_t* args);
 int ccv_linrec_update(const ccv_linrec_update_args_t* args, void* hip_stream);
+
+/* ---- rotary positions ----------------------------------------------------------------------
+ *
+ * Queries and keys turned by the positions of their steps (those of ccv_seq_tables, say).  The first `turned` elements of
+ * a head make turned / 2 pairs: elements i and i + turned / 2, or with interleaved = 1 elements 2 i and 2 i + 1.  Pair i at
+ * position p becomes, with the angle p frequencies[i] (inverse = 1: its negative),
+ *
+ *   (u, v) -> scale (u cos - v sin, v cos + u sin)
+ *
+ * and the other elements are copied.  q, q_out: [B, L, Hq, D]; k, k_out: [B, L, Hk, D] (Hk or Hq may be 0), element
+ * (b, t, h, d) at b s[0] + t s[1] + h s[2] + d: unit stride inside a head; x_dtype; D at most 2048 (CCV_E_UNSUPPORTED), turned even.
+ * positions: int32, step (b, t) at b s[0] + t s[1] (s[0] = 0: the same for all rows); frequencies: 64-bit, radians
+ * a position, contiguous [turned / 2].  Angles are 64-bit, their cosines and sines and the products fp32, results rounded once.
+ * q_out may be q itself and k_out k (same strides); what is not turned then stays as it is.  The gradient
+ * of q is the gradient of q_out under the same call with inverse = 1 (the scale is not inverted). */
+typedef struct ccv_rotary_args {
+  int64_t struct_size;          /* = sizeof(ccv_rotary_args_t) */
+  int64_t B, L, Hq, Hk, D, turned;
+  int32_t x_dtype;
+  int32_t interleaved, inverse; /* 0 or 1 */
+  float scale;
+  const void* q;                int64_t q_stride[3];      /* (row, step, head) */
+  const void* k;                int64_t k_stride[3];
+  const int32_t* positions;     int64_t pos_stride[2];    /* (row, step) */
+  const double* frequencies;
+  void* q_out;                  int64_t q_out_stride[3];
+  void* k_out;                  int64_t k_out_stride[3];
+} ccv_rotary_args_t;
+
+int ccv_rotary_check(const ccv_rotary_args_t* args);
+int ccv_rotary(const ccv_rotary_args_t* args, void* hip_stream);
 
 /* Static, NUL-terminated name of a status code ("CCV_OK", ...). */
 const char* ccv_status_str(int status);

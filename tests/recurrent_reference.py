@@ -10,6 +10,7 @@ M[t] = a M[t-1] + |b[t]| and K[t] = a (K[t-1] + M[t-1]) give as 3 u (K + 24 M). 
 values.  A weight sqrt(1 - a^2), from 1 - a good to 2 u, is good to 4 u, a reciprocal of it to 6 u; what has more
 roundings than that is counted with 24 u.  Outputs of 16 bits are rounded once more: half a spacing.
 """
+import numpy as np
 import torch
 
 from layer_reference import DT, half_spacing  # noqa: F401
@@ -176,3 +177,25 @@ def group_norm(x, groups, w, b, z, silu, eps, dout=None):
     ans["dw"] = ((dy * n).sum(0).flatten(), (edy * n.abs() + dy.abs() * en + edy * en + chain * (dy * n).abs()).sum(0).flatten())
     ans["db"] = (dy.sum(0).flatten(), (edy + chain * dy.abs()).sum(0).flatten())
     return ans
+
+
+# ---- rotary positions -----------------------------------------------------------------------------
+#
+# The kernel's angle p f is rounded three times in 64 bits, 3 2^-53 |p f|, and its remainder and the two series a few
+# times in 32: cosines and sines are off by at most 3 2^-53 |p f| + 3 u, times the scale, and a pair's products and
+# their sum are rounded once each.  The angle itself is made in 80 bits here.
+
+def rotary(x, positions, freq, interleaved=False, scale=1.0, inverse=False):
+    """(value, bound) of x [B, L, H, D] turned."""
+    angle = positions.numpy().astype(np.longdouble)[..., None] * freq.cpu().numpy().astype(np.longdouble)
+    cos, sin = (torch.from_numpy(f(angle).astype(np.float64))[:, :, None] * scale for f in (np.cos, np.sin))
+    sin = -sin if inverse else sin
+    off = (torch.from_numpy(np.abs(angle).astype(np.float64))[:, :, None] * 3 * 2.0 ** -53 + 3 * U) * abs(scale) + 2 * U * abs(scale)
+    half = freq.numel()
+    x = x.double()
+    y, bound = x.clone(), torch.zeros_like(x)
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    u, v = x[..., a], x[..., b]
+    y[..., a], y[..., b] = u * cos - v * sin, v * cos + u * sin
+    bound[..., a] = bound[..., b] = (u.abs() + v.abs()) * off + 2 * U * abs(scale) * (u.abs() + v.abs())
+    return y, bound
