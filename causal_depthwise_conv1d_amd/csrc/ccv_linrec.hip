@@ -3,12 +3,12 @@
 //
 //   h <- e^g[t] h + s[t] x[t],  out[t] = h;   s = 1, or sqrt(1 - e^2g) where x is normalised.
 //
-// One pass over the data.  A workgroup takes a tile of 128 steps and 64 channels into registers: pairs of
+// One pass over the data.  A workgroup takes tiles of 128 steps and 64 channels into registers: pairs of
 // channels a lane, 32 lanes a row, 8 consecutive steps a lane, so that loads are whole 128-byte
-// lines and a lane walks its steps with one fused multiply-add each.  Each lane makes the map
-// (A, H) of its 8 steps, folds those of the lanes before it out of LDS, and the tiles of a
-// sequence pass their maps on through memory (ccv_linrec_device.hpp), so x and g are read once.
-// With the state before its steps a lane walks them again from registers and stores.
+// lines and a lane walks its steps with one fused multiply-add each.  Each lane makes the map (A, H) of
+// its 8 steps, a wave joins its two, the workgroup's eight meet in LDS, and the tiles of a sequence pass their
+// maps on through memory (ccv_linrec_device.hpp), so x and g are read once.  With the state before its
+// steps a lane walks them again from registers and stores.
 #include "ccv_linrec_device.hpp"
 
 #include <algorithm>
@@ -16,71 +16,53 @@
 namespace ccv {
 namespace {
 
-template <int DT, int GT, bool NORM>
-__global__ __launch_bounds__(512, 4) void fwd_kernel(const LinrecArgs a) {
+struct FwdShared {
+  alignas(16) Map maps[kLrWaves][kLrChannels];
+  Heard heard;
+};
+
+template <int DT, int GT, bool NORM, bool MARKS>
+__device__ __forceinline__ void fwd_tile(const LinrecArgs& a, const Place& at, int wave, const Pair<DT> (&xr)[kLrSteps], const Pair<GT> (&gr)[kLrSteps],
+                                         FwdShared& shared) {
   constexpr int S = kLrSteps;
-  __shared__ f32x4 maps[kLrRows][32];                      // (A, H) of two channels
-  __shared__ LrWait wait;
-  __shared__ uint32_t ticket;
-  const uint32_t item = take_ticket(a, &ticket);
-  const uint32_t tile = item / a.chains, chain = item - tile * a.chains;
-  const uint32_t b = chain / a.cblocks, cb = chain - b * a.cblocks;
-  const LrLane me(cb, a.C);
-  const bool one = a.C < 2;
-  const int64_t T = (int64_t)tile * kLrTile + 2 * S * me.wave;       // the wave's first step
-  const bool tail = T + 2 * S > a.L;
-
-  Pair<DT> xr[S];
-  Pair<GT> gr[S];
-  const char* xb = static_cast<const char*>(a.x) + (b * a.x_s[0] + T * a.x_s[1]) * kBytes<DT>;
-  const char* gb = static_cast<const char*>(a.g) + (b * a.g_s[0] + T * a.g_s[1]) * kBytes<GT>;
-  if (!tail) {
-    const uint32_t xo = (uint32_t)((me.half * S * a.x_s[1] + me.c) * kBytes<DT>);
-    const uint32_t go = (uint32_t)((me.half * S * a.g_s[1] + me.c) * kBytes<GT>);
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      gr[j] = load_pair<GT>(gb + j * a.g_s[1] * kBytes<GT>, go, one);
-      xr[j] = load_pair<DT>(xb + j * a.x_s[1] * kBytes<DT>, xo, one);
-    }
-  } else {                                                 // steps past the last are read as it
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const int64_t t = T + S * me.half + j, d = (t < a.L ? t : a.L - 1) - T;
-      gr[j] = load_pair<GT>(gb + d * a.g_s[1] * kBytes<GT>, me.c * kBytes<GT>, one);
-      xr[j] = load_pair<DT>(xb + d * a.x_s[1] * kBytes<DT>, me.c * kBytes<DT>, one);
-    }
-  }
-  const Marks marks = marks_at(a, b, T);
-  const uint32_t start = marks.start >> (S * me.half), end = marks.end >> (S * me.half), dead = marks.dead >> (S * me.half);
-
+  const int lane = threadIdx.x & 63, half = lane >> 5, slot = 2 * (lane & 31);
+  Marks marks{};
+  if constexpr (MARKS) marks = marks_of(a, at);
+  // decays and weighted inputs of the lane's steps, and their map
   float A[S][2], H[S][2];
-  Map own[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
-#pragma unroll
-  for (int j = 0; j < S; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float y;
-      decay(pair_value<GT>(gr[j], e), A[j][e], y);
-      const float x = pair_value<DT>(xr[j], e);
-      H[j][e] = NORM ? input_weight(y) * x : x;
-    }
-  if (!marks.any) {
+  if (all_slow<GT>(gr)) {
 #pragma unroll
     for (int j = 0; j < S; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        own[e].H = __builtin_fmaf(A[j][e], own[e].H, H[j][e]);
-        own[e].A *= A[j][e];
+        float y;
+        slow_decay(pair_value<GT>(gr[j], e), A[j][e], y);
+        const float x = pair_value<DT>(xr[j], e);
+        H[j][e] = NORM ? slow_weight(y) * x : x;
       }
   } else {
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      const bool starts = start >> j & 1, none = dead >> j & 1;
-      const int64_t seq = __shfl(marks.id, S * me.half + j);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        float y;
+        decay(pair_value<GT>(gr[j], e), A[j][e], y);
+        const float x = pair_value<DT>(xr[j], e);
+        H[j][e] = NORM ? input_weight(y) * x : x;
+      }
+      __builtin_amdgcn_sched_barrier(0);                   // a step after the other, in few registers
+    }
+  }
+  Map own[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};
+#pragma unroll
+  for (int j = 0; j < S; ++j) {
+    [[maybe_unused]] const bool starts = marks.start >> j & 1, none = marks.dead >> j & 1;
+    [[maybe_unused]] const int64_t seq = MARKS ? __shfl(marks.id, S * half + j) : 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (MARKS) {
         if (starts) {
-          if (a.init && e + me.own >= 2) H[j][e] = __builtin_fmaf(A[j][e], a.init[seq * a.init_s + me.c + (one ? 0 : e)], H[j][e]);
+          if (a.init && (at.own >> e & 1)) H[j][e] = __builtin_fmaf(A[j][e], a.init[seq * a.init_s + at.c + e], H[j][e]);
           A[j][e] = kCut;
         }
         if (none) {
@@ -88,61 +70,68 @@ __global__ __launch_bounds__(512, 4) void fwd_kernel(const LinrecArgs a) {
           H[j][e] = 0.0f;
         }
         own[e] = then(own[e], Map{A[j][e], H[j][e]});
+      } else {
+        own[e].H = __builtin_fmaf(A[j][e], own[e].H, H[j][e]);
+        own[e].A *= A[j][e];
       }
     }
   }
-  maps[me.row][threadIdx.x & 31] = f32x4{own[0].A, own[0].H, own[1].A, own[1].H};
-  lds_barrier();
-  Map pre[2] = {{1.0f, 0.0f}, {1.0f, 0.0f}};               // of the tile's steps before the lane's
-#pragma unroll 4
-  for (int r = 0; r < me.row; ++r) {
-    const f32x4 m = maps[r][threadIdx.x & 31];
+  Map early[2];                                            // of the half before this one
 #pragma unroll
-    for (int e = 0; e < 2; ++e) pre[e] = then(pre[e], Map{m[2 * e], m[2 * e + 1]});
+  for (int e = 0; e < 2; ++e) {
+    early[e] = other_half(own[e]);
+    if (half) shared.maps[wave][slot + e] = then(early[e], own[e]);
   }
+  lds_barrier();
   float h[2] = {0.0f, 0.0f};
   if (a.tiles > 1) {
-    const bool last = me.row == kLrRows - 1 && tile + 1 < a.tiles;
-    Map all[2];
+    exchange(a, at, wave, shared.heard, [&]() {
+      Map m = shared.maps[0][lane];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      all[e] = then(pre[e], own[e]);
-      if (last) put(map_word(a, chain, tile, me.slot + e), all[e]);
-    }
-    if (tile > 0) wait_state(a, me, chain, tile, wait, h);
-    if (last && tile % kLrGroup == kLrGroup - 1)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) put(state_word(a, chain, tile / kLrGroup, me.slot + e), Map{0.0f, apply(all[e], h[e])});
+      for (int w = 1; w < kLrWaves; ++w) m = then(m, shared.maps[w][lane]);
+      return m;
+    });
+    state_before(a, at, shared.heard, slot, h);
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) h[e] = apply(pre[e], h[e]);
-  if (a.carries && me.row == 0)
+  if (a.carries && wave == 0 && half == 0)
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (e + me.own >= 2) a.carries[((int64_t)b * a.tiles + tile) * a.C + me.c + (one ? 0 : e)] = h[e];
+      if (at.own >> e & 1) a.carries[((int64_t)at.b * a.tiles + at.tile) * a.C + at.c + e] = h[e];
   if (!a.out) return;
-  char* ob = static_cast<char*>(a.out) + (b * a.o_s[0] + T * a.o_s[1] - one) * kBytes<DT>;
-  const uint32_t oo = (uint32_t)((me.half * S * a.o_s[1] + me.c) * kBytes<DT>);
-  if (!marks.any) {
+  apply_parts<false>(shared.maps, wave, slot, h);
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) h[e] = __builtin_fmaf(A[j][e], h[e], H[j][e]);
-      store_pair<DT>(ob + j * a.o_s[1] * kBytes<DT>, oo, h[0], h[1], me.own);
-    }
-    return;
-  }
+  for (int e = 0; e < 2; ++e)
+    if (half) h[e] = apply(early[e], h[e]);
 #pragma unroll
   for (int j = 0; j < S; ++j) {
-    const bool none = dead >> j & 1, ends = end >> j & 1;
-    const int64_t seq = __shfl(marks.id, S * me.half + j);
+    [[maybe_unused]] const bool none = marks.dead >> j & 1, ends = marks.end >> j & 1;
+    [[maybe_unused]] const int64_t seq = MARKS ? __shfl(marks.id, S * half + j) : 0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      h[e] = apply(Map{A[j][e], H[j][e]}, h[e]);
-      if (ends && a.final && e + me.own >= 2) a.final[seq * a.final_s + me.c + (one ? 0 : e)] = h[e];
+      if constexpr (MARKS) {
+        h[e] = apply(Map{A[j][e], H[j][e]}, h[e]);
+        if (ends && a.final && (at.own >> e & 1)) a.final[seq * a.final_s + at.c + e] = h[e];
+        H[j][e] = none ? 0.0f : h[e];
+      } else {
+        H[j][e] = h[e] = __builtin_fmaf(A[j][e], h[e], H[j][e]);
+      }
     }
-    if (T + S * me.half + j < a.L) store_pair<DT>(ob + j * a.o_s[1] * kBytes<DT>, oo, none ? 0.0f : h[0], none ? 0.0f : h[1], me.own);
   }
+  store_steps<DT>(a.out, a.o_s, at, a.L, H);
+}
+
+template <int DT, int GT, bool NORM>
+__global__ __launch_bounds__(64 * kLrWaves, 6) void fwd_kernel(const LinrecArgs a) {
+  __shared__ FwdShared shared;
+  __shared__ uint32_t ticket[2];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const Place at = place_of<false>(a, take_ticket(a, ticket), wave);
+  Pair<DT> xr[kLrSteps];
+  Pair<GT> gr[kLrSteps];
+  load_steps<GT>(gr, a.g, a.g_s, at, a.L, a.C);
+  load_steps<DT>(xr, a.x, a.x_s, at, a.L, a.C);
+  if (has_marks(a, at)) fwd_tile<DT, GT, NORM, true>(a, at, wave, xr, gr, shared);
+  else fwd_tile<DT, GT, NORM, false>(a, at, wave, xr, gr, shared);
 }
 
 // ---- before the tiles ---------------------------------------------------------------------------
@@ -232,31 +221,34 @@ template <int DT, int GT, bool NORM>
 __global__ __launch_bounds__(256) void step_kernel(const LinrecStepArgs a, uint32_t pairs, int64_t items) {
   const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (item >= items) return;
-  const uint32_t b = (uint32_t)(item / pairs), p = (uint32_t)(item - (int64_t)b * pairs);
-  const bool one = a.C < 2;
-  const int64_t at = 2 * (int64_t)p;
-  const int own = at + 2 <= a.C ? 2 : 1;
-  const uint32_t c = (uint32_t)(one ? 0 : own == 2 ? at : a.C - 2);
+  const uint32_t b = (uint32_t)(item / pairs), c = 2 * (uint32_t)(item - (int64_t)b * pairs);
+  const bool both = c + 1 < a.C;                        // else the last of an odd number, by itself
+  const uint32_t next = both ? 1 : 0;
   const char* xp = static_cast<const char*>(a.x) + (b * a.x_s[0] + c) * kBytes<DT>;
   const char* gp = static_cast<const char*>(a.g) + (b * a.g_s[0] + c) * kBytes<GT>;
-  char* op = static_cast<char*>(a.out) + (b * a.o_s[0] + (int64_t)c - one) * kBytes<DT>;
-  Pair<DT> x = load_pair<DT>(xp, 0, one);
-  Pair<GT> g = load_pair<GT>(gp, 0, one);
+  char* op = static_cast<char*>(a.out) + (b * a.o_s[0] + c) * kBytes<DT>;
+  const auto load = [&](Pair<DT>& x, Pair<GT>& g, int64_t t) {
+    x = both ? load_pair<DT>(xp + t * a.x_s[1] * kBytes<DT>, 0) : load_one<DT>(xp + t * a.x_s[1] * kBytes<DT>, 0);
+    g = both ? load_pair<GT>(gp + t * a.g_s[1] * kBytes<GT>, 0) : load_one<GT>(gp + t * a.g_s[1] * kBytes<GT>, 0);
+  };
+  const auto store = [&](int64_t t, float y0, float y1) {
+    if (both) store_pair<DT>(op + t * a.o_s[1] * kBytes<DT>, 0, y0, y1);
+    else store1<DT>(op + t * a.o_s[1] * kBytes<DT>, y0);
+  };
+  Pair<DT> x;
+  Pair<GT> g;
+  load(x, g, 0);
   const int64_t slot = a.slots ? a.slots[b] : b;
   if (slot < 0 || slot >= a.nslots) {                   // an idle row
-    for (int64_t t = 0; t < a.T; ++t) store_pair<DT>(op + t * a.o_s[1] * kBytes<DT>, 0, 0.0f, 0.0f, own);
+    for (int64_t t = 0; t < a.T; ++t) store(t, 0.0f, 0.0f);
     return;
   }
-  char* st = reinterpret_cast<char*>(a.state + slot * a.st_s + c);
-  const Pair<CCV_DT_F32> s = load_pair<CCV_DT_F32>(st, 0, one);
-  float h[2] = {pair_value<CCV_DT_F32>(s, 0), pair_value<CCV_DT_F32>(s, 1)};
+  float* st = a.state + slot * a.st_s + c;
+  float h[2] = {st[0], st[next]};
   for (int64_t t = 0; t < a.T; ++t) {
     const Pair<DT> xt = x;
     const Pair<GT> gt = g;
-    if (t + 1 < a.T) {
-      x = load_pair<DT>(xp + (t + 1) * a.x_s[1] * kBytes<DT>, 0, one);
-      g = load_pair<GT>(gp + (t + 1) * a.g_s[1] * kBytes<GT>, 0, one);
-    }
+    if (t + 1 < a.T) load(x, g, t + 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float d, y;
@@ -264,16 +256,17 @@ __global__ __launch_bounds__(256) void step_kernel(const LinrecStepArgs a, uint3
       const float v = pair_value<DT>(xt, e);
       h[e] = __builtin_fmaf(d, h[e], NORM ? input_weight(y) * v : v);
     }
-    store_pair<DT>(op + t * a.o_s[1] * kBytes<DT>, 0, h[0], h[1], own);
+    store(t, h[0], h[1]);
   }
-  store_pair<CCV_DT_F32>(st - 4 * one, 0, h[0], h[1], own);
+  st[0] = h[0];
+  if (both) st[1] = h[1];
 }
 
 template <int DT, int GT>
 void fwd(const LinrecArgs& a, hipStream_t st) {
   const uint32_t grid = a.tiles * a.chains;
-  if (a.normalize) fwd_kernel<DT, GT, true><<<grid, 512, 0, st>>>(a);
-  else fwd_kernel<DT, GT, false><<<grid, 512, 0, st>>>(a);
+  if (a.normalize) fwd_kernel<DT, GT, true><<<grid, 64 * kLrWaves, 0, st>>>(a);
+  else fwd_kernel<DT, GT, false><<<grid, 64 * kLrWaves, 0, st>>>(a);
 }
 template <int DT, int GT>
 void step(const LinrecStepArgs& a, hipStream_t st) {

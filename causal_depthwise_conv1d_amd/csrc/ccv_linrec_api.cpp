@@ -3,6 +3,7 @@
 // touches a device except the launches.
 #include <stdint.h>
 
+#include <algorithm>
 #include <initializer_list>
 
 #include "ccv.h"
@@ -17,7 +18,7 @@ using namespace ccv::checks;
 
 constexpr int64_t kMostBlocks = ((int64_t)1 << 32) / 512 - 1;      // a launch has fewer than 2^32 threads
 constexpr int64_t kMostStep = (int64_t)32 << 20;                   // bytes between steps: a lane's offsets are 32-bit
-constexpr int64_t kTicketWords = 8;
+constexpr int64_t kTicketWords = kLrQueues * kLrTicketWords;
 
 // A [B, L, C] array with unit stride along the channels.
 int check_steps(const int64_t s[2], int64_t B, int64_t L, int64_t C, int es, bool written) {
@@ -47,6 +48,13 @@ int check_sizes(int64_t B, int64_t L, int64_t C, int64_t N, const void* cu, int 
 
 int64_t ceil_div(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// Division by an invariant as Granlund and Montgomery (1994) have it: exact for all 32-bit n.
+LrDivisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while (l < 32 && ((uint64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((((uint64_t)1 << l) - d) << 32) / d) + 1), l < 1 ? l : 1, l > 0 ? l - 1 : 0};
+}
+
 // The tiles of a walk and the words that they need; false when there are too many.
 bool tile(LinrecArgs* a, int64_t* words) {
   const int64_t tiles = ceil_div(a->L, kLrTile), cblocks = ceil_div(a->C, kLrChannels);
@@ -55,8 +63,18 @@ bool tile(LinrecArgs* a, int64_t* words) {
   a->tiles = (uint32_t)tiles;
   a->cblocks = (uint32_t)cblocks;
   a->chains = (uint32_t)chains;
-  a->groups = (uint32_t)ceil_div(tiles, kLrGroup);
-  *words = tiles > 1 ? kTicketWords + (blocks + chains * a->groups) * kLrChannels : 0;
+  a->queues = (uint32_t)std::min<int64_t>(chains, kLrQueues);
+  a->fewer = a->chains / a->queues;
+  a->longer = a->chains % a->queues;
+  a->by_more = divisor(a->fewer + 1);
+  a->by_fewer = divisor(a->fewer);
+  a->by_cblocks = divisor(a->cblocks);
+  // A tile reads a word a channel of each tile of its group before it and of each group of its stretch; a stretch's last tile
+  // waits for the stretch before it.  With few chains the waits decide, with many the words.
+  a->group_shift = chains >= 128 ? 2 : chains >= 32 ? 3 : 4;
+  a->groups = (uint32_t)ceil_div(tiles, (int64_t)1 << a->group_shift);
+  a->stretches = (uint32_t)ceil_div(a->groups, kLrStretch);
+  *words = tiles > 1 ? kTicketWords + (blocks + chains * (a->groups + a->stretches)) * kLrChannels : 0;
   return true;
 }
 
@@ -150,10 +168,8 @@ int validate_bwd(const ccv_linrec_bwd_args_t* p, LinrecArgs* a, LinrecArgs* f, i
   if ((st = check_states(p->initial_state, p->init_stride, seqs, p->C, false)) != CCV_OK) return st;
   if ((st = check_states(p->dfinal_state, p->dfinal_stride, seqs, p->C, false)) != CCV_OK) return st;
   if ((st = check_states(p->dinitial_state, p->dinit_stride, seqs, p->C, true)) != CCV_OK) return st;
-  if (p->dinitial_state && p->dinitial_state == p->dfinal_state && seqs > 1 && p->dinit_stride != p->dfinal_stride) return CCV_E_ALIAS;
-  const auto inputs = {p->x, p->g, p->dout, (const void*)p->cu_seqlens, (const void*)p->initial_state, (const void*)p->carries};
-  if (hits(p->dx, inputs) || hits(p->dg, inputs) || hits(p->dinitial_state, inputs) || hits(p->dx, {p->dg, p->dinitial_state, p->dfinal_state}) ||
-      hits(p->dg, {p->dinitial_state, p->dfinal_state}))
+  const auto inputs = {p->x, p->g, p->dout, (const void*)p->cu_seqlens, (const void*)p->initial_state, (const void*)p->dfinal_state, (const void*)p->carries};
+  if (hits(p->dx, inputs) || hits(p->dg, inputs) || hits(p->dinitial_state, inputs) || hits(p->dx, {p->dg, p->dinitial_state}) || hits(p->dg, {p->dinitial_state}))
     return CCV_E_ALIAS;
   a->x = p->x;
   a->g = p->g;

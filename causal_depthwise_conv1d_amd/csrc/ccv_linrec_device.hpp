@@ -13,18 +13,28 @@ namespace ccv {
 // e^r - 1 = r (1 + r q(r)), q of degree 4 fitted to it (off by at most 1.4e-8 of e^r - 1).  The
 // hardware's exponential does not serve: next to 1 its results lie 0.11 units of the last place too
 // low on average (measured), which over a memory of a thousand steps and more adds up to 1e-5 of a state.
+__device__ inline float expm1_near(float r) {
+  float q = __builtin_fmaf(r, 0.001394649618305266f, 0.00836661085486412f);
+  q = __builtin_fmaf(r, q, 0.04166628047823906f);
+  q = __builtin_fmaf(r, q, 0.1666654348373413f);
+  q = __builtin_fmaf(r, q, 0.5f);
+  return r * __builtin_fmaf(r, q, 1.0f);
+}
 __device__ inline void decay(float g, float& a, float& y) {
   g = g < -150.0f ? -150.0f : g;                       // also -inf; NaN stays
   const float k = __builtin_rintf(g * 1.44269504088896341f);
   float r = __builtin_fmaf(k, -0.693145751953125f, g);   // ln 2 in two parts, the first exact in products with k
   r = __builtin_fmaf(k, -1.42860676e-06f, r);
-  float q = __builtin_fmaf(r, 0.001394649618305266f, 0.00836661085486412f);
-  q = __builtin_fmaf(r, q, 0.04166628047823906f);
-  q = __builtin_fmaf(r, q, 0.1666654348373413f);
-  q = __builtin_fmaf(r, q, 0.5f);
-  const float m = r * __builtin_fmaf(r, q, 1.0f);
+  const float m = expm1_near(r);
   a = __builtin_ldexpf(1.0f + m, (int)k);
   y = k == 0.0f ? -m : 1.0f - a;
+}
+// The same for kSlow <= g <= 0, where k is 0: the same bits.
+constexpr float kSlow = -0.34f;
+__device__ inline void slow_decay(float g, float& a, float& y) {
+  const float m = expm1_near(g);
+  a = 1.0f + m;
+  y = -m;
 }
 
 // What x is weighted with: sqrt(1 - a^2) = sqrt(y (2 - y)); 0 where a > 1.
@@ -32,6 +42,7 @@ __device__ inline float input_weight(float y) {
   const float v = y * (2.0f - y);
   return __builtin_amdgcn_sqrtf(v < 0.0f ? 0.0f : v);
 }
+__device__ inline float slow_weight(float y) { return __builtin_amdgcn_sqrtf(y * (2.0f - y)); }
 
 // Two neighbouring channels as stored.
 template <int DT> struct Pair { uint32_t d[DT == CCV_DT_F32 ? 2 : 1]; };
@@ -40,22 +51,30 @@ template <int DT> constexpr int kBytes = DT == CCV_DT_F32 ? 4 : 2;
 typedef const char __attribute__((address_space(1)))* gcptr;
 typedef char __attribute__((address_space(1)))* gptr;
 
-// From a uniform address and a lane's offset.  one: there is only one channel, at the address.
+// From a uniform address and a lane's offset.
 template <int DT>
-__device__ inline Pair<DT> load_pair(const char* base, uint32_t off, bool one) {
+__device__ inline Pair<DT> load_pair(const char* base, uint32_t off) {
   const gcptr p = (gcptr)base + off;
   Pair<DT> r;
   if constexpr (DT == CCV_DT_F32) {
-    if (one) {
-      r.d[0] = r.d[1] = *(const uint32_t __attribute__((address_space(1)))*)p;
-    } else {
-      const u32x2 v = *(const u32x2 __attribute__((address_space(1)))*)p;
-      r.d[0] = v[0];
-      r.d[1] = v[1];
-    }
+    const u32x2 v = *(const u32x2 __attribute__((address_space(1)))*)p;
+    r.d[0] = v[0];
+    r.d[1] = v[1];
   } else {
-    if (one) r.d[0] = *(const uint16_t __attribute__((address_space(1)))*)p * 0x10001u;
-    else r.d[0] = *(const uint32_t __attribute__((address_space(1)))*)p;
+    r.d[0] = *(const uint32_t __attribute__((address_space(1)))*)p;
+  }
+  return r;
+}
+// One element, and 0.
+template <int DT>
+__device__ inline Pair<DT> load_one(const char* base, uint32_t off) {
+  const gcptr p = (gcptr)base + off;
+  Pair<DT> r;
+  if constexpr (DT == CCV_DT_F32) {
+    r.d[0] = *(const uint32_t __attribute__((address_space(1)))*)p;
+    r.d[1] = 0;
+  } else {
+    r.d[0] = *(const uint16_t __attribute__((address_space(1)))*)p;
   }
   return r;
 }
@@ -65,165 +84,355 @@ __device__ inline float pair_value(const Pair<DT>& r, int e) {
   else if constexpr (DT == CCV_DT_BF16) return __builtin_bit_cast(float, e ? r.d[0] & 0xffff0000u : r.d[0] << 16);
   else return F16::to_f((uint16_t)(r.d[0] >> (16 * e)));
 }
-// own: which of the two are stored (2: both, 1: the second alone, 0: none).
+// The same registers, of which the compiler no longer knows what was made of them before.
+template <int DT, int N>
+__device__ inline void hide_steps(Pair<DT> (&r)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < (DT == CCV_DT_F32 ? 2 : 1); ++i) asm("" : "+v"(r[j].d[i]));
+}
 template <int DT>
-__device__ inline void store_pair(char* base, uint32_t off, float y0, float y1, int own) {
+__device__ inline void store_pair(char* base, uint32_t off, float y0, float y1) {
   const gptr p = (gptr)base + off;
-  if (own == 2) {
-    if constexpr (DT == CCV_DT_F32) {
-      *(u32x2 __attribute__((address_space(1)))*)p = u32x2{__builtin_bit_cast(uint32_t, y0), __builtin_bit_cast(uint32_t, y1)};
-    } else {
-      const f32x2 y = {as_f32(y0), as_f32(y1)};
-      uint32_t d;
-      if constexpr (DT == CCV_DT_BF16) d = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
-      else d = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, f16x2));
-      *(uint32_t __attribute__((address_space(1)))*)p = d;
-    }
-  } else if (own == 1) {
-    if constexpr (DT == CCV_DT_F32) *(float __attribute__((address_space(1)))*)(p + 4) = y1;
-    else if constexpr (DT == CCV_DT_BF16) *(uint16_t __attribute__((address_space(1)))*)(p + 2) = BF16::from_f(y1);
-    else *(uint16_t __attribute__((address_space(1)))*)(p + 2) = F16::from_f(y1);
+  if constexpr (DT == CCV_DT_F32) {
+    *(u32x2 __attribute__((address_space(1)))*)p = u32x2{__builtin_bit_cast(uint32_t, y0), __builtin_bit_cast(uint32_t, y1)};
+  } else {
+    const f32x2 y = {as_f32(y0), as_f32(y1)};
+    uint32_t d;
+    if constexpr (DT == CCV_DT_BF16) d = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
+    else d = __builtin_bit_cast(uint32_t, __builtin_convertvector(y, f16x2));
+    *(uint32_t __attribute__((address_space(1)))*)p = d;
   }
+}
+
+// Whether all of a wave's decays are slow ones.
+template <int GT>
+__device__ inline bool all_slow(const Pair<GT> (&g)[kLrSteps]) {
+  float least = 0.0f, most = kSlow;                // of a NaN either way makes a NaN
+#pragma unroll
+  for (int j = 0; j < kLrSteps; ++j) {
+    const float g0 = pair_value<GT>(g[j], 0), g1 = pair_value<GT>(g[j], 1);
+    least = __builtin_fminf(least, __builtin_fminf(g0, g1));
+    most = __builtin_fmaxf(most, __builtin_fmaxf(g0, g1));
+  }
+  return __builtin_amdgcn_ballot_w64(!(least >= kSlow && most <= 0.0f)) == 0;
 }
 
 // The map h -> A h + H of a run of steps.  A sequence that starts within the run cuts off what was
 // before it: then A is -0 and h is not looked at, so that no infinity or NaN of one
 // sequence reaches another.
-struct Map { float A, H; };
+struct alignas(8) Map { float A, H; };
 constexpr float kCut = -0.0f;          // decays are never negative, and so no product of them is
 __device__ inline bool is_cut(float A) { return __builtin_bit_cast(uint32_t, A) == 0x80000000u; }
-__device__ inline float apply(Map m, float h) { return is_cut(m.A) ? m.H : __builtin_fmaf(m.A, h, m.H); }
+__device__ inline float apply(Map m, float h) { return __builtin_fmaf(m.A, is_cut(m.A) ? 0.0f : h, m.H); }
 // First `before`, then m.
 __device__ inline Map then(Map before, Map m) {
   return {is_cut(m.A) ? kCut : is_cut(before.A) ? kCut : m.A * before.A, apply(m, before.H)};
 }
 
-// A lane's place: the tile's row of lanes it belongs to, its two channels from `c`, of which it owns `own`
-// (the last of an odd number of channels is the second of a pair), `slot` its first place of 64.
-struct LrLane {
-  int wave, half, row, slot, own;
-  uint32_t c;
-  __device__ inline LrLane(uint32_t cb, int64_t C) {
-    const int l = threadIdx.x & 63;
-    wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    half = l >> 5;
-    row = 2 * wave + half;
-    slot = 2 * (l & 31);
-    const int64_t at = (int64_t)cb * kLrChannels + slot;
-    own = at + 2 <= C ? 2 : at < C ? 1 : 0;
-    c = (uint32_t)(C < 2 ? 0 : at + 2 <= C ? at : C - 2);
-  }
-};
+// n / d for a divisor whose magic the host has made, in scalar instructions.
+__device__ inline uint32_t divide(uint32_t n, const LrDivisor& d) {
+  const uint32_t t = (uint32_t)(((uint64_t)n * d.magic) >> 32);
+  return (t + ((n - t) >> d.first)) >> d.second;
+}
 
-// The 16 steps from T of a wave, 8 a half: bit i of the masks belongs to step T + i.
+// The i-th pair of the channels from `first`: its first channel, and which of the two are its own (bit 0, bit 1): of
+// an odd number of channels the last is the second of a pair, a single one the first; pairs past the last have none.
+struct Channels { uint32_t c, own; };
+__device__ inline Channels channels_of(uint32_t first, uint32_t i, int64_t C) {
+  const uint32_t at = first + 2 * i;
+  if (at + 2 <= C) return {at, 3u};
+  return C < 2 ? Channels{0u, at < C ? 1u : 0u} : Channels{(uint32_t)C - 2, at < C ? 2u : 0u};
+}
+
+// A workgroup's tile: its queue, and its number there.
+struct Ticket { uint32_t queue, number; };
+
+// A tile's place, the same in every lane of a wave but for c and own, the lane's channels; T: the wave's first step.
+struct Place {
+  uint32_t order, chain, tile, b, first, c, own;       // order: of the tile in its chain's walk; first: its first channel
+  int64_t T;
+  bool edge;                               // the wave has steps past the last, or the tile channels past the last
+};
+template <bool REVERSE>
+__device__ inline Place place_of(const LinrecArgs& a, const Ticket& t, int wave) {
+  Place p;
+  p.order = a.tiles == 1 ? 0 : divide(t.number, t.queue < a.longer ? a.by_more : a.by_fewer);
+  p.chain = a.tiles == 1 ? t.number : t.number - p.order * a.chains_of(t.queue) + a.first_chain(t.queue);
+  p.tile = REVERSE ? a.tiles - 1 - p.order : p.order;
+  p.b = divide(p.chain, a.by_cblocks);
+  const uint32_t cb = p.chain - p.b * a.cblocks;
+  p.first = cb * kLrChannels;
+  const Channels ch = channels_of(p.first, threadIdx.x & 31, a.C);
+  p.c = ch.c;
+  p.own = ch.own;
+  p.T = (int64_t)p.tile * kLrTile + 2 * kLrSteps * wave;
+  p.edge = p.T + 2 * kLrSteps > a.L || (int64_t)(cb + 1) * kLrChannels > a.C;
+  return p;
+}
+
+// A lane's eight steps of an array, at a uniform address for each step and a lane's offset; at an edge, steps past the last
+// are read as it.
+template <int DT>
+__device__ inline void load_steps(Pair<DT> (&r)[kLrSteps], const void* p, const int64_t (&s)[2], const Place& at, int64_t L, int64_t C) {
+  const int half = (threadIdx.x >> 5) & 1;
+  const char* base = static_cast<const char*>(p) + (at.b * s[0] + at.T * s[1]) * kBytes<DT>;
+  int64_t step = s[1] * kBytes<DT>;
+  if (!at.edge) {
+    const uint32_t off = (uint32_t)(half * kLrSteps * (int)step) + at.c * kBytes<DT>;
+    asm("" : "+s"(step));                  // not a multiple of it kept for each step
+#pragma unroll
+    for (int j = 0; j < kLrSteps; ++j, base += step) r[j] = load_pair<DT>(base, off);
+  } else {
+    const int most = (int)(L - 1 - at.T < 2 * kLrSteps ? L - 1 - at.T : 2 * kLrSteps);    // of the wave's steps; < 0: all lie past the last
+    base += (most < 0 ? most : 0) * step;
+    const int top = most < 0 ? 0 : most;
+    const auto off = [&](int j) { return (uint32_t)(min(kLrSteps * half + j, top) * (int)step) + at.c * kBytes<DT>; };
+    if (C < 2) {
+#pragma unroll
+      for (int j = 0; j < kLrSteps; ++j) r[j] = load_one<DT>(base, off(j));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kLrSteps; ++j) r[j] = load_pair<DT>(base, off(j));
+    }
+  }
+}
+template <int DT>
+__device__ inline void store_steps(void* p, const int64_t (&s)[2], const Place& at, int64_t L, const float (&y)[kLrSteps][2]) {
+  const int half = (threadIdx.x >> 5) & 1;
+  char* base = static_cast<char*>(p) + (at.b * s[0] + at.T * s[1]) * kBytes<DT>;
+  int64_t step = s[1] * kBytes<DT>;
+  const uint32_t off = (uint32_t)(half * kLrSteps * (int)step) + at.c * kBytes<DT>;
+  if (!at.edge) {
+    asm("" : "+s"(step));
+#pragma unroll
+    for (int j = 0; j < kLrSteps; ++j, base += step) store_pair<DT>(base, off, y[j][0], y[j][1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (at.own >> e & 1)
+#pragma unroll
+        for (int j = 0; j < kLrSteps; ++j)
+          if (at.T + kLrSteps * half + j < L) store1<DT>(base + j * step + off + e * kBytes<DT>, y[j][e]);
+  }
+}
+
+// Whether a tile has steps at which a sequence starts or ends, or steps of none; the same in the whole workgroup.  With such
+// steps it takes a code path of its own, through which the other one's values need not be kept in registers.
+__device__ inline bool has_marks(const LinrecArgs& a, const Place& at) {
+  const int64_t t0 = (int64_t)at.tile * kLrTile, t1 = t0 + kLrTile;
+  if (t0 == 0 || t1 >= a.L) return true;
+  if (!a.sid) return false;
+  const int id = a.sid[t0];                        // of a row's steps the sequences' numbers ascend, and then come steps of none
+  return id < 0 || a.sid[t0 - 1] != id || a.sid[t1] != id;
+}
+// Bit j of the masks belongs to the lane's step j.
 struct Marks {
   uint32_t start, end, dead;           // first and last steps of sequences; steps of none
-  int id;                              // the sequence of step T + lane % 16
-  bool any;                            // whether there are such steps at all; the same in every lane
+  int id;                              // the sequence of step T + lane % 16 of the wave's 16 from T
 };
-__device__ inline Marks marks_at(const LinrecArgs& a, int64_t b, int64_t T) {
-  Marks m;
-  const int l = threadIdx.x & 15;
-  const int64_t t = T + l;
-  bool start, end, dead = t >= a.L;
+__device__ inline Marks marks_of(const LinrecArgs& a, const Place& at) {
+  const int64_t t = at.T + (threadIdx.x & 15);
+  bool start = t == 0, end = t == a.L - 1, dead = t >= a.L;
+  int id = (int)at.b;
   if (a.sid) {
-    const int64_t in = dead ? a.L - 1 : t;
-    m.id = a.sid[in];
-    const int before = t > 0 && !dead ? a.sid[t - 1] : -2, after = t + 1 < a.L ? a.sid[t + 1] : -2;
-    dead = dead || m.id < 0;
-    start = !dead && m.id != before;
-    end = !dead && m.id != after;
-  } else {
-    m.id = (int)b;
-    start = t == 0;
-    end = t == a.L - 1;
+    const int64_t in = t < a.L ? t : a.L - 1;
+    id = a.sid[in];
+    dead = dead || id < 0;
+    start = !dead && (start || id != a.sid[in > 0 ? in - 1 : 0]);
+    end = !dead && (end || id != a.sid[in + 1 < a.L ? in + 1 : in]);
   }
-  m.start = (uint32_t)(__builtin_amdgcn_ballot_w64(start) & 0xffff);
-  m.end = (uint32_t)(__builtin_amdgcn_ballot_w64(end) & 0xffff);
-  m.dead = (uint32_t)(__builtin_amdgcn_ballot_w64(dead) & 0xffff);
-  m.any = (m.start | m.end | m.dead) != 0;
-  return m;
+  const uint32_t s = (uint32_t)__builtin_amdgcn_ballot_w64(start) & 0xffff, e = (uint32_t)__builtin_amdgcn_ballot_w64(end) & 0xffff,
+                 d = (uint32_t)__builtin_amdgcn_ballot_w64(dead) & 0xffff;
+  const int shift = threadIdx.x & 32 ? kLrSteps : 0;
+  return {s >> shift, e >> shift, d >> shift, id};
 }
+
+// The map of the other 32 lanes' steps of the same channels.
+__device__ inline Map other_half(Map m) { return {__shfl_xor(m.A, 32), __shfl_xor(m.H, 32)}; }
 
 // ---- the chain of tiles -----------------------------------------------------------------------
 //
-// A tile's map reaches the later tiles of its sequence's chain through one 64-bit word a channel,
-// (A, H), written once a call by an atomic store: the word is the message and its own flag, so no
-// fence is needed.  ~0 is an empty word (A is then no NaN that a tile could write: put() makes
-// NaNs positive).  Tiles are grouped by 32: a tile takes the state behind the group before
-// its own (one word, written by that group's last tile) through the maps of the tiles before it in the group, in their
-// order, so results do not depend on which word came first.  Every wait ends: a tile waits only for tiles with
-// lower tickets, whose workgroups run already and wait only for lower ones again; those of ticket 0 wait for nothing.
+// A tile's map reaches the later tiles of its chain through one 64-bit word a channel, (A, H), written
+// once a call by an atomic store: the word is the message and its own flag, so no fence is needed.  ~0 is an empty
+// word (A is then no NaN that a tile could write: put() makes NaNs positive).  Tiles are grouped, and 16 groups to a
+// stretch.  A group's last tile joins its maps into the group's, as soon as they are there; a stretch's last tile gives
+// the state behind it.  A tile applies to the state behind the stretch before its own the maps of the groups and then
+// of the tiles between, in their order: results do not depend on which word came first, and what
+// has to wait for each other is one tile in 16 groups.
+// Tiles are taken in the order of their chains' walks, by tickets; a queue of tickets has the chains of one of the eight dies,
+// whose L2 then passes their words on, and its own counter: one counter for all gives a ticket in 12 ns, which is
+// a third of the time that a tile's data take.  A workgroup whose die's queue is empty takes from another's.  Every wait
+// ends: a tile waits only for tiles with lower tickets of its own queue, whose workgroups run already, and the lowest unfinished
+// one waits for nothing.  How many workgroups run at a time, of this call or of others, does not matter.
 constexpr uint64_t kEmpty = ~0ull;
 
+// Words of a chain's tile i, group i, stretch i, for slot 0.
+__device__ inline uint64_t* tile_words(const LinrecArgs& a, const Place& at, uint32_t i) {
+  return a.words + ((int64_t)at.chain * a.tiles + i) * kLrChannels;
+}
+__device__ inline uint64_t* group_words(const LinrecArgs& a, const Place& at, uint32_t i) {
+  return a.words + ((int64_t)a.chains * a.tiles + (int64_t)at.chain * a.groups + i) * kLrChannels;
+}
+__device__ inline uint64_t* stretch_words(const LinrecArgs& a, const Place& at, uint32_t i) {
+  return a.words + ((int64_t)a.chains * (a.tiles + a.groups) + (int64_t)at.chain * a.stretches + i) * kLrChannels;
+}
+// The word of this lane's slot, from that of slot 0.
 __device__ inline void put(uint64_t* w, Map m) {
   uint32_t A = __builtin_bit_cast(uint32_t, m.A);
   if (m.A != m.A) A = 0x7fc00000u;
-  __hip_atomic_store(w, ((uint64_t)__builtin_bit_cast(uint32_t, m.H) << 32) | A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  auto p = (uint64_t __attribute__((address_space(1)))*)((gptr)(char*)w + 8 * (threadIdx.x & 63));
+  __hip_atomic_store(p, ((uint64_t)__builtin_bit_cast(uint32_t, m.H) << 32) | A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ inline uint64_t peek(const uint64_t* w) { return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ inline uint64_t peek(const uint64_t* w) {
+  auto p = (const uint64_t __attribute__((address_space(1)))*)((gcptr)(const char*)w + 8 * (threadIdx.x & 63));
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 __device__ inline Map map_of(uint64_t w) {
   return {__builtin_bit_cast(float, (uint32_t)w), __builtin_bit_cast(float, (uint32_t)(w >> 32))};
 }
 
-// The state before tile `i` of a chain (in the order of the walk), for the slots me.slot and + 1; the whole workgroup calls it.
-// Each wave takes four of the tiles before it in the group, slot by lane, and folds their maps in order.
-struct LrWait { Map part[kLrRows / 2][kLrChannels]; float state[kLrChannels]; };
+// Counters start from cleared words, all bits set.  There is a workgroup for each tile, so one that finds
+// all queues empty would have found every tile taken by another.  Calls of one tile a chain wait for nothing: there the
+// tickets are the workgroups' numbers.
+__device__ inline Ticket take_ticket(const LinrecArgs& a, uint32_t* shared) {
+  if (a.tiles == 1) return {0, blockIdx.x};
+  if (threadIdx.x == 0) {
+    constexpr int kXccId = 20 | (31 << 11);                // the hardware register XCC_ID, all bits
+    uint32_t q = ((uint32_t)__builtin_amdgcn_s_getreg(kXccId) & 7u) % a.queues, t;
+    while ((t = 1u + __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ticket + kLrTicketWords * q), 1u, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT)) >= a.chains_of(q) * a.tiles)
+      q = q + 1 < a.queues ? q + 1 : 0;
+    shared[0] = q;
+    shared[1] = t;
+  }
+  __syncthreads();
+  return {(uint32_t)__builtin_amdgcn_readfirstlane(shared[0]), (uint32_t)__builtin_amdgcn_readfirstlane(shared[1])};
+}
 
-__device__ inline void wait_state(const LinrecArgs& a, const LrLane& me, uint32_t chain, uint32_t i, LrWait& shared, float (&h)[2]) {
-  constexpr int each = kLrGroup / (kLrRows / 2);
-  const int lane = threadIdx.x & 63;
-  const uint32_t group = i / kLrGroup, first = group * kLrGroup, n = i - first, j0 = me.wave * each;
-  if (j0 < n || me.wave == 0) {
-    const uint64_t* maps = a.words + ((int64_t)chain * a.tiles + first + j0) * kLrChannels + lane;
-    const uint64_t* state = a.words + ((int64_t)a.chains * a.tiles + (int64_t)chain * a.groups + group - 1) * kLrChannels + lane;
-    const bool behind = me.wave == 0 && group > 0;
-    uint64_t w[each], s = kEmpty;
+// What a tile hears of those before it, by slot: joint maps by wave of tiles and of groups, and a state.
+struct Heard {
+  alignas(16) Map tiles[kLrWaves][kLrChannels], groups[kLrWaves][kLrChannels];
+  float state[kLrChannels];
+};
+// A wave's share of `n` words: `each` of them from number wave * each on.
+struct Share {
+  uint32_t n, each, from;
+  __device__ inline Share(uint32_t count, uint32_t most, int wave) : n(count), each(most > kLrWaves ? most / kLrWaves : 1), from(wave * each) {}
+  __device__ inline bool has(uint32_t j) const { return j < each && from + j < n; }
+};
+constexpr int kShare = kLrMostGroup / kLrWaves;
+// Asks for a wave's words; true: they are there.
+__device__ inline bool look(const uint64_t* ws, const Share& share, uint64_t (&w)[kShare]) {
+  bool ok = true;
 #pragma unroll
-    for (int j = 0; j < each; ++j) w[j] = kEmpty;
-    for (;;) {
-      bool ok = true;
-      if (behind) {
-        if (s == kEmpty) s = peek(state);
-        ok = s != kEmpty;
-      }
+  for (int j = 0; j < kShare; ++j)
+    if (share.has(j)) w[j] = peek(ws + j * kLrChannels);
 #pragma unroll
-      for (int j = 0; j < each; ++j)
-        if (j0 + j < n && w[j] == kEmpty) w[j] = peek(maps + j * kLrChannels);
-#pragma unroll
-      for (int j = 0; j < each; ++j) ok = ok && (j0 + j >= n || w[j] != kEmpty);
-      if (__builtin_amdgcn_ballot_w64(!ok) == 0) break;
+  for (int j = 0; j < kShare; ++j) ok = ok && !(share.has(j) && w[j] == kEmpty);
+  return ok;
+}
+// Waits until they are.  While something is missing one lane alone asks: words come a wave's store at a time.
+__device__ inline void wait_words(const uint64_t* ws, const Share& share, uint64_t (&w)[kShare], bool ok) {
+  while (__builtin_amdgcn_ballot_w64(!ok) != 0) {
+    for (ok = false; __builtin_amdgcn_ballot_w64(ok) == 0;) {
       __builtin_amdgcn_s_sleep(1);
+      if ((threadIdx.x & 63) == 0) ok = look(ws, share, w);
     }
-    Map m = {1.0f, 0.0f};
+    ok = look(ws, share, w);
+  }
+}
+__device__ inline Map joined(const Share& share, const uint64_t (&w)[kShare]) {
+  Map m = map_of(w[0]);
 #pragma unroll
-    for (int j = 0; j < each; ++j)
-      if (j0 + j < n) m = then(m, map_of(w[j]));
-    shared.part[me.wave][lane] = m;
-    if (me.wave == 0) shared.state[lane] = behind ? map_of(s).H : 0.0f;
+  for (int j = 1; j < kShare; ++j)
+    if (share.has(j)) m = then(m, map_of(w[j]));
+  return m;
+}
+
+// The tile's own map is given to the others, and theirs are waited for; the whole workgroup calls this, `all()` gives the
+// tile's map by slot (lane) to one wave.  Afterwards heard holds what state_before() needs, but for a chain's first tile.
+template <class F>
+__device__ inline void exchange(const LinrecArgs& a, const Place& at, int wave, Heard& heard, F all) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t size = 1u << a.group_shift, in_group = at.order & (size - 1), group = at.order >> a.group_shift;
+  const uint32_t in_stretch = group % kLrStretch, stretch = group / kLrStretch;
+  const bool talks = wave == kLrWaves - 1, follows = at.order + 1 < a.tiles, closes = in_group == size - 1 && follows;
+  Map mine = {1.0f, 0.0f};
+  if (talks && follows) {
+    mine = all();
+    put(tile_words(a, at, at.order), mine);
+  }
+  if (at.order == 0) return;
+  const Share t(in_group, size, wave), g(in_stretch, kLrStretch, wave);
+  const uint64_t *tw = tile_words(a, at, at.order - in_group + t.from), *gw = group_words(a, at, group - in_stretch + g.from);
+  uint64_t wt[kShare], wg[kShare];
+  const bool gok = look(gw, g, wg), tok = look(tw, t, wt);
+  if (t.has(0)) {
+    wait_words(tw, t, wt, tok);
+    heard.tiles[wave][lane] = joined(t, wt);
+  }
+  if (closes) {                                            // the same for the whole workgroup
+    lds_barrier();
+    if (talks) {
+      Map m = mine;
+      if (in_group > 0) {
+        m = heard.tiles[0][lane];
+        for (uint32_t k = 1; k * t.each < in_group; ++k) m = then(m, heard.tiles[k][lane]);
+        m = then(m, mine);
+      }
+      if (in_stretch < kLrStretch - 1) put(group_words(a, at, group), m);
+      mine = m;
+    }
+  }
+  if (g.has(0)) {
+    wait_words(gw, g, wg, gok);
+    heard.groups[wave][lane] = joined(g, wg);
+  }
+  if (talks) {
+    float h = 0.0f;                                        // a chain begins with a sequence: nothing looks at the 0
+    if (stretch > 0) {
+      const uint64_t* ss = stretch_words(a, at, stretch - 1);
+      uint64_t s;
+      while (__builtin_amdgcn_ballot_w64((s = peek(ss)) == kEmpty) != 0) __builtin_amdgcn_s_sleep(1);
+      h = map_of(s).H;
+    }
+    heard.state[lane] = h;
   }
   lds_barrier();
+  if (talks && closes && in_stretch == kLrStretch - 1) {
+    float h = heard.state[lane];
+    for (uint32_t k = 0; k * g.each < in_stretch; ++k) h = apply(heard.groups[k][lane], h);
+    put(stretch_words(a, at, stretch), Map{0.0f, apply(mine, h)});
+  }
+}
+// Two slots' maps, by wave in LDS, applied from the first to the n-th, or from the last to the n-th; four are read at a time.
+template <bool BACK>
+__device__ inline void apply_parts(const Map (&parts)[kLrWaves][kLrChannels], uint32_t n, int slot, float (&h)[2]) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) h[e] = shared.state[me.slot + e];
-  for (uint32_t k = 0; k * each < n; ++k)
+  for (int k0 = 0; k0 < kLrWaves; k0 += 4) {
+    f32x4 m[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) h[e] = apply(shared.part[k][me.slot + e], h[e]);
+    for (int i = 0; i < 4; ++i) m[i] = *reinterpret_cast<const f32x4*>(&parts[BACK ? kLrWaves - 1 - k0 - i : k0 + i][slot]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (BACK ? (uint32_t)(kLrWaves - 1 - k0 - i) >= n : (uint32_t)(k0 + i) < n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) h[e] = apply(Map{m[i][2 * e], m[i][2 * e + 1]}, h[e]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
-
-__device__ inline uint64_t* map_word(const LinrecArgs& a, uint32_t chain, uint32_t i, int slot) {
-  return a.words + ((int64_t)chain * a.tiles + i) * kLrChannels + slot;
-}
-__device__ inline uint64_t* state_word(const LinrecArgs& a, uint32_t chain, uint32_t group, int slot) {
-  return a.words + ((int64_t)a.chains * a.tiles + (int64_t)chain * a.groups + group) * kLrChannels + slot;
-}
-
-// This workgroup's place in the order of tiles: all chains' first ones, then their second ones ...
-__device__ inline uint32_t take_ticket(const LinrecArgs& a, uint32_t* shared) {
-  if (a.tiles == 1) return blockIdx.x;
-  if (threadIdx.x == 0)        // from a cleared word, all bits set
-    *shared = 1u + __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ticket), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*shared);
+// The state before the tile, for two slots.
+__device__ inline void state_before(const LinrecArgs& a, const Place& at, const Heard& heard, int slot, float (&h)[2]) {
+  if (at.order == 0) return;
+  const uint32_t size = 1u << a.group_shift, in_group = at.order & (size - 1), in_stretch = (at.order >> a.group_shift) % kLrStretch;
+  h[0] = heard.state[slot];
+  h[1] = heard.state[slot + 1];
+  constexpr uint32_t ge = kLrStretch / kLrWaves;
+  const uint32_t te = size > kLrWaves ? size / kLrWaves : 1;
+  apply_parts<false>(heard.groups, (in_stretch + ge - 1) / ge, slot, h);
+  apply_parts<false>(heard.tiles, te > 1 ? (in_group + 1) / 2 : in_group, slot, h);
 }
 
 // The types' numbers as constants: f(x's, g's).

@@ -6,6 +6,12 @@
 
 #include "ccv.h"
 
+#ifdef __HIPCC__
+#define LR_HOST_DEVICE __host__ __device__
+#else
+#define LR_HOST_DEVICE
+#endif
+
 namespace ccv {
 
 // A tile is 64 channels of 128 steps, one workgroup's work: 16 rows of lanes, each with 8 consecutive
@@ -14,8 +20,14 @@ constexpr int kLrChannels = 64;
 constexpr int kLrRows = 16;
 constexpr int kLrTile = CCV_LINREC_CHUNK;
 constexpr int kLrSteps = kLrTile / kLrRows;
-// Tiles in a row of them that look at each other's maps directly.
-constexpr int kLrGroup = 32;
+constexpr int kLrWaves = kLrRows / 2;
+// Tiles of a chain in a group, at most, and groups in a stretch.
+constexpr uint32_t kLrMostGroup = 16, kLrStretch = 16;
+// Queues of tickets, at most, and the words from one's counter to the next: 128 bytes.
+constexpr uint32_t kLrQueues = 8, kLrTicketWords = 16;
+
+// A divisor as the kernels use it: n / d = (t + ((n - t) >> first)) >> second with t the upper half of n magic.
+struct LrDivisor { uint32_t magic, first, second; };
 
 struct LinrecArgs {
   const void *x, *g, *dout;
@@ -27,13 +39,19 @@ struct LinrecArgs {
   const int32_t* cu;                  // [nseq + 1] or nullptr
   int32_t* sid;                       // packed: each step's sequence, -1 past the last
   float* carries;                     // [B, chunks, C]: the state before each tile
-  uint64_t* ticket;                   // of tiles
-  uint64_t* words;                    // [chains, tiles][64] maps of tiles, then [chains, groups][64] states
+  uint64_t* ticket;                   // counters of the queues
+  uint64_t* words;                    // [chains, tiles][64] maps of tiles, [chains, groups][64] of groups, [chains, stretches][64] states
   uint64_t* clear;                    // tickets and words: all bits set by launch_linrec_prepare
   int64_t B, L, C, nseq;
   int64_t clear_count;
-  uint32_t tiles, cblocks, chains, groups;
+  uint32_t tiles, cblocks, chains, groups, stretches;
+  uint32_t queues, fewer, longer;     // queues of neighbouring chains: fewer + 1 in the first `longer`, fewer in the others
+  LrDivisor by_more, by_fewer, by_cblocks;
+  uint32_t group_shift;               // log2 of a group's tiles
   int32_t x_dtype, g_dtype, normalize;
+
+  LR_HOST_DEVICE uint32_t first_chain(uint32_t queue) const { return queue * fewer + (queue < longer ? queue : longer); }
+  LR_HOST_DEVICE uint32_t chains_of(uint32_t queue) const { return fewer + (queue < longer ? 1 : 0); }
 };
 
 struct LinrecStepArgs {

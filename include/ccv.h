@@ -668,8 +668,7 @@ int ccv_linrec_fwd(const ccv_linrec_fwd_args_t* args, void* hip_stream);
  * dx in x_dtype, dg in g_dtype, dinitial_state fp32 (NULL: not wanted; needs initial_state, else
  * CCV_E_UNSUPPORTED), from dout (x_dtype) and dfinal_state (fp32, NULL: zeros).  carries: what the forward call left for the
  * same inputs, or NULL: they are then made again first, by another pass over x and g.
- * dinitial_state may be dfinal_state itself, with the same stride; other outputs may be no input and no other
- * output (CCV_E_ALIAS). */
+ * Outputs may be no input and no other output (CCV_E_ALIAS). */
 typedef struct ccv_linrec_bwd_args {
   int64_t struct_size;          /* = sizeof(ccv_linrec_bwd_args_t) */
   int64_t B, L, C, N;

@@ -145,30 +145,14 @@ def test_outputs_given():
 
 @pytest.mark.parametrize("lengths", [[100, 0, 5000, 3, 700], [130, 130]])
 def test_states_in_place(lengths):
-    """final_state over initial_state, and dinitial_state over dfinal_state, in a long chain."""
+    """final_state over initial_state, in a long chain."""
     L = sum(lengths) + 5
     x, g, h0 = (t.cuda() for t in ref.inputs(1, L, 130, seed=12, seqs=len(lengths)))
     cu = cu_of(lengths).cuda()
-    o, ht, ca = ccv.gated_linear_recurrence_fwd(x, g, cu, h0, True, return_carries=True)
+    o, ht = ccv.gated_linear_recurrence_fwd(x, g, cu, h0, True)
     state = h0.clone()
     o2, _ = ccv.gated_linear_recurrence_fwd(x, g, cu, state, True, final_state_out=state)
     assert torch.equal(o, o2) and torch.equal(state, ht)
-    dout, dht = torch.randn_like(x), torch.randn_like(h0)
-    dx, dg, dh = ccv.gated_linear_recurrence_bwd(x, g, dout, cu, h0, dht, False, ca, True)
-    a = ccv.ccv_linrec_bwd_args_t()
-    a.B, a.L, a.C, a.N = 1, L, 130, len(lengths)
-    dx2, dg2 = torch.empty_like(x), torch.empty_like(g)
-    for n, t in (("x", x), ("g", g), ("dout", dout), ("dx", dx2), ("dg", dg2)):
-        setattr(a, n, t.data_ptr())
-        setattr(a, n + "_stride", (a.x_stride.__class__)(*t.stride()[:2]))
-    a.cu_seqlens, a.initial_state, a.init_stride = cu.data_ptr(), h0.data_ptr(), 130
-    a.dfinal_state = a.dinitial_state = dht.data_ptr()
-    a.dfinal_stride = a.dinit_stride = 130
-    a.carries = ca.data_ptr()
-    ws = torch.empty(ccv.ccv_linrec_bwd_workspace_size(a), dtype=torch.uint8, device="cuda")
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-    assert ccv.ccv_linrec_bwd(a) == 0
-    assert torch.equal(dx, dx2) and torch.equal(dg, dg2) and torch.equal(dh, dht)
 
 
 def test_decays_at_the_ends():
