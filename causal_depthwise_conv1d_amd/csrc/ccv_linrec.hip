@@ -120,16 +120,20 @@ __device__ __forceinline__ void fwd_tile(const LinrecArgs& a, const Place& at, i
   store_steps<DT>(a.out, a.o_s, at, a.L, H);
 }
 
+// Three workgroups a compute unit where the data are 32-bit, in 80 registers; else two (1 x 65536 x 2560 with x in fp16: 394 us with
+// three, whose registers spill, 384 with two; 2 x 1048576 x 128 in fp32: 739 and 779).
+template <int DT, int GT> constexpr int kFwdWaves = DT == CCV_DT_F32 && GT == CCV_DT_F32 ? 6 : 4;
+
 template <int DT, int GT, bool NORM>
-__global__ __launch_bounds__(64 * kLrWaves, 6) void fwd_kernel(const LinrecArgs a) {
+__global__ __launch_bounds__(64 * kLrWaves, (kFwdWaves<DT, GT>)) void fwd_kernel(const LinrecArgs a) {
   __shared__ FwdShared shared;
   __shared__ uint32_t ticket[2];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const Place at = place_of<false>(a, take_ticket(a, ticket), wave);
   Pair<DT> xr[kLrSteps];
   Pair<GT> gr[kLrSteps];
-  load_steps<GT>(gr, a.g, a.g_s, at, a.L, a.C);
-  load_steps<DT>(xr, a.x, a.x_s, at, a.L, a.C);
+  load_steps<true>(gr, a.g, a.g_s, at, a.L, a.C);
+  load_steps<true>(xr, a.x, a.x_s, at, a.L, a.C);
   if (has_marks(a, at)) fwd_tile<DT, GT, NORM, true>(a, at, wave, xr, gr, shared);
   else fwd_tile<DT, GT, NORM, false>(a, at, wave, xr, gr, shared);
 }

@@ -167,9 +167,9 @@ __global__ __launch_bounds__(64 * kLrWaves, 4) void bwd_kernel(const LinrecArgs 
   const Place at = place_of<true>(a, take_ticket(a, ticket), wave);
   Pair<DT> xr[kLrSteps], dr[kLrSteps];
   Pair<GT> gr[kLrSteps];
-  load_steps<GT>(gr, a.g, a.g_s, at, a.L, a.C);
-  load_steps<DT>(xr, a.x, a.x_s, at, a.L, a.C);
-  load_steps<DT>(dr, a.dout, a.do_s, at, a.L, a.C);
+  load_steps<false>(gr, a.g, a.g_s, at, a.L, a.C);
+  load_steps<false>(xr, a.x, a.x_s, at, a.L, a.C);
+  load_steps<false>(dr, a.dout, a.do_s, at, a.L, a.C);
   if (has_marks(a, at)) bwd_tile<DT, GT, NORM, true>(a, at, wave, xr, dr, gr, shared);
   else bwd_tile<DT, GT, NORM, false>(a, at, wave, xr, dr, gr, shared);
 }
