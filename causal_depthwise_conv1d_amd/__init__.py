@@ -951,8 +951,8 @@ class _Call:
         self.fn = fn
 
     def __call__(self, device, *values):
-        """Enqueue on the device's current stream; the workspace, which follows the values in
-        the struct, is allocated here, through torch."""
+        """Enqueue on the current stream of the device (or of its index); the workspace, which follows the
+        values in the struct, is allocated here, through torch."""
         if self.fn is None:
             self.bind()
         if self.workspace:
@@ -960,10 +960,10 @@ class _Call:
             if ws < 0:
                 _raise(int(ws), self.name)
             buf = torch.empty(ws or 16, dtype=torch.uint8, device=device)
-            values += (buf.data_ptr(), buf.numel())
+            values += (buf.data_ptr(), ws or 16)
         args = self.pack(self.size, *values)
-        index = device.index
-        if index == torch.cuda.current_device():
+        index = device if type(device) is int else device.index
+        if index == _current_device():
             st = self.fn(args, _raw_stream(index))
         else:
             with torch.cuda.device(device):
@@ -974,6 +974,8 @@ class _Call:
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# of a process that has tensors on a GPU, and so has initialised it
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _CALLS = {name: _Call(name) for name in _LAYER_CALLS}
 
 
@@ -1039,6 +1041,17 @@ def _same_device(x, **others):
     for name, t in others.items():
         if t is not None and t.device != d:
             raise ValueError(f"{name} must be on {d}")
+    return d
+
+
+def _one_device(x, **others):
+    """The index of the GPU that all of the tensors are on."""
+    d = x.get_device()
+    if d < 0:
+        return _same_device(x)
+    for t in others.values():
+        if t is not None and t.get_device() != d:
+            return _same_device(x, **others).index
     return d
 
 
@@ -1252,9 +1265,8 @@ def _linrec_sizes(x, g, one=False):
     s = x.shape
     if len(s) != (2 if one else 3) or g.shape != s:
         raise ValueError("expected x and g [B, C]" if one else "expected x and g [B, L, C]")
-    for name, t in (("x", x), ("g", g)):
-        if t.dtype not in DTYPE_CODE:
-            raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    if x.dtype not in DTYPE_CODE or g.dtype not in DTYPE_CODE:
+        raise ValueError(f"x and g must be float32, float16 or bfloat16, not {x.dtype} and {g.dtype}")
     return s[0], 1 if one else s[1], s[-1]
 
 
@@ -1264,6 +1276,11 @@ def _rows2(t):
         return (0, 0, 0)
     s = t.stride()
     return (t.data_ptr(), s[0], s[1])
+
+
+def _row1(t):
+    """The same of a single step without its dimension."""
+    return (t.data_ptr(), t.stride(0), 0)
 
 
 def _state_at(t):
@@ -1290,8 +1307,8 @@ def gated_linear_recurrence_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Op
     if final_state_out is not None and not return_final_state:
         raise ValueError("final_state_out given but return_final_state is False")
     B, L, C = _linrec_sizes(x, g)
-    device = _same_device(x, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, final_state_out=final_state_out, out=out)
-    given = (("x", x), ("g", g), ("initial_state", initial_state))
+    device = _one_device(x, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, final_state_out=final_state_out, out=out)
+    given = (x, g, initial_state)
     x, g = _unit_heads(x), _unit_heads(g)
     N, seqs = _delta_sequences(cu_seqlens, B)
     if _delta_states("initial_state", initial_state, (seqs, C)) is not None:
@@ -1314,7 +1331,7 @@ def gated_linear_recurrence_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Op
                              _p(cu_seqlens), *_state_at(initial_state), *_state_at(ht), *_rows2(out), _p(carries))
     _written(*written)
     if info is not None:
-        info["copied"] = [name for (name, t), u in zip(given, (x, g, initial_state)) if t is not u]
+        info["copied"] = [name for name, t, u in zip(("x", "g", "initial_state"), given, (x, g, initial_state)) if t is not u]
     res = (out,) + ((ht,) if return_final_state else ()) + ((carries,) if return_carries else ())
     return res if len(res) > 1 else out
 
@@ -1331,7 +1348,7 @@ def gated_linear_recurrence_bwd(x: torch.Tensor, g: torch.Tensor, dout: torch.Te
     return_dinitial_state, which needs initial_state.
     """
     B, L, C = _linrec_sizes(x, g)
-    device = _same_device(x, g=g, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state, dfinal_state=dfinal_state,
+    device = _one_device(x, g=g, dout=dout, cu_seqlens=cu_seqlens, initial_state=initial_state, dfinal_state=dfinal_state,
                           carries=carries)
     if dout.dtype != x.dtype or dout.shape != x.shape:
         raise ValueError("dout must be [B, L, C] in x's dtype")
@@ -1371,8 +1388,7 @@ class _GatedLinearRecurrenceFn(torch.autograd.Function):
         dout = torch.zeros_like(x) if dout is None else dout.to(x.dtype)
         want_dh = initial_state is not None and ctx.needs_input_grad[3]
         with torch.no_grad():
-            grads = gated_linear_recurrence_bwd(x, g, dout, cu_seqlens, initial_state, None if dht is None else dht.float(),
-                                                ctx.normalize, carries, want_dh)
+            grads = gated_linear_recurrence_bwd(x, g, dout, cu_seqlens, initial_state, dht, ctx.normalize, carries, want_dh)
         dx, dg, dh = _first_order("gated_linear_recurrence_fn", (x, g, initial_state, dout, dht), grads)
         return dx, dg, None, dh, None, None
 
@@ -1397,7 +1413,7 @@ def gated_linear_recurrence_update(x: torch.Tensor, g: torch.Tensor, state: torc
     """
     one = x.dim() == 2
     B, L, C = _linrec_sizes(x, g, one)
-    device = _same_device(x, g=g, state=state, state_indices=state_indices, out=out)
+    device = _one_device(x, g=g, state=state, state_indices=state_indices, out=out)
     if state.dtype != torch.float32 or state.dim() != 2 or state.shape[1] != C:
         raise ValueError("state must be float32 [slots, C]")
     if state.stride(-1) != 1 and C > 1:
@@ -1413,7 +1429,7 @@ def gated_linear_recurrence_update(x: torch.Tensor, g: torch.Tensor, state: torc
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype != x.dtype or out.shape != x.shape or (out.stride(-1) != 1 and C > 1):
         raise ValueError("out must have x's shape and dtype with unit stride in its last dimension")
-    at = (lambda t: (t.data_ptr(), t.stride(0), 0)) if one else _rows2
+    at = _row1 if one else _rows2
     _CALLS["ccv_linrec_update"](device, B, L, C, state.shape[0], DTYPE_CODE[x.dtype], DTYPE_CODE[g.dtype], int(normalize), 0,
                                 *at(x), *at(g), _p(state_indices), *_state_at(state), *at(out))
     _written(*written)
@@ -1574,7 +1590,7 @@ def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     Returns out (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [..., num_groups].
     """
     rows, groups, width, act = _group_sizes(x, num_groups, activation, weight, bias, gate)
-    device = _same_device(x, weight=weight, bias=bias, gate=gate, out=out)
+    device = _one_device(x, weight=weight, bias=bias, gate=gate, out=out)
     weight, bias = (None if t is None else t.contiguous() for t in (weight, bias))
     written = out
     if out is None:
@@ -1604,7 +1620,7 @@ def group_norm_bwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     a fixed order.
     """
     rows, groups, width, act = _group_sizes(x, num_groups, activation, weight, bias, gate)
-    device = _same_device(x, weight=weight, bias=bias, dout=dout, mean=mean, rstd=rstd, gate=gate)
+    device = _one_device(x, weight=weight, bias=bias, dout=dout, mean=mean, rstd=rstd, gate=gate)
     if dout.dtype != x.dtype or dout.shape != x.shape:
         raise ValueError("dout must have x's shape and dtype")
     for name, t in (("mean", mean), ("rstd", rstd)):
@@ -1726,7 +1742,7 @@ def rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tens
     without k.
     """
     B, L, Hq, Hk, D = _rotary_sizes(q, k, positions, frequencies)
-    device = _same_device(q, k=k, positions=positions, frequencies=frequencies, q_out=q_out, k_out=k_out)
+    device = _one_device(q, k=k, positions=positions, frequencies=frequencies, q_out=q_out, k_out=k_out)
     if k is None and k_out is not None:
         raise ValueError("k_out given without k")
     written = (q_out, k_out)
