@@ -114,6 +114,7 @@ int validate(const ccv_rotary_args_t* p, RotaryArgs* a) {
   const int64_t each = (int64_t)std::max(a->units, 1) * (heads[0] + heads[1]);
   const int64_t span = a->units ? std::max<int64_t>(1, 1024 / each) : std::max<int64_t>(1, 2048 / ((int64_t)a->D * (heads[0] + heads[1])));
   a->span = (int32_t)std::min<int64_t>(span, kRotaryAngles / std::max(a->half, 1));
+  if ((tokens + a->span - 1) / a->span >= (int64_t)1 << 24) return CCV_E_SHAPE;      // a launch has fewer than 2^32 threads
   if (units == 0 && in_place && turned == 0) a->tokens = 0;      // nothing is turned and nothing is copied
   return CCV_OK;
 }

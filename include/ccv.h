@@ -627,7 +627,7 @@ int ccv_seq_tables(const ccv_seq_tables_args_t* args, void* hip_stream);
  *     written arrays may not map two elements to one address.  L below 2^31 - 8192, C at most 2^24.
  *   - x_dtype is the storage type of x and out, g_dtype of g; states and sums are fp32, out is rounded once.
  *   - g is meant to be at most 0 (-inf gives a decay of 0).  Greater ones grow as the formula says, as long
- *     as the products of the decays of 4096 successive steps stay finite; s is then 0 and has no gradient.
+ *     as the products of the decays of 32768 successive steps stay finite; s is then 0 and has no gradient.
  *   - cu_seqlens NULL: each of the B rows is one sequence (N must be 0).  Otherwise B is 1 and the row packs N sequences: s
  *     has the steps cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32, on the device, never read by the host).
  *     Offsets count as their running maximum, clamped to [0, L], and the first as 0.  Steps past the last
@@ -721,7 +721,8 @@ int ccv_linrec_update(const ccv_linrec_update_args_t* args, void* hip_stream);
  *   (u, v) -> scale (u cos - v sin, v cos + u sin)
  *
  * and the other elements are copied.  q, q_out: [B, L, Hq, D]; k, k_out: [B, L, Hk, D] (Hk or Hq may be 0), element
- * (b, t, h, d) at b s[0] + t s[1] + h s[2] + d: unit stride inside a head; x_dtype; D at most 2048 (CCV_E_UNSUPPORTED), turned even.
+ * (b, t, h, d) at b s[0] + t s[1] + h s[2] + d: unit stride inside a head; x_dtype; D at most 2048 (CCV_E_UNSUPPORTED), turned even,
+ * B L below 2^24, or more where the heads of a step are small (CCV_E_SHAPE).
  * positions: int32, step (b, t) at b s[0] + t s[1] (s[0] = 0: the same for all rows); frequencies: 64-bit, radians
  * a position, contiguous [turned / 2].  Angles are 64-bit, their cosines and sines and the products fp32, results rounded once.
  * q_out may be q itself and k_out k (same strides); what is not turned then stays as it is.  The gradient

@@ -145,7 +145,8 @@ TABLE = [
                               {"turned": 0, "positions": None, "frequencies": None}, {"q_out": X}, {"q_out": X, "k_out": Z}, {"pos_stride": (0, 1)},
                               {"pos_stride": (0, 0)}, {"q_stride": (0, 0, 0)}, {"interleaved": 1, "inverse": 1}, {"scale": 0.0}]),
     ("ccv_rotary", "CCV_E_SHAPE", [{"B": -1}, {"L": -1}, {"Hq": -1}, {"Hk": -1}, {"D": 0}, {"turned": -2}, {"turned": 66}, {"turned": 3},
-                                   {"Hq": 65537}, {"B": 2 ** 16, "L": 2 ** 15}, {"q_stride": (2 ** 62, 256, 64)}, {"pos_stride": (2 ** 62, 1)}]),
+                                   {"Hq": 65537}, {"B": 2 ** 16, "L": 2 ** 15}, {"q_stride": (2 ** 62, 256, 64)}, {"pos_stride": (2 ** 62, 1)},
+                                   {"B": 1, "L": 2 ** 24, "D": 2048, "Hk": 0}]),
     ("ccv_rotary", "CCV_E_DTYPE", [{"x_dtype": 3}]),
     ("ccv_rotary", "CCV_E_UNSUPPORTED", [{"D": 2049}, {"interleaved": 2}, {"inverse": -1}, {"scale": math.nan}, {"scale": math.inf}]),
     ("ccv_rotary", "CCV_E_NULL", [{"q": None}, {"k": None}, {"q_out": None}, {"k_out": None}, {"positions": None}, {"frequencies": None}]),
