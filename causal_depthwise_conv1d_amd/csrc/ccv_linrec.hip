@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * kLrWaves, (kFwdWaves<DT, GT>)) void fwd_kernel
 // Clears the words and the tickets; of a packed row also makes each step's sequence, and passes the
 // states of empty sequences on (from -> to).  Offsets count as their running maximum, clamped to [0, L], the first as 0.
 
-constexpr int kPiece = 4096, kSpan = 4096;
+constexpr int kPiece = 4096, kSpan = 1024;
 
 __device__ inline uint32_t wave_max(uint32_t x) {
 #pragma unroll
@@ -161,7 +161,9 @@ __device__ inline void pass_on(const float* from, int64_t from_s, float* to, int
 __global__ __launch_bounds__(1024) void prepare_kernel(const LinrecArgs a, const float* from, int64_t from_s, float* to, int64_t to_s) {
   __shared__ uint32_t wave[16];
   __shared__ uint32_t start[kPiece + 1];
-  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < a.clear_count; i += (int64_t)gridDim.x * 1024) a.clear[i] = kEmpty;
+  // two words a store: their number is even
+  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; 2 * i < a.clear_count; i += (int64_t)gridDim.x * 1024)
+    store16(reinterpret_cast<char*>(a.clear + 2 * i), u32x4{~0u, ~0u, ~0u, ~0u});
   if (!a.cu) {
     if (a.L == 0 && to)
       for (int64_t s = blockIdx.x; s < a.B; s += gridDim.x) pass_on(from, from_s, to, to_s, s, a.C);
@@ -198,15 +200,12 @@ __global__ __launch_bounds__(1024) void prepare_kernel(const LinrecArgs a, const
     // the steps of this piece's sequences, in spans dealt to the workgroups
     for (int64_t span = blockIdx.x; span * kSpan < (int64_t)all; span += gridDim.x) {
       if ((span + 1) * kSpan <= (int64_t)carry) continue;
+      const uint32_t t = (uint32_t)(span * kSpan) + tid;
+      if (t < carry || t >= all) continue;
+      int s0 = 0;                                       // the last sequence that starts at or before the step: not empty
 #pragma unroll
-      for (int i = 0; i < kSpan / 1024; ++i) {
-        const uint32_t t = (uint32_t)(span * kSpan) + i * 1024 + tid;
-        if (t < carry || t >= all) continue;
-        int s0 = 0;                                     // the last sequence that starts at or before the step: not empty
-#pragma unroll
-        for (int d = kPiece / 2; d; d >>= 1) s0 += start[s0 + d] <= t ? d : 0;
-        a.sid[t] = (int)base + s0;
-      }
+      for (int d = kPiece / 2; d; d >>= 1) s0 += start[s0 + d] <= t ? d : 0;
+      a.sid[t] = (int)base + s0;
     }
     if (to)
       for (int i = blockIdx.x; i < n; i += gridDim.x)
@@ -284,8 +283,8 @@ void step(const LinrecStepArgs& a, hipStream_t st) {
 
 int launch_linrec_prepare(const LinrecArgs& a, const float* from, int64_t from_s, float* to, int64_t to_s, void* stream) {
   int64_t need = a.cu ? (a.L + kSpan - 1) / kSpan : 1;
-  need = std::max(need, (a.clear_count + 8191) / 8192);
-  prepare_kernel<<<(uint32_t)std::min<int64_t>(std::max<int64_t>(need, 1), 512), 1024, 0, static_cast<hipStream_t>(stream)>>>(a, from, from_s, to, to_s);
+  need = std::max(need, (a.clear_count + 4095) / 4096);
+  prepare_kernel<<<(uint32_t)std::min<int64_t>(std::max<int64_t>(need, 1), 1024), 1024, 0, static_cast<hipStream_t>(stream)>>>(a, from, from_s, to, to_s);
   return (int)hipGetLastError();
 }
 
