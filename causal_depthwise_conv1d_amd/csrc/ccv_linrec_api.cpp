@@ -69,10 +69,7 @@ bool tile(LinrecArgs* a, int64_t* words) {
   a->by_more = divisor(a->fewer + 1);
   a->by_fewer = divisor(a->fewer);
   a->by_cblocks = divisor(a->cblocks);
-  // A tile reads a word a channel of each tile of its group before it and of each group of its stretch; a stretch's last tile
-  // waits for the stretch before it.  With few chains the waits decide, with many the words.
-  a->group_shift = chains >= 128 ? 2 : chains >= 32 ? 3 : 4;
-  a->groups = (uint32_t)ceil_div(tiles, (int64_t)1 << a->group_shift);
+  a->groups = (uint32_t)ceil_div(tiles, kLrGroup);
   a->stretches = (uint32_t)ceil_div(a->groups, kLrStretch);
   *words = tiles > 1 ? kTicketWords + (blocks + chains * (a->groups + a->stretches)) * kLrChannels : 0;
   return true;

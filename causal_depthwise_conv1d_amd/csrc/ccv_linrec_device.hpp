@@ -259,11 +259,12 @@ __device__ inline Map other_half(Map m) { return {__shfl_xor(m.A, 32), __shfl_xo
 //
 // A tile's map reaches the later tiles of its chain through one 64-bit word a channel, (A, H), written
 // once a call by an atomic store: the word is the message and its own flag, so no fence is needed.  ~0 is an empty
-// word (A is then no NaN that a tile could write: put() makes NaNs positive).  Tiles are grouped, and 16 groups to a
+// word (A is then no NaN that a tile could write: put() makes NaNs positive).  8 tiles are a group, and 8 groups a
 // stretch.  A group's last tile joins its maps into the group's, as soon as they are there; a stretch's last tile gives
 // the state behind it.  A tile applies to the state behind the stretch before its own the maps of the groups and then
 // of the tiles between, in their order: results do not depend on which word came first, and what
-// has to wait for each other is one tile in 16 groups.
+// has to wait for each other is one tile in 64.  Each wave asks for one tile's word and one group's: groups of 4 or 16 tiles, and
+// stretches of 16 or of one group, take the same time to 1 %.
 // Tiles are taken in the order of their chains' walks, by tickets; a queue of tickets has the chains of one of the eight dies,
 // whose L2 then passes their words on, and its own counter: one counter for all gives a ticket in 12 ns, which is
 // a third of the time that a tile's data take.  A workgroup whose die's queue is empty takes from another's.  Every wait
@@ -314,44 +315,21 @@ __device__ inline Ticket take_ticket(const LinrecArgs& a, uint32_t* shared) {
   return {(uint32_t)__builtin_amdgcn_readfirstlane(shared[0]), (uint32_t)__builtin_amdgcn_readfirstlane(shared[1])};
 }
 
-// What a tile hears of those before it, by slot: joint maps by wave of tiles and of groups, and a state.
+// What a tile hears of those before it, by slot: the maps of the group's tiles and of the stretch's groups, a wave each, and a state.
 struct Heard {
   alignas(16) Map tiles[kLrWaves][kLrChannels], groups[kLrWaves][kLrChannels];
   float state[kLrChannels];
 };
-// A wave's share of `n` words: `each` of them from number wave * each on.
-struct Share {
-  uint32_t n, each, from;
-  __device__ inline Share(uint32_t count, uint32_t most, int wave) : n(count), each(most > kLrWaves ? most / kLrWaves : 1), from(wave * each) {}
-  __device__ inline bool has(uint32_t j) const { return j < each && from + j < n; }
-};
-constexpr int kShare = kLrMostGroup / kLrWaves;
-// Asks for a wave's words; true: they are there.
-__device__ inline bool look(const uint64_t* ws, const Share& share, uint64_t (&w)[kShare]) {
-  bool ok = true;
-#pragma unroll
-  for (int j = 0; j < kShare; ++j)
-    if (share.has(j)) w[j] = peek(ws + j * kLrChannels);
-#pragma unroll
-  for (int j = 0; j < kShare; ++j) ok = ok && !(share.has(j) && w[j] == kEmpty);
-  return ok;
-}
-// Waits until they are.  While something is missing one lane alone asks: words come a wave's store at a time.
-__device__ inline void wait_words(const uint64_t* ws, const Share& share, uint64_t (&w)[kShare], bool ok) {
-  while (__builtin_amdgcn_ballot_w64(!ok) != 0) {
-    for (ok = false; __builtin_amdgcn_ballot_w64(ok) == 0;) {
+// Waits for a wave's word, w as it was found first.  While it is missing one lane alone asks: words come a wave's store at a time.
+__device__ inline Map wait_word(const uint64_t* at, uint64_t w) {
+  while (__builtin_amdgcn_ballot_w64(w == kEmpty) != 0) {
+    for (bool there = false; __builtin_amdgcn_ballot_w64(there) == 0;) {
       __builtin_amdgcn_s_sleep(1);
-      if ((threadIdx.x & 63) == 0) ok = look(ws, share, w);
+      if ((threadIdx.x & 63) == 0) there = peek(at) != kEmpty;
     }
-    ok = look(ws, share, w);
+    w = peek(at);
   }
-}
-__device__ inline Map joined(const Share& share, const uint64_t (&w)[kShare]) {
-  Map m = map_of(w[0]);
-#pragma unroll
-  for (int j = 1; j < kShare; ++j)
-    if (share.has(j)) m = then(m, map_of(w[j]));
-  return m;
+  return map_of(w);
 }
 
 // The tile's own map is given to the others, and theirs are waited for; the whole workgroup calls this, `all()` gives the
@@ -359,40 +337,32 @@ __device__ inline Map joined(const Share& share, const uint64_t (&w)[kShare]) {
 template <class F>
 __device__ inline void exchange(const LinrecArgs& a, const Place& at, int wave, Heard& heard, F all) {
   const int lane = threadIdx.x & 63;
-  const uint32_t size = 1u << a.group_shift, in_group = at.order & (size - 1), group = at.order >> a.group_shift;
+  const uint32_t in_group = at.order % kLrGroup, group = at.order / kLrGroup;
   const uint32_t in_stretch = group % kLrStretch, stretch = group / kLrStretch;
-  const bool talks = wave == kLrWaves - 1, follows = at.order + 1 < a.tiles, closes = in_group == size - 1 && follows;
+  const bool talks = wave == kLrWaves - 1, follows = at.order + 1 < a.tiles, closes = in_group == kLrGroup - 1 && follows;
   Map mine = {1.0f, 0.0f};
   if (talks && follows) {
     mine = all();
     put(tile_words(a, at, at.order), mine);
   }
   if (at.order == 0) return;
-  const Share t(in_group, size, wave), g(in_stretch, kLrStretch, wave);
-  const uint64_t *tw = tile_words(a, at, at.order - in_group + t.from), *gw = group_words(a, at, group - in_stretch + g.from);
-  uint64_t wt[kShare], wg[kShare];
-  const bool gok = look(gw, g, wg), tok = look(tw, t, wt);
-  if (t.has(0)) {
-    wait_words(tw, t, wt, tok);
-    heard.tiles[wave][lane] = joined(t, wt);
-  }
+  const bool of_tile = (uint32_t)wave < in_group, of_group = (uint32_t)wave < in_stretch;
+  const uint64_t *tw = tile_words(a, at, at.order - in_group + wave), *gw = group_words(a, at, group - in_stretch + wave);
+  uint64_t wt = 0, wg = 0;
+  if (of_group) wg = peek(gw);
+  if (of_tile) wt = peek(tw);
+  if (of_tile) heard.tiles[wave][lane] = wait_word(tw, wt);
   if (closes) {                                            // the same for the whole workgroup
     lds_barrier();
     if (talks) {
-      Map m = mine;
-      if (in_group > 0) {
-        m = heard.tiles[0][lane];
-        for (uint32_t k = 1; k * t.each < in_group; ++k) m = then(m, heard.tiles[k][lane]);
-        m = then(m, mine);
-      }
-      if (in_stretch < kLrStretch - 1) put(group_words(a, at, group), m);
-      mine = m;
+      Map m = heard.tiles[0][lane];
+#pragma unroll 1                                           // in few registers: else fp32 loads are spilled, at twice the time
+      for (uint32_t k = 1; k < kLrGroup - 1; ++k) m = then(m, heard.tiles[k][lane]);
+      mine = then(m, mine);
+      if (in_stretch < kLrStretch - 1) put(group_words(a, at, group), mine);
     }
   }
-  if (g.has(0)) {
-    wait_words(gw, g, wg, gok);
-    heard.groups[wave][lane] = joined(g, wg);
-  }
+  if (of_group) heard.groups[wave][lane] = wait_word(gw, wg);
   if (talks) {
     float h = 0.0f;                                        // a chain begins with a sequence: nothing looks at the 0
     if (stretch > 0) {
@@ -406,7 +376,7 @@ __device__ inline void exchange(const LinrecArgs& a, const Place& at, int wave, 
   lds_barrier();
   if (talks && closes && in_stretch == kLrStretch - 1) {
     float h = heard.state[lane];
-    for (uint32_t k = 0; k * g.each < in_stretch; ++k) h = apply(heard.groups[k][lane], h);
+    for (uint32_t k = 0; k < in_stretch; ++k) h = apply(heard.groups[k][lane], h);
     put(stretch_words(a, at, stretch), Map{0.0f, apply(mine, h)});
   }
 }
@@ -429,13 +399,10 @@ __device__ inline void apply_parts(const Map (&parts)[kLrWaves][kLrChannels], ui
 // The state before the tile, for two slots.
 __device__ inline void state_before(const LinrecArgs& a, const Place& at, const Heard& heard, int slot, float (&h)[2]) {
   if (at.order == 0) return;
-  const uint32_t size = 1u << a.group_shift, in_group = at.order & (size - 1), in_stretch = (at.order >> a.group_shift) % kLrStretch;
   h[0] = heard.state[slot];
   h[1] = heard.state[slot + 1];
-  constexpr uint32_t ge = kLrStretch / kLrWaves;
-  const uint32_t te = size > kLrWaves ? size / kLrWaves : 1;
-  apply_parts<false>(heard.groups, (in_stretch + ge - 1) / ge, slot, h);
-  apply_parts<false>(heard.tiles, te > 1 ? (in_group + 1) / 2 : in_group, slot, h);
+  apply_parts<false>(heard.groups, at.order / kLrGroup % kLrStretch, slot, h);
+  apply_parts<false>(heard.tiles, at.order % kLrGroup, slot, h);
 }
 
 // The types' numbers as constants: f(x's, g's).

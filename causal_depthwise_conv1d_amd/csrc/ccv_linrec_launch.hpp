@@ -21,8 +21,8 @@ constexpr int kLrRows = 16;
 constexpr int kLrTile = CCV_LINREC_CHUNK;
 constexpr int kLrSteps = kLrTile / kLrRows;
 constexpr int kLrWaves = kLrRows / 2;
-// Tiles of a chain in a group, at most, and groups in a stretch.
-constexpr uint32_t kLrMostGroup = 16, kLrStretch = 16;
+// Tiles of a chain in a group, and groups in a stretch: a word for each wave of a workgroup to wait for.
+constexpr uint32_t kLrGroup = kLrWaves, kLrStretch = kLrWaves;
 // Queues of tickets, at most, and the words from one's counter to the next: 128 bytes.
 constexpr uint32_t kLrQueues = 8, kLrTicketWords = 16;
 
@@ -47,7 +47,6 @@ struct LinrecArgs {
   uint32_t tiles, cblocks, chains, groups, stretches;
   uint32_t queues, fewer, longer;     // queues of neighbouring chains: fewer + 1 in the first `longer`, fewer in the others
   LrDivisor by_more, by_fewer, by_cblocks;
-  uint32_t group_shift;               // log2 of a group's tiles
   int32_t x_dtype, g_dtype, normalize;
 
   LR_HOST_DEVICE uint32_t first_chain(uint32_t queue) const { return queue * fewer + (queue < longer ? queue : longer); }

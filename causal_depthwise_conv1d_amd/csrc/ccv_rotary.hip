@@ -4,6 +4,8 @@
 // pairs of neighbours, or of elements half of the turned part apart.  Bound by memory: each array in and out
 // once.  A workgroup makes the cosines and sines of a few tokens, once for all their heads, into LDS; then each
 // thread has one place in a head (a vector of pairs, or one of what is only copied) and walks tokens and heads.
+// 4 x 4096 tokens of 16 and 4 heads of 128 in bf16 (168 MB): 35 to 38 us, 4.4 to 4.8 TB/s; 512 or 2048 units a workgroup, and streaming
+// loads or stores, take the same time.  256 tokens of 32 and 8 heads in fp16: 4.7 us, a launch and the angles' latency.
 #include "ccv_delta_device.hpp"
 #include "ccv_rotary_launch.hpp"
 

@@ -627,7 +627,7 @@ int ccv_seq_tables(const ccv_seq_tables_args_t* args, void* hip_stream);
  *     written arrays may not map two elements to one address.  L below 2^31 - 8192, C at most 2^24.
  *   - x_dtype is the storage type of x and out, g_dtype of g; states and sums are fp32, out is rounded once.
  *   - g is meant to be at most 0 (-inf gives a decay of 0).  Greater ones grow as the formula says, as long
- *     as the products of the decays of 32768 successive steps stay finite; s is then 0 and has no gradient.
+ *     as the products of the decays of 8192 successive steps stay finite; s is then 0 and has no gradient.
  *   - cu_seqlens NULL: each of the B rows is one sequence (N must be 0).  Otherwise B is 1 and the row packs N sequences: s
  *     has the steps cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32, on the device, never read by the host).
  *     Offsets count as their running maximum, clamped to [0, L], and the first as 0.  Steps past the last
