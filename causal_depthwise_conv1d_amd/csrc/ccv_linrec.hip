@@ -10,9 +10,10 @@
 // maps on through memory (ccv_linrec_device.hpp), so x and g are read once.  With the state before its
 // steps a lane walks them again from registers and stores.
 //
-// 4 x 4096 x 2048 in bf16, normalised: 56 us, 3.6 TB/s; 65536 x 2560 in fp16 with fp32 decays, 64 sequences: 355 us, 3.8; 2 x 1048576 x 128
-// in fp32: 680 us, 4.7.  The loads, the arithmetic and the stores alone, without the exchange, take 46, 287 and 536 us, without the
-// arithmetic too 41, 262 and 534: the rest is waiting in order, for the slowest of the tiles under way before one's own.
+// Calls of 4 x 4096 x 2048 in bf16, normalised, take 56 to 58 us, 3.5 TB/s; 65536 x 2560 in fp16 with fp32 decays, 64 sequences,
+// normalised: 359 to 364 us, 3.7; 2 x 1048576 x 128 in fp32: 680 us, 4.7.  Without the exchange of maps they would take 52, 287 and
+// 536 us, without the decays' arithmetic too 46, 262 and 534: what is between is waiting in order, for the slowest of the
+// tiles under way before one's own.
 #include "ccv_linrec_device.hpp"
 
 #include <algorithm>

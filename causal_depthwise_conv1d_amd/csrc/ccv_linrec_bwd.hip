@@ -8,9 +8,8 @@
 // maps, E <- A E + E' with A the product of the steps' decays, tiles taken last first.  h[t-1] is made again
 // inside a tile from the state before it, which the forward left (or makes now).
 //
-// 2 x 4096 x 4096 in bf16, normalised: 82 us, 4.1 TB/s (the forward before it 52).  Two walks and the decays are 41 vector instructions
-// an element, which keep the vector units busy for two thirds of that; two workgroups a compute unit, in 128 registers
-// (three, in 80: 235 us for the two calls against 152).
+// 2 x 4096 x 4096 in bf16, normalised: 83 us, 4.0 TB/s (the forward before it 50), with the vector units issuing for 63 % of that.
+// Two workgroups a compute unit, in 128 registers (three, in 80: 235 us for the two calls against 152).
 #include "ccv_linrec_device.hpp"
 
 namespace ccv {
