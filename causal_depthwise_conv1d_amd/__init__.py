@@ -933,6 +933,9 @@ CCV_LINREC_CHUNK = 128       # steps between the states that gated_linear_recurr
 _FORMAT = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "P", _I64x2: "2q", _I64x3: "3q"}
 
 
+_pack_workspace = struct.Struct("@Pq").pack      # the last two fields of every call that takes one
+
+
 class _Call:
     """One C entry point with its packed args."""
 
@@ -956,12 +959,14 @@ class _Call:
         if self.fn is None:
             self.bind()
         if self.workspace:
-            ws = self.ws_fn(self.pack(self.size, *values, 0, 0))
+            args = self.pack(self.size, *values, 0, 0)
+            ws = self.ws_fn(args)
             if ws < 0:
                 _raise(int(ws), self.name)
             buf = torch.empty(ws or 16, dtype=torch.uint8, device=device)
-            values += (buf.data_ptr(), ws or 16)
-        args = self.pack(self.size, *values)
+            args = args[:-16] + _pack_workspace(buf.data_ptr(), ws or 16)
+        else:
+            args = self.pack(self.size, *values)
         index = device if type(device) is int else device.index
         if index == _current_device():
             st = self.fn(args, _raw_stream(index))
