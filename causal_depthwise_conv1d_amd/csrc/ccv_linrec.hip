@@ -125,13 +125,14 @@ __device__ __forceinline__ void fwd_tile(const LinrecArgs& a, const Place& at, i
   store_steps<DT>(a.out, a.o_s, at, a.L, H);
 }
 
-// Three workgroups a compute unit, in 80 registers, for 32-bit data that are not normalised (2 x 1048576 x 128: 680 us, 716 with two;
-// 4 x 8192 x 2048: 156 and 152); else two: with more to compute, or halves to convert, 80 registers spill (the same sizes in
-// fp32, normalised: 835 and 192 us with three, 731 and 155 with two; bf16 training on 2 x 4096 x 4096: 142 and 140).
-template <int DT, int GT, bool NORM> constexpr int kFwdWaves = DT == CCV_DT_F32 && GT == CCV_DT_F32 && !NORM ? 6 : 4;
+// Three workgroups a compute unit, in 80 registers, for 32-bit data that are not normalised and have kManyTiles and more: 680 us for
+// 2 x 1048576 x 128, 722 with two; 557 and 613 for 2 x 32768 x 4096.  Else two, in 128.  The registers that 80 are short of cost a small
+// call more: 17.4 us for 1 x 16384 x 128, 13.5 with two; 101 and 96 for 1 x 65536 x 512 (4096 tiles).  With more to compute, or halves to
+// convert, three are slower at any size (2 x 1048576 x 128 normalised: 835 us, 731 with two).
+constexpr uint32_t kManyTiles = 12288;
 
-template <int DT, int GT, bool NORM>
-__global__ __launch_bounds__(64 * kLrWaves, (kFwdWaves<DT, GT, NORM>)) void fwd_kernel(const LinrecArgs a) {
+template <int DT, int GT, bool NORM, int GROUPS>
+__global__ __launch_bounds__(64 * kLrWaves, 2 * GROUPS) void fwd_kernel(const LinrecArgs a) {
   __shared__ FwdShared shared;
   __shared__ uint32_t ticket[2];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -276,8 +277,13 @@ __global__ __launch_bounds__(256) void step_kernel(const LinrecStepArgs a, uint3
 template <int DT, int GT>
 void fwd(const LinrecArgs& a, hipStream_t st) {
   const uint32_t grid = a.tiles * a.chains;
-  if (a.normalize) fwd_kernel<DT, GT, true><<<grid, 64 * kLrWaves, 0, st>>>(a);
-  else fwd_kernel<DT, GT, false><<<grid, 64 * kLrWaves, 0, st>>>(a);
+  if constexpr (DT == CCV_DT_F32 && GT == CCV_DT_F32)
+    if (!a.normalize && grid >= kManyTiles) {
+      fwd_kernel<DT, GT, false, 3><<<grid, 64 * kLrWaves, 0, st>>>(a);
+      return;
+    }
+  if (a.normalize) fwd_kernel<DT, GT, true, 2><<<grid, 64 * kLrWaves, 0, st>>>(a);
+  else fwd_kernel<DT, GT, false, 2><<<grid, 64 * kLrWaves, 0, st>>>(a);
 }
 template <int DT, int GT>
 void step(const LinrecStepArgs& a, hipStream_t st) {
