@@ -9,7 +9,9 @@
 // inside a tile from the state before it, which the forward left (or makes now).
 //
 // 2 x 4096 x 4096 in bf16, normalised: 83 us, 4.0 TB/s (the forward before it 50), with the vector units issuing for 63 % of that.
-// Two workgroups a compute unit, in 128 registers (three, in 80: 235 us for the two calls against 152).
+// Two workgroups a compute unit, in 128 registers (three, in 80: 235 us for the two calls against 152).  fp32 x and dout are some registers
+// more than that: calls of at most kFewTiles take one a compute unit, and spill none (normalised: 34 us for 1 x 16384 x 128 with two, 19 with
+// one; 95 and 83 for 2 x 4096 x 2048, 2048 tiles; 167 and 174 for 2 x 4096 x 4096.  bf16: 36 and 41 for 2 x 4096 x 1024).
 #include "ccv_linrec_device.hpp"
 
 namespace ccv {
@@ -162,8 +164,10 @@ __device__ __forceinline__ void bwd_tile(const LinrecArgs& a, const Place& at, i
   store_steps<GT>(a.dg, a.dg_s, at, a.L, G);
 }
 
-template <int DT, int GT, bool NORM>
-__global__ __launch_bounds__(64 * kLrWaves, 4) void bwd_kernel(const LinrecArgs a) {
+constexpr uint32_t kFewTiles = 2048;
+
+template <int DT, int GT, bool NORM, int GROUPS>
+__global__ __launch_bounds__(64 * kLrWaves, 2 * GROUPS) void bwd_kernel(const LinrecArgs a) {
   __shared__ BwdShared shared;
   __shared__ uint32_t ticket[2];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -184,8 +188,14 @@ int launch_linrec_bwd(const LinrecArgs& a, void* stream) {
     constexpr int DT = decltype(dt)::value, GT = decltype(gt)::value;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const uint32_t grid = a.tiles * a.chains;
-    if (a.normalize) bwd_kernel<DT, GT, true><<<grid, 64 * kLrWaves, 0, st>>>(a);
-    else bwd_kernel<DT, GT, false><<<grid, 64 * kLrWaves, 0, st>>>(a);
+    if constexpr (DT == CCV_DT_F32)
+      if (grid <= kFewTiles) {
+        if (a.normalize) bwd_kernel<DT, GT, true, 1><<<grid, 64 * kLrWaves, 0, st>>>(a);
+        else bwd_kernel<DT, GT, false, 1><<<grid, 64 * kLrWaves, 0, st>>>(a);
+        return;
+      }
+    if (a.normalize) bwd_kernel<DT, GT, true, 2><<<grid, 64 * kLrWaves, 0, st>>>(a);
+    else bwd_kernel<DT, GT, false, 2><<<grid, 64 * kLrWaves, 0, st>>>(a);
   });
   return (int)hipGetLastError();
 }

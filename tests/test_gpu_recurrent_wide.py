@@ -87,3 +87,24 @@ def test_rotary_far_apart(interleaved):
     ccv.rotary_fwd(qf, kf, pf, freq, interleaved, q_out=qf, k_out=kf)
     ref.assert_within("q in place", qf, wq)
     ref.assert_within("k in place", kf, wk)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_rows_of_a_large_call_are_those_of_smaller_ones(normalize):
+    """Calls of many tiles run in other numbers of workgroups a compute unit: the same bits, and the 64-bit results."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    x, g, dout, h0, dht = rand(100, 300, 2688), -rand(100, 300, 2688).abs(), rand(100, 300, 2688), rand(100, 2688), rand(100, 2688)
+
+    def results(rows, channels=slice(None)):
+        a, b, d, h, e = (t[rows][..., channels] for t in (x, g, dout, h0, dht))
+        out, ht, ca = ccv.gated_linear_recurrence_fwd(a, b, initial_state=h, return_final_state=True, normalize=normalize, return_carries=True)
+        dx, dg, dh = ccv.gated_linear_recurrence_bwd(a, b, d, initial_state=h, dfinal_state=e, normalize=normalize, carries=ca, return_dinitial_state=True)
+        return {"out": out, "ht": ht, "dx": dx, "dg": dg, "dh0": dh}
+
+    large, few = results(slice(None)), slice(40, 44)
+    for n, t in results(few).items():
+        assert torch.equal(t, large[n][few]), n
+    want = ref.linrec(*(t[few][..., :96].cpu() for t in (x, g)), None, h0[few][..., :96].cpu(), normalize, dout[few][..., :96].cpu(), dht[few][..., :96].cpu())
+    for n, t in large.items():
+        ref.assert_within(n, t[few][..., :96], want[n])
