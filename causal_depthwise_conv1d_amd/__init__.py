@@ -1687,7 +1687,8 @@ def rotary_frequencies(turned: int, base: float = 10000.0, scaling: Optional[str
       "base"    the base raised by factor^(turned / (turned - 2)), so that the slowest pair is divided by the
                 factor and the fastest not at all
       "parts"   pairs that make more than ``fast`` turns over ``original_length`` positions stay, those that make fewer
-                than ``slow`` are divided, with a ramp between; scale = 0.1 ln(factor) + 1
+                than ``slow`` are divided, with a ramp between, which begins at the first pair at the earliest and may
+                end behind the last; scale = 0.1 ln(factor) + 1
     """
     if turned < 2 or turned % 2:
         raise ValueError("turned must be a positive even number")
@@ -1706,7 +1707,7 @@ def rotary_frequencies(turned: int, base: float = 10000.0, scaling: Optional[str
         if original_length is None or original_length < 1:
             raise ValueError("scaling 'parts' needs original_length")
         pair = lambda turns: turned * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
-        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), turned // 2 - 1)
+        lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), turned - 1)
         whole = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         f = f / factor * (1 - whole) + f * whole
         scale = 0.1 * math.log(factor) + 1

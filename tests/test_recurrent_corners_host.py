@@ -1,0 +1,39 @@
+"""Corners of the gated linear recurrence, group norm and rotary positions, on the CPU."""
+import math
+
+import pytest
+import torch
+
+import causal_depthwise_conv1d_amd as ccv
+
+
+# ---- the frequencies of stretched contexts ---------------------------------------------------
+
+def plain(turned, base):
+    return torch.tensor([base ** (-2 * i / turned) for i in range(turned // 2)], dtype=torch.float64)
+
+
+@pytest.mark.parametrize("turned,base,length", [
+    (128, 10000.0, 2048), (128, 10000.0, 54000), (128, 10000.0, 65536), (128, 10000.0, 131072), (128, 10000.0, 1 << 24),
+    (64, 500000.0, 8192), (64, 500000.0, 1 << 23), (4, 10000.0, 2048), (2, 10000.0, 2048), (16, 100.0, 4096), (128, 10000.0, 100)])
+def test_parts_is_a_ramp_over_pairs(turned, base, length):
+    """The share of a frequency that stays: 1 up to the last whole pair before the one of 32 turns, 0 from the first whole pair behind
+    that of one turn on, wherever these lie, and straight between."""
+    factor = 8.0
+    f, scale = ccv.rotary_frequencies(turned, base, "parts", factor, length, device="cpu")
+    assert math.isclose(scale, 0.1 * math.log(factor) + 1)
+    at = [turned * math.log(length / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (32.0, 1.0)]
+    first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), turned - 1)
+    for i, w in enumerate(plain(turned, base).tolist()):
+        stays = 1.0 if i <= first else 0.0 if i >= last else 1 - (i - first) / (last - first)
+        assert math.isclose(float(f[i]), w * (stays + (1 - stays) / factor), rel_tol=1e-13), (i, first, last)
+
+
+def test_parts_divides_no_pair_whole_that_makes_a_turn():
+    """131072 steps: the slowest of 64 pairs makes 2.4 turns, so it keeps a share; over 2^24 steps it makes more than 32, and every pair stays."""
+    want = plain(128, 10000.0)
+    f, _ = ccv.rotary_frequencies(128, scaling="parts", factor=8, original_length=131072, device="cpu")
+    turns = 131072 * want / (2 * math.pi)
+    assert float(turns[-1]) > 2 and bool((f[turns > 1.4] > want[turns > 1.4] / 8 * 1.01).all())
+    f, _ = ccv.rotary_frequencies(128, scaling="parts", factor=8, original_length=1 << 24, device="cpu")
+    assert torch.equal(f, want)
