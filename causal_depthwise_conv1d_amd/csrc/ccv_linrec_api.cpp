@@ -57,6 +57,8 @@ LrDivisor divisor(uint32_t d) {
 
 // The tiles of a walk and the words that they need; false when there are too many.
 bool tile(LinrecArgs* a, int64_t* words) {
+  *words = 0;
+  if (a->L == 0) return true;                  // no tiles, however many rows and channels
   const int64_t tiles = ceil_div(a->L, kLrTile), cblocks = ceil_div(a->C, kLrChannels);
   int64_t chains, blocks;
   if (__builtin_mul_overflow(a->B, cblocks, &chains) || __builtin_mul_overflow(chains, tiles, &blocks) || blocks > kMostBlocks) return false;

@@ -1,10 +1,12 @@
 """Corners of the gated linear recurrence, group norm and rotary positions, on the CPU."""
+import ctypes
 import math
 
 import pytest
 import torch
 
 import causal_depthwise_conv1d_amd as ccv
+from test_recurrent_host import CALLS
 
 
 # ---- the frequencies of stretched contexts ---------------------------------------------------
@@ -37,3 +39,15 @@ def test_parts_divides_no_pair_whole_that_makes_a_turn():
     assert float(turns[-1]) > 2 and bool((f[turns > 1.4] > want[turns > 1.4] / 8 * 1.01).all())
     f, _ = ccv.rotary_frequencies(128, scaling="parts", factor=8, original_length=1 << 24, device="cpu")
     assert torch.equal(f, want)
+
+
+# ---- the recurrence's sizes ------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,C", [(2 ** 30, 256), (2 ** 26, 4096), (2 ** 31 - 1, 2 ** 24), (2 ** 31 - 1, 1), (1, 1)])
+@pytest.mark.parametrize("call", ["ccv_linrec_fwd", "ccv_linrec_bwd"])
+def test_no_steps_of_many_rows(call, B, C):
+    """Without steps there are no tiles, so that no number of rows and channels is too many for them: the calls need no workspace and do nothing."""
+    args = CALLS[call](B=B, L=0, C=C, workspace=None, workspace_bytes=0)
+    assert ccv.STATUS[getattr(ccv, call + "_check")(args)] == "CCV_OK"
+    assert getattr(ccv, call + "_workspace_size")(args) == 0
+    assert getattr(ccv.lib(), call)(ctypes.byref(args), None) == 0
