@@ -267,10 +267,16 @@ int validate_group_bwd(const ccv_group_norm_bwd_args_t* p, GroupNormArgs* a, int
   a->w_dtype = p->w_dtype;
   a->silu = p->activation == CCV_ACT_SILU;
   const NormShape s = group_norm_shape(p->width, es);
-  if (p->rows == 0) a->walkers = 0;
-  else if (s.lanes) a->walkers = std::max(group_walkers(p->rows, p->groups, 256 / s.lanes, kGroups, 4), (int32_t)((p->rows + kNormRows - 1) / kNormRows));
-  else a->walkers = (int32_t)std::min<int64_t>(p->rows, 64);
-  if ((int64_t)a->walkers * p->groups > INT32_MAX / 256) return CCV_E_SHAPE;      // of threads in a launch
+  if (p->rows == 0) {
+    a->walkers = 0;
+  } else if (s.lanes) {
+    // no more than a launch has threads for, at least 128; such calls' arrays are larger than the memory
+    const int64_t most = ((int64_t)1 << 31) / (p->groups * s.lanes);
+    a->walkers = std::max(group_walkers(p->rows, p->groups, 256 / s.lanes, kGroups, 4), (int32_t)((p->rows + kNormRows - 1) / kNormRows));
+    a->walkers = (int32_t)std::min<int64_t>(a->walkers, most);
+  } else {
+    a->walkers = (int32_t)std::min<int64_t>(p->rows, 64);
+  }
   if (p->dweight || p->dbias) {
     *bytes = (int64_t)a->walkers * 2 * C * 4;
     if (with_ws && *bytes) {

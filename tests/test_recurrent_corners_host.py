@@ -51,3 +51,25 @@ def test_no_steps_of_many_rows(call, B, C):
     assert ccv.STATUS[getattr(ccv, call + "_check")(args)] == "CCV_OK"
     assert getattr(ccv, call + "_workspace_size")(args) == 0
     assert getattr(ccv.lib(), call)(ctypes.byref(args), None) == 0
+
+
+# ---- group norm's sizes ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [ccv.CCV_F32, ccv.CCV_F16, ccv.CCV_BF16])
+@pytest.mark.parametrize("rows,groups,width", [
+    (64, 131071, 1), (64, 131072, 1), (100, 200000, 4), (1, 2 ** 24, 1), (2 ** 31 - 1, 2 ** 24, 1), (2 ** 31 - 1, 2 ** 22, 4), (2 ** 31 - 1, 2 ** 21, 8),
+    (2 ** 31 - 1, 5, 64), (2 ** 20, 2 ** 15, 512), (2 ** 31 - 1, 2 ** 16, 256), (2 ** 31 - 1, 1, 2 ** 24), (2 ** 31 - 1, 2, 2 ** 23)])
+def test_group_norm_differentiates_what_it_takes(dtype, rows, groups, width):
+    """Every size that the forward takes, the backward takes too: all up to 2^31 - 1 rows and 2^24 channels."""
+    sizes = dict(rows=rows, groups=groups, width=width, x_dtype=dtype)
+    C, back = groups * width, CALLS["ccv_group_norm_bwd"](**sizes, workspace_bytes=1 << 62)
+    assert ccv.STATUS[ccv.ccv_group_norm_fwd_check(CALLS["ccv_group_norm_fwd"](**sizes))] == "CCV_OK"
+    need = ccv.ccv_group_norm_bwd_workspace_size(back)
+    assert need > 0 and need % (8 * C) == 0, need
+    assert ccv.STATUS[ccv.ccv_group_norm_bwd_check(back)] == "CCV_OK"
+    walkers, vector = need // (8 * C), 4 if dtype == ccv.CCV_F32 else 8
+    assert 1 <= walkers <= rows
+    if vector <= width <= 1024 * vector:                     # in vectors, by at least 4 threads each, of which a launch has fewer than 2^32
+        assert walkers * groups * 4 <= 2 ** 31
+    else:
+        assert walkers <= 64
