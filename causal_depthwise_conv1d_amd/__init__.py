@@ -1555,7 +1555,7 @@ def _flat_rows(t):
     """t [..., C] as [rows, C] with unit stride along the channels, copied only where its strides allow no
     such view."""
     t = _unit_heads(t)
-    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    return t if t.dim() == 2 else t.reshape(math.prod(t.shape[:-1]), t.shape[-1])
 
 
 def _group_sizes(x, num_groups, activation, weight, bias, gate):
@@ -1592,7 +1592,7 @@ def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     y = (x - mean) rstd weight + bias (weight and bias [C] or None) returns act(y), or with
     ``gate`` (x's shape and dtype) y act(gate); activation None or "silu".  Strided rows are used
     as they are when channels are unit-stride and the leading dimensions lie at one stride.
-    Returns out (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [..., num_groups].
+    Returns out (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [..., num_groups] (NaN without channels).
     """
     rows, groups, width, act = _group_sizes(x, num_groups, activation, weight, bias, gate)
     device = _one_device(x, weight=weight, bias=bias, gate=gate, out=out)
@@ -1606,6 +1606,9 @@ def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     mean = rstd = None
     if return_stats:
         mean, rstd = (torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=device) for _ in range(2))
+        if width == 0:                       # of no values: no call writes them
+            for t in (mean, rstd):
+                t.fill_(math.nan)
     w = weight if weight is not None else bias if bias is not None else x
     x2, z2 = _flat_rows(x), None if gate is None else _flat_rows(gate)
     _CALLS["ccv_group_norm_fwd"](device, rows, groups, width, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], act, eps, *_state_at(x2),

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import causal_depthwise_conv1d_amd as ccv
-from test_recurrent_host import CALLS
+from test_recurrent_host import CALLS, calls_do_nothing  # noqa: F401
 
 
 # ---- the frequencies of stretched contexts ---------------------------------------------------
@@ -73,3 +73,17 @@ def test_group_norm_differentiates_what_it_takes(dtype, rows, groups, width):
         assert walkers * groups * 4 <= 2 ** 31
     else:
         assert walkers <= 64
+
+
+@pytest.mark.parametrize("shape", [(0,), (5, 0), (2, 3, 0), (2, 0, 0), (2, 3, 4, 0)])
+def test_group_norm_without_channels(calls_do_nothing, shape):  # noqa: F811
+    """As the C entries take it: nothing to normalise, and statistics of nothing."""
+    x = torch.zeros(3, *shape)
+    out, mean, rstd = ccv.group_norm_fwd(x, 2, gate=x, return_stats=True)
+    assert out.shape == x.shape and mean.shape == rstd.shape == (*x.shape[:-1], 2)
+    assert bool(mean.isnan().all()) and bool(rstd.isnan().all())
+    dx, dw, db, dz = ccv.group_norm_bwd(x, 2, None, None, x, mean, rstd, x)
+    assert dx.shape == dz.shape == x.shape and dw.shape == db.shape == (0,)
+    y = torch.zeros(3, *shape, requires_grad=True)
+    ccv.group_norm_fn(y, 2).sum().backward()
+    assert y.grad.shape == y.shape
