@@ -1802,7 +1802,9 @@ class _RotaryFn(torch.autograd.Function):
 def rotary_fn(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, frequencies: torch.Tensor,
               interleaved: bool = False, scale: float = 1.0):
     """Differentiable rotary positions (rotary_fwd, with gradients for q and k by the inverse turn).
-    Differentiable once: a second derivative raises."""
+    Differentiable once: a second derivative raises.  The frequencies get no gradient, and may not want one."""
+    if frequencies.requires_grad and torch.is_grad_enabled():
+        raise ValueError("frequencies get no gradient: detach them")
     return _RotaryFn.apply(q, k, positions, frequencies, interleaved, scale)
 
 

@@ -87,3 +87,18 @@ def test_group_norm_without_channels(calls_do_nothing, shape):  # noqa: F811
     y = torch.zeros(3, *shape, requires_grad=True)
     ccv.group_norm_fn(y, 2).sum().backward()
     assert y.grad.shape == y.shape
+
+
+# ---- rotary positions ------------------------------------------------------------------------
+
+def test_rotary_refuses_frequencies_that_want_gradients(calls_do_nothing):  # noqa: F811
+    q, pos = torch.zeros(2, 5, 3, 8), torch.zeros(2, 5, dtype=torch.int32)
+    freq = torch.ones(2, dtype=torch.float64, requires_grad=True)
+    for leaf in (q, q.clone().requires_grad_()):
+        with pytest.raises(ValueError, match="frequencies"):
+            ccv.rotary_fn(leaf, None, pos, freq)
+        with pytest.raises(ValueError, match="frequencies"):
+            ccv.rotary_fn(leaf, None, pos, freq * 2)
+        with torch.no_grad():
+            ccv.rotary_fn(leaf, None, pos, freq)
+        assert ccv.rotary_fn(leaf, None, pos, freq.detach())[0].requires_grad == leaf.requires_grad
