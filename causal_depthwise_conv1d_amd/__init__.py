@@ -1468,6 +1468,18 @@ def _norm_weights(x, weight, bias):
     return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous())
 
 
+def _gradient_types(weight_dtype, x, weight, bias=None):
+    """(type of dweight and dbias, the call's, weight, bias): a call has one type for the parameters and their gradients, so
+    where the caller wants another than the parameters' they go in 32 bits, which hold either's values, and the sums come back so."""
+    own = x if weight is None and bias is None else bias if weight is None else weight
+    wd = weight_dtype or own.dtype
+    if wd not in DTYPE_CODE:
+        raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
+    if own is x or own.dtype == wd:
+        return wd, wd, weight, bias
+    return wd, torch.float32, *(None if t is None else t.float() for t in (weight, bias))
+
+
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                    eps: float = 1e-5, return_stats: bool = False, out: Optional[torch.Tensor] = None):
     """Layer norm over x's last dimension on the GPU: (x - mean) rstd weight + bias.
@@ -1510,9 +1522,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.shape != x.shape[:-1] or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32 with x's leading shape")
-    wd = weight.dtype if weight is not None else weight_dtype or x.dtype
-    if wd not in DTYPE_CODE:
-        raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
+    wanted, wd, weight, _ = _gradient_types(weight_dtype, x, weight)
     (rows, shape, s), (drows, _, d) = _norm_rows(x), _norm_rows(dout)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
     dw = torch.empty(x.shape[-1], dtype=wd, device=device) if want_dweight else None
@@ -1520,6 +1530,8 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], dout: torch.
     _CALLS["ccv_norm_bwd"](device, *shape, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], rows.data_ptr(), s[0], s[1], _p(weight),
                            drows.data_ptr(), d[0], d[1], mean.data_ptr(), rstd.data_ptr(), _p(dx), shape[1] * shape[2], shape[2],
                            _p(dw), _p(db))
+    if wd != wanted:
+        dw, db = (None if t is None else t.to(wanted) for t in (dw, db))
     return dx, dw, db
 
 
@@ -1635,9 +1647,7 @@ def group_norm_bwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
         if t.dtype != torch.float32 or tuple(t.shape) != (*x.shape[:-1], groups) or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32 [..., num_groups]")
     weight, bias = (None if t is None else t.contiguous() for t in (weight, bias))
-    wd = weight.dtype if weight is not None else bias.dtype if bias is not None else weight_dtype or x.dtype
-    if wd not in DTYPE_CODE:
-        raise ValueError(f"weight_dtype must be float32, float16 or bfloat16, not {wd}")
+    wanted, wd, weight, bias = _gradient_types(weight_dtype, x, weight, bias)
     C = x.shape[-1]
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dx else None
     dz = torch.empty_like(x, memory_format=torch.contiguous_format) if want_dgate and gate is not None else None
@@ -1647,6 +1657,8 @@ def group_norm_bwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     _CALLS["ccv_group_norm_bwd"](device, rows, groups, width, DTYPE_CODE[x.dtype], DTYPE_CODE[wd], act, 0, *_state_at(x2),
                                  _p(weight), _p(bias), *_state_at(z2), *_state_at(d2), mean.data_ptr(), rstd.data_ptr(),
                                  _p(dx), C, _p(dz), C, _p(dw), _p(db))
+    if wd != wanted:
+        dw, db = (None if t is None else t.to(wanted) for t in (dw, db))
     return dx, dw, db, dz
 
 

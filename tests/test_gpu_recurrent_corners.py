@@ -23,3 +23,19 @@ def test_group_norm_without_channels():
     y = x.clone().requires_grad_()
     ccv.group_norm_fn(y, 4).sum().backward()
     assert y.grad.shape == y.shape
+
+
+@pytest.mark.parametrize("wanted", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("weight", ["f32", "f16", "bf16"])
+def test_gradients_in_a_type_of_the_callers(weight, wanted):
+    """The 32-bit sums of a call with the weight's values in 32 bits, rounded once."""
+    x, w, b, z, dout = (t.cuda() for t in inputs(300, 96, "bf16", weight, True, 5))
+    o, mean, rstd = ccv.group_norm_fwd(x, 3, w, b, z, "silu", return_stats=True)
+    wide = ccv.group_norm_bwd(x, 3, w.float(), b.float(), dout, mean, rstd, z, "silu")
+    got = ccv.group_norm_bwd(x, 3, w, b, dout, mean, rstd, z, "silu", weight_dtype=wanted)
+    assert torch.equal(got[0], wide[0]) and torch.equal(got[3], wide[3])
+    assert torch.equal(got[1], wide[1].to(wanted)) and torch.equal(got[2], wide[2].to(wanted))
+    o, mean, rstd = ccv.layer_norm_fwd(x, w, b, return_stats=True)
+    wide = ccv.layer_norm_bwd(x, w.float(), dout, mean, rstd)
+    got = ccv.layer_norm_bwd(x, w, dout, mean, rstd, weight_dtype=wanted)
+    assert torch.equal(got[0], wide[0]) and torch.equal(got[1], wide[1].to(wanted)) and torch.equal(got[2], wide[2].to(wanted))

@@ -102,3 +102,25 @@ def test_rotary_refuses_frequencies_that_want_gradients(calls_do_nothing):  # no
         with torch.no_grad():
             ccv.rotary_fn(leaf, None, pos, freq)
         assert ccv.rotary_fn(leaf, None, pos, freq.detach())[0].requires_grad == leaf.requires_grad
+
+
+# ---- the parameters' gradients in a type of the caller's --------------------------------------
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.mark.parametrize("wanted", [None, *TYPES])
+@pytest.mark.parametrize("weight", [None, *TYPES])
+@pytest.mark.parametrize("norm", ["group", "layer"])
+def test_weight_dtype_is_that_of_the_gradients(calls_do_nothing, monkeypatch, norm, weight, wanted):  # noqa: F811
+    """dweight and dbias come in weight_dtype, whatever the weight's own."""
+    monkeypatch.setattr(ccv, "_same_device", lambda x, **others: x.device)
+    monkeypatch.setitem(ccv._CALLS, "ccv_norm_bwd", lambda *values: None)
+    x, w = torch.zeros(5, 8, dtype=torch.bfloat16), None if weight is None else torch.ones(8, dtype=weight)
+    if norm == "group":
+        _, dw, db, _ = ccv.group_norm_bwd(x, 2, w, None, x, torch.zeros(5, 2), torch.ones(5, 2), weight_dtype=wanted)
+        _, _, alone, _ = ccv.group_norm_bwd(x, 2, None, w, x, torch.zeros(5, 2), torch.ones(5, 2), want_dweight=False, weight_dtype=wanted)
+    else:
+        _, dw, db = ccv.layer_norm_bwd(x, w, x, torch.zeros(5), torch.ones(5), weight_dtype=wanted)
+        _, _, alone = ccv.layer_norm_bwd(x, w, x, torch.zeros(5), torch.ones(5), want_dweight=False, weight_dtype=wanted)
+    assert dw.dtype == db.dtype == alone.dtype == (wanted or weight or x.dtype)
