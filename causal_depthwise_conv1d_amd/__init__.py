@@ -1305,6 +1305,7 @@ def gated_linear_recurrence_fwd(x: torch.Tensor, g: torch.Tensor, cu_seqlens: Op
     are used as they are when channels are unit-stride; others are copied (``info["copied"]``
     lists them).  ``cu_seqlens`` (int32 [N + 1], on the GPU) packs N sequences in one row (B = 1).
     States are float32 [sequences, C]; ``final_state_out`` may be ``initial_state`` itself.
+    B ceil(L / 128) ceil(C / 64) has to be below 2^23.
     Returns out [B, L, C] in x's dtype, then the final state if wanted, then with
     ``return_carries`` the states that gated_linear_recurrence_bwd can start from (float32
     [B, ceil(L / 128), C]).

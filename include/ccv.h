@@ -624,7 +624,9 @@ int ccv_seq_tables(const ccv_seq_tables_args_t* args, void* hip_stream);
  *
  *   - x, g (log decay) and out: [B, L, C], element (b, t, c) at b s[0] + t s[1] + c elements: unit stride
  *     along the channels; steps may lie at most 32 MB apart (CCV_E_LAYOUT).  Inputs may have zero strides;
- *     written arrays may not map two elements to one address.  L below 2^31 - 8192, C at most 2^24.
+ *     written arrays may not map two elements to one address.  L and N below 2^31 - 8192, B below 2^31, C at most
+ *     2^24, and, of the forward and the backward, B ceil(L / CCV_LINREC_CHUNK) ceil(C / 64) below 2^23: a launch's
+ *     workgroups, each with the 64 channels of a chunk of a row, however few steps that holds (CCV_E_SHAPE).
  *   - x_dtype is the storage type of x and out, g_dtype of g; states and sums are fp32, out is rounded once.
  *   - g is meant to be at most 0 (-inf gives a decay of 0).  Greater ones grow as the formula says, as long
  *     as the products of the decays of 8192 successive steps stay finite; s is then 0 and has no gradient.
@@ -695,7 +697,7 @@ int ccv_linrec_bwd(const ccv_linrec_bwd_args_t* args, void* hip_stream);
 /* Decoding: L new steps of B rows, one after the other, against fp32 states in a cache [slots, C], advanced in
  * place.  Row b uses slot state_indices[b] (int32, device), or slot b when state_indices is NULL (then B <= slots, else
  * CCV_E_SHAPE).  A row whose index lies outside [0, slots) is idle: its outputs are zeros and no state is
- * touched.  Two rows may not use one slot in the same call.  Needs no workspace. */
+ * touched.  Two rows may not use one slot in the same call.  B ceil(C / 2) below 2^31 - 256 (CCV_E_SHAPE).  Needs no workspace. */
 typedef struct ccv_linrec_update_args {
   int64_t struct_size;          /* = sizeof(ccv_linrec_update_args_t) */
   int64_t B, L, C, slots;
@@ -722,7 +724,7 @@ int ccv_linrec_update(const ccv_linrec_update_args_t* args, void* hip_stream);
  *
  * and the other elements are copied.  q, q_out: [B, L, Hq, D]; k, k_out: [B, L, Hk, D] (Hk or Hq may be 0), element
  * (b, t, h, d) at b s[0] + t s[1] + h s[2] + d: unit stride inside a head; x_dtype; D at most 2048 (CCV_E_UNSUPPORTED), turned even,
- * B L below 2^24, or more where the heads of a step are small (CCV_E_SHAPE).
+ * Hq and Hk at most 65536, B L below 2^24, or more where the heads of a step are small (CCV_E_SHAPE).
  * positions: int32, step (b, t) at b s[0] + t s[1] (s[0] = 0: the same for all rows); frequencies: 64-bit, radians
  * a position, contiguous [turned / 2].  Angles are 64-bit, their cosines and sines and the products fp32, results rounded once.
  * q_out may be q itself and k_out k (same strides); what is not turned then stays as it is.  The gradient

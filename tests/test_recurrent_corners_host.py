@@ -53,6 +53,26 @@ def test_no_steps_of_many_rows(call, B, C):
     assert getattr(ccv.lib(), call)(ctypes.byref(args), None) == 0
 
 
+@pytest.mark.parametrize("B,L,C", [(2 ** 23 - 1, 1, 64), (2 ** 22 - 1, 128, 65), (65535, 1, 8192), (1, 128 * (2 ** 23 - 1), 1), (31, 128 * 31, 64 * 8729)])
+@pytest.mark.parametrize("call", ["ccv_linrec_fwd", "ccv_linrec_bwd"])
+def test_most_tiles(call, B, L, C):
+    """B ceil(L / 128) ceil(C / 64) below 2^23, as the header has it."""
+    tiles = lambda B, L, C: B * -(-L // 128) * -(-C // 64)  # noqa: E731
+    for more in ((0, 0, 0), (1, 0, 0), (0, 128, 0), (0, 0, 64)):
+        b, n, c = (i + j for i, j in zip((B, L, C), more))
+        want = "CCV_OK" if tiles(b, n, c) < 2 ** 23 else "CCV_E_SHAPE"
+        args = CALLS[call](B=b, L=n, C=c, workspace_bytes=1 << 62)
+        assert ccv.STATUS[getattr(ccv, call + "_check")(args)] == want, (b, n, c)
+        assert (getattr(ccv, call + "_workspace_size")(args) >= 0) == (want == "CCV_OK")
+
+
+@pytest.mark.parametrize("B,C,want", [(2 ** 31 - 257, 1, "CCV_OK"), (2 ** 31 - 256, 2, "CCV_E_SHAPE"), (2 ** 31 - 257, 3, "CCV_E_SHAPE"),
+                                      (2 ** 20, 4094, "CCV_OK"), (2 ** 20, 4095, "CCV_E_SHAPE"), (255, 2 ** 24, "CCV_OK"), (256, 2 ** 24, "CCV_E_SHAPE")])
+def test_most_rows_of_a_step(B, C, want):
+    """B ceil(C / 2) below 2^31 - 256, as the header has it."""
+    assert ccv.STATUS[ccv.ccv_linrec_update_check(CALLS["ccv_linrec_update"](B=B, C=C, slots=B))] == want
+
+
 # ---- group norm's sizes ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [ccv.CCV_F32, ccv.CCV_F16, ccv.CCV_BF16])
