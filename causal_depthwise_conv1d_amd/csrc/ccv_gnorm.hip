@@ -74,7 +74,9 @@ __global__ __launch_bounds__(256) void fwd_kernel(const GroupNormArgs a) {
   }
 }
 
-// Element by element: groups narrower than a vector (THREADS 1) or wider than 256 threads hold.
+// Element by element: groups narrower than a vector (THREADS 1) or wider than 256 threads hold.  Far from the copy's rate, for accesses of
+// an element and a second and third walk of wide ones: calls with a gate of 65536 rows of 4 groups of 5 in fp16 take 10 us, 262144 of 32 of 6 in
+// bf16 218 (their bytes need 58), 4096 of one of 16384 in bf16 403 (77).
 template <int DT, int THREADS>
 __global__ __launch_bounds__(THREADS == 1 ? 256 : THREADS) void any_fwd_kernel(const GroupNormArgs a) {
   __shared__ float red[16];

@@ -12,8 +12,9 @@
 //
 // Calls of 4 x 4096 x 2048 in bf16, normalised, take 56 to 58 us, 3.5 TB/s; 65536 x 2560 in fp16 with fp32 decays, 64 sequences,
 // normalised: 359 to 364 us, 3.7; 2 x 1048576 x 128 in fp32: 680 us, 4.7.  Without the exchange of maps they would take 52, 287 and
-// 536 us, without the decays' arithmetic too 46, 262 and 534: what is between is waiting in order, for the slowest of the
-// tiles under way before one's own.
+// 536 us, without the decays' arithmetic too 46, 262 and 534.  The two longer ones wait in order, for the slowest of the
+// tiles under way before one's own.  The first, whose bytes alone need 39 us, is bound by no one thing: its loads and stores
+// with what comes before the tiles take 7 more, the decays 6, the exchange and its waits 4 to 6.
 #include "ccv_linrec_device.hpp"
 
 #include <algorithm>
@@ -126,8 +127,10 @@ __device__ __forceinline__ void fwd_tile(const LinrecArgs& a, const Place& at, i
 }
 
 // Three workgroups a compute unit, in 80 registers, for 32-bit data that are not normalised and have kManyTiles and more: 680 us for
-// 2 x 1048576 x 128, 722 with two; 557 and 613 for 2 x 32768 x 4096.  Else two, in 128.  The registers that 80 are short of cost a small
-// call more: 17.4 us for 1 x 16384 x 128, 13.5 with two; 101 and 96 for 1 x 65536 x 512 (4096 tiles).  With more to compute, or halves to
+// 2 x 1048576 x 128, 722 with two; 557 and 613 for 2 x 32768 x 4096.  Else two, in 128.  The 58 registers that 80 are short of cost a small
+// call more: 17.4 us for 1 x 16384 x 128, 13.5 with two; 101 and 96 for 1 x 65536 x 512 (4096 tiles).  They cross between 6144 tiles (three and
+// two: 142 and 142 us in rows of 128 channels, 139 and 137 of 512, 121 and 113 of 4096) and 10240 (225 and 230, 221 and 222, 188 and 188); at 12288
+// three are the faster in all (266 and 274, 262 and 265, 221 and 228).  With more to compute, or halves to
 // convert, three are slower at any size (2 x 1048576 x 128 normalised: 835 us, 731 with two).
 constexpr uint32_t kManyTiles = 12288;
 
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(64 * kLrWaves, 2 * GROUPS) void fwd_kernel(const Li
 //
 // Clears the words and the tickets; of a packed row also makes each step's sequence, and passes the
 // states of empty sequences on (from -> to).  Offsets count as their running maximum, clamped to [0, L], the first as 0.
-// A kernel's launch and the stores: 3 us for 2 x 4096 x 4096, 10 for 1 x 65536 x 2560 with 64 sequences (10 MB of words).
+// A kernel's launch and the stores: 3 us for 2 x 4096 x 4096, 10 for 1 x 65536 x 2560 with 64 sequences (12 MB of words).
 
 constexpr int kPiece = 4096, kSpan = 1024;
 

@@ -9,8 +9,9 @@
 // inside a tile from the state before it, which the forward left (or makes now).
 //
 // 2 x 4096 x 4096 in bf16, normalised: 83 us, 4.0 TB/s (the forward before it 50), with the vector units issuing for 63 % of that.
-// Two workgroups a compute unit, in 128 registers (three, in 80: 235 us for the two calls against 152).  fp32 x and dout are some registers
-// more than that: calls of at most kFewTiles take one a compute unit, and spill none (normalised: 34 us for 1 x 16384 x 128 with two, 19 with
+// Two workgroups a compute unit, in 128 registers (three, in 80: 235 us for the two calls against 152).  Normalised 16-bit data are 9 to 15
+// registers more than that (40 to 64 bytes a lane through memory), fp32 x and dout 102 when normalised, else 43 (62 and 13 with 16-bit
+// decays): fp32 calls of at most kFewTiles take one a compute unit, and spill none (normalised: 34 us for 1 x 16384 x 128 with two, 19 with
 // one; 95 and 83 for 2 x 4096 x 2048, 2048 tiles; 167 and 174 for 2 x 4096 x 4096.  bf16: 36 and 41 for 2 x 4096 x 1024).
 #include "ccv_linrec_device.hpp"
 

@@ -1,7 +1,10 @@
 """Corners of the gated linear recurrence, group norm and rotary positions, on the CPU."""
 import ctypes
 import math
+import os
+import re
 
+import numpy as np
 import pytest
 import torch
 
@@ -71,6 +74,22 @@ def test_most_tiles(call, B, L, C):
 def test_most_rows_of_a_step(B, C, want):
     """B ceil(C / 2) below 2^31 - 256, as the header has it."""
     assert ccv.STATUS[ccv.ccv_linrec_update_check(CALLS["ccv_linrec_update"](B=B, C=C, slots=B))] == want
+
+
+def test_the_decays_polynomial():
+    """The coefficients in the kernels' header against expm1 in 64 bits: within 1.9e-8 of e^r - 1, and so within an eighth of 2^-24 of e^r, over
+    |r| <= ln 2 / 2.  The bounds that the kernels are held to allow two units of 2^-24 for it and its rounding."""
+    path = os.path.join(os.path.dirname(ccv.__file__), "csrc", "ccv_linrec_device.hpp")
+    with open(path) as f:
+        body = f.read().split("inline float expm1_near(float r) {")[1].split("}")[0]
+    c = [np.float64(np.float32(v)) for v in re.findall(r"(\d+\.\d+)f", body)]
+    assert len(c) == 6 and c[-1] == 1.0
+    r = np.linspace(-math.log(2) / 2, math.log(2) / 2, 1000000)          # an even number: 0 is none of them
+    q = c[0]
+    for k in c[1:]:
+        q = r * q + k
+    off = np.abs(r * q - np.expm1(r))
+    assert (off / np.abs(np.expm1(r))).max() < 1.9e-8 and (off / np.exp(r)).max() < 2.0 ** -24 / 8
 
 
 # ---- group norm's sizes ----------------------------------------------------------------------
