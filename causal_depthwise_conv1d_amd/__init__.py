@@ -1469,6 +1469,12 @@ def _norm_weights(x, weight, bias):
     return (None if weight is None else weight.contiguous(), None if bias is None else bias.contiguous())
 
 
+def _statistics(x, shape, device):
+    """Room for mean and rstd; those of no values, which no call writes, are NaN."""
+    new = torch.empty if x.shape[-1] else lambda shape, **kw: torch.full(shape, math.nan, **kw)
+    return [new(shape, dtype=torch.float32, device=device) for _ in range(2)]
+
+
 def _gradient_types(weight_dtype, x, weight, bias=None):
     """(type of dweight and dbias, the call's, weight, bias): a call has one type for the parameters and their gradients, so
     where the caller wants another than the parameters' they go in 32 bits, which hold either's values, and the sums come back so."""
@@ -1487,7 +1493,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
 
     x [..., width], any strides (views of up to three dimensions that are unit-stride along
     the width are used as they are); weight and bias [width] or None.  Returns out
-    (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [...].
+    (contiguous, x's dtype), or (out, mean, rstd) with float32 statistics [...] (NaN where width is 0).
     """
     weight, bias = _norm_weights(x, weight, bias)
     device = _same_device(x, weight=weight, bias=bias, out=out)
@@ -1499,7 +1505,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
         raise ValueError("out must be contiguous with x's shape and dtype")
     mean = rstd = None
     if return_stats:
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=device) for _ in range(2))
+        mean, rstd = _statistics(x, x.shape[:-1], device)
     w = weight if weight is not None else bias if bias is not None else x
     _CALLS["ccv_norm_fwd"](device, *shape, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], eps, 0, rows.data_ptr(), s[0], s[1],
                            _p(weight), _p(bias), out.data_ptr(), shape[1] * shape[2], shape[2], _p(mean), _p(rstd))
@@ -1618,10 +1624,7 @@ def group_norm_fwd(x: torch.Tensor, num_groups: int, weight: Optional[torch.Tens
     C = x.shape[-1]
     mean = rstd = None
     if return_stats:
-        mean, rstd = (torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=device) for _ in range(2))
-        if width == 0:                       # of no values: no call writes them
-            for t in (mean, rstd):
-                t.fill_(math.nan)
+        mean, rstd = _statistics(x, (*x.shape[:-1], groups), device)
     w = weight if weight is not None else bias if bias is not None else x
     x2, z2 = _flat_rows(x), None if gate is None else _flat_rows(gate)
     _CALLS["ccv_group_norm_fwd"](device, rows, groups, width, DTYPE_CODE[x.dtype], DTYPE_CODE[w.dtype], act, eps, *_state_at(x2),

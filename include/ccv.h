@@ -485,7 +485,7 @@ int ccv_delta_update(const ccv_delta_update_args_t* args, void* hip_stream);
  *   out  = n weight + bias
  *
  * weight and bias ([width], contiguous, w_dtype) may each be NULL (ones, zeros); out has x's
- * dtype; mean and rstd (fp32 [n0 n1], row by row) are written when not NULL.  eps >= 0 and
+ * dtype; mean and rstd (fp32 [n0 n1], row by row) are written when not NULL and width is not 0.  eps >= 0 and
  * finite, else CCV_E_UNSUPPORTED.  out may not be x.  Statistics are fp32, the variance
  * summed from the deviations. */
 typedef struct ccv_norm_fwd_args {
@@ -541,7 +541,8 @@ int ccv_norm_bwd(const ccv_norm_bwd_args_t* args, void* hip_stream);
  *   out  = act(y), or with a gate [rows, groups width]: out = y act(gate)
  *
  * Row r of an array lies at r times its stride in elements; gate and out have x's dtype; weight and bias ([groups width],
- * contiguous, w_dtype) may each be NULL (ones, zeros); mean and rstd (fp32 [rows, groups]) are written when not NULL.
+ * contiguous, w_dtype) may each be NULL (ones, zeros); mean and rstd (fp32 [rows, groups]) are written when not NULL and
+ * width is not 0.
  * activation is CCV_ACT_NONE or CCV_ACT_SILU, eps >= 0 and finite (else CCV_E_UNSUPPORTED).  rows below
  * 2^31, groups width at most 2^24.  out may be no input.  Statistics are fp32, the variance summed from the deviations. */
 typedef struct ccv_group_norm_fwd_args {

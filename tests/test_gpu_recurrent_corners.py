@@ -16,13 +16,15 @@ def test_group_norm_of_very_many_narrow_groups(rows, groups, width, dtype, weigh
     check(f"{rows} rows of {groups} groups of {width}", x, groups, w, b, z, dout, "silu")
 
 
-def test_group_norm_without_channels():
+def test_norms_without_values():
     x = torch.zeros(2, 3, 0).cuda()
     out, mean, rstd = ccv.group_norm_fwd(x, 4, gate=x, activation="silu", return_stats=True)
     assert out.shape == x.shape and mean.shape == rstd.shape == (2, 3, 4) and bool((mean.isnan() & rstd.isnan()).all())
     y = x.clone().requires_grad_()
     ccv.group_norm_fn(y, 4).sum().backward()
     assert y.grad.shape == y.shape
+    out, mean, rstd = ccv.layer_norm_fwd(x, return_stats=True)
+    assert out.shape == x.shape and mean.shape == rstd.shape == (2, 3) and bool((mean.isnan() & rstd.isnan()).all())
 
 
 @pytest.mark.parametrize("wanted", [torch.float32, torch.float16, torch.bfloat16])

@@ -128,6 +128,17 @@ def test_group_norm_without_channels(calls_do_nothing, shape):  # noqa: F811
     assert y.grad.shape == y.shape
 
 
+@pytest.mark.parametrize("shape", [(0,), (5, 0), (2, 3, 4, 0)])
+def test_layer_norm_without_values(monkeypatch, shape):
+    """Statistics of nothing here too."""
+    monkeypatch.setattr(ccv, "_same_device", lambda x, **others: x.device)
+    monkeypatch.setitem(ccv._CALLS, "ccv_norm_fwd", lambda *values: None)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: torch.full(*a, 7.0, **kw))
+    out, mean, rstd = ccv.layer_norm_fwd(torch.zeros(shape), return_stats=True)
+    assert out.shape == shape and mean.shape == rstd.shape == shape[:-1]
+    assert bool(mean.isnan().all()) and bool(rstd.isnan().all())
+
+
 # ---- rotary positions ------------------------------------------------------------------------
 
 def test_rotary_refuses_frequencies_that_want_gradients(calls_do_nothing):  # noqa: F811
